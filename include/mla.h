@@ -316,6 +316,140 @@ MLA_API mla_status mla_up_project(const void* o_lat, const void* w_uv, void* o_o
                                   uint32_t* status, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * From new tokens to the rows that the sparse attention reads. The pages stop
+ * at the decode itself; these calls are this library's own: they write the
+ * caches that the decode reads, rotate its queries, and produce the `indices`
+ * of its token-sparse mode, or a block table that names only the pages worth
+ * attending, for the paged mode of any cache format.
+ *
+ * Rotary positions. A row of 64 dims at position p has its 32 pairs turned by
+ * the angles of row p of `rope_table` (device) fp32 [max_positions, 64], 32
+ * cosines then 32 sines, 16-B aligned: y0 = x0 cos - x1 sin, y1 = x0 sin +
+ * x1 cos, with every product and sum rounded to fp32 and the result rounded
+ * once to the type it is stored in. Pair i is dims (2i, 2i + 1) with
+ * MLA_ROPE_PAIRS, dims (i, i + 32) with MLA_ROPE_HALVES.
+ * `positions` (device) int32, one per token.
+ *
+ * Common to the writers: a token with slot < 0 (for the calls without slots:
+ * position < 0) is padding and leaves its destination as it was; a slot or
+ * position out of range is skipped and recorded as an index error (bit 1) in
+ * `status` (device, optional, 4-B aligned; read it with mla_read_status).
+ * Values must be finite. Strides are in elements and multiples of 8, row
+ * starts are 16-B aligned.
+ */
+typedef enum { MLA_ROPE_PAIRS = 0, MLA_ROPE_HALVES = 1 } mla_rope_style;
+
+/*
+ * Append n tokens to the paged latent cache, rotating the RoPE dims on the way.
+ * c_kv   (device) [n, 512] latent dims (V4.1 rows: 448), `dtype`, rows c_stride apart.
+ * k_rope (device) [n, 64] RoPE dims before rotation, rows r_stride apart; both
+ *        may be column ranges of one projection output.
+ * slots  (device) int32 [n] cache row page * 64 + offset of each token. The
+ *        slots of one call are distinct (of two equal ones, either token's
+ *        bytes may end up in the row).
+ * kvcache (device) written: rows of `kv_format` as mla_decode_with_kvcache
+ *        reads them. 16-bit rows: [latent, rotated RoPE] in `dtype`. 656-byte
+ *        rows: the latent dims quantised as in mla_quantize_kv_fp8, the rotated
+ *        RoPE dims rounded to bf16. V4.1 rows: 448 latent and 64 rotated RoPE
+ *        dims as one row of 512 values, quantised (the RoPE dims from their
+ *        fp32 values) as in mla_quantize_kv_fp8_528 / mla_quantize_kv_fp4_288.
+ *        Quantised formats take bf16 input (else MLA_ERR_UNSUPPORTED).
+ */
+MLA_API mla_status mla_append_kv(const void* c_kv, int64_t c_stride, const void* k_rope, int64_t r_stride, int dtype,
+                                 const int32_t* slots, const int32_t* positions, const float* rope_table,
+                                 int64_t max_positions, int rope_style, int64_t n, void* kvcache,
+                                 int64_t num_blocks, int page_block, int kv_format, uint32_t* status, void* stream);
+
+/*
+ * Rotate the RoPE dims of queries: out[t, h, :] = R(x[t, h, :]) over rows of 64.
+ * x, out (device) [tokens, heads, 64] with token and head strides; a typical
+ * call reads a slice of the query projection and writes dims [512, 576) of the
+ * decode's query (the ones mla_absorb_q leaves). out may be x (in place) or
+ * other columns of the same rows; any other overlap is refused.
+ */
+MLA_API mla_status mla_rotate_q(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                                int64_t out_token_stride, int64_t out_head_stride, int dtype,
+                                const int32_t* positions, const float* rope_table, int64_t max_positions,
+                                int rope_style, int64_t tokens, int heads, uint32_t* status, void* stream);
+
+/*
+ * The index cache: one 128-wide key per cached token, in pages of 64 like the
+ * latent cache and addressed by the same block table.
+ *  MLA_INDEX_16BIT  [num_blocks, 64, 128] of bf16 or fp16;
+ *  MLA_INDEX_FP8    pages of 8448 bytes: 64 rows of 128 e4m3 codes, then 64
+ *                   fp32 scales (amax / 448 of the row, 1 for a zero row).
+ *
+ * mla_append_index_k: k (device) [n, 128] of `dtype`, rows k_stride apart; dims
+ * [0, 64) are rotated, [64, 128) are kept; a 16-bit cache has type `dtype`.
+ *
+ * mla_quantize_index_q: the queries of an FP8 index. q (device) [tokens, heads,
+ * 128] with strides, dims [0, 64) rotated, every row quantised like a key; its
+ * scale is folded into the head's weight: q_out (device) uint8 [tokens, heads,
+ * 128] e4m3, weights_out[t, h] = weights[t, h] * scale (device fp32, contiguous;
+ * may be the same array). Index queries for a 16-bit cache are rotated by
+ * mla_rotate_q.
+ */
+typedef enum { MLA_INDEX_16BIT = 0, MLA_INDEX_FP8 = 1 } mla_index_format;
+
+#define MLA_INDEX_DIM 128
+#define MLA_INDEX_FP8_PAGE_BYTES 8448
+
+MLA_API mla_status mla_append_index_k(const void* k, int64_t k_stride, int dtype, const int32_t* slots,
+                                      const int32_t* positions, const float* rope_table, int64_t max_positions,
+                                      int rope_style, int64_t n, void* index_cache, int64_t num_blocks,
+                                      int page_block, int index_format, uint32_t* status, void* stream);
+MLA_API mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
+                                        const float* weights, const int32_t* positions, const float* rope_table,
+                                        int64_t max_positions, int rope_style, int64_t tokens, int heads,
+                                        uint8_t* q_out, float* weights_out, uint32_t* status, void* stream);
+
+/*
+ * The cheap score:
+ *     s[b, i, t] = ks_t * sum_h weights[b, i, h] * max(0, q[b, i, h, :] . k_t)
+ * over the visible tokens t of request b (L_b, or L_b - s_q + 1 + i when
+ * causal), accumulated in fp32; ks_t is the scale of an e4m3 key, else 1.
+ * q       (device) [batch, s_q, heads, 128] contiguous, 16-B aligned: `q_dtype`
+ *         and a 16-bit index cache of the same type, or e4m3 (q_dtype is not
+ *         read) with MLA_INDEX_FP8. heads is 1 to 64.
+ * weights (device) fp32 [batch, s_q, heads] (softmax scale and head gate).
+ * block   1: scores (device) fp32, column t of row b * s_q + i is token t;
+ *         64: column j is the maximum over the visible tokens of page j.
+ *         Rows are score_stride floats apart; columns [0, width) are written,
+ *         -inf where no token is visible.
+ * A request longer than `width` or its block-table row is scored as far as they
+ * reach, a token on an out-of-range page scores -inf; both are recorded as an
+ * index error in `status`.
+ */
+MLA_API mla_status mla_index_score(const void* q, int q_dtype, const float* weights, const void* index_cache,
+                                   int index_format, int64_t num_blocks, int page_block,
+                                   const int32_t* block_table, int max_blocks, const int32_t* cache_seqlens,
+                                   int batch, int s_q, int heads, int causal, int block, float* scores,
+                                   int64_t score_stride, int width, uint32_t* status, void* stream);
+
+/*
+ * The topk best columns of each row of `scores` (any fp32 matrix laid out like
+ * mla_index_score's; only the visible columns are read). Equal scores go to the
+ * lower position, NaN ranks below every number; the selected ones are written
+ * in ascending position.
+ * block = 1:  indices (device) int32 [batch, s_q, topk]: absolute cache rows
+ *             page * 64 + offset, -1 behind the last one: the `indices` of
+ *             mla_decode_with_kvcache. lens (device, optional) int32
+ *             [batch, s_q]: how many are selected.
+ * block = 64: indices: physical pages, -1 behind the last one; lens (required)
+ *             the tokens they hold. The last visible page always takes part and
+ *             comes last, so (indices, lens) are a block table [batch * s_q,
+ *             topk] and the cache_seqlens of a paged decode with one query per
+ *             request (batch * s_q requests, s_q = 1).
+ * A row with no visible token gets -1 everywhere and lens 0. An out-of-range
+ * page yields -1 in its place and an index error in `status`.
+ */
+MLA_API mla_status mla_select_topk(const float* scores, int64_t score_stride, int width,
+                                   const int32_t* cache_seqlens, int batch, int s_q, int causal, int block, int topk,
+                                   const int32_t* block_table, int max_blocks, int64_t num_blocks, int page_block,
+                                   int32_t* indices, int32_t* lens, uint32_t* status, void* stream);
+
+/*
  * Synchronise `stream`, read and clear the status word of `workspace` (or of
  * any 4-B status word, e.g. the one given to mla_absorb_q), and return the
  * first error it records, in the order timeout, stale metadata, index, range
@@ -326,8 +460,8 @@ MLA_API mla_status mla_read_status(void* workspace, void* stream, uint32_t* bits
 
 /*
  * Test hook for the time-out path (0, the default, turns it off). While it is
- * non-zero, every decode kernel (mla_decode_with_kvcache and its variants)
- * and absorption kernel (mla_absorb_q, mla_up_project) launched by this
+ * non-zero, every decode kernel (mla_decode_with_kvcache and its variants),
+ * absorption kernel (mla_absorb_q, mla_up_project) and index score launched by this
  * library first has one thread per CTA wait `cycles` SM cycles on a barrier
  * that nothing arrives at, before any copy or MMA is issued; the wait gives up, the kernel records the wait
  * time-out (status bit 2, MLA_ERR_TIMEOUT) and the CTA skips its work, so the

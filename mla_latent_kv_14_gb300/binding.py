@@ -5,6 +5,7 @@ the shared library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -76,6 +77,18 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
             f = getattr(lib, name)
             f.restype = c.c_int
             f.argtypes = [vp, vp, vp, c.c_int, c.c_int, c.c_int, vp, vp]
+        i32, i64 = c.c_int, c.c_int64
+        rope = [vp, vp, i64, i32]  # positions, table, its rows, style
+        lib.mla_append_kv.argtypes = [vp, i64, vp, i64, i32, vp] + rope + [i64, vp, i64, i32, i32, vp, vp]
+        lib.mla_rotate_q.argtypes = [vp, i64, i64, vp, i64, i64, i32] + rope + [i64, i32, vp, vp]
+        lib.mla_append_index_k.argtypes = [vp, i64, i32, vp] + rope + [i64, vp, i64, i32, i32, vp, vp]
+        lib.mla_quantize_index_q.argtypes = [vp, i64, i64, i32, vp] + rope + [i64, i32, vp, vp, vp, vp]
+        lib.mla_index_score.argtypes = [vp, i32, vp, vp, i32, i64, i32, vp, i32, vp, i32, i32, i32, i32, i32, vp,
+                                        i64, i32, vp, vp]
+        lib.mla_select_topk.argtypes = [vp, i64, i32, vp, i32, i32, i32, i32, i32, vp, i32, i64, i32, vp, vp, vp, vp]
+        for name in ("mla_append_kv", "mla_rotate_q", "mla_append_index_k", "mla_quantize_index_q",
+                     "mla_index_score", "mla_select_topk"):
+            getattr(lib, name).restype = c.c_int
         lib.mla_set_test_stall.restype = None
         lib.mla_set_test_stall.argtypes = [c.c_uint32]
         if path is None:
@@ -353,3 +366,246 @@ def mla_set_test_stall(cycles: int) -> None:
     absorption launch first waits ``cycles`` SM cycles on a barrier nothing
     arrives at, records a wait time-out and skips its work. 0 turns it off."""
     load_library().mla_set_test_stall(int(cycles))
+
+
+# ---------------------------------------------------------------------------
+# New tokens, index scores, selection
+# ---------------------------------------------------------------------------
+ROPE_PAIRS, ROPE_HALVES = 0, 1        # rope_style: pairs (2i, 2i+1), or (i, i+32)
+INDEX_16BIT, INDEX_FP8 = 0, 1         # index_format
+INDEX_DIM, INDEX_FP8_PAGE_BYTES = 128, 8448
+_KV_ROW = {KV_16BIT: 576, KV_FP8_656: 656, KV_FP8_528: 528, KV_FP4_288: 288}
+
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise MLAError(1, what)
+
+
+def _i32(t: torch.Tensor, shape: tuple, what: str):
+    _require(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape, what)
+
+
+def _place(where: str, *tensors: Optional[torch.Tensor]):
+    """The one device of the tensors, and a context in which it is current."""
+    given = [t for t in tensors if t is not None]
+    dev = given[0].device
+    _require(dev.type == "cuda" and all(t.device == dev for t in given), f"{where}: tensors of one cuda device")
+    same = torch.cuda.current_device() == dev.index
+    return dev, contextlib.nullcontext() if same else torch.cuda.device(dev)
+
+
+def _rope_args(where: str, positions: torch.Tensor, rope_table: torch.Tensor, rope_style: int, tokens: int):
+    _i32(positions, (tokens,), f"{where}: positions int32 [{tokens}]")
+    _require(rope_table.dtype == torch.float32 and rope_table.dim() == 2 and rope_table.shape[1] == 64 and
+             rope_table.is_contiguous(), f"{where}: rope_table fp32 [positions, 64]")
+    return _ptr(positions), _ptr(rope_table), int(rope_table.shape[0]), int(rope_style)
+
+
+def mla_rope_table(max_positions: int, base: float = 10000.0, inv_freq: Optional[torch.Tensor] = None,
+                   scale: float = 1.0, device=None) -> torch.Tensor:
+    """The rotation table [max_positions, 64] fp32: 32 cosines, then 32 sines, of
+    position * inv_freq (base ** (-i / 32) unless given), times ``scale``. The
+    angles are formed in 64 bits: far positions lose nothing."""
+    dev = _dev(device)
+    if inv_freq is None:
+        inv_freq = base ** (-torch.arange(32, dtype=torch.float64) / 32)
+    _require(tuple(inv_freq.shape) == (32,), "mla_rope_table: inv_freq [32]")
+    angle = torch.arange(max_positions, dtype=torch.float64, device=dev)[:, None] * inv_freq.to(dev, torch.float64)
+    return torch.cat((angle.cos() * scale, angle.sin() * scale), 1).float()
+
+
+def mla_append_kv(c_kv: torch.Tensor, k_rope: torch.Tensor, kvcache: torch.Tensor, slots: torch.Tensor,
+                  positions: torch.Tensor, rope_table: torch.Tensor, kv_format: int = KV_16BIT,
+                  rope_style: int = ROPE_PAIRS, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Append tokens to the paged cache in place: c_kv [n, 512] (V4.1 rows: 448)
+    and k_rope [n, 64], which is rotated on the way; ``slots`` int32 [n] are cache
+    rows (page * 64 + offset, negative: skip). Returns kvcache."""
+    lib, where = load_library(), "mla_append_kv"
+    fmt = _kv_format(False, kv_format)
+    latent = 448 if fmt >= KV_FP8_528 else 512
+    n = int(c_kv.shape[0])
+    _require(tuple(c_kv.shape) == (n, latent) and tuple(k_rope.shape) == (n, 64) and c_kv.stride(1) == 1 and
+             k_rope.stride(1) == 1 and k_rope.dtype == c_kv.dtype, f"{where}: c_kv [n, {latent}], k_rope [n, 64]")
+    _i32(slots, (n,), f"{where}: slots int32 [n]")
+    cache_type = c_kv.dtype if fmt == KV_16BIT else torch.uint8
+    _require(kvcache.is_contiguous() and kvcache.dtype == cache_type and kvcache.dim() >= 3 and
+             kvcache.shape[-1] == _KV_ROW[fmt] and kvcache.numel() == kvcache.shape[0] * kvcache.shape[1] * _KV_ROW[fmt],
+             f"{where}: kvcache [num_blocks, page_block, 1, {_KV_ROW[fmt]}] of {cache_type}")
+    rope = _rope_args(where, positions, rope_table, rope_style, n)
+    dev, current = _place(where, c_kv, k_rope, kvcache, slots, positions, rope_table, status)
+    with current:
+        st = lib.mla_append_kv(_ptr(c_kv), _stride(c_kv, 0, latent), _ptr(k_rope), _stride(k_rope, 0, 64),
+                               _dtype_code(c_kv), _ptr(slots), *rope, n, _ptr(kvcache), int(kvcache.shape[0]),
+                               int(kvcache.shape[1]), fmt, _ptr(status), _stream(dev))
+    _check(st, where)
+    return kvcache
+
+
+def _stride(t: torch.Tensor, dim: int, dense: int) -> int:
+    """The stride of ``dim``; of a dim with at most one entry, which is never
+    stepped over, the dense one (PyTorch leaves any number there)."""
+    return int(t.stride(dim)) if t.shape[dim] > 1 else dense
+
+
+def mla_rotate_q(x: torch.Tensor, positions: torch.Tensor, rope_table: torch.Tensor,
+                 out: Optional[torch.Tensor] = None, rope_style: int = ROPE_PAIRS,
+                 status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotate query rows: x [tokens, heads, 64] (any token and head strides, for
+    example ``q[..., 128:]`` of the projection) -> out, of the same shape
+    (``q_abs[..., 512:]``, ``x`` itself, or allocated; rows of tokens whose
+    position is negative are left as they are)."""
+    lib, where = load_library(), "mla_rotate_q"
+    _require(x.dim() == 3 and x.shape[2] == 64 and x.stride(2) == 1, f"{where}: x [tokens, heads, 64]")
+    tokens, heads = int(x.shape[0]), int(x.shape[1])
+    if out is None:
+        out = torch.zeros(tokens, heads, 64, dtype=x.dtype, device=x.device)
+    _require(out.shape == x.shape and out.dtype == x.dtype and out.stride(2) == 1, f"{where}: out like x")
+    rope = _rope_args(where, positions, rope_table, rope_style, tokens)
+    dev, current = _place(where, x, out, positions, rope_table, status)
+    with current:
+        st = lib.mla_rotate_q(_ptr(x), _stride(x, 0, 64 * heads), _stride(x, 1, 64), _ptr(out),
+                              _stride(out, 0, 64 * heads), _stride(out, 1, 64), _dtype_code(x), *rope, tokens, heads,
+                              _ptr(status), _stream(dev))
+    _check(st, where)
+    return out
+
+
+def _index_cache(where: str, cache: torch.Tensor, fmt: int, dtype: Optional[torch.dtype]) -> Tuple[int, int]:
+    """(num_blocks, page_block) of an index cache."""
+    _require(fmt in (INDEX_16BIT, INDEX_FP8), f"{where}: unknown index_format {fmt}")
+    if fmt == INDEX_FP8:
+        _require(cache.dim() == 2 and cache.shape[1] == INDEX_FP8_PAGE_BYTES and cache.dtype == torch.uint8 and
+                 cache.is_contiguous(), f"{where}: FP8 index cache uint8 [num_blocks, {INDEX_FP8_PAGE_BYTES}]")
+        return int(cache.shape[0]), 64
+    _require(cache.dim() >= 3 and cache.shape[-1] == INDEX_DIM and cache.is_contiguous() and cache.dtype == dtype and
+             cache.numel() == cache.shape[0] * cache.shape[1] * INDEX_DIM,
+             f"{where}: index cache [num_blocks, page_block, 1, {INDEX_DIM}] of {dtype}")
+    return int(cache.shape[0]), int(cache.shape[1])
+
+
+def mla_append_index_k(k: torch.Tensor, index_cache: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor,
+                       rope_table: torch.Tensor, index_format: int = INDEX_16BIT, rope_style: int = ROPE_PAIRS,
+                       status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Append index keys k [n, 128] (dims [0, 64) are rotated) to the paged index
+    cache in place: [num_blocks, 64, 1, 128] of k's type, or uint8 [num_blocks,
+    8448] with INDEX_FP8. ``slots`` as in :func:`mla_append_kv`."""
+    lib, where = load_library(), "mla_append_index_k"
+    n = int(k.shape[0])
+    _require(tuple(k.shape) == (n, INDEX_DIM) and k.stride(1) == 1, f"{where}: k [n, {INDEX_DIM}]")
+    _i32(slots, (n,), f"{where}: slots int32 [n]")
+    blocks, page = _index_cache(where, index_cache, index_format, k.dtype)
+    rope = _rope_args(where, positions, rope_table, rope_style, n)
+    dev, current = _place(where, k, index_cache, slots, positions, rope_table, status)
+    with current:
+        st = lib.mla_append_index_k(_ptr(k), _stride(k, 0, INDEX_DIM), _dtype_code(k), _ptr(slots), *rope, n,
+                                    _ptr(index_cache), blocks, page, index_format, _ptr(status), _stream(dev))
+    _check(st, where)
+    return index_cache
+
+
+def mla_quantize_index_q(q: torch.Tensor, weights: torch.Tensor, positions: torch.Tensor, rope_table: torch.Tensor,
+                         rope_style: int = ROPE_PAIRS, q_out: Optional[torch.Tensor] = None,
+                         weights_out: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Index queries q [tokens, heads, 128] (dims [0, 64) are rotated) as e4m3 rows,
+    with each row's scale folded into ``weights`` fp32 [tokens, heads]. Returns
+    (float8_e4m3fn [tokens, heads, 128], fp32 [tokens, heads])."""
+    lib, where = load_library(), "mla_quantize_index_q"
+    _require(q.dim() == 3 and q.shape[2] == INDEX_DIM and q.stride(2) == 1, f"{where}: q [tokens, heads, {INDEX_DIM}]")
+    tokens, heads = int(q.shape[0]), int(q.shape[1])
+    if q_out is None:
+        q_out = torch.zeros(tokens, heads, INDEX_DIM, dtype=torch.uint8, device=q.device).view(torch.float8_e4m3fn)
+    if weights_out is None:
+        weights_out = torch.zeros(tokens, heads, dtype=torch.float32, device=q.device)
+    _require(q_out.shape == q.shape and q_out.is_contiguous() and
+             q_out.dtype in (torch.float8_e4m3fn, torch.uint8), f"{where}: q_out e4m3 like q")
+    for w in (weights, weights_out):
+        _require(tuple(w.shape) == (tokens, heads) and w.is_contiguous() and w.dtype == torch.float32,
+                 f"{where}: weights fp32 [tokens, heads]")
+    rope = _rope_args(where, positions, rope_table, rope_style, tokens)
+    dev, current = _place(where, q, weights, positions, rope_table, q_out, weights_out, status)
+    with current:
+        st = lib.mla_quantize_index_q(_ptr(q), _stride(q, 0, INDEX_DIM * heads), _stride(q, 1, INDEX_DIM),
+                                      _dtype_code(q), _ptr(weights), *rope, tokens, heads, _ptr(q_out),
+                                      _ptr(weights_out), _ptr(status), _stream(dev))
+    _check(st, where)
+    return q_out, weights_out
+
+
+def mla_index_score(q: torch.Tensor, weights: torch.Tensor, index_cache: torch.Tensor, block_table: torch.Tensor,
+                    cache_seqlens: torch.Tensor, width: Optional[int] = None, causal: bool = False, block: int = 1,
+                    index_format: int = INDEX_16BIT, scores: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Scores fp32 [B, s_q, width] of the cached tokens (block=1) or pages
+    (block=64): sum_h weights[b, i, h] * relu(q[b, i, h] . k_t), -inf where
+    nothing is visible. q [B, s_q, heads, 128] of the index cache's type (e4m3
+    with INDEX_FP8); ``width`` defaults to what the block table reaches."""
+    lib, where = load_library(), "mla_index_score"
+    _require(q.dim() == 4 and q.shape[3] == INDEX_DIM and q.is_contiguous(), f"{where}: q [B, s_q, heads, {INDEX_DIM}]")
+    B, s_q, heads = (int(x) for x in q.shape[:3])
+    fp8 = index_format == INDEX_FP8
+    _require(q.dtype in (torch.float8_e4m3fn, torch.uint8) if fp8 else q.dtype in DTYPE_CODES, f"{where}: q's type")
+    _require(weights.dtype == torch.float32 and tuple(weights.shape) == (B, s_q, heads) and weights.is_contiguous(),
+             f"{where}: weights fp32 [B, s_q, heads]")
+    blocks, page = _index_cache(where, index_cache, index_format, q.dtype)
+    _require(block_table.dim() == 2, f"{where}: block_table int32 [B, max_blocks]")
+    max_blocks = int(block_table.shape[1])
+    _i32(block_table, (B, max_blocks), f"{where}: block_table int32 [B, max_blocks]")
+    _i32(cache_seqlens, (B,), f"{where}: cache_seqlens int32 [B]")
+    _require(block in (1, 64), f"{where}: block 1 or 64")
+    if width is None:
+        width = int(scores.shape[2]) if scores is not None else max_blocks * (64 // block)
+    if scores is None:
+        scores = torch.empty(B, s_q, width, dtype=torch.float32, device=q.device)
+    stride = _score_stride(where, scores, B, s_q, width)
+    dev, current = _place(where, q, weights, index_cache, block_table, cache_seqlens, scores, status)
+    with current:
+        st = lib.mla_index_score(_ptr(q), 0 if fp8 else DTYPE_CODES[q.dtype], _ptr(weights), _ptr(index_cache),
+                                 index_format, blocks, page, _ptr(block_table), max_blocks, _ptr(cache_seqlens), B,
+                                 s_q, heads, int(causal), block, _ptr(scores), stride, width, _ptr(status),
+                                 _stream(dev))
+    _check(st, where)
+    return scores
+
+
+def _score_stride(where: str, scores: torch.Tensor, B: int, s_q: int, width: int) -> int:
+    """Row stride of scores [B, s_q, width] (a column range of a wider buffer is fine)."""
+    _require(scores.dtype == torch.float32 and tuple(scores.shape) == (B, s_q, width) and
+             (width == 1 or scores.stride(2) == 1), f"{where}: scores fp32 [B, s_q, width]")
+    stride = scores.stride(1) if s_q > 1 else scores.stride(0) if B > 1 else width
+    _require(B == 1 or s_q == 1 or scores.stride(0) == s_q * stride, f"{where}: rows of scores equally spaced")
+    return int(stride)
+
+
+def mla_select_topk(scores: torch.Tensor, cache_seqlens: torch.Tensor, topk: int, block_table: torch.Tensor,
+                    num_blocks: int, causal: bool = False, block: int = 1, indices: Optional[torch.Tensor] = None,
+                    lens: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The ``topk`` best visible columns of scores [B, s_q, width], in ascending
+    position. block=1: (indices int32 [B, s_q, topk] of cache rows, -1 padded, and
+    their number [B, s_q]); block=64: (pages [B, s_q, topk] and the tokens they
+    hold [B, s_q]), the block table and lengths of a decode with B * s_q requests
+    of one query. ``num_blocks``: pages of the cache that the rows index."""
+    lib, where = load_library(), "mla_select_topk"
+    _require(scores.dim() == 3, f"{where}: scores fp32 [B, s_q, width]")
+    B, s_q, width = (int(x) for x in scores.shape)
+    stride = _score_stride(where, scores, B, s_q, width)
+    _require(block_table.dim() == 2, f"{where}: block_table int32 [B, max_blocks]")
+    max_blocks = int(block_table.shape[1])
+    _i32(block_table, (B, max_blocks), f"{where}: block_table int32 [B, max_blocks]")
+    _i32(cache_seqlens, (B,), f"{where}: cache_seqlens int32 [B]")
+    _require(topk > 0, f"{where}: topk")
+    if indices is None:
+        indices = torch.empty(B, s_q, topk, dtype=torch.int32, device=scores.device)
+    if lens is None:
+        lens = torch.empty(B, s_q, dtype=torch.int32, device=scores.device)
+    _i32(indices, (B, s_q, topk), f"{where}: indices int32 [B, s_q, topk]")
+    _i32(lens, (B, s_q), f"{where}: lens int32 [B, s_q]")
+    dev, current = _place(where, scores, cache_seqlens, block_table, indices, lens, status)
+    with current:
+        st = lib.mla_select_topk(_ptr(scores), stride, width, _ptr(cache_seqlens), B, s_q, int(causal), block, topk,
+                                 _ptr(block_table), max_blocks, int(num_blocks), 64, _ptr(indices), _ptr(lens),
+                                 _ptr(status), _stream(dev))
+    _check(st, where)
+    return indices, lens

@@ -21,7 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["mla_api.cu"]
+SOURCES = ["mla_api.cu", "cache_api.cu"]
 
 
 def _nvcc() -> str:

@@ -1,0 +1,324 @@
+// cache_api.cu -- the C entry points around the decode that write new tokens
+// and choose what the sparse attention reads: rotary positions, appends to the
+// paged caches, index queries, the index score and the selection
+// (include/mla.h). Every argument check happens before anything is enqueued.
+#include "host.h"
+#include "index_score.cuh"
+#include "params.h"
+#include "rows.cuh"
+#include "select.cuh"
+
+using namespace mla;
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+
+bool dtype_ok(int dtype) { return dtype == MLA_DTYPE_BF16 || dtype == MLA_DTYPE_FP16; }
+bool cache_ok(int64_t num_blocks, int page_block) {
+  return num_blocks > 0 && page_block == kTile && num_blocks < kMaxRows / kTile;
+}
+// strides in elements that keep 16-byte rows aligned
+bool stride_ok(int64_t s, int64_t least) { return s >= least && s % 8 == 0; }
+
+// Launched as a programmatic dependent: every kernel here waits for the grid
+// before it (griddepcontrol.wait) ahead of its first global access, so only
+// its launch overlaps that grid.
+template <typename P, typename... A>
+mla_status launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, void* stream, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  MLA_CUDA(cudaLaunchKernelEx(&cfg, kernel, p));
+  return MLA_OK;
+}
+
+// SMs of the current device, asked once per device
+mla_status sm_count(int* dev, int* sms) {
+  static std::atomic<int> known[kMaxDevices];
+  MLA_CUDA(cudaGetDevice(dev));
+  if (*dev >= kMaxDevices) return MLA_ERR_UNSUPPORTED;
+  *sms = known[*dev].load(std::memory_order_relaxed);
+  if (*sms > 0) return MLA_OK;
+  MLA_CUDA(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev));
+  known[*dev].store(*sms, std::memory_order_relaxed);
+  return MLA_OK;
+}
+
+mla_status check_positions(const rows::Positions& p) {
+  if (!p.positions || !p.table || !aligned(p.positions, 4) || !aligned(p.table, 16)) return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_append_kv(const void* c_kv, int64_t c_stride, const void* k_rope, int64_t r_stride, int dtype,
+                         const int32_t* slots, const int32_t* positions, const float* rope_table,
+                         int64_t max_positions, int rope_style, int64_t n, void* kvcache, int64_t num_blocks,
+                         int page_block, int kv_format, uint32_t* status, void* stream) {
+  if (n < 0 || n >= kMaxRows || max_positions <= 0 || !cache_ok(num_blocks, page_block)) return MLA_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || kv_format < MLA_KV_16BIT || kv_format > MLA_KV_FP4_288) return MLA_ERR_INVALID_ARG;
+  if (rope_style != MLA_ROPE_PAIRS && rope_style != MLA_ROPE_HALVES) return MLA_ERR_INVALID_ARG;
+  const int latent = kv_format >= MLA_KV_FP8_528 ? kDV41 - rows::kRope : kDV;
+  if (!stride_ok(c_stride, latent) || !stride_ok(r_stride, rows::kRope)) return MLA_ERR_INVALID_ARG;
+  if (status && !aligned(status, 4)) return MLA_ERR_INVALID_ARG;
+  if (kv_format && dtype != MLA_DTYPE_BF16) return MLA_ERR_UNSUPPORTED;  // quantised rows pair with bf16
+  if (n == 0) return MLA_OK;
+  if (!c_kv || !k_rope || !slots || !kvcache || !aligned(c_kv, 16) || !aligned(k_rope, 16) || !aligned(slots, 4) ||
+      !aligned(kvcache, 16))
+    return MLA_ERR_INVALID_ARG;
+  rows::AppendParams p{c_kv, k_rope, c_stride, r_stride, slots,
+                       {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
+                       n, static_cast<uint8_t*>(kvcache), num_blocks * kTile};
+  if (const mla_status v = check_positions(p.pos)) return v;
+  const dim3 grid((unsigned)((n + rows::kAppendWarps - 1) / rows::kAppendWarps));
+  const int threads = 32 * rows::kAppendWarps;
+  if (kv_format == MLA_KV_FP8_656)
+    return launch(rows::mla_append_kv_kernel<false, MLA_KV_FP8_656>, grid, threads, 0, stream, p);
+  if (kv_format == MLA_KV_FP8_528)
+    return launch(rows::mla_append_kv_kernel<false, MLA_KV_FP8_528>, grid, threads, 0, stream, p);
+  if (kv_format == MLA_KV_FP4_288)
+    return launch(rows::mla_append_kv_kernel<false, MLA_KV_FP4_288>, grid, threads, 0, stream, p);
+  if (dtype == MLA_DTYPE_FP16)
+    return launch(rows::mla_append_kv_kernel<true, MLA_KV_16BIT>, grid, threads, 0, stream, p);
+  return launch(rows::mla_append_kv_kernel<false, MLA_KV_16BIT>, grid, threads, 0, stream, p);
+}
+
+mla_status mla_rotate_q(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                        int64_t out_token_stride, int64_t out_head_stride, int dtype, const int32_t* positions,
+                        const float* rope_table, int64_t max_positions, int rope_style, int64_t tokens, int heads,
+                        uint32_t* status, void* stream) {
+  if (tokens < 0 || heads < 1 || tokens >= kMaxRows / heads || max_positions <= 0) return MLA_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || (rope_style != MLA_ROPE_PAIRS && rope_style != MLA_ROPE_HALVES)) return MLA_ERR_INVALID_ARG;
+  const int64_t xt = x_token_stride, xh = x_head_stride, ot = out_token_stride, oh = out_head_stride, w = rows::kRope;
+  if (!stride_ok(xt, 0) || !stride_ok(xh, 0) || !stride_ok(ot, w) || !stride_ok(oh, w)) return MLA_ERR_INVALID_ARG;
+  if (status && !aligned(status, 4)) return MLA_ERR_INVALID_ARG;
+  if (tokens == 0) return MLA_OK;
+  if (!x || !out || !aligned(x, 16) || !aligned(out, 16)) return MLA_ERR_INVALID_ARG;
+  // rows of the output must not overlap one another
+  if (tokens > 1 && heads > 1 && ot < (heads - 1) * oh + w && oh < (tokens - 1) * ot + w) return MLA_ERR_INVALID_ARG;
+  // in place (the same rows), in other columns of the same rows, or apart
+  const intptr_t xb = reinterpret_cast<intptr_t>(x), ob = reinterpret_cast<intptr_t>(out);
+  const int64_t xspan = 2 * ((tokens - 1) * xt + (heads - 1) * xh + w), ospan = 2 * ((tokens - 1) * ot + (heads - 1) * oh + w);
+  if (xb < ob + ospan && ob < xb + xspan) {
+    const bool same = (xt == ot || tokens == 1) && (xh == oh || heads == 1);
+    const int64_t apart = (xb < ob ? ob - xb : xb - ob) / 2, pitch = heads > 1 && (oh < ot || tokens == 1) ? oh : ot;
+    if (!same || (apart != 0 && (apart < w || apart > pitch - w))) return MLA_ERR_INVALID_ARG;
+  }
+  rows::RotateParams p{static_cast<const uint16_t*>(x), static_cast<uint16_t*>(out), xt, xh, ot, oh,
+                       {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
+                       tokens, heads, 0};
+  if (const mla_status v = check_positions(p.pos)) return v;
+  constexpr int kU = 4;
+  p.heads_per_slot = (uint32_t)((heads + kU - 1) / kU);
+  const int64_t items = tokens * p.heads_per_slot * 4;
+  const dim3 grid((unsigned)((items + rows::kRotateThreads - 1) / rows::kRotateThreads));
+  if (dtype == MLA_DTYPE_FP16)
+    return launch(rows::mla_rotate_kernel<true, kU>, grid, rows::kRotateThreads, 0, stream, p);
+  return launch(rows::mla_rotate_kernel<false, kU>, grid, rows::kRotateThreads, 0, stream, p);
+}
+
+mla_status mla_append_index_k(const void* k, int64_t k_stride, int dtype, const int32_t* slots,
+                              const int32_t* positions, const float* rope_table, int64_t max_positions,
+                              int rope_style, int64_t n, void* index_cache, int64_t num_blocks, int page_block,
+                              int index_format, uint32_t* status, void* stream) {
+  if (n < 0 || n >= kMaxRows || max_positions <= 0 || !cache_ok(num_blocks, page_block)) return MLA_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || (index_format != MLA_INDEX_16BIT && index_format != MLA_INDEX_FP8)) return MLA_ERR_INVALID_ARG;
+  if (rope_style != MLA_ROPE_PAIRS && rope_style != MLA_ROPE_HALVES) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(k_stride, rows::kIndexDim) || (status && !aligned(status, 4))) return MLA_ERR_INVALID_ARG;
+  if (n == 0) return MLA_OK;
+  if (!k || !slots || !index_cache || !aligned(k, 16) || !aligned(slots, 4) || !aligned(index_cache, 16))
+    return MLA_ERR_INVALID_ARG;
+  rows::IndexRowParams p{static_cast<const uint16_t*>(k), k_stride, 0, slots, nullptr,
+                         {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
+                         n, 1, static_cast<uint8_t*>(index_cache), nullptr, num_blocks * kTile};
+  if (const mla_status v = check_positions(p.pos)) return v;
+  const int per = rows::kIndexThreads / 16;
+  const dim3 grid((unsigned)((n + per - 1) / per));
+  const bool fp16 = dtype == MLA_DTYPE_FP16;
+  if (index_format == MLA_INDEX_FP8)
+    return fp16 ? launch(rows::mla_index_rows_kernel<true, true, true>, grid, rows::kIndexThreads, 0, stream, p)
+                : launch(rows::mla_index_rows_kernel<false, true, true>, grid, rows::kIndexThreads, 0, stream, p);
+  return fp16 ? launch(rows::mla_index_rows_kernel<true, false, true>, grid, rows::kIndexThreads, 0, stream, p)
+              : launch(rows::mla_index_rows_kernel<false, false, true>, grid, rows::kIndexThreads, 0, stream, p);
+}
+
+mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
+                                const float* weights, const int32_t* positions, const float* rope_table,
+                                int64_t max_positions, int rope_style, int64_t tokens, int heads, uint8_t* q_out,
+                                float* weights_out, uint32_t* status, void* stream) {
+  if (tokens < 0 || heads < 1 || tokens >= kMaxRows / heads || max_positions <= 0) return MLA_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || (rope_style != MLA_ROPE_PAIRS && rope_style != MLA_ROPE_HALVES)) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(q_token_stride, 0) || !stride_ok(q_head_stride, 0) || (status && !aligned(status, 4)))
+    return MLA_ERR_INVALID_ARG;
+  if (tokens == 0) return MLA_OK;
+  if (!q || !weights || !q_out || !weights_out || !aligned(q, 16) || !aligned(weights, 4) || !aligned(q_out, 16) ||
+      !aligned(weights_out, 4))
+    return MLA_ERR_INVALID_ARG;
+  rows::IndexRowParams p{static_cast<const uint16_t*>(q), q_token_stride, q_head_stride, nullptr, weights,
+                         {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
+                         tokens * heads, heads, q_out, weights_out, 0};
+  if (const mla_status v = check_positions(p.pos)) return v;
+  const int per = rows::kIndexThreads / 16;
+  const dim3 grid((unsigned)((p.rows + per - 1) / per));
+  if (dtype == MLA_DTYPE_FP16)
+    return launch(rows::mla_index_rows_kernel<true, true, false>, grid, rows::kIndexThreads, 0, stream, p);
+  return launch(rows::mla_index_rows_kernel<false, true, false>, grid, rows::kIndexThreads, 0, stream, p);
+}
+
+}  // extern "C"
+
+namespace {
+
+// rows of 128-byte chunks {x, y, z} with a 128-byte-swizzled box {128 B, by, bz}
+bool make_map_rows(CUtensorMap* m, const void* base, bool fp8, CUtensorMapDataType dt, uint64_t y, uint64_t z,
+                   uint64_t y_bytes, uint64_t z_bytes, uint32_t by, uint32_t bz) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)score::kDim, y, z};
+  cuuint64_t strides[2] = {y_bytes, z_bytes};
+  cuuint32_t box[3] = {fp8 ? 128u : 64u, by, bz};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kType, int kHp, bool kPages>
+mla_status launch_score(int dev, int grid, uint32_t smem, void* stream, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const score::ScoreParams& p) {
+  static std::atomic<bool> set[kMaxDevices];
+  auto kernel = score::mla_index_score_kernel<kType, kHp, kPages>;
+  if (!set[dev].load(std::memory_order_relaxed)) {
+    MLA_CUDA(set_smem(kernel, 232448));
+    set[dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(score::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  MLA_CUDA(cudaLaunchKernelEx(&cfg, kernel, tq, tk, p));
+  return MLA_OK;
+}
+template <int kType, int kHp, typename... A>
+mla_status launch_score_block(bool pages, A&&... a) {
+  return pages ? launch_score<kType, kHp, true>(a...) : launch_score<kType, kHp, false>(a...);
+}
+template <int kType, typename... A>
+mla_status launch_score_heads(int hp, A&&... a) {
+  if (hp == 16) return launch_score_block<kType, 16>(a...);
+  if (hp == 32) return launch_score_block<kType, 32>(a...);
+  return launch_score_block<kType, 64>(a...);
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_index_score(const void* q, int q_dtype, const float* weights, const void* index_cache,
+                           int index_format, int64_t num_blocks, int page_block, const int32_t* block_table,
+                           int max_blocks, const int32_t* cache_seqlens, int batch, int s_q, int heads, int causal,
+                           int block, float* scores, int64_t score_stride, int width, uint32_t* status,
+                           void* stream) {
+  if (index_format != MLA_INDEX_16BIT && index_format != MLA_INDEX_FP8) return MLA_ERR_INVALID_ARG;
+  const bool fp8 = index_format == MLA_INDEX_FP8, pages = block == kTile;
+  if (!fp8 && !dtype_ok(q_dtype)) return MLA_ERR_INVALID_ARG;
+  if (!cache_ok(num_blocks, page_block) || max_blocks <= 0 || batch <= 0 || s_q <= 0 || width <= 0 ||
+      score_stride < width || (block != 1 && !pages))
+    return MLA_ERR_INVALID_ARG;
+  if (heads < 1) return MLA_ERR_INVALID_ARG;
+  if (heads > 64) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)batch * s_q >= kMaxRows / heads) return MLA_ERR_INVALID_ARG;
+  if (!q || !weights || !index_cache || !block_table || !cache_seqlens || !scores || !aligned(q, 16) ||
+      !aligned(weights, 4) || !aligned(index_cache, 16) || !aligned(block_table, 4) || !aligned(cache_seqlens, 4) ||
+      !aligned(scores, 4) || (status && !aligned(status, 4)))
+    return MLA_ERR_INVALID_ARG;
+  const int64_t columns = (int64_t)width * (pages ? kTile : 1), reach = (int64_t)max_blocks * kTile;
+  const int64_t cover = columns < reach ? columns : reach;
+  if (cover >= kMaxRows - score::kTokens) return MLA_ERR_INVALID_ARG;
+
+  score::ScoreParams p{};
+  const int hp = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
+  const int most = score::kMaxN / hp, all = (s_q + most - 1) / most;  // groups of a request
+  p.nq = (s_q + all - 1) / all;
+  p.groups = all > 1 ? 2 : 1;
+  p.units = (s_q + p.nq * p.groups - 1) / (p.nq * p.groups);
+  const int64_t pairs = (int64_t)batch * p.units * ((cover + score::kTokens - 1) / score::kTokens);
+  if (pairs >= kMaxRows) return MLA_ERR_UNSUPPORTED;
+  const uint32_t q_bytes = (uint32_t)(p.groups * p.nq * hp) * (fp8 ? 128u : 256u);
+  uint32_t ring = (232448u - score::smem_bytes(q_bytes, 0)) / score::kUnit;
+  ring = ring > score::kMaxRing ? score::kMaxRing : ring;
+  p.ring = (int)ring;
+  p.weights = weights;
+  p.cache = static_cast<const uint8_t*>(index_cache);
+  p.block_table = block_table;
+  p.seqlens = cache_seqlens;
+  p.scores = scores;
+  p.stride = score_stride;
+  p.num_blocks = num_blocks;
+  p.max_blocks = max_blocks;
+  p.batch = batch;
+  p.s_q = s_q;
+  p.heads = heads;
+  p.causal = causal ? 1 : 0;
+  p.cover = (int)cover;
+  p.width = width;
+  p.status = status;
+  p.stall_cycles = g_test_stall.load(std::memory_order_relaxed);
+
+  int dev = 0, sms = 0;
+  if (const mla_status v = sm_count(&dev, &sms)) return v;
+  const int grid = (int)(pairs < sms ? pairs : sms);
+  const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : q_dtype == MLA_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t row = fp8 ? 128 : 256, page = fp8 ? rows::kIndexPageFp8 : kTile * 256;
+  CUtensorMap tq, tk;
+  if (!make_map_rows(&tq, q, fp8, dt, heads, (uint64_t)batch * s_q, row, row * heads, hp, p.nq) ||
+      !make_map_rows(&tk, index_cache, fp8, dt, kTile, num_blocks, row, page, kTile, 1))
+    return MLA_ERR_CUDA;
+  const uint32_t smem = score::smem_bytes(q_bytes, ring);
+  if (fp8) return launch_score_heads<score::K_FP8>(hp, pages, dev, grid, smem, stream, tq, tk, p);
+  if (q_dtype == MLA_DTYPE_FP16)
+    return launch_score_heads<score::K_FP16>(hp, pages, dev, grid, smem, stream, tq, tk, p);
+  return launch_score_heads<score::K_BF16>(hp, pages, dev, grid, smem, stream, tq, tk, p);
+}
+
+mla_status mla_select_topk(const float* scores, int64_t score_stride, int width, const int32_t* cache_seqlens,
+                           int batch, int s_q, int causal, int block, int topk, const int32_t* block_table,
+                           int max_blocks, int64_t num_blocks, int page_block, int32_t* indices, int32_t* lens,
+                           uint32_t* status, void* stream) {
+  const bool pages = block == kTile;
+  if (!cache_ok(num_blocks, page_block) || max_blocks <= 0 || batch <= 0 || s_q <= 0 || width <= 0 || topk <= 0 ||
+      score_stride < width || (block != 1 && !pages))
+    return MLA_ERR_INVALID_ARG;
+  if ((int64_t)batch * s_q >= kMaxRows) return MLA_ERR_INVALID_ARG;
+  const int64_t columns = (int64_t)width * (pages ? kTile : 1), reach = (int64_t)max_blocks * kTile;
+  if ((columns < reach ? columns : reach) >= kMaxRows - kTile) return MLA_ERR_INVALID_ARG;
+  if (!scores || !cache_seqlens || !block_table || !indices || (pages && !lens) || !aligned(scores, 4) ||
+      !aligned(cache_seqlens, 4) || !aligned(block_table, 4) || !aligned(indices, 4) || (lens && !aligned(lens, 4)) ||
+      (status && !aligned(status, 4)))
+    return MLA_ERR_INVALID_ARG;
+  select::SelectParams p{scores, score_stride, width, cache_seqlens, block_table, num_blocks, max_blocks,
+                         batch, s_q, causal ? 1 : 0, topk, indices, lens, status};
+  const dim3 grid((unsigned)(batch * s_q));
+  return pages ? launch(select::mla_select_topk_kernel<true>, grid, select::kThreads, 0, stream, p)
+               : launch(select::mla_select_topk_kernel<false>, grid, select::kThreads, 0, stream, p);
+}
+
+}  // extern "C"

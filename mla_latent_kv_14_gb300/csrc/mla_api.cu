@@ -1,19 +1,13 @@
 // mla_api.cu -- the C ABI declared in include/mla.h: argument checks, tensor
 // maps, launches. Every argument check happens before anything is enqueued.
-#include <cuda.h>
-#include <cuda_runtime.h>
-#include <cudaTypedefs.h>
-
-#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
-#include <mutex>
 
-#include "../../include/mla.h"
 #include "absorb.cuh"
 #include "decode_dense.cuh"
 #include "decode_fewheads.cuh"
+#include "host.h"
 #include "params.h"
 #include "quant.cuh"
 #include "sched.cuh"
@@ -22,49 +16,7 @@ using namespace mla;
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int kFewHeads = few::kNH;  // query heads of the transposed few-heads kernel
-
-mla_status cuda_fail(cudaError_t e) {
-  (void)cudaGetLastError();
-  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
-}
-
-#define MLA_CUDA(x)                              \
-  do {                                           \
-    cudaError_t e_ = (x);                        \
-    if (e_ != cudaSuccess) return cuda_fail(e_); \
-  } while (0)
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    (void)cudaGetLastError();
-  });
-  return fn;
-}
-
-// 2-D row-major tensor [rows, cols] of `elem` bytes, box [box_rows, box_cols]
-bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem, uint64_t rows, uint64_t cols,
-              uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {row_stride_bytes};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  (void)elem;
-  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // A [rows, 576] 16-bit tensor seen as [rows][9 chunks of 64 dims]: dims {64,
 // rows, 9} with chunk stride 128 B; one box = box_rows rows x box_chunks chunks,
@@ -92,20 +44,11 @@ bool make_map_4d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, const
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// test hook (mla_set_test_stall): cycles the next launches wait on a barrier
-// nothing arrives at before giving up; 0 in normal use
-std::atomic<uint32_t> g_test_stall{0};
-
 // per-device number of co-resident 2-CTA clusters of the 128-head decode
 // kernel, and of co-resident CTAs of the few-heads kernel
 std::atomic<int> g_parts[kMaxDevices];
 std::atomic<int> g_parts_few[kMaxDevices];
 std::once_flag g_attr_once[kMaxDevices];
-
-template <typename K>
-cudaError_t set_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
 
 template <int kMode>
 cudaError_t set_mode_smem() {

@@ -13,4 +13,8 @@ from .mla_oracle import (  # noqa: F401
     quantize_kv_fp8_528, dequantize_kv_fp8_528, quantize_kv_fp4_288, dequantize_kv_fp4_288,
     attend, visible_rows, mla_decode, absorb_q, up_project,
     bf16_to_f64, to_f64,
+    encode_kv_fp8_528, encode_kv_fp4_288,
+)
+from .index_oracle import (  # noqa: F401
+    rope_table, rotate, round_to, append_rows, index_row_codes, index_score, index_score_error, page_max, select_topk,
 )

@@ -228,7 +228,11 @@ def quantize_kv_fp8_528(rows) -> np.ndarray:
     512 + j holds k + 127. Byte d holds e4m3_rne(x_d / 2^k), the division
     being exact.
     """
-    x = _rows_bf16_f64(rows, V41_DIM)
+    return encode_kv_fp8_528(_rows_bf16_f64(rows, V41_DIM))
+
+
+def encode_kv_fp8_528(x: np.ndarray) -> np.ndarray:
+    """The same for values [N, 512] of any precision (float64)."""
     n = x.shape[0]
     blocks = x.reshape(n, 16, 32)
     amax = np.max(np.abs(blocks), axis=2)
@@ -279,7 +283,11 @@ def quantize_kv_fp4_288(rows) -> np.ndarray:
     value becomes e2m1_rne(x / v) (0 with the sign of x when v = 0); byte i
     holds value 2i in its low nibble and value 2i + 1 in its high nibble.
     """
-    x = _rows_bf16_f64(rows, V41_DIM)
+    return encode_kv_fp4_288(_rows_bf16_f64(rows, V41_DIM))
+
+
+def encode_kv_fp4_288(x: np.ndarray) -> np.ndarray:
+    """The same for values [N, 512] of any precision (float64)."""
     n = x.shape[0]
     blocks = x.reshape(n, 32, 16)
     amax = np.max(np.abs(blocks), axis=2)

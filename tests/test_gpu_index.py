@@ -1,0 +1,525 @@
+"""GPU parity of the calls around the decode: appends to the paged caches,
+rotation, index rows, the index score and the selection, against the 64-bit
+oracle; and a run of them together, as a serving step uses them.
+
+Rows are compared bit for bit (the rotation's roundings are part of its
+definition). Scores carry the oracle's own bound of an fp32 evaluation.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from tests.helpers import assert_close_attn
+
+pytestmark = pytest.mark.gpu
+
+mla = pytest.importorskip("mla_latent_kv_14_gb300")
+DEV = "cuda"
+PAGE = 64
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    mla.load_library()
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def _bits(status):
+    torch.cuda.synchronize()
+    return int(status.item())
+
+
+TABLE = oracle.rope_table(5000)
+
+
+def _table():
+    return torch.from_numpy(TABLE).to(DEV)
+
+
+def _new(n, seed, pages):
+    """Distinct slots with some -1 and one behind the cache, positions with one out of range."""
+    rng = np.random.default_rng(seed)
+    slots = rng.permutation(pages * PAGE)[:n].astype(np.int32)
+    pos = rng.integers(0, 5000, n).astype(np.int32)
+    bad = 0
+    if n > 8:
+        slots[[1, n - 1]] = -1
+        slots[3], pos[5], pos[6] = pages * PAGE, 5000, -1
+        bad = 1
+    keep = (slots >= 0) & (slots < pages * PAGE) & (pos >= 0) & (pos < 5000)
+    return slots, pos, keep, bad
+
+
+# ---------------------------------------------------------------------------
+# appends
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("halves", [0, 1])
+@pytest.mark.parametrize("fmt,dtype", [(0, BF), (0, HF), (1, BF), (2, BF), (3, BF)])
+@pytest.mark.parametrize("n", [1, 63, 130])
+def test_append_kv(n, fmt, dtype, halves):
+    latent, pages = (448 if fmt >= 2 else 512), 5
+    kv = torch.randn(n, latent + 64 + 8, generator=_gen(n)).to(dtype)
+    if n > 20:
+        kv[10] = 0                                     # a zero block
+        kv[11, :latent] *= 1e-6                        # tiny scales
+        kv[12, 3] = 60000.0 if dtype == HF else 3.0e4
+    slots, pos, keep, bad = _new(n, n + fmt, pages)
+    width = {0: 576, 1: 656, 2: 528, 3: 288}[fmt]
+    cache = torch.randint(0, 256, (pages, PAGE, 1, width * (2 if fmt == 0 else 1)), dtype=torch.uint8, generator=_gen(7))
+    want = cache.clone().view(pages * PAGE, -1)
+    rows = oracle.append_rows(kv[:, :latent], kv[:, latent:latent + 64], TABLE[np.clip(pos, 0, 4999)], bool(halves), fmt)
+    want[torch.from_numpy(slots[keep]).long()] = rows[torch.from_numpy(keep)]
+    dev, st = kv.to(DEV), _status()
+    got = cache.to(DEV)
+    got = got.view(dtype) if fmt == 0 else got
+    back = mla.mla_append_kv(dev[:, :latent], dev[:, latent:latent + 64], got, torch.from_numpy(slots).to(DEV),
+                             torch.from_numpy(pos).to(DEV), _table(), kv_format=fmt, rope_style=halves, status=st)
+    assert back is got and _bits(st) == bad
+    assert torch.equal(got.view(torch.uint8).cpu().view(pages * PAGE, -1), want)
+
+
+def test_append_equals_the_contiguous_quantisers():
+    """At position 0 (no turn) the rows are those of mla_quantize_kv_*."""
+    n = 64
+    for fmt, quant, w in ((1, mla.mla_quantize_kv_fp8, 576), (2, mla.mla_quantize_kv_fp8_528, 512),
+                          (3, mla.mla_quantize_kv_fp4_288, 512)):
+        kv = torch.randn(n, w, generator=_gen(fmt)).to(BF).to(DEV)
+        want = quant(kv)
+        cache = torch.zeros(1, 64, 1, want.shape[-1], dtype=torch.uint8, device=DEV)
+        zero = torch.zeros(n, dtype=torch.int32, device=DEV)
+        mla.mla_append_kv(kv[:, : w - 64], kv[:, w - 64:], cache, torch.arange(n, dtype=torch.int32, device=DEV), zero,
+                          _table(), kv_format=fmt)
+        assert torch.equal(cache.view(n, -1), want)
+
+
+@pytest.mark.parametrize("halves", [0, 1])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("tokens,heads", [(1, 1), (3, 128), (65, 5), (7, 16), (40, 33)])
+def test_rotate_q(tokens, heads, dtype, halves):
+    x = torch.randn(tokens, heads, 192, generator=_gen(tokens)).to(dtype)
+    rng = np.random.default_rng(tokens)
+    pos = rng.integers(0, 5000, tokens).astype(np.int32)
+    bad = 0
+    if tokens > 4:
+        pos[2], pos[4], bad = -1, 5000, 1
+    keep = torch.from_numpy((pos >= 0) & (pos < 5000))
+    rot = oracle.round_to(oracle.rotate(x[..., 128:], TABLE[np.clip(pos, 0, 4999)][:, None], bool(halves)), dtype)
+    p = torch.from_numpy(pos).to(DEV)
+    # a slice of the projection into a slice of the decode's query
+    q = torch.full((tokens, heads, 576), 7.0, dtype=dtype, device=DEV)
+    xd, st = x.to(DEV), _status()
+    mla.mla_rotate_q(xd[..., 128:], p, _table(), out=q[..., 512:], rope_style=halves, status=st)
+    assert _bits(st) == bad
+    want = torch.full((tokens, heads, 576), 7.0, dtype=dtype)
+    want[..., 512:][keep] = rot[keep]
+    assert torch.equal(q.cpu(), want)
+    # in place, and into other columns of the same rows
+    inplace, beside = x.to(DEV), x.to(DEV)
+    mla.mla_rotate_q(inplace[..., 128:], p, _table(), out=inplace[..., 128:], rope_style=halves)
+    mla.mla_rotate_q(beside[..., 128:], p, _table(), out=beside[..., :64], rope_style=halves)
+    want, want2 = x.clone(), x.clone()
+    want[..., 128:][keep] = rot[keep]
+    want2[..., :64][keep] = rot[keep]
+    assert torch.equal(inplace.cpu(), want) and torch.equal(beside.cpu(), want2)
+    # heads-major storage, and one row for every head
+    major = x[..., 128:].transpose(0, 1).contiguous().to(DEV).transpose(0, 1)
+    got = mla.mla_rotate_q(major, p, _table(), rope_style=halves)
+    assert torch.equal(got.cpu()[keep], rot[keep]) and (got.cpu()[~keep] == 0).all()
+    shared = mla.mla_rotate_q(xd[:, :1, 128:].expand(-1, heads, -1), p, _table(), rope_style=halves)
+    assert torch.equal(shared.cpu()[keep], rot[:, :1].expand(-1, heads, -1)[keep])
+
+
+@pytest.mark.parametrize("halves", [0, 1])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [1, 17, 130])
+def test_append_index_k(n, fp8, dtype, halves):
+    pages = 4
+    k = torch.randn(n, 160, generator=_gen(n)).to(dtype)
+    if n > 12:
+        k[12] = 0
+    slots, pos, keep, bad = _new(n, n, pages)
+    v, codes, scale = oracle.index_row_codes(k[:, :128], TABLE[np.clip(pos, 0, 4999)], bool(halves))
+    at = slots[keep]
+    cache = torch.randint(0, 256, (pages, 8448 if fp8 else PAGE * 256), dtype=torch.uint8, generator=_gen(3))
+    want = cache.clone().numpy()
+    if fp8:
+        want[:, :8192].reshape(pages, PAGE, 128)[at // PAGE, at % PAGE] = codes[keep]
+        w = want[:, 8192:].copy().view(np.float32)
+        w[at // PAGE, at % PAGE] = scale[keep]
+        want[:, 8192:] = w.view(np.uint8)
+        got = cache.to(DEV)
+    else:
+        rows = oracle.round_to(v, dtype).view(torch.uint8).numpy()
+        want.reshape(pages * PAGE, 256)[at] = rows[keep]
+        got = cache.to(DEV).view(dtype).view(pages, PAGE, 1, 128)
+    st = _status()
+    mla.mla_append_index_k(k.to(DEV)[:, :128], got, torch.from_numpy(slots).to(DEV), torch.from_numpy(pos).to(DEV), _table(),
+                           index_format=mla.INDEX_FP8 if fp8 else mla.INDEX_16BIT, rope_style=halves, status=st)
+    assert _bits(st) == bad
+    assert (got.view(torch.uint8).cpu().numpy().reshape(pages, -1) == want).all()
+
+
+@pytest.mark.parametrize("halves", [0, 1])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("tokens,heads", [(1, 64), (9, 3), (33, 32)])
+def test_quantize_index_q(tokens, heads, dtype, halves):
+    q = torch.randn(tokens, heads, 192, generator=_gen(heads)).to(dtype)
+    w = torch.randn(tokens, heads, generator=_gen(heads + 1))
+    q[0, 0] = 0
+    pos = np.random.default_rng(heads).integers(0, 5000, tokens).astype(np.int32)
+    bad = 0
+    if tokens > 4:
+        pos[2], pos[4], bad = -1, 5000, 1
+    keep = (pos >= 0) & (pos < 5000)
+    _, codes, scale = oracle.index_row_codes(q[..., 64:], TABLE[np.clip(pos, 0, 4999)][:, None], bool(halves))
+    st = _status()
+    q8, wo = mla.mla_quantize_index_q(q.to(DEV)[..., 64:], w.to(DEV), torch.from_numpy(pos).to(DEV), _table(), rope_style=halves, status=st)
+    assert _bits(st) == bad and q8.dtype == torch.float8_e4m3fn
+    assert (q8.view(torch.uint8).cpu().numpy() == np.where(keep[:, None, None], codes, 0)).all()
+    assert (wo.cpu().numpy() == np.where(keep[:, None], w.numpy() * scale, 0)).all()
+    wd = w.to(DEV)
+    mla.mla_quantize_index_q(q.to(DEV)[..., 64:], wd, torch.from_numpy(pos).to(DEV), _table(), rope_style=halves, weights_out=wd)
+    assert (wd.cpu().numpy() == np.where(keep[:, None], w.numpy() * scale, w.numpy())).all()
+
+
+# ---------------------------------------------------------------------------
+# score
+# ---------------------------------------------------------------------------
+def _score_case(lens, s_q, heads, kind, seed, spare=1):
+    """Queries, weights, a paged index cache, its block table, and the values they stand for."""
+    rng = np.random.default_rng(seed)
+    B, most = len(lens), max(1, -(-max(lens) // PAGE))
+    pages = B * most + spare
+    bt = rng.permutation(pages)[: B * most].reshape(B, most).astype(np.int32)
+    g = _gen(seed)
+    q, k = torch.randn(B, s_q, heads, 128, generator=g), torch.randn(pages, PAGE, 128, generator=g)
+    w = torch.randn(B, s_q, heads, generator=g) / heads
+    if kind == "fp8":
+        _, qc, qs = oracle.index_row_codes(q.to(BF), TABLE[:1], False)
+        _, kc, ks = oracle.index_row_codes(k.to(BF), TABLE[:1], False)
+        q8 = torch.from_numpy(qc).view(torch.float8_e4m3fn)
+        w = w * torch.from_numpy(qs)
+        cache = torch.from_numpy(np.concatenate((kc.reshape(pages, -1), ks.view(np.uint8).reshape(pages, -1)), axis=1))
+        vals = oracle.e4m3_value_table()
+        return q8, w, cache, bt, vals[qc], vals[kc] * ks.astype(np.float64)[..., None]
+    dtype = BF if kind == "bf16" else HF
+    q, k = q.to(dtype), k.to(dtype)
+    return q, w, k.unsqueeze(2).contiguous(), bt, oracle.to_f64(q), oracle.to_f64(k)
+
+
+def _score_ref(lens, s_q, causal, bt, qv, w, kv, width, bad=()):
+    """(scores, bound) [B, s_q, width] by tokens."""
+    B = len(lens)
+    ref, err = np.full((B, s_q, width), -np.inf), np.zeros((B, s_q, width))
+    for b in range(B):
+        keys = kv[bt[b]].reshape(-1, 128)
+        s, e = (f(qv[b], oracle.to_f64(w[b]), keys) for f in (oracle.index_score, oracle.index_score_error))
+        for i in range(s_q):
+            v = max(0, min(lens[b] - (s_q - 1 - i if causal else 0), width, keys.shape[0]))
+            ref[b, i, :v], err[b, i, :v] = s[i, :v], e[i, :v]
+        for p in bad:
+            if p[0] == b:
+                ref[b, :, p[1] * PAGE:(p[1] + 1) * PAGE] = -np.inf
+    return ref, err
+
+
+def _check_scores(got, ref, err, what):
+    got = got.double().cpu().numpy()
+    inf = np.isneginf(ref)
+    assert (np.isneginf(got) == inf).all(), f"{what}: -inf at other places"
+    off = np.abs(np.where(inf, 0, got) - np.where(inf, 0, ref))
+    bad = off > err
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.size} beyond the bound, worst {(off / np.maximum(err, 1e-30)).max():.3g} of it"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("lens,s_q,heads,causal", [
+    ([1], 1, 1, False),
+    ([64, 65, 127, 128, 129], 1, 64, False),
+    ([0, 300, 0, 1], 2, 16, True),                 # no token; fewer tokens than queries
+    ([700, 33], 5, 64, True),                      # two groups of three queries, one of them empty
+    ([513], 17, 33, False),                        # padded heads
+    ([250, 900], 9, 20, True),
+    ([190], 40, 7, True),                          # several units of 32 queries
+])
+def test_index_score(lens, s_q, heads, causal, kind):
+    q, w, cache, bt, qv, kv = _score_case(lens, s_q, heads, kind, seed=heads + s_q)
+    fmt = mla.INDEX_FP8 if kind == "fp8" else mla.INDEX_16BIT
+    args = (q.to(DEV), w.to(DEV), cache.to(DEV), torch.from_numpy(bt).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV))
+    st = _status()
+    width = max(1, max(lens))
+    ref, err = _score_ref(lens, s_q, causal, bt, qv, w, kv, width)
+    got = mla.mla_index_score(*args, width=width, causal=causal, index_format=fmt, status=st)
+    assert _bits(st) == 0
+    _check_scores(got, ref, err, f"{kind} tokens")
+    # the default width (the block table's reach), into a column range of a wider buffer
+    wide = torch.full((len(lens), s_q, bt.shape[1] * PAGE + 3), 7.0, device=DEV)
+    mla.mla_index_score(*args, causal=causal, index_format=fmt, scores=wide[..., :-3], status=st)
+    ref, err = _score_ref(lens, s_q, causal, bt, qv, w, kv, bt.shape[1] * PAGE)
+    _check_scores(wide[..., :-3], ref, err, f"{kind} wide")
+    assert (wide[..., -3:] == 7.0).all() and _bits(st) == 0
+    pages = mla.mla_index_score(*args, causal=causal, index_format=fmt, block=64, status=st)
+    _check_scores(pages, oracle.page_max(ref), np.maximum(oracle.page_max(err), 0), f"{kind} pages")
+    assert _bits(st) == 0
+
+
+def test_index_score_many_tiles_per_cta():
+    """More (unit, tile) pairs than CTAs, ragged: ranges that end inside a unit, rings that wrap."""
+    lens, s_q, heads = [9000, 0, 17000, 130, 4096], 11, 64
+    for kind in ("bf16", "fp8"):
+        q, w, cache, bt, qv, kv = _score_case(lens, s_q, heads, kind, seed=5)
+        fmt = mla.INDEX_FP8 if kind == "fp8" else mla.INDEX_16BIT
+        got = mla.mla_index_score(q.to(DEV), w.to(DEV), cache.to(DEV), torch.from_numpy(bt).to(DEV),
+                                  torch.tensor(lens, dtype=torch.int32, device=DEV), width=17000, causal=True, index_format=fmt)
+        ref, err = _score_ref(lens, s_q, True, bt, qv, w, kv, 17000)
+        _check_scores(got, ref, err, kind)
+
+
+def test_index_score_bad_pages_and_short_columns():
+    lens = [300, 200]
+    for kind in ("bf16", "fp8"):
+        q, w, cache, bt, qv, kv = _score_case(lens, 1, 64, kind, seed=9)
+        bad = bt.copy()
+        bad[0, 1], bad[1, 3], bad[1, 4] = -1, cache.shape[0], -7        # the last one is behind the request
+        st = _status()
+        fmt = mla.INDEX_FP8 if kind == "fp8" else mla.INDEX_16BIT
+        args = (q.to(DEV), w.to(DEV), cache.to(DEV), torch.from_numpy(bad).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV))
+        got = mla.mla_index_score(*args, index_format=fmt, status=st)
+        assert _bits(st) == 1
+        ref, err = _score_ref(lens, 1, False, bt, qv, w, kv, bt.shape[1] * PAGE, bad=[(0, 1), (1, 3)])
+        _check_scores(got, ref, err, kind)
+        st = _status()
+        args = args[:3] + (torch.from_numpy(bt).to(DEV),) + args[4:]
+        got = mla.mla_index_score(*args, width=77, index_format=fmt, status=st)   # narrower than the requests
+        assert _bits(st) == 1
+        ref, err = _score_ref(lens, 1, False, bt, qv, w, kv, 77)
+        _check_scores(got, ref, err, kind)
+
+
+def test_index_score_timeout_is_reported():
+    q, w, cache, bt, qv, kv = _score_case([200], 1, 16, "bf16", seed=1)
+    args = (q.to(DEV), w.to(DEV), cache.to(DEV), torch.from_numpy(bt).to(DEV), torch.tensor([200], dtype=torch.int32, device=DEV))
+    st = _status()
+    mla.mla_set_test_stall(100000)
+    try:
+        mla.mla_index_score(*args, status=st)
+    finally:
+        mla.mla_set_test_stall(0)
+    code, bits = mla.mla_read_status(st)
+    assert code == 5 and bits == 2
+    ref, err = _score_ref([200], 1, False, bt, qv, w, kv, 256)
+    _check_scores(mla.mla_index_score(*args, status=st), ref, err, "after the time-out")
+    assert _bits(st) == 0
+
+
+# ---------------------------------------------------------------------------
+# selection
+# ---------------------------------------------------------------------------
+def _select_ref(scores, lens, s_q, causal, block, topk, bt, pages):
+    B, width = len(lens), scores.shape[-1]
+    idx, out = np.full((B, s_q, topk), -1, np.int64), np.zeros((B, s_q), np.int64)
+    for b in range(B):
+        for i in range(s_q):
+            seen = max(0, min(lens[b] - (s_q - 1 - i if causal else 0), width * block, bt.shape[1] * PAGE))
+            n = -(-seen // block)
+            at = oracle.select_topk(scores[b, i], n, topk, last=block > 1)
+            pg = bt[b, at if block > 1 else at // PAGE].astype(np.int64)
+            rows = pg if block > 1 else pg * PAGE + at % PAGE
+            idx[b, i, : len(at)] = np.where((pg >= 0) & (pg < pages), rows, -1)
+            out[b, i] = len(at) if block == 1 else (len(at) - 1) * PAGE + seen - (n - 1) * PAGE if n else 0
+    return idx, out
+
+
+def _select_both(scores, lens, s_q, causal, block, topk, bt, pages, bits=0):
+    st = _status()
+    idx, out = mla.mla_select_topk(scores.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), topk,
+                                   torch.from_numpy(bt).to(DEV), pages, causal=causal, block=block, status=st)
+    assert _bits(st) == bits
+    ref, want = _select_ref(scores.numpy(), lens, s_q, causal, block, topk, bt, pages)
+    assert (out.cpu().numpy() == want).all()
+    assert (idx.cpu().numpy() == ref).all()
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties", "equal", "special"])
+@pytest.mark.parametrize("block,topk", [(1, 1), (1, 64), (1, 2048), (64, 1), (64, 7), (64, 100)])
+def test_select_topk(block, topk, kind):
+    lens, s_q = [0, 1, 64, 65, 2500, 2047, 2048], 3
+    rng = np.random.default_rng(topk)
+    most = -(-max(lens) // PAGE)
+    pages = len(lens) * most + 2
+    bt = rng.permutation(pages)[: len(lens) * most].reshape(len(lens), most).astype(np.int32)
+    width = most * PAGE // block
+    s = torch.randn(len(lens), s_q, width, generator=_gen(topk))
+    if kind == "ties":
+        s = (s * 2).round() / 2
+    elif kind == "equal":
+        s = torch.zeros_like(s)
+        s[..., ::2] = -0.0
+    elif kind == "special":
+        r = torch.rand(s.shape, generator=_gen(1))
+        s[r < 0.3], s[r < 0.2], s[r < 0.1], s[r < 0.05] = float("nan"), float("inf"), float("-inf"), 0.0
+        s[r > 0.9] = 1e-41                             # a subnormal
+    for causal in (False, True):
+        _select_both(s, lens, s_q, causal, block, topk, bt, pages)
+
+
+def test_select_bad_pages_and_hidden_columns():
+    """Columns behind the visible ones are not read; bad pages come out as -1."""
+    lens = [200, 130]
+    bt = np.array([[0, -1, 2, 3], [4, 5, 9, -1]], dtype=np.int32)
+    s = torch.randn(2, 1, 256, generator=_gen(2))
+    s[0, 0, 200:], s[1, 0, 130:] = float("nan"), float("inf")
+    _select_both(s, lens, 1, False, 1, 100, bt, 8, bits=1)
+    _select_both(s, lens, 1, False, 1, 300, bt, 8, bits=1)
+    _select_both(s[..., :4].contiguous(), lens, 1, False, 64, 3, bt, 8, bits=1)
+    _select_both(s[..., :100].contiguous(), lens, 1, False, 1, 20, np.abs(bt) % 8, 8, bits=1)   # fewer columns than tokens
+
+
+@pytest.mark.parametrize("n", [5000, 40000, 131072, 300001])
+def test_select_long_rows(n):
+    rng = np.random.default_rng(n)
+    most = -(-n // PAGE)
+    bt = rng.permutation(most).reshape(1, most).astype(np.int32)
+    s = torch.relu(torch.randn(1, 2, n, generator=_gen(n)))           # half of it exactly zero
+    for topk in (2048, n // 2 + 100, n - 1, n + 5):                   # inside the positive half, among the zeros, all
+        _select_both(s, [n], 2, True, 1, topk, bt, most)
+
+
+# ---------------------------------------------------------------------------
+# a run of them together
+# ---------------------------------------------------------------------------
+def _step(lens, seed, kv_format, index_format, kv_dtype=BF):
+    """Appends every token of each request, rotates the queries and scores: what a serving step has in hand."""
+    B, h, hi = len(lens), 128, 32
+    rng = np.random.default_rng(seed)
+    most = -(-max(lens) // PAGE)
+    pages = B * most
+    bt = rng.permutation(pages).reshape(B, most).astype(np.int32)
+    slots = np.concatenate([bt[b, np.arange(L) // PAGE] * PAGE + np.arange(L) % PAGE for b, L in enumerate(lens)]).astype(np.int32)
+    pos = np.concatenate([np.arange(L) for L in lens]).astype(np.int32)
+    n = len(slots)
+    g = _gen(seed)
+    kv = torch.randn(n, 576, generator=g).to(kv_dtype)
+    q = torch.randn(B, h, 576, generator=g).to(kv_dtype)
+    k_idx, q_idx = torch.randn(n, 128, generator=g).to(BF), torch.randn(B, hi, 128, generator=g).to(BF)
+    w = torch.randn(B, hi, generator=g) / hi
+    qpos = np.array(lens, dtype=np.int32) - 1
+    d = lambda t: (torch.from_numpy(t) if isinstance(t, np.ndarray) else t).to(DEV)  # noqa: E731
+    table = _table()
+    kvc = (torch.zeros(pages, PAGE, 1, 576, dtype=kv_dtype, device=DEV) if kv_format == 0 else
+           torch.zeros(pages, PAGE, 1, 656, dtype=torch.uint8, device=DEV))
+    kvd = d(kv)
+    mla.mla_append_kv(kvd[:, :512], kvd[:, 512:], kvc, d(slots), d(pos), table, kv_format=kv_format)
+    qa = d(q)
+    mla.mla_rotate_q(qa[..., 512:], d(qpos), table, out=qa[..., 512:])
+    ic = (torch.zeros(pages, 8448, dtype=torch.uint8, device=DEV) if index_format else
+          torch.zeros(pages, PAGE, 1, 128, dtype=BF, device=DEV))
+    mla.mla_append_index_k(d(k_idx), ic, d(slots), d(pos), table, index_format=index_format)
+    qi, wi = d(q_idx), d(w)
+    if index_format:
+        qi, wi = mla.mla_quantize_index_q(qi, wi, d(qpos), table)
+    else:
+        mla.mla_rotate_q(qi[..., :64], d(qpos), table, out=qi[..., :64])
+    return dict(B=B, bt=bt, btd=d(bt), sl=d(np.array(lens, np.int32)), pages=pages, kvc=kvc, q=qa, ic=ic, qi=qi.view(B, 1, hi, 128),
+                wi=wi.view(B, 1, hi), kv=kv, q_in=q, slots=slots, pos=pos, qpos=qpos)
+
+
+def _plain_keys(s, fmt):
+    """The cache rows the appends should have left, in float64, by physical row, and the rotated queries."""
+    rows = oracle.append_rows(s["kv"][:, :512], s["kv"][:, 512:], TABLE[s["pos"]], False, fmt)
+    dense = oracle.dequantize_kv_fp8(rows.numpy()) if fmt else oracle.to_f64(rows.view(s["kv"].dtype))
+    all_rows = np.zeros((s["pages"] * PAGE, 576))
+    all_rows[s["slots"]] = dense
+    q = oracle.to_f64(s["q_in"]).copy()
+    q[..., 512:] = oracle.to_f64(oracle.round_to(oracle.rotate(s["q_in"][..., 512:], TABLE[s["qpos"]][:, None], False), s["q_in"].dtype))
+    return all_rows, q
+
+
+def test_tokens_from_append_to_sparse_attention():
+    """append -> index -> score -> select -> token-sparse decode of the 656-byte cache."""
+    lens, topk = [900, 130, 2000], 256
+    s = _step(lens, 21, mla.KV_FP8_656, mla.INDEX_FP8)
+    scores = mla.mla_index_score(s["qi"], s["wi"], s["ic"], s["btd"], s["sl"], index_format=mla.INDEX_FP8)
+    idx, cnt = mla.mla_select_topk(scores, s["sl"], topk, s["btd"], s["pages"])
+    meta, ns = mla.mla_get_metadata(None, 1, 128, batch=s["B"], topk=topk, is_fp8=True, device=DEV)
+    out, lse = mla.mla_decode_with_kvcache(s["q"].view(s["B"], 1, 128, 576), s["kvc"], None, None, 512, meta, ns, is_fp8=True,
+                                           indices=idx)
+    torch.cuda.synchronize()
+    ref, want = _select_ref(scores.cpu().numpy(), lens, 1, False, 1, topk, s["bt"], s["pages"])
+    assert (idx.cpu().numpy() == ref).all() and (cnt.cpu().numpy() == want).all()
+    rows, q = _plain_keys(s, 1)
+    ro, rl, _ = oracle.mla_decode(q[:, None], rows, indices=ref, softmax_scale=576 ** -0.5)
+    assert_close_attn(out, lse, ro, rl, "token-sparse")
+
+
+@pytest.mark.parametrize("heads,dtype", [(128, BF), (16, HF)])
+def test_pages_from_append_to_paged_attention(heads, dtype):
+    """append -> index -> page scores -> page lists -> paged decode of a 16-bit cache."""
+    lens, topk = [900, 130, 2000, 64], 5
+    s = _step(lens, 22, mla.KV_16BIT, mla.INDEX_16BIT, kv_dtype=dtype)
+    scores = mla.mla_index_score(s["qi"], s["wi"], s["ic"], s["btd"], s["sl"], block=64)
+    table, sel = mla.mla_select_topk(scores, s["sl"], topk, s["btd"], s["pages"], block=64)
+    table, sel = table.view(s["B"], topk), sel.view(s["B"])
+    q = s["q"][:, :heads].contiguous().view(s["B"], 1, heads, 576)
+    meta, ns = mla.mla_get_metadata(sel, 1, heads)
+    out, lse = mla.mla_decode_with_kvcache(q, s["kvc"], table, sel, 512, meta, ns)
+    st, bits = mla.mla_read_status(device=DEV)
+    assert st == 0 and bits == 0
+    ref, want = _select_ref(scores.cpu().numpy(), lens, 1, False, 64, topk, s["bt"], s["pages"])
+    assert (table.cpu().numpy() == ref[:, 0]).all() and (sel.cpu().numpy() == want[:, 0]).all()
+    rows, qv = _plain_keys(s, 0)
+    ro, rl, _ = oracle.mla_decode(qv[:, None, :heads], rows, cache_seqlens=want[:, 0], block_table=ref[:, 0], softmax_scale=576 ** -0.5)
+    assert_close_attn(out, lse, ro, rl, "paged")
+
+
+def test_captured_and_replayed_on_another_stream():
+    """The chain captured into a graph, replayed with new inputs, while the same calls run eagerly beside it."""
+    lens, topk = [700, 300], 128
+    s = _step(lens, 23, mla.KV_FP8_656, mla.INDEX_FP8)
+    scores = torch.empty(2, 1, s["bt"].shape[1] * PAGE, device=DEV)
+    idx, cnt = torch.empty(2, 1, topk, dtype=torch.int32, device=DEV), torch.empty(2, 1, dtype=torch.int32, device=DEV)
+
+    def chain(sc, ix, ct):
+        mla.mla_index_score(s["qi"], s["wi"], s["ic"], s["btd"], s["sl"], index_format=mla.INDEX_FP8, scores=sc)
+        mla.mla_select_topk(sc, s["sl"], topk, s["btd"], s["pages"], indices=ix, lens=ct)
+
+    chain(scores, idx, cnt)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        chain(scores, idx, cnt)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(scores, idx, cnt)
+    for step in range(3):
+        s["wi"].mul_(-0.5)
+        s["sl"].sub_(17)
+        torch.cuda.synchronize()
+        sc2, ix2, ct2 = torch.empty_like(scores), torch.empty_like(idx), torch.empty_like(cnt)
+        graph.replay()
+        with torch.cuda.stream(stream):
+            chain(sc2, ix2, ct2)
+        torch.cuda.synchronize()
+        assert torch.equal(scores, sc2) and torch.equal(idx, ix2) and torch.equal(cnt, ct2)
+
+
+def test_same_inputs_same_bits():
+    lens = [5000, 3000, 100]
+    q, w, cache, bt, _, _ = _score_case(lens, 3, 48, "bf16", seed=31)
+    args = (q.to(DEV), w.to(DEV), cache.to(DEV), torch.from_numpy(bt).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV))
+    first = mla.mla_index_score(*args, causal=True)
+    for _ in range(3):
+        assert torch.equal(first, mla.mla_index_score(*args, causal=True))

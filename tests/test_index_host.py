@@ -1,0 +1,208 @@
+"""CPU checks of the calls that write new tokens and choose what the sparse
+attention reads: arguments are refused on the host before anything is
+enqueued (on a machine without a GPU any CUDA call would return 6), and the
+oracle of those calls is pinned to closed forms and brute force."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+FAKE = ctypes.c_void_p(1 << 20)          # aligned, never dereferenced: checks fail first
+ODD = ctypes.c_void_p((1 << 20) + 2)
+FAR = ctypes.c_void_p(1 << 40)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import mla_latent_kv_14_gb300 as m
+    if not os.path.exists(m.LIB_PATH):
+        from mla_latent_kv_14_gb300 import build
+        build.build()
+    return m.load_library()
+
+
+def _call(lib, name, base, **kw):
+    args = dict(base)
+    assert set(kw) <= set(args), kw
+    args.update(kw)
+    return getattr(lib, name)(*args.values())
+
+
+APPEND = dict(c=FAKE, cs=576, r=FAKE, rs=576, dtype=0, slots=FAKE, pos=FAKE, table=FAKE, maxp=4096, style=0, n=4,
+              kv=FAKE, blocks=8, page=64, fmt=0, status=None, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), 1), (dict(n=1 << 31), 1), (dict(maxp=0), 1), (dict(blocks=0), 1), (dict(blocks=1 << 26), 1),
+    (dict(page=32), 1), (dict(fmt=4), 1), (dict(fmt=-1), 1), (dict(dtype=2), 1), (dict(style=2), 1),
+    (dict(cs=504), 1), (dict(cs=577), 1), (dict(rs=56), 1), (dict(rs=65), 1), (dict(fmt=2, cs=440), 1),
+    (dict(fmt=1, dtype=1), 2), (dict(fmt=2, dtype=1), 2), (dict(fmt=3, dtype=1), 2),
+    (dict(c=None), 1), (dict(r=None), 1), (dict(slots=None), 1), (dict(pos=None), 1), (dict(table=None), 1),
+    (dict(kv=None), 1), (dict(c=ODD), 1), (dict(r=ODD), 1), (dict(kv=ODD), 1), (dict(table=ODD), 1),
+    (dict(slots=ODD), 1), (dict(pos=ODD), 1), (dict(status=ODD), 1), (dict(n=0, c=None, kv=None), 0),
+])
+def test_append_kv_argument_checks(lib, kw, code):
+    assert _call(lib, "mla_append_kv", APPEND, **kw) == code
+
+
+ROTATE = dict(x=FAKE, xt=192 * 8, xh=192, out=FAR, ot=576 * 8, oh=576, dtype=0, pos=FAKE, table=FAKE, maxp=4096,
+              style=0, tokens=4, heads=8, status=None, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tokens=-1), 1), (dict(heads=0), 1), (dict(tokens=1 << 28), 1), (dict(maxp=0), 1), (dict(dtype=3), 1),
+    (dict(style=-1), 1), (dict(xt=-8), 1), (dict(xh=4), 1), (dict(ot=4604), 1), (dict(oh=0), 1), (dict(ot=0), 1),
+    (dict(oh=64, ot=128), 1),                                     # rows of the output overlap one another
+    (dict(x=ODD), 1), (dict(out=ODD), 1), (dict(x=None), 1), (dict(out=None), 1), (dict(pos=None), 1),
+    (dict(table=None), 1), (dict(status=ODD), 1), (dict(tokens=0, x=None, out=None), 0),
+    (dict(out=FAKE), 1),                                          # overlaps x with other strides
+    (dict(out=ctypes.c_void_p((1 << 20) + 64), ot=192 * 8, oh=192), 1),   # 32 elements into x's rows
+    (dict(out=ctypes.c_void_p((1 << 20) + 320), ot=192 * 8, oh=192), 1),  # 160 of 192: into the next head's dims
+])
+def test_rotate_q_argument_checks(lib, kw, code):
+    assert _call(lib, "mla_rotate_q", ROTATE, **kw) == code
+
+
+INDEX_K = dict(k=FAKE, ks=128, dtype=0, slots=FAKE, pos=FAKE, table=FAKE, maxp=4096, style=0, n=4, cache=FAKE,
+               blocks=8, page=64, fmt=0, status=None, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), 1), (dict(ks=120), 1), (dict(ks=132), 1), (dict(fmt=2), 1), (dict(dtype=2), 1), (dict(page=128), 1),
+    (dict(blocks=-1), 1), (dict(style=7), 1), (dict(maxp=-1), 1), (dict(k=ODD), 1), (dict(cache=ODD), 1),
+    (dict(k=None), 1), (dict(slots=None), 1), (dict(pos=None), 1), (dict(table=None), 1), (dict(status=ODD), 1),
+    (dict(n=0, k=None), 0),
+])
+def test_append_index_k_argument_checks(lib, kw, code):
+    assert _call(lib, "mla_append_index_k", INDEX_K, **kw) == code
+
+
+INDEX_Q = dict(q=FAKE, qt=64 * 128, qh=128, dtype=0, w=FAKE, pos=FAKE, table=FAKE, maxp=4096, style=0, tokens=4,
+               heads=64, out=FAKE, wout=FAKE, status=None, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tokens=-1), 1), (dict(heads=0), 1), (dict(tokens=1 << 25), 1), (dict(qt=-8), 1), (dict(qh=130), 1),
+    (dict(dtype=2), 1), (dict(style=2), 1), (dict(q=None), 1), (dict(w=None), 1), (dict(out=None), 1),
+    (dict(wout=None), 1), (dict(q=ODD), 1), (dict(out=ODD), 1), (dict(w=ODD), 1), (dict(pos=None), 1),
+    (dict(status=ODD), 1), (dict(tokens=0, q=None), 0),
+])
+def test_quantize_index_q_argument_checks(lib, kw, code):
+    assert _call(lib, "mla_quantize_index_q", INDEX_Q, **kw) == code
+
+
+SCORE = dict(q=FAKE, dtype=0, w=FAKE, cache=FAKE, fmt=0, blocks=8, page=64, bt=FAKE, maxb=8, sl=FAKE, batch=2, s_q=1,
+             heads=64, causal=0, block=1, scores=FAKE, stride=512, width=512, status=None, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(fmt=2), 1), (dict(dtype=2), 1), (dict(blocks=0), 1), (dict(page=32), 1), (dict(maxb=0), 1),
+    (dict(batch=0), 1), (dict(s_q=0), 1), (dict(heads=0), 1), (dict(heads=65), 2), (dict(block=2), 1),
+    (dict(stride=511), 1), (dict(width=0), 1), (dict(q=None), 1), (dict(w=None), 1), (dict(cache=None), 1),
+    (dict(bt=None), 1), (dict(sl=None), 1), (dict(scores=None), 1), (dict(q=ODD), 1), (dict(cache=ODD), 1),
+    (dict(w=ODD), 1), (dict(scores=ODD), 1), (dict(status=ODD), 1), (dict(batch=1 << 20, s_q=1 << 10), 1),
+    (dict(width=(1 << 31) - 1, stride=1 << 31, maxb=1 << 26), 1),
+    (dict(batch=1 << 16, width=1 << 24, stride=1 << 24, maxb=1 << 20), 2),   # more tiles than the list counts
+])
+def test_index_score_argument_checks(lib, kw, code):
+    assert _call(lib, "mla_index_score", SCORE, **kw) == code
+
+
+SELECT = dict(scores=FAKE, stride=512, width=512, sl=FAKE, batch=2, s_q=1, causal=0, block=1, topk=64, bt=FAKE,
+              maxb=8, blocks=8, page=64, idx=FAKE, lens=FAKE, status=None, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(stride=100), 1), (dict(width=0), 1), (dict(batch=0), 1), (dict(s_q=-1), 1), (dict(block=32), 1),
+    (dict(topk=0), 1), (dict(maxb=0), 1), (dict(blocks=0), 1), (dict(page=16), 1), (dict(scores=None), 1),
+    (dict(sl=None), 1), (dict(bt=None), 1), (dict(idx=None), 1), (dict(block=64, lens=None), 1), (dict(idx=ODD), 1),
+    (dict(lens=ODD), 1), (dict(scores=ODD), 1), (dict(status=ODD), 1), (dict(batch=1 << 16, s_q=1 << 16), 1),
+])
+def test_select_topk_argument_checks(lib, kw, code):
+    assert _call(lib, "mla_select_topk", SELECT, **kw) == code
+
+
+def test_binding_refuses_before_the_library():
+    """Shapes, types and devices that the C ABI cannot see."""
+    import mla_latent_kv_14_gb300 as m
+    i32 = torch.int32
+    c, r = torch.zeros(4, 512, dtype=torch.bfloat16), torch.zeros(4, 64, dtype=torch.bfloat16)
+    kv, ix = torch.zeros(2, 64, 1, 576, dtype=torch.bfloat16), torch.zeros(4, dtype=i32)
+    table = torch.zeros(16, 64)
+    bad = [
+        lambda: m.mla_append_kv(c[:, :448], r, kv, ix, ix, table),                  # latent width of another format
+        lambda: m.mla_append_kv(c, r[:3], kv, ix, ix, table),
+        lambda: m.mla_append_kv(c, r.half(), kv, ix, ix, table),
+        lambda: m.mla_append_kv(c, r, kv.half(), ix, ix, table),                    # cache of another type
+        lambda: m.mla_append_kv(c, r, kv, ix.long(), ix, table),
+        lambda: m.mla_append_kv(c, r, kv, ix, ix[:3], table),
+        lambda: m.mla_append_kv(c, r, kv, ix, ix, table.double()),
+        lambda: m.mla_append_kv(c, r, kv[..., :512], ix, ix, table),
+        lambda: m.mla_append_kv(c, r, kv, ix, ix, table),                           # not on a cuda device
+        lambda: m.mla_rotate_q(c, ix, table),
+        lambda: m.mla_rotate_q(r.view(4, 1, 64), ix, table, out=torch.zeros(4, 2, 64, dtype=torch.bfloat16)),
+        lambda: m.mla_append_index_k(c, kv, ix, ix, table),
+        lambda: m.mla_append_index_k(c[:, :128], torch.zeros(2, 8192, dtype=torch.uint8), ix, ix, table, m.INDEX_FP8),
+        lambda: m.mla_quantize_index_q(c.view(4, 4, 128), torch.zeros(4, 3), ix, table),
+        lambda: m.mla_index_score(c.view(1, 4, 4, 128), torch.zeros(1, 4, 4), torch.zeros(2, 64, 1, 128), ix.view(1, 4), ix[:1]),
+        lambda: m.mla_index_score(c.view(1, 4, 4, 128), torch.zeros(1, 4, 4), torch.zeros(2, 64, 1, 128, dtype=torch.bfloat16),
+                                  ix.view(1, 4), ix[:1], block=16),
+        lambda: m.mla_select_topk(torch.zeros(1, 1, 8), ix[:1], 0, ix.view(1, 4), 8),
+        lambda: m.mla_select_topk(torch.zeros(2, 3, 8).transpose(0, 1), ix[:3], 4, ix.view(1, 4), 8),
+    ]
+    for k, f in enumerate(bad):
+        with pytest.raises(m.MLAError) as e:
+            f()
+        assert e.value.status == 1, k
+
+
+# ---- the oracle ----
+@pytest.mark.parametrize("halves", [False, True])
+def test_oracle_rotation_is_a_complex_product(halves):
+    rng = np.random.default_rng(0)
+    x = torch.from_numpy(rng.standard_normal((5, 64)).astype(np.float32)).to(torch.bfloat16)
+    table = oracle.rope_table(70000)[[0, 1, 63, 4096, 69999]]
+    got = oracle.rotate(x, table, halves).astype(np.float64)
+    v = oracle.to_f64(x)
+    a, b = (v[:, :32], v[:, 32:]) if halves else (v[:, 0::2], v[:, 1::2])
+    z = (a + 1j * b) * (table[:, :32].astype(np.float64) + 1j * table[:, 32:].astype(np.float64))
+    want = np.concatenate((z.real, z.imag), 1) if halves else np.stack((z.real, z.imag), -1).reshape(5, 64)
+    # two products and a sum, each rounded by 2^-24 of at most |a| + |b|
+    size = np.abs(a) + np.abs(b)
+    size = np.concatenate((size, size), 1) if halves else np.repeat(size, 2, axis=1)
+    assert (np.abs(got - want) <= 2 * 2.0 ** -24 * size).all()
+    assert (got[0] == v[0]).all()                                  # position 0 does nothing
+
+
+def test_oracle_rotation_keeps_relative_positions():
+    """The dot of two rotated rows depends on the distance of their positions alone."""
+    rng = np.random.default_rng(1)
+    q, k = (torch.from_numpy(rng.standard_normal(64).astype(np.float32)).to(torch.bfloat16) for _ in range(2))
+    t = oracle.rope_table(300)
+    for halves in (False, True):
+        dots = [oracle.rotate(q, t[p + 17], halves, exact=True) @ oracle.rotate(k, t[p], halves, exact=True)
+                for p in (0, 5, 211)]
+        # the table's own roundings: 2^-24 per cosine and sine of each row
+        assert np.ptp(dots) <= 8 * 2.0 ** -24 * np.abs(oracle.to_f64(q)).sum() * np.abs(oracle.to_f64(k)).max() * 2
+
+
+def test_oracle_selection_by_brute_force():
+    s = np.array([0.0, 3.0, -0.0, np.nan, 3.0, -np.inf, 1.0, np.inf])
+    assert oracle.select_topk(s, 8, 1).tolist() == [7]
+    assert oracle.select_topk(s, 8, 2).tolist() == [1, 7]          # of two 3.0 the first
+    assert oracle.select_topk(s, 8, 5).tolist() == [0, 1, 4, 6, 7]  # 0.0 and -0.0 are equal
+    assert oracle.select_topk(s, 8, 7).tolist() == [0, 1, 2, 4, 5, 6, 7]
+    assert oracle.select_topk(s, 6, 2, last=True).tolist() == [1, 5]
+    assert oracle.select_topk(s, 4, 9).tolist() == [0, 1, 2, 3]
+    assert oracle.select_topk(s, 0, 3).tolist() == []
+
+
+def test_oracle_score_of_one_head():
+    q, k = np.zeros((1, 1, 128)), np.zeros((3, 128))
+    q[0, 0, 5], k[0, 5], k[1, 5], k[2, 6] = 2.0, 3.0, -1.0, 9.0
+    assert oracle.index_score(q, np.array([[0.5]]), k).tolist() == [[3.0, 0.0, 0.0]]
+    assert oracle.page_max(np.arange(65.0)[None]).tolist() == [[63.0, 64.0]]
