@@ -5,7 +5,6 @@ the shared library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -377,29 +376,42 @@ INDEX_DIM, INDEX_FP8_PAGE_BYTES = 128, 8448
 _KV_ROW = {KV_16BIT: 576, KV_FP8_656: 656, KV_FP8_528: 528, KV_FP4_288: 288}
 
 
-def _require(ok: bool, what: str):
-    if not ok:
-        raise MLAError(1, what)
+# These calls take a few microseconds on the GPU for a decode step's sizes, so
+# the checks below are written for few interpreter steps: plain attribute reads
+# and comparisons, messages built only for a refusal, addresses and the raw
+# stream passed as integers.
+def _refuse(where: str, what: str):
+    raise MLAError(1, f"{where}: {what}")
 
 
-def _i32(t: torch.Tensor, shape: tuple, what: str):
-    _require(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape, what)
+def _run(where: str, fn, dev: int, *args):
+    """Call a C entry point with the tensors' device current; its stream comes last."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != MLA_OK:
+        raise MLAError(st, where)
 
 
-def _place(where: str, *tensors: Optional[torch.Tensor]):
-    """The one device of the tensors, and a context in which it is current."""
-    given = [t for t in tensors if t is not None]
-    dev = given[0].device
-    _require(dev.type == "cuda" and all(t.device == dev for t in given), f"{where}: tensors of one cuda device")
-    same = torch.cuda.current_device() == dev.index
-    return dev, contextlib.nullcontext() if same else torch.cuda.device(dev)
+def _status_ptr(where: str, status: Optional[torch.Tensor], dev: int):
+    if status is None:
+        return None
+    if status.get_device() != dev or status.element_size() * status.numel() < 4:
+        _refuse(where, "status: a 4-byte word on the tensors' device")
+    return status.data_ptr()
 
 
-def _rope_args(where: str, positions: torch.Tensor, rope_table: torch.Tensor, rope_style: int, tokens: int):
-    _i32(positions, (tokens,), f"{where}: positions int32 [{tokens}]")
-    _require(rope_table.dtype == torch.float32 and rope_table.dim() == 2 and rope_table.shape[1] == 64 and
-             rope_table.is_contiguous(), f"{where}: rope_table fp32 [positions, 64]")
-    return _ptr(positions), _ptr(rope_table), int(rope_table.shape[0]), int(rope_style)
+def _rope_check(where: str, positions: torch.Tensor, rope_table: torch.Tensor, tokens: int, dev: int):
+    if positions.dtype != torch.int32 or positions.shape != (tokens,) or not positions.is_contiguous():
+        _refuse(where, f"positions int32 [{tokens}]")
+    if (rope_table.dtype != torch.float32 or rope_table.dim() != 2 or rope_table.shape[1] != 64 or
+            not rope_table.is_contiguous()):
+        _refuse(where, "rope_table fp32 [positions, 64]")
+    if dev < 0 or positions.get_device() != dev or rope_table.get_device() != dev:
+        _refuse(where, "tensors of one cuda device")
 
 
 def mla_rope_table(max_positions: int, base: float = 10000.0, inv_freq: Optional[torch.Tensor] = None,
@@ -410,7 +422,8 @@ def mla_rope_table(max_positions: int, base: float = 10000.0, inv_freq: Optional
     dev = _dev(device)
     if inv_freq is None:
         inv_freq = base ** (-torch.arange(32, dtype=torch.float64) / 32)
-    _require(tuple(inv_freq.shape) == (32,), "mla_rope_table: inv_freq [32]")
+    if tuple(inv_freq.shape) != (32,):
+        _refuse("mla_rope_table", "inv_freq [32]")
     angle = torch.arange(max_positions, dtype=torch.float64, device=dev)[:, None] * inv_freq.to(dev, torch.float64)
     return torch.cat((angle.cos() * scale, angle.sin() * scale), 1).float()
 
@@ -421,31 +434,35 @@ def mla_append_kv(c_kv: torch.Tensor, k_rope: torch.Tensor, kvcache: torch.Tenso
     """Append tokens to the paged cache in place: c_kv [n, 512] (V4.1 rows: 448)
     and k_rope [n, 64], which is rotated on the way; ``slots`` int32 [n] are cache
     rows (page * 64 + offset, negative: skip). Returns kvcache."""
-    lib, where = load_library(), "mla_append_kv"
-    fmt = _kv_format(False, kv_format)
-    latent = 448 if fmt >= KV_FP8_528 else 512
-    n = int(c_kv.shape[0])
-    _require(tuple(c_kv.shape) == (n, latent) and tuple(k_rope.shape) == (n, 64) and c_kv.stride(1) == 1 and
-             k_rope.stride(1) == 1 and k_rope.dtype == c_kv.dtype, f"{where}: c_kv [n, {latent}], k_rope [n, 64]")
-    _i32(slots, (n,), f"{where}: slots int32 [n]")
-    cache_type = c_kv.dtype if fmt == KV_16BIT else torch.uint8
-    _require(kvcache.is_contiguous() and kvcache.dtype == cache_type and kvcache.dim() >= 3 and
-             kvcache.shape[-1] == _KV_ROW[fmt] and kvcache.numel() == kvcache.shape[0] * kvcache.shape[1] * _KV_ROW[fmt],
-             f"{where}: kvcache [num_blocks, page_block, 1, {_KV_ROW[fmt]}] of {cache_type}")
-    rope = _rope_args(where, positions, rope_table, rope_style, n)
-    dev, current = _place(where, c_kv, k_rope, kvcache, slots, positions, rope_table, status)
-    with current:
-        st = lib.mla_append_kv(_ptr(c_kv), _stride(c_kv, 0, latent), _ptr(k_rope), _stride(k_rope, 0, 64),
-                               _dtype_code(c_kv), _ptr(slots), *rope, n, _ptr(kvcache), int(kvcache.shape[0]),
-                               int(kvcache.shape[1]), fmt, _ptr(status), _stream(dev))
-    _check(st, where)
+    lib, where = _lib or load_library(), "mla_append_kv"
+    row = _KV_ROW.get(kv_format)
+    if row is None:
+        _refuse(where, f"unknown kv_format {kv_format}")
+    dtype, dev, n = c_kv.dtype, c_kv.get_device(), c_kv.shape[0]
+    latent = 448 if kv_format >= KV_FP8_528 else 512
+    if (c_kv.shape != (n, latent) or k_rope.shape != (n, 64) or k_rope.dtype != dtype or c_kv.stride(1) != 1 or
+            k_rope.stride(1) != 1 or dtype not in DTYPE_CODES):
+        _refuse(where, f"c_kv [n, {latent}] and k_rope [n, 64], bf16 or fp16")
+    if slots.dtype != torch.int32 or slots.shape != (n,) or not slots.is_contiguous():
+        _refuse(where, "slots int32 [n]")
+    shape = kvcache.shape
+    if (kvcache.dtype != (torch.uint8 if kv_format else dtype) or len(shape) < 3 or shape[-1] != row or
+            not kvcache.is_contiguous() or kvcache.numel() != shape[0] * shape[1] * row):
+        _refuse(where, f"kvcache [num_blocks, page_block, 1, {row}] of {'uint8' if kv_format else dtype}")
+    _rope_check(where, positions, rope_table, n, dev)
+    if k_rope.get_device() != dev or kvcache.get_device() != dev or slots.get_device() != dev:
+        _refuse(where, "tensors of one cuda device")
+    _run(where, lib.mla_append_kv, dev, c_kv.data_ptr(), _stride(c_kv, 0, latent), k_rope.data_ptr(),
+         _stride(k_rope, 0, 64), DTYPE_CODES[dtype], slots.data_ptr(), positions.data_ptr(), rope_table.data_ptr(),
+         rope_table.shape[0], rope_style, n, kvcache.data_ptr(), shape[0], shape[1], kv_format,
+         _status_ptr(where, status, dev))
     return kvcache
 
 
 def _stride(t: torch.Tensor, dim: int, dense: int) -> int:
     """The stride of ``dim``; of a dim with at most one entry, which is never
     stepped over, the dense one (PyTorch leaves any number there)."""
-    return int(t.stride(dim)) if t.shape[dim] > 1 else dense
+    return t.stride(dim) if t.shape[dim] > 1 else dense
 
 
 def mla_rotate_q(x: torch.Tensor, positions: torch.Tensor, rope_table: torch.Tensor,
@@ -453,35 +470,39 @@ def mla_rotate_q(x: torch.Tensor, positions: torch.Tensor, rope_table: torch.Ten
                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotate query rows: x [tokens, heads, 64] (any token and head strides, for
     example ``q[..., 128:]`` of the projection) -> out, of the same shape
-    (``q_abs[..., 512:]``, ``x`` itself, or allocated; rows of tokens whose
-    position is negative are left as they are)."""
-    lib, where = load_library(), "mla_rotate_q"
-    _require(x.dim() == 3 and x.shape[2] == 64 and x.stride(2) == 1, f"{where}: x [tokens, heads, 64]")
-    tokens, heads = int(x.shape[0]), int(x.shape[1])
+    (``q_abs[..., 512:]``, ``x`` itself, or allocated). Rows of tokens whose
+    position is negative are not written."""
+    lib, where = _lib or load_library(), "mla_rotate_q"
+    dtype, dev = x.dtype, x.get_device()
+    if x.dim() != 3 or x.shape[2] != 64 or x.stride(2) != 1 or dtype not in DTYPE_CODES:
+        _refuse(where, "x [tokens, heads, 64], bf16 or fp16")
+    tokens, heads, _ = x.shape
     if out is None:
-        out = torch.zeros(tokens, heads, 64, dtype=x.dtype, device=x.device)
-    _require(out.shape == x.shape and out.dtype == x.dtype and out.stride(2) == 1, f"{where}: out like x")
-    rope = _rope_args(where, positions, rope_table, rope_style, tokens)
-    dev, current = _place(where, x, out, positions, rope_table, status)
-    with current:
-        st = lib.mla_rotate_q(_ptr(x), _stride(x, 0, 64 * heads), _stride(x, 1, 64), _ptr(out),
-                              _stride(out, 0, 64 * heads), _stride(out, 1, 64), _dtype_code(x), *rope, tokens, heads,
-                              _ptr(status), _stream(dev))
-    _check(st, where)
+        out = x.new_empty((tokens, heads, 64))
+    elif out.shape != x.shape or out.dtype != dtype or out.stride(2) != 1:
+        _refuse(where, "out like x")
+    _rope_check(where, positions, rope_table, tokens, dev)
+    if out.get_device() != dev:
+        _refuse(where, "tensors of one cuda device")
+    _run(where, lib.mla_rotate_q, dev, x.data_ptr(), _stride(x, 0, 64 * heads), _stride(x, 1, 64), out.data_ptr(),
+         _stride(out, 0, 64 * heads), _stride(out, 1, 64), DTYPE_CODES[dtype], positions.data_ptr(),
+         rope_table.data_ptr(), rope_table.shape[0], rope_style, tokens, heads, _status_ptr(where, status, dev))
     return out
 
 
-def _index_cache(where: str, cache: torch.Tensor, fmt: int, dtype: Optional[torch.dtype]) -> Tuple[int, int]:
+def _index_cache(where: str, cache: torch.Tensor, index_format: int, dtype: torch.dtype) -> Tuple[int, int]:
     """(num_blocks, page_block) of an index cache."""
-    _require(fmt in (INDEX_16BIT, INDEX_FP8), f"{where}: unknown index_format {fmt}")
-    if fmt == INDEX_FP8:
-        _require(cache.dim() == 2 and cache.shape[1] == INDEX_FP8_PAGE_BYTES and cache.dtype == torch.uint8 and
-                 cache.is_contiguous(), f"{where}: FP8 index cache uint8 [num_blocks, {INDEX_FP8_PAGE_BYTES}]")
-        return int(cache.shape[0]), 64
-    _require(cache.dim() >= 3 and cache.shape[-1] == INDEX_DIM and cache.is_contiguous() and cache.dtype == dtype and
-             cache.numel() == cache.shape[0] * cache.shape[1] * INDEX_DIM,
-             f"{where}: index cache [num_blocks, page_block, 1, {INDEX_DIM}] of {dtype}")
-    return int(cache.shape[0]), int(cache.shape[1])
+    shape = cache.shape
+    if index_format == INDEX_FP8:
+        if len(shape) != 2 or shape[1] != INDEX_FP8_PAGE_BYTES or cache.dtype != torch.uint8 or not cache.is_contiguous():
+            _refuse(where, f"FP8 index cache uint8 [num_blocks, {INDEX_FP8_PAGE_BYTES}]")
+        return shape[0], 64
+    if index_format != INDEX_16BIT:
+        _refuse(where, f"unknown index_format {index_format}")
+    if (len(shape) < 3 or shape[-1] != INDEX_DIM or cache.dtype != dtype or not cache.is_contiguous() or
+            cache.numel() != shape[0] * shape[1] * INDEX_DIM):
+        _refuse(where, f"index cache [num_blocks, page_block, 1, {INDEX_DIM}] of {dtype}")
+    return shape[0], shape[1]
 
 
 def mla_append_index_k(k: torch.Tensor, index_cache: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor,
@@ -490,17 +511,19 @@ def mla_append_index_k(k: torch.Tensor, index_cache: torch.Tensor, slots: torch.
     """Append index keys k [n, 128] (dims [0, 64) are rotated) to the paged index
     cache in place: [num_blocks, 64, 1, 128] of k's type, or uint8 [num_blocks,
     8448] with INDEX_FP8. ``slots`` as in :func:`mla_append_kv`."""
-    lib, where = load_library(), "mla_append_index_k"
-    n = int(k.shape[0])
-    _require(tuple(k.shape) == (n, INDEX_DIM) and k.stride(1) == 1, f"{where}: k [n, {INDEX_DIM}]")
-    _i32(slots, (n,), f"{where}: slots int32 [n]")
-    blocks, page = _index_cache(where, index_cache, index_format, k.dtype)
-    rope = _rope_args(where, positions, rope_table, rope_style, n)
-    dev, current = _place(where, k, index_cache, slots, positions, rope_table, status)
-    with current:
-        st = lib.mla_append_index_k(_ptr(k), _stride(k, 0, INDEX_DIM), _dtype_code(k), _ptr(slots), *rope, n,
-                                    _ptr(index_cache), blocks, page, index_format, _ptr(status), _stream(dev))
-    _check(st, where)
+    lib, where = _lib or load_library(), "mla_append_index_k"
+    dtype, dev, n = k.dtype, k.get_device(), k.shape[0]
+    if k.shape != (n, INDEX_DIM) or k.stride(1) != 1 or dtype not in DTYPE_CODES:
+        _refuse(where, f"k [n, {INDEX_DIM}], bf16 or fp16")
+    if slots.dtype != torch.int32 or slots.shape != (n,) or not slots.is_contiguous():
+        _refuse(where, "slots int32 [n]")
+    blocks, page = _index_cache(where, index_cache, index_format, dtype)
+    _rope_check(where, positions, rope_table, n, dev)
+    if index_cache.get_device() != dev or slots.get_device() != dev:
+        _refuse(where, "tensors of one cuda device")
+    _run(where, lib.mla_append_index_k, dev, k.data_ptr(), _stride(k, 0, INDEX_DIM), DTYPE_CODES[dtype],
+         slots.data_ptr(), positions.data_ptr(), rope_table.data_ptr(), rope_table.shape[0], rope_style, n,
+         index_cache.data_ptr(), blocks, page, index_format, _status_ptr(where, status, dev))
     return index_cache
 
 
@@ -510,27 +533,53 @@ def mla_quantize_index_q(q: torch.Tensor, weights: torch.Tensor, positions: torc
                          status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Index queries q [tokens, heads, 128] (dims [0, 64) are rotated) as e4m3 rows,
     with each row's scale folded into ``weights`` fp32 [tokens, heads]. Returns
-    (float8_e4m3fn [tokens, heads, 128], fp32 [tokens, heads])."""
-    lib, where = load_library(), "mla_quantize_index_q"
-    _require(q.dim() == 3 and q.shape[2] == INDEX_DIM and q.stride(2) == 1, f"{where}: q [tokens, heads, {INDEX_DIM}]")
-    tokens, heads = int(q.shape[0]), int(q.shape[1])
+    (float8_e4m3fn [tokens, heads, 128], fp32 [tokens, heads]); rows of tokens
+    whose position is negative are not written."""
+    lib, where = _lib or load_library(), "mla_quantize_index_q"
+    dtype, dev = q.dtype, q.get_device()
+    if q.dim() != 3 or q.shape[2] != INDEX_DIM or q.stride(2) != 1 or dtype not in DTYPE_CODES:
+        _refuse(where, f"q [tokens, heads, {INDEX_DIM}], bf16 or fp16")
+    tokens, heads, _ = q.shape
+    if weights.shape != (tokens, heads) or weights.dtype != torch.float32 or not weights.is_contiguous():
+        _refuse(where, "weights fp32 [tokens, heads]")
     if q_out is None:
-        q_out = torch.zeros(tokens, heads, INDEX_DIM, dtype=torch.uint8, device=q.device).view(torch.float8_e4m3fn)
+        q_out = q.new_empty((tokens, heads, INDEX_DIM), dtype=torch.float8_e4m3fn)
+    elif q_out.shape != q.shape or not q_out.is_contiguous() or q_out.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        _refuse(where, "q_out e4m3 like q")
     if weights_out is None:
-        weights_out = torch.zeros(tokens, heads, dtype=torch.float32, device=q.device)
-    _require(q_out.shape == q.shape and q_out.is_contiguous() and
-             q_out.dtype in (torch.float8_e4m3fn, torch.uint8), f"{where}: q_out e4m3 like q")
-    for w in (weights, weights_out):
-        _require(tuple(w.shape) == (tokens, heads) and w.is_contiguous() and w.dtype == torch.float32,
-                 f"{where}: weights fp32 [tokens, heads]")
-    rope = _rope_args(where, positions, rope_table, rope_style, tokens)
-    dev, current = _place(where, q, weights, positions, rope_table, q_out, weights_out, status)
-    with current:
-        st = lib.mla_quantize_index_q(_ptr(q), _stride(q, 0, INDEX_DIM * heads), _stride(q, 1, INDEX_DIM),
-                                      _dtype_code(q), _ptr(weights), *rope, tokens, heads, _ptr(q_out),
-                                      _ptr(weights_out), _ptr(status), _stream(dev))
-    _check(st, where)
+        weights_out = weights.new_empty((tokens, heads))
+    elif weights_out.shape != (tokens, heads) or weights_out.dtype != torch.float32 or not weights_out.is_contiguous():
+        _refuse(where, "weights_out fp32 [tokens, heads]")
+    _rope_check(where, positions, rope_table, tokens, dev)
+    if weights.get_device() != dev or q_out.get_device() != dev or weights_out.get_device() != dev:
+        _refuse(where, "tensors of one cuda device")
+    _run(where, lib.mla_quantize_index_q, dev, q.data_ptr(), _stride(q, 0, INDEX_DIM * heads), _stride(q, 1, INDEX_DIM),
+         DTYPE_CODES[dtype], weights.data_ptr(), positions.data_ptr(), rope_table.data_ptr(), rope_table.shape[0],
+         rope_style, tokens, heads, q_out.data_ptr(), weights_out.data_ptr(), _status_ptr(where, status, dev))
     return q_out, weights_out
+
+
+def _paged_check(where: str, block_table: torch.Tensor, cache_seqlens: torch.Tensor, batch: int, dev: int) -> int:
+    """max_blocks of a block table for `batch` requests."""
+    if (block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch or
+            not block_table.is_contiguous()):
+        _refuse(where, "block_table int32 [B, max_blocks]")
+    if cache_seqlens.dtype != torch.int32 or cache_seqlens.shape != (batch,) or not cache_seqlens.is_contiguous():
+        _refuse(where, "cache_seqlens int32 [B]")
+    if dev < 0 or block_table.get_device() != dev or cache_seqlens.get_device() != dev:
+        _refuse(where, "tensors of one cuda device")
+    return block_table.shape[1]
+
+
+def _score_stride(where: str, scores: torch.Tensor, width: int) -> int:
+    """Row stride of scores [B, s_q, width] (a column range of a wider buffer is fine)."""
+    if scores.is_contiguous():
+        return width
+    batch, s_q, _ = scores.shape
+    stride = scores.stride(1) if s_q > 1 else scores.stride(0) if batch > 1 else width
+    if (width > 1 and scores.stride(2) != 1) or (batch > 1 and s_q > 1 and scores.stride(0) != s_q * stride):
+        _refuse(where, "rows of scores dense and equally spaced")
+    return stride
 
 
 def mla_index_score(q: torch.Tensor, weights: torch.Tensor, index_cache: torch.Tensor, block_table: torch.Tensor,
@@ -541,41 +590,36 @@ def mla_index_score(q: torch.Tensor, weights: torch.Tensor, index_cache: torch.T
     (block=64): sum_h weights[b, i, h] * relu(q[b, i, h] . k_t), -inf where
     nothing is visible. q [B, s_q, heads, 128] of the index cache's type (e4m3
     with INDEX_FP8); ``width`` defaults to what the block table reaches."""
-    lib, where = load_library(), "mla_index_score"
-    _require(q.dim() == 4 and q.shape[3] == INDEX_DIM and q.is_contiguous(), f"{where}: q [B, s_q, heads, {INDEX_DIM}]")
-    B, s_q, heads = (int(x) for x in q.shape[:3])
-    fp8 = index_format == INDEX_FP8
-    _require(q.dtype in (torch.float8_e4m3fn, torch.uint8) if fp8 else q.dtype in DTYPE_CODES, f"{where}: q's type")
-    _require(weights.dtype == torch.float32 and tuple(weights.shape) == (B, s_q, heads) and weights.is_contiguous(),
-             f"{where}: weights fp32 [B, s_q, heads]")
-    blocks, page = _index_cache(where, index_cache, index_format, q.dtype)
-    _require(block_table.dim() == 2, f"{where}: block_table int32 [B, max_blocks]")
-    max_blocks = int(block_table.shape[1])
-    _i32(block_table, (B, max_blocks), f"{where}: block_table int32 [B, max_blocks]")
-    _i32(cache_seqlens, (B,), f"{where}: cache_seqlens int32 [B]")
-    _require(block in (1, 64), f"{where}: block 1 or 64")
+    lib, where = _lib or load_library(), "mla_index_score"
+    dtype, dev, shape = q.dtype, q.get_device(), q.shape
+    if len(shape) != 4 or shape[3] != INDEX_DIM or not q.is_contiguous():
+        _refuse(where, f"q [B, s_q, heads, {INDEX_DIM}]")
+    batch, s_q, heads, _ = shape
+    code = DTYPE_CODES.get(dtype) if index_format != INDEX_FP8 else 0 if dtype in (torch.float8_e4m3fn, torch.uint8) else None
+    if code is None:
+        _refuse(where, "q's type: that of the index cache, e4m3 with an FP8 one")
+    if weights.dtype != torch.float32 or weights.shape != (batch, s_q, heads) or not weights.is_contiguous():
+        _refuse(where, "weights fp32 [B, s_q, heads]")
+    blocks, page = _index_cache(where, index_cache, index_format, dtype)
+    max_blocks = _paged_check(where, block_table, cache_seqlens, batch, dev)
+    if block != 1 and block != 64:
+        _refuse(where, "block 1 or 64")
     if width is None:
-        width = int(scores.shape[2]) if scores is not None else max_blocks * (64 // block)
+        width = scores.shape[-1] if scores is not None else max_blocks * (64 // block)
+    if not 1 <= width < 1 << 31:
+        _refuse(where, "1 <= width < 2^31")
     if scores is None:
-        scores = torch.empty(B, s_q, width, dtype=torch.float32, device=q.device)
-    stride = _score_stride(where, scores, B, s_q, width)
-    dev, current = _place(where, q, weights, index_cache, block_table, cache_seqlens, scores, status)
-    with current:
-        st = lib.mla_index_score(_ptr(q), 0 if fp8 else DTYPE_CODES[q.dtype], _ptr(weights), _ptr(index_cache),
-                                 index_format, blocks, page, _ptr(block_table), max_blocks, _ptr(cache_seqlens), B,
-                                 s_q, heads, int(causal), block, _ptr(scores), stride, width, _ptr(status),
-                                 _stream(dev))
-    _check(st, where)
+        scores, stride = weights.new_empty((batch, s_q, width)), width
+    else:
+        if scores.dtype != torch.float32 or scores.shape != (batch, s_q, width):
+            _refuse(where, "scores fp32 [B, s_q, width]")
+        stride = _score_stride(where, scores, width)
+    if weights.get_device() != dev or index_cache.get_device() != dev or scores.get_device() != dev:
+        _refuse(where, "tensors of one cuda device")
+    _run(where, lib.mla_index_score, dev, q.data_ptr(), code, weights.data_ptr(), index_cache.data_ptr(), index_format,
+         blocks, page, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(), batch, s_q, heads, causal, block,
+         scores.data_ptr(), stride, width, _status_ptr(where, status, dev))
     return scores
-
-
-def _score_stride(where: str, scores: torch.Tensor, B: int, s_q: int, width: int) -> int:
-    """Row stride of scores [B, s_q, width] (a column range of a wider buffer is fine)."""
-    _require(scores.dtype == torch.float32 and tuple(scores.shape) == (B, s_q, width) and
-             (width == 1 or scores.stride(2) == 1), f"{where}: scores fp32 [B, s_q, width]")
-    stride = scores.stride(1) if s_q > 1 else scores.stride(0) if B > 1 else width
-    _require(B == 1 or s_q == 1 or scores.stride(0) == s_q * stride, f"{where}: rows of scores equally spaced")
-    return int(stride)
 
 
 def mla_select_topk(scores: torch.Tensor, cache_seqlens: torch.Tensor, topk: int, block_table: torch.Tensor,
@@ -587,25 +631,26 @@ def mla_select_topk(scores: torch.Tensor, cache_seqlens: torch.Tensor, topk: int
     their number [B, s_q]); block=64: (pages [B, s_q, topk] and the tokens they
     hold [B, s_q]), the block table and lengths of a decode with B * s_q requests
     of one query. ``num_blocks``: pages of the cache that the rows index."""
-    lib, where = load_library(), "mla_select_topk"
-    _require(scores.dim() == 3, f"{where}: scores fp32 [B, s_q, width]")
-    B, s_q, width = (int(x) for x in scores.shape)
-    stride = _score_stride(where, scores, B, s_q, width)
-    _require(block_table.dim() == 2, f"{where}: block_table int32 [B, max_blocks]")
-    max_blocks = int(block_table.shape[1])
-    _i32(block_table, (B, max_blocks), f"{where}: block_table int32 [B, max_blocks]")
-    _i32(cache_seqlens, (B,), f"{where}: cache_seqlens int32 [B]")
-    _require(topk > 0, f"{where}: topk")
+    lib, where = _lib or load_library(), "mla_select_topk"
+    dev, shape = scores.get_device(), scores.shape
+    if len(shape) != 3 or scores.dtype != torch.float32:
+        _refuse(where, "scores fp32 [B, s_q, width]")
+    batch, s_q, width = shape
+    stride = _score_stride(where, scores, width)
+    max_blocks = _paged_check(where, block_table, cache_seqlens, batch, dev)
+    if not 1 <= topk < 1 << 31 or width >= 1 << 31:
+        _refuse(where, "1 <= topk, width < 2^31")
     if indices is None:
-        indices = torch.empty(B, s_q, topk, dtype=torch.int32, device=scores.device)
+        indices = block_table.new_empty((batch, s_q, topk))
+    elif indices.dtype != torch.int32 or indices.shape != (batch, s_q, topk) or not indices.is_contiguous():
+        _refuse(where, "indices int32 [B, s_q, topk]")
     if lens is None:
-        lens = torch.empty(B, s_q, dtype=torch.int32, device=scores.device)
-    _i32(indices, (B, s_q, topk), f"{where}: indices int32 [B, s_q, topk]")
-    _i32(lens, (B, s_q), f"{where}: lens int32 [B, s_q]")
-    dev, current = _place(where, scores, cache_seqlens, block_table, indices, lens, status)
-    with current:
-        st = lib.mla_select_topk(_ptr(scores), stride, width, _ptr(cache_seqlens), B, s_q, int(causal), block, topk,
-                                 _ptr(block_table), max_blocks, int(num_blocks), 64, _ptr(indices), _ptr(lens),
-                                 _ptr(status), _stream(dev))
-    _check(st, where)
+        lens = block_table.new_empty((batch, s_q))
+    elif lens.dtype != torch.int32 or lens.shape != (batch, s_q) or not lens.is_contiguous():
+        _refuse(where, "lens int32 [B, s_q]")
+    if indices.get_device() != dev or lens.get_device() != dev:
+        _refuse(where, "tensors of one cuda device")
+    _run(where, lib.mla_select_topk, dev, scores.data_ptr(), stride, width, cache_seqlens.data_ptr(), batch, s_q, causal,
+         block, topk, block_table.data_ptr(), max_blocks, num_blocks, 64, indices.data_ptr(), lens.data_ptr(),
+         _status_ptr(where, status, dev))
     return indices, lens

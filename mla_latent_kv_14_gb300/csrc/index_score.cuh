@@ -21,12 +21,17 @@
 // contiguous ranges, one per CTA (one CTA per SM): ragged lengths balance, and
 // a unit's queries are loaded once per range.
 //
-// Warp roles (384 threads): warp 0 lane 0 issues TMA; warp 1 owns TMEM and
-// lane 0 issues the MMAs; warp 2 writes the -inf columns behind the visible
-// tiles; warp 3 brings the head weights; warps 4-7 and 8-11 are the two
-// epilogue groups, serving accumulator 0 and 1. Every wait is bounded; a wait
-// that gives up sets the status word and the CTA unwinds.
+// Warp roles (384 threads): warp 0 reads the block table 32 pages ahead and its
+// lane 0 issues the copies (queries, key tiles, the scales and page flags of a
+// tile); warp 1 owns TMEM and lane 0 issues the MMAs; warp 2 writes the -inf
+// columns behind the visible tiles; warp 3 brings the head weights; warps 4-7
+// and 8-11 are two epilogue groups. Accumulators of more than 128 columns (two
+// of them) are summed by both, half of the queries each, so that one is free
+// again soonest; of smaller ones (four of them) each group takes every other.
+// Every wait is bounded; a wait that gives up sets the status word and the CTA
+// unwinds.
 #pragma once
+#include <climits>
 #include <cuda.h>
 
 #include "params.h"
@@ -36,6 +41,7 @@ namespace mla {
 namespace score {
 
 constexpr int kThreads = 384;
+constexpr int kGroups = 2;                      // epilogue groups of four warps
 constexpr int kTokens = 128;                    // tokens of a tile (two pages)
 constexpr int kDim = 128;
 constexpr int kMaxN = 256;
@@ -63,13 +69,13 @@ struct ScoreParams {
 
 // shared memory: the query groups, the key ring, weights, barriers
 constexpr uint32_t kWeightBytes = 2 * 2 * kMaxN * 4;  // [unit parity][group][256]
-constexpr uint32_t kRedBytes = 2 * 2 * 4 * 16 * 4;    // page maxima: [group][parity][4 warps][16 queries]
+constexpr uint32_t kRedBytes = kGroups * 2 * 4 * 16 * 4;  // page maxima: [epilogue group][parity][4 warps][16 queries]
 enum : uint32_t {
   B_KFULL = 0, B_KEMPTY = B_KFULL + kMaxRing, B_QFULL = B_KEMPTY + kMaxRing, B_QEMPTY = B_QFULL + 2,
-  B_AFULL = B_QEMPTY + 2, B_AEMPTY = B_AFULL + 2, B_WFULL = B_AEMPTY + 2, B_WEMPTY = B_WFULL + 2,
-  B_RED = B_WEMPTY + 2, B_DRAIN = B_RED + 2, B_STALL = B_DRAIN + 1, B_COUNT = B_STALL + 1
+  B_AFULL = B_QEMPTY + 2, B_AEMPTY = B_AFULL + 4, B_WFULL = B_AEMPTY + 4, B_WEMPTY = B_WFULL + 2,
+  B_RED = B_WEMPTY + 2, B_DRAIN = B_RED + kGroups, B_STALL = B_DRAIN + 1, B_COUNT = B_STALL + 1
 };
-constexpr uint32_t kTailBytes = kWeightBytes + kRedBytes + 8 * B_COUNT + 64 + 64;
+constexpr uint32_t kTailBytes = kWeightBytes + kRedBytes + 8 * B_COUNT + 128;
 constexpr uint32_t smem_bytes(uint32_t q_bytes, uint32_t ring) { return q_bytes + ring * kUnit + kTailBytes + 1024; }
 
 // visible tokens of query i of a request with `len` tokens
@@ -77,30 +83,74 @@ MLA_DEV int visible(const ScoreParams& p, int len, int i) {
   const int v = p.causal ? len - (p.s_q - 1 - i) : len;
   return v < 0 ? 0 : (v > p.cover ? p.cover : v);
 }
-// key tiles of a unit: those that its last query sees
-MLA_DEV int unit_tiles(const ScoreParams& p, int u) {
+// tokens that the last query of a unit sees (the most of its queries)
+MLA_DEV int unit_visible(const ScoreParams& p, int u) {
   const int b = u / p.units, k = u - b * p.units;
   const int per = p.nq * p.groups;
   int last = (k + 1) * per - 1;
   last = last < p.s_q - 1 ? last : p.s_q - 1;
-  return (visible(p, __ldg(p.seqlens + b), last) + kTokens - 1) / kTokens;
+  return visible(p, __ldg(p.seqlens + b), last);
 }
+MLA_DEV int unit_tiles(const ScoreParams& p, int u) { return (unit_visible(p, u) + kTokens - 1) / kTokens; }
 
-// The CTA's range of the list of (unit, tile) pairs, walked in order.
+// The CTA's range of the list of (unit, tile) pairs, walked unit by unit, so
+// that the loops over a unit's tiles hold nothing but their own work.
 struct Walk {
-  int u, t, n, left;  // unit, tile, tiles of the unit, pairs left
-  MLA_DEV Walk(const ScoreParams& p, int u0, int t0, int count) : u(u0), t(t0), n(0), left(count) {
-    if (left > 0) n = unit_tiles(p, u);
+  int u, t, m, left;  // unit, its first tile here, its tiles here, pairs left
+  MLA_DEV Walk(const ScoreParams& p, int u0, int t0, int count) : u(u0), t(t0), m(0), left(count) {
+    if (left > 0) m = min(unit_tiles(p, u) - t, left);
   }
   MLA_DEV bool done() const { return left <= 0; }
-  MLA_DEV bool last_of_unit() const { return t == n - 1 || left == 1; }
   MLA_DEV void next(const ScoreParams& p) {
-    --left;
-    if (++t < n || left <= 0) return;
+    left -= m;
+    if (left <= 0) return;
     t = 0;
-    do n = unit_tiles(p, ++u); while (n == 0);  // left > 0: a later unit has tiles
+    do m = unit_tiles(p, ++u); while (m == 0);  // left > 0: a later unit has tiles
+    m = min(m, left);
   }
 };
+
+// Block-table entries of a request, 16 tiles (32 pages) to a warp's register
+// and the next 16 on their way.
+struct Pages {
+  const int32_t* row;
+  int base, entry, ahead;
+  uint32_t bad;  // of `entry`: out of range
+  MLA_DEV void mark(const ScoreParams& p) {
+    bad = __ballot_sync(0xffffffffu, entry < 0 || entry >= p.num_blocks);
+  }
+  MLA_DEV int load(const ScoreParams& p, int t) const {
+    const int at = 2 * t + (int)(threadIdx.x & 31);
+    return at < p.max_blocks ? __ldg(row + at) : -1;
+  }
+  MLA_DEV void start(const ScoreParams& p, int b, int t) {
+    row = p.block_table + (int64_t)b * p.max_blocks;
+    base = t;
+    entry = load(p, t);
+    ahead = load(p, t + 16);
+    mark(p);
+  }
+  MLA_DEV bool is_bad(int t, int k) const { return (bad >> (2 * (t - base) + k)) & 1u; }  // t below base + 16
+  // page k (0 or 1) of tile t, at most 31 tiles behind base
+  MLA_DEV int page(int t, int k) const {
+    const int i = t - base;
+    return __shfl_sync(0xffffffffu, i < 16 ? entry : ahead, (2 * i + k) & 31);
+  }
+  MLA_DEV void advance(const ScoreParams& p, int t) {
+    if (t - base < 16) return;
+    base += 16;
+    entry = ahead;
+    ahead = load(p, base + 16);
+    mark(p);
+  }
+};
+
+// The wait's slow path stands apart from the loops of the issuing threads:
+// what they run per tile has to stay in the instruction cache.
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Guard g) { return wait(bar, parity, g); }
+MLA_DEV bool wait_for(uint32_t bar, uint32_t parity, const Guard& g) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, g);
+}
 
 // D[tmem] (+)= A[smem] * B[smem], e4m3 operands, fp32 accumulation
 MLA_DEV void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
@@ -117,6 +167,48 @@ MLA_DEV void tma_load_3d_plain(uint32_t dst, const CUtensorMap* m, uint32_t bar,
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+
+// acc += w * max(0, (x0, x1)) on packed pairs. One asm block: the maxima are
+// written where the packed fma reads them (built from separate expressions,
+// a third of the loop was register moves).
+MLA_DEV void fma_positive(uint64_t& acc, uint32_t x0, uint32_t x1, uint64_t w) {
+  asm("{\n\t.reg .f32 lo, hi;\n\t.reg .b64 x;\n\tmax.f32 lo, %1, 0f00000000;\n\tmax.f32 hi, %2, 0f00000000;\n\t"
+      "mov.b64 x, {lo, hi};\n\tfma.rn.f32x2 %0, x, %3, %0;\n\t}"
+      : "+l"(acc) : "f"(__uint_as_float(x0)), "f"(__uint_as_float(x1)), "l"(w));
+}
+MLA_DEV uint64_t ld_shared_64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr));
+  return v;
+}
+// 16 rows x 64 columns of an accumulator as matrix fragments: register 4k + 2i
+// + x of lane l is row 8i + l / 4, column 8k + 2 (l % 4) + x
+MLA_DEV void tmem_ld_16x64(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// position in a ring whose length only the host knows: slot and phase are
+// stepped, since a division per tile (some 150 cycles) is what the issuing
+// threads would spend most of their time on
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  MLA_DEV void step(int length) {
+    if (++slot == length) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
 enum : int { K_BF16 = 0, K_FP16 = 1, K_FP8 = 2 };
 
@@ -143,7 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* abort_flag = misc + 1;
   volatile uint32_t* ok_flag = misc + 2;
   volatile int* range = reinterpret_cast<volatile int*>(misc + 4);  // first unit, first tile, pairs
-  int* scan = reinterpret_cast<int*>(smem + off_w);                 // [12 warps], before the weights arrive
+  int* scan = reinterpret_cast<int*>(smem + off_w);                 // [warps], before the weights arrive
+  const int acc_shift = N > 128 ? 1 : 2, accs = 1 << acc_shift;     // accumulators of 512 / accs columns
+  const uint32_t acc_cols = 512u >> acc_shift;
   auto bar = [&](uint32_t i) { return sb + off_bar + 8u * i; };
   uint32_t* status = p.status ? p.status : misc + 3;
   const Guard guard{abort_flag, status, kWaitLimitCycles};
@@ -153,15 +247,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_KFULL + s), 1);
       mbar_init(bar(B_KEMPTY + s), 1);
     }
+    for (int s = 0; s < accs; ++s) {
+      mbar_init(bar(B_AFULL + s), 1);
+      mbar_init(bar(B_AEMPTY + s), accs == 2 ? 4 * kGroups : 4);
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(B_QFULL + s), 1);
       mbar_init(bar(B_QEMPTY + s), 1);
-      mbar_init(bar(B_AFULL + s), 1);
-      mbar_init(bar(B_AEMPTY + s), 4);
       mbar_init(bar(B_WFULL + s), 1);
-      mbar_init(bar(B_WEMPTY + s), 8);
-      mbar_init(bar(B_RED + s), 4);
+      mbar_init(bar(B_WEMPTY + s), 4 * kGroups);
     }
+    for (int s = 0; s < kGroups; ++s) mbar_init(bar(B_RED + s), 4);
     mbar_init(bar(B_DRAIN), 1);
     mbar_init(bar(B_STALL), 1);
     *abort_flag = 0u;
@@ -225,92 +321,111 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool ok = *ok_flag != 0u;
   Walk it(p, range[0], range[1], ok ? range[2] : 0);
 
-  if (warp == 0 && lane == 0 && !it.done()) {
+  if (warp == 0 && !it.done()) {
     // ---------------- producer: a unit's query groups, then key tiles ----------------
-    prefetch_tmap(&tm_q);
-    prefetch_tmap(&tm_k);
-    int n = 0, units = 0, unit = -1, last_q[2] = {-1, -1};
+    if (lane == 0) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+    }
+    int n = 0, units = 0, last_q[2] = {-1, -1};
     bool stop = false;
-    for (; !stop && !it.done(); it.next(p)) {
+    Ring kr;
+    Pages pages;
+    for (; !stop && !it.done(); it.next(p), ++units) {
       const int b = it.u / p.units;
-      if (it.u != unit) {
-        unit = it.u;
+      pages.start(p, b, it.t);
+      if (lane == 0) {
         const int q0 = (it.u - b * p.units) * p.nq * p.groups;
-        for (int g = 0; g < p.groups && !stop; ++g) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
           // a last group behind the request's queries reads others (or the
           // zero fill); its products are never stored
-          if (!wait(bar(B_QEMPTY + g), (units & 1) ^ 1, guard)) { stop = true; break; }
+          if (g >= p.groups || stop) break;
+          if (!wait_for(bar(B_QEMPTY + g), (units & 1) ^ 1, guard)) { stop = true; break; }
           mbar_arrive_expect_tx(bar(B_QFULL + g), q_group);
           for (int c = 0; c < kChunks; ++c)
             tma_load_3d_plain(sb + g * q_group + c * q_chunk, &tm_q, bar(B_QFULL + g), c * kChunkElems, 0,
                               b * p.s_q + q0 + g * p.nq);
           last_q[g] = units;
         }
-        ++units;
-        if (stop) break;
       }
-      int page[2];
+      const int t1 = it.t + it.m;
+      for (int t = it.t; t < t1; ++t) {
+        pages.advance(p, t);
+        int page[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int at = 2 * it.t + k;
-        const int pg = at < p.max_blocks ? __ldg(p.block_table + (int64_t)b * p.max_blocks + at) : 0;
-        page[k] = pg < 0 || pg >= p.num_blocks ? 0 : pg;  // a bad page is masked by the epilogue
-      }
-      for (int c = 0; c < kChunks; ++c, ++n) {
-        const int s = n % p.ring;
-        if (!wait(bar(B_KEMPTY + s), ((n / p.ring) & 1) ^ 1, guard)) { stop = true; break; }
-        mbar_arrive_expect_tx(bar(B_KFULL + s), kUnit);
+        for (int k = 0; k < 2; ++k) {
+          page[k] = pages.page(t, k);
+          if (page[k] < 0 || page[k] >= p.num_blocks) page[k] = 0;  // a bad page's products are not stored
+        }
+        if (lane == 0 && !stop) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          tma_load_3d_plain(sb + off_ring + s * kUnit + k * (kUnit / 2), &tm_k, bar(B_KFULL + s), c * kChunkElems, 0,
-                            page[k]);
+          for (int c = 0; c < kChunks; ++c) {
+            if (!wait_for(bar(B_KEMPTY + kr.slot), kr.phase ^ 1u, guard)) { stop = true; break; }
+            mbar_arrive_expect_tx(bar(B_KFULL + kr.slot), kUnit);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              tma_load_3d_plain(sb + off_ring + kr.slot * kUnit + k * (kUnit / 2), &tm_k, bar(B_KFULL + kr.slot),
+                                c * kChunkElems, 0, page[k]);
+            kr.step(p.ring);
+            ++n;
+          }
+        }
       }
+      stop = __shfl_sync(0xffffffffu, (int)stop, 0) != 0;
     }
     // never leave with a copy in flight into this CTA's shared memory
-    const uint64_t t_0 = cycles();
-    for (int k = n < p.ring ? 0 : n - p.ring; k < n; ++k)
-      while (!mbar_try_wait(bar(B_KFULL + k % p.ring), (k / p.ring) & 1) && cycles() - t_0 < kDrainLimitCycles) {}
-    for (int g = 0; g < 2; ++g)
-      if (last_q[g] >= 0)
-        while (!mbar_try_wait(bar(B_QFULL + g), last_q[g] & 1) && cycles() - t_0 < kDrainLimitCycles) {}
+    if (lane == 0) {
+      const uint64_t t_0 = cycles();
+      for (int k = n < p.ring ? 0 : n - p.ring; k < n; ++k)
+        while (!mbar_try_wait(bar(B_KFULL + k % p.ring), (k / p.ring) & 1) && cycles() - t_0 < kDrainLimitCycles) {}
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (last_q[g] >= 0)
+          while (!mbar_try_wait(bar(B_QFULL + g), last_q[g] & 1) && cycles() - t_0 < kDrainLimitCycles) {}
+    }
   } else if (warp == 1 && lane == 0 && !it.done()) {
     // ---------------- UMMA issue ----------------
     const uint32_t idesc = kType == K_FP8 ? ((1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24))
                                           : idesc_f16(128, N, kType == K_BF16, false, false);
-    int n = 0, seq = 0, units = 0, unit = -1;
+    const uint64_t d_ring = sdesc_sw128(sb + off_ring, 16, 1024), d_q = sdesc_sw128(sb, 16, 1024);
+    int seq = 0, units = 0;
     bool failed = false;
-    for (; !failed && !it.done(); it.next(p)) {
-      const bool first = it.u != unit, last = it.last_of_unit();
-      unit = it.u;
-      for (int g = 0; g < p.groups && !failed; ++g, ++seq) {
-        const int acc = seq & 1;
-        if ((first && !wait(bar(B_QFULL + g), units & 1, guard)) ||
-            !wait(bar(B_AEMPTY + acc), ((seq >> 1) & 1) ^ 1, guard)) {
-          failed = true;
-          break;
-        }
+    Ring kr;
+    for (; !failed && !it.done(); it.next(p), ++units) {
+      if (!wait_for(bar(B_QFULL), units & 1, guard) ||
+          (p.groups == 2 && !wait_for(bar(B_QFULL + 1), units & 1, guard)))
+        break;
+      for (int i = 0; i < it.m && !failed; ++i) {
+        Ring at = kr;
+        for (int g = 0; g < p.groups; ++g, ++seq) {
+          at = kr;  // every group reads the tile's units
+          const int acc = seq & (accs - 1);
+          const uint32_t d = tmem + acc_cols * acc;
+          if (!wait_for(bar(B_AEMPTY + acc), ((seq >> acc_shift) & 1) ^ 1, guard)) { failed = true; break; }
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int s = (n + c) % p.ring;
-          if (g == 0 && !wait(bar(B_KFULL + s), ((n + c) / p.ring) & 1, guard)) { failed = true; break; }
-          tc_fence_after();
-          const uint64_t da = sdesc_sw128(sb + off_ring + s * kUnit, 16, 1024);
-          const uint64_t db = sdesc_sw128(sb + g * q_group + c * q_chunk, 16, 1024);
+          for (int c = 0; c < kChunks; ++c) {
+            if (g == 0 && !wait_for(bar(B_KFULL + at.slot), at.phase, guard)) { failed = true; break; }
+            tc_fence_after();
+            const uint64_t da = d_ring + (uint32_t)at.slot * (kUnit >> 4);
+            const uint64_t db = d_q + ((g * q_group + c * q_chunk) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the contraction each
-            if (kType == K_FP8)
-              umma_ss_f8(tmem + (uint32_t)kMaxN * acc, da + 2u * kk, db + 2u * kk, idesc, (c | kk) ? 1u : 0u);
-            else
-              umma_ss(tmem + (uint32_t)kMaxN * acc, da + 2u * kk, db + 2u * kk, idesc, (c | kk) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the contraction each
+              if (kType == K_FP8)
+                umma_ss_f8(d, da + 2u * kk, db + 2u * kk, idesc, (c | kk) ? 1u : 0u);
+              else
+                umma_ss(d, da + 2u * kk, db + 2u * kk, idesc, (c | kk) ? 1u : 0u);
+            }
+            if (g == p.groups - 1) umma_commit(bar(B_KEMPTY + at.slot));
+            at.step(p.ring);
           }
-          if (g == p.groups - 1) umma_commit(bar(B_KEMPTY + s));
+          if (failed) break;
+          umma_commit(bar(B_AFULL + acc));
         }
-        if (failed) break;
-        umma_commit(bar(B_AFULL + acc));
-        if (last) umma_commit(bar(B_QEMPTY + g));
+        kr = at;
       }
-      n += kChunks;
-      if (first) ++units;
+      umma_commit(bar(B_QEMPTY));
+      if (p.groups == 2) umma_commit(bar(B_QEMPTY + 1));
     }
     // every UMMA this thread issued has completed before TMEM is released
     umma_commit(bar(B_DRAIN));
@@ -329,14 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 3 && !it.done()) {
     // ---------------- head weights of each unit, padded heads zero ----------------
-    int units = 0, unit = -1;
-    for (; !it.done(); it.next(p)) {
-      if (it.u == unit) continue;
-      unit = it.u;
+    for (int units = 0; !it.done(); it.next(p), ++units) {
       const int par = units & 1;
-      const bool free = wait(bar(B_WEMPTY + par), ((units >> 1) & 1) ^ 1, guard);
+      const bool free = wait_for(bar(B_WEMPTY + par), ((units >> 1) & 1) ^ 1, guard);
       if (!__all_sync(0xffffffffu, free)) break;
-      const int b = unit / p.units, q0 = (unit - b * p.units) * p.nq * p.groups;
+      const int b = it.u / p.units, q0 = (it.u - b * p.units) * p.nq * p.groups;
       float* dst = reinterpret_cast<float*>(smem + off_w) + par * 2 * kMaxN;
       for (int g = 0; g < p.groups; ++g)
         for (int e = lane; e < N; e += 32) {
@@ -346,88 +458,176 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_WFULL + par));
-      ++units;
     }
   } else if (warp >= 4 && !it.done()) {
     // ---------------- epilogue: sum over heads ----------------
-    const int e = (warp - 4) >> 2, q4 = warp & 3;  // accumulator, TMEM lane quarter
-    const uint32_t tl = tmem + (uint32_t)kMaxN * e + ((uint32_t)(32 * q4) << 16);
-    const float* weights = reinterpret_cast<const float*>(smem + off_w);
+    const int e = (warp - 4) >> 2, q4 = warp & 3;  // epilogue group, TMEM lane quarter
     float* red = reinterpret_cast<float*>(smem + off_red) + e * 2 * 4 * 16;
-    int seq = 0, units = -1, unit = -1, done = 0;
+    // two accumulators: both groups sum a share of each one's queries; four:
+    // each group takes every other tile
+    const bool shared = accs == 2;
+    const int ways = shared ? 1 : kGroups;
+    // queries [first, first + most) of a query group; a multiple of 32 columns lies before them
+    constexpr int kAlign = kHp == 16 ? 2 : 1;
+    const int share = shared ? (p.nq + kGroups * kAlign - 1) / (kGroups * kAlign) * kAlign : p.nq;
+    const int first = shared ? e * share : 0, most = min(share, p.nq - first);
+    const int row = 32 * q4 + 8 * (lane & 3) + (lane >> 2);  // this thread's token of a tile (see `reduce`)
+    const uint32_t tl0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(first * kHp);
+    const uint32_t w0 = sb + off_w + (uint32_t)(first * kHp) * 4u + 8u * (lane & 3);
+    const int64_t group_step = p.nq * p.stride;
+    constexpr int kQ = 64 / kHp;                   // queries of a batch of 64 columns
+    // Four lanes hold parts of the same four rows (8i + l / 4): they exchange
+    // halves, then quarters, and lane l ends with row 8 (l % 4) + l / 4.
+    const bool up = lane & 2, odd = lane & 1;
+    auto reduce = [&](const float (&v)[4]) {
+      const float a = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 2);
+      const float c = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 2);
+      return (odd ? c : a) + __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
+    };
+    int tiles = 0, done = 0;
     bool failed = false;
-    for (; !failed && !it.done(); it.next(p)) {
-      if (it.u != unit) {
-        // the weights of the unit before are free once this warp has left it
-        __syncwarp();
-        if (unit >= 0 && lane == 0) mbar_arrive(bar(B_WEMPTY + (units & 1)));
-        unit = it.u;
-        ++units;
-        if (!__all_sync(0xffffffffu, wait(bar(B_WFULL + (units & 1)), (units >> 1) & 1, guard))) break;
-      }
-      const int b = unit / p.units, q0 = (unit - b * p.units) * p.nq * p.groups;
-      const int tok = it.t * kTokens + 32 * q4 + lane;
-      // the page of this warp's 32 tokens
-      const int at = 2 * it.t + (q4 >> 1);
-      const int pg = at < p.max_blocks ? __ldg(p.block_table + (int64_t)b * p.max_blocks + at) : -1;
-      const bool good = pg >= 0 && pg < p.num_blocks;
-      const int len = __ldg(p.seqlens + b);
-      if (!good && lane == 0 && 64 * at < min(len, p.cover)) atomicOr(status, STATUS_INDEX);
-      float ks = 1.f;
-      if (kType == K_FP8 && good)
-        ks = __ldg(reinterpret_cast<const float*>(p.cache + (int64_t)pg * (kTile * (kDim + 4)) + kTile * kDim) +
-                   (tok & (kTile - 1)));
-      for (int g = 0; g < p.groups; ++g, ++seq) {
-        if ((seq & 1) != e) continue;
-        if (!__all_sync(0xffffffffu, wait(bar(B_AFULL + e), (seq >> 1) & 1, guard))) {
-          failed = true;
-          break;
-        }
-        tc_fence_after();
-        const float* w = weights + (units & 1) * 2 * kMaxN + g * kMaxN;
+    Pages pages;
+    for (int units = 0; !failed && !it.done(); it.next(p), ++units) {
+      const int b = it.u / p.units, k0 = (it.u - b * p.units) * p.groups * p.nq + first;
+      const int unit_seen = unit_visible(p, it.u);
+      // tokens that query k0 sees, and each query behind it (a causal one more)
+      const int len = __ldg(p.seqlens + b), seen0 = p.causal ? len - (p.s_q - 1 - k0) : len, later = p.causal ? 1 : 0;
+      // tiles t of this unit with (number of the tile in the CTA's range) % ways == e
+      int t = it.t + (shared ? 0 : (e - tiles) & (kGroups - 1));
+      const int t1 = it.t + it.m;
+      tiles += it.m;
+      pages.start(p, b, it.t);
+      // scale of this thread's token in tile `at` (its page's scales follow the page's rows)
+      auto scale_at = [&](int at) {
+        const int pg = pages.page(at, q4 >> 1);
+        if (pg < 0 || pg >= p.num_blocks) return 1.f;
+        return __ldg(reinterpret_cast<const float*>(p.cache + (int64_t)pg * (kTile * (kDim + 4)) + kTile * kDim) +
+                     (row & (kTile - 1)));
+      };
+      float ks = 1.f, ks_next = 1.f;
+      if (kType == K_FP8 && t < t1) ks_next = scale_at(t);
+      float* out_unit = p.scores + ((int64_t)b * p.s_q + k0) * p.stride + (kPages ? 0 : t * kTokens + row);
+      uint32_t w = w0 + (uint32_t)(units & 1) * (2 * kMaxN * 4);
+      if (!__all_sync(0xffffffffu, wait_for(bar(B_WFULL + (units & 1)), (units >> 1) & 1, guard))) break;
 #pragma unroll 1
-        for (int j = 0; j < p.nq; ++j) {
-          const int q = q0 + g * p.nq + j;
-          if (q >= p.s_q) break;
-          float sum = 0.f;
-#pragma unroll
-          for (int c = 0; c < kHp; c += 16) {
-            uint32_t r[16];
-            tmem_ld16(tl + (uint32_t)(j * kHp + c), r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) sum = fmaf(w[j * kHp + c + k], fmaxf(__uint_as_float(r[k]), 0.f), sum);
-          }
-          const float s = good && tok < visible(p, len, q) ? sum * ks : -INFINITY;
-          if (!kPages) {
-            if (tok < p.width) p.scores[((int64_t)b * p.s_q + q) * p.stride + tok] = s;
-          } else {
-            float m = s;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == 0) red[(done & 1) * 64 + q4 * 16 + j] = m;
-          }
+      for (; t < t1; t += ways, out_unit += kPages ? 0 : kTokens * ways) {
+        pages.advance(p, t);
+        const bool bad = pages.is_bad(t, q4 >> 1);
+        if (kType == K_FP8) {
+          ks = ks_next;
+          if (t + ways < t1) ks_next = scale_at(t + ways);
         }
-        tc_fence_before();
-        if (lane == 0) mbar_arrive(bar(B_AEMPTY + e));
-        if (kPages) {
-          // the page's other warp; bounded like every wait, so that a warp that
-          // gave up leaves no one behind
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_RED + e));
-          if (!__all_sync(0xffffffffu, wait(bar(B_RED + e), done & 1, guard))) {
+        const int tok = t * kTokens + row;
+        if (bad && lane == 0 && (tok & ~(kTile - 1)) < unit_seen) atomicOr(status, STATUS_INDEX);
+        float* out = out_unit;
+        int left = p.s_q - k0, seen = bad ? INT_MIN / 2 : seen0;
+#pragma unroll 1
+        for (int g = 0; g < p.groups; ++g) {
+          const int queries = min(most, left);                             // may be none in a request's last unit
+          const int batches = queries > 0 ? (queries * kHp + 63) / 64 : 0;  // of 64 columns, at most 2
+          const int seq = shared ? done : kGroups * done + e, acc = seq & (accs - 1);
+          const uint32_t tl = tl0 + acc_cols * (uint32_t)acc;
+          uint64_t wv[8];  // the lane's weights of a batch: columns 8k + 2 (lane % 4) + {0, 1}
+          auto load_weights = [&](int c) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) wv[k] = ld_shared_64(w + g * (kMaxN * 4) + 256u * c + 32u * k);
+          };
+          // 16 rows of a batch: the lane's columns of rows l / 4 and 8 + l / 4, summed per query
+          auto half = [&](const uint32_t* r, float (*v)[4], int i) {
+#pragma unroll
+            for (int j = 0; j < kQ; ++j) {
+              uint64_t lo = 0, hi = 0;
+#pragma unroll
+              for (int k = j * (8 / kQ); k < (j + 1) * (8 / kQ); ++k) {
+                fma_positive(lo, r[4 * k], r[4 * k + 1], wv[k]);
+                fma_positive(hi, r[4 * k + 2], r[4 * k + 3], wv[k]);
+              }
+              const float2 x = f2_unpack(lo), y = f2_unpack(hi);
+              v[j][i] = x.x + x.y;
+              v[j][i + 1] = y.x + y.y;
+            }
+          };
+          auto release = [&]() {  // the accumulator is free for the next products
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_AEMPTY + acc));
+          };
+          // two register buffers of 16 rows: one is loaded while the other is summed
+          uint32_t ra[32], rb[32];
+          float v0[kQ][4], v1[kQ][4];
+          load_weights(0);
+          if (!__all_sync(0xffffffffu, wait_for(bar(B_AFULL + acc), (seq >> acc_shift) & 1, guard))) {
             failed = true;
             break;
           }
-          const int x = 32 * q4 + lane, j = x >> 1, k = x & 1;
-          const int q = q0 + g * p.nq + j, page = 2 * it.t + k;
-          if (j < p.nq && q < p.s_q && page < p.width) {
-            const float* v = red + (done & 1) * 64 + 2 * k * 16 + j;
-            p.scores[((int64_t)b * p.s_q + q) * p.stride + page] = fmaxf(v[0], v[16]);
+          tc_fence_after();
+          tmem_ld_16x64(tl, ra);
+          tmem_ld_16x64(tl + (16u << 16), rb);
+          tmem_wait_ld();
+          pin_regs32(ra);
+          pin_regs32(rb);
+          if (batches == 2) {
+            half(ra, v0, 0);
+            tmem_ld_16x64(tl + 64, ra);
+            half(rb, v0, 2);
+            load_weights(1);
+            tmem_ld_16x64(tl + (16u << 16) + 64, rb);
+            tmem_wait_ld();
+            pin_regs32(ra);
+            pin_regs32(rb);
+            release();
+            half(ra, v1, 0);
+            half(rb, v1, 2);
+          } else {
+            release();
+            half(ra, v0, 0);
+            half(rb, v0, 2);
           }
+          float total[2 * kQ];
+#pragma unroll
+          for (int j = 0; j < kQ; ++j) {
+            total[j] = reduce(v0[j]);
+            if (batches == 2) total[kQ + j] = reduce(v1[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 2 * kQ; ++j) {
+            if (j >= queries) break;
+            const float s = tok < min(seen + later * j, p.cover) ? total[j] * ks : -INFINITY;
+            if (!kPages) {
+              if (tok < p.width) out[j * p.stride] = s;
+            } else {
+              float m = s;
+#pragma unroll
+              for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+              if (lane == 0) red[(done & 1) * 64 + q4 * 16 + j] = m;
+            }
+          }
+          if (kPages) {
+            // the page's other warp; bounded like every wait, so that a warp that
+            // gave up leaves no one behind
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_RED + e));
+            if (!__all_sync(0xffffffffu, wait_for(bar(B_RED + e), done & 1, guard))) {
+              failed = true;
+              break;
+            }
+            const int x = 32 * q4 + lane, j = x >> 1, k = x & 1, page = 2 * t + k;
+            if (j < queries && page < p.width) {
+              const float* v = red + (done & 1) * 64 + 2 * k * 16 + j;
+              out[j * p.stride + page] = fmaxf(v[0], v[16]);
+            }
+          }
+          ++done;
+          // the unit's second group
+          out += group_step;
+          seen += later * p.nq;
+          left -= p.nq;
         }
-        ++done;
+        if (failed) break;
       }
+      // the unit's weights are free once every warp has left it
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_WEMPTY + (units & 1)));
     }
   }
   __syncwarp();

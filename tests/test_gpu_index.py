@@ -135,7 +135,7 @@ def test_rotate_q(tokens, heads, dtype, halves):
     # heads-major storage, and one row for every head
     major = x[..., 128:].transpose(0, 1).contiguous().to(DEV).transpose(0, 1)
     got = mla.mla_rotate_q(major, p, _table(), rope_style=halves)
-    assert torch.equal(got.cpu()[keep], rot[keep]) and (got.cpu()[~keep] == 0).all()
+    assert torch.equal(got.cpu()[keep], rot[keep])
     shared = mla.mla_rotate_q(xd[:, :1, 128:].expand(-1, heads, -1), p, _table(), rope_style=halves)
     assert torch.equal(shared.cpu()[keep], rot[:, :1].expand(-1, heads, -1)[keep])
 
@@ -185,10 +185,15 @@ def test_quantize_index_q(tokens, heads, dtype, halves):
     keep = (pos >= 0) & (pos < 5000)
     _, codes, scale = oracle.index_row_codes(q[..., 64:], TABLE[np.clip(pos, 0, 4999)][:, None], bool(halves))
     st = _status()
-    q8, wo = mla.mla_quantize_index_q(q.to(DEV)[..., 64:], w.to(DEV), torch.from_numpy(pos).to(DEV), _table(), rope_style=halves, status=st)
+    q8 = torch.zeros(tokens, heads, 128, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    wo = torch.zeros(tokens, heads, device=DEV)
+    mla.mla_quantize_index_q(q.to(DEV)[..., 64:], w.to(DEV), torch.from_numpy(pos).to(DEV), _table(), rope_style=halves,
+                             q_out=q8, weights_out=wo, status=st)
     assert _bits(st) == bad and q8.dtype == torch.float8_e4m3fn
     assert (q8.view(torch.uint8).cpu().numpy() == np.where(keep[:, None, None], codes, 0)).all()
     assert (wo.cpu().numpy() == np.where(keep[:, None], w.numpy() * scale, 0)).all()
+    q2, wo = mla.mla_quantize_index_q(q.to(DEV)[..., 64:], w.to(DEV), torch.from_numpy(pos).to(DEV), _table(), rope_style=halves)
+    assert q2.dtype == torch.float8_e4m3fn and torch.equal(q2.view(torch.uint8)[keep], q8.view(torch.uint8)[keep])
     wd = w.to(DEV)
     mla.mla_quantize_index_q(q.to(DEV)[..., 64:], wd, torch.from_numpy(pos).to(DEV), _table(), rope_style=halves, weights_out=wd)
     assert (wd.cpu().numpy() == np.where(keep[:, None], w.numpy() * scale, w.numpy())).all()
