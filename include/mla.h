@@ -430,8 +430,8 @@ MLA_API mla_status mla_index_score(const void* q, int q_dtype, const float* weig
 /*
  * The topk best columns of each row of `scores` (any fp32 matrix laid out like
  * mla_index_score's; only the visible columns are read). Equal scores go to the
- * lower position, NaN ranks below every number; the selected ones are written
- * in ascending position.
+ * lower position, NaN counts as -inf; the selected ones are written in
+ * ascending position.
  * block = 1:  indices (device) int32 [batch, s_q, topk]: absolute cache rows
  *             page * 64 + offset, -1 behind the last one: the `indices` of
  *             mla_decode_with_kvcache. lens (device, optional) int32

@@ -215,6 +215,45 @@ mla_status launch_score(int dev, int grid, uint32_t smem, void* stream, const CU
   MLA_CUDA(cudaLaunchKernelEx(&cfg, kernel, tq, tk, p));
   return MLA_OK;
 }
+// `most`: columns of the longest possible row
+template <bool kPages>
+mla_status launch_select(select::SelectParams p, int64_t most, int sms, void* stream) {
+  const int64_t rows = (int64_t)p.batch * p.s_q;
+  constexpr int kSmall = 4, kBlockSmall = select::kThreads * kSmall;
+  auto blocks = [](int64_t n, int per) {
+    int c = 1;
+    while (c < select::kMaxCluster && (int64_t)c * per < n) c *= 2;
+    return c;
+  };
+  int keys = select::kMaxKeys;
+  const int small = blocks(most, kBlockSmall);
+  if ((int64_t)small * kBlockSmall >= most && rows * small <= 2 * sms) {
+    keys = kSmall;
+    p.cluster = small;
+  } else {
+    p.cluster = blocks(most, select::kBlockKeys);
+    if ((int64_t)p.cluster * select::kBlockKeys < most) keys = 0;
+  }
+  auto kernel = keys == kSmall ? select::mla_select_topk_kernel<kPages, kSmall>
+                : keys         ? select::mla_select_topk_kernel<kPages, select::kMaxKeys>
+                               : select::mla_select_topk_kernel<kPages, 0>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * p.cluster), 1, 1);
+  cfg.blockDim = dim3(select::kThreads, 1, 1);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)p.cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+  MLA_CUDA(cudaLaunchKernelEx(&cfg, kernel, p));
+  return MLA_OK;
+}
+
 template <int kType, int kHp, typename... A>
 mla_status launch_score_block(bool pages, A&&... a) {
   return pages ? launch_score<kType, kHp, true>(a...) : launch_score<kType, kHp, false>(a...);
@@ -310,15 +349,17 @@ mla_status mla_select_topk(const float* scores, int64_t score_stride, int width,
   if ((int64_t)batch * s_q >= kMaxRows) return MLA_ERR_INVALID_ARG;
   const int64_t columns = (int64_t)width * (pages ? kTile : 1), reach = (int64_t)max_blocks * kTile;
   if ((columns < reach ? columns : reach) >= kMaxRows - kTile) return MLA_ERR_INVALID_ARG;
+  if ((int64_t)batch * s_q >= kMaxRows / select::kMaxCluster) return MLA_ERR_UNSUPPORTED;
   if (!scores || !cache_seqlens || !block_table || !indices || (pages && !lens) || !aligned(scores, 4) ||
       !aligned(cache_seqlens, 4) || !aligned(block_table, 4) || !aligned(indices, 4) || (lens && !aligned(lens, 4)) ||
       (status && !aligned(status, 4)))
     return MLA_ERR_INVALID_ARG;
   select::SelectParams p{scores, score_stride, width, cache_seqlens, block_table, num_blocks, max_blocks,
-                         batch, s_q, causal ? 1 : 0, topk, indices, lens, status};
-  const dim3 grid((unsigned)(batch * s_q));
-  return pages ? launch(select::mla_select_topk_kernel<true>, grid, select::kThreads, 0, stream, p)
-               : launch(select::mla_select_topk_kernel<false>, grid, select::kThreads, 0, stream, p);
+                         batch, s_q, causal ? 1 : 0, topk, 1, indices, lens, status};
+  int dev = 0, sms = 0;
+  if (const mla_status v = sm_count(&dev, &sms)) return v;
+  const int64_t most = pages ? ((columns < reach ? columns : reach) + kTile - 1) / kTile : columns < reach ? columns : reach;
+  return pages ? launch_select<true>(p, most, sms, stream) : launch_select<false>(p, most, sms, stream);
 }
 
 }  // extern "C"

@@ -6,7 +6,7 @@
   (i, i + 32) with ``halves``.
 * Index score: sum over heads of weight x max(0, q . k), in float64.
 * Selection: the topk largest, equal ones in the order of their positions, NaN
-  below every number, the result in ascending position.
+  as -inf, the result in ascending position.
 """
 from __future__ import annotations
 
@@ -91,7 +91,7 @@ def page_max(scores: np.ndarray, page: int = 64) -> np.ndarray:
 def select_topk(scores, n: int, topk: int, last: bool = False) -> np.ndarray:
     """Positions selected among scores[:n], ascending; ``last`` forces n - 1."""
     s = [float(v) for v in scores[:n]]
-    key = [(-np.inf, 0) if np.isnan(v) else (v, 1) for v in s]   # NaN behind -inf
+    key = [(-np.inf, 1) if np.isnan(v) else (v, 1) for v in s]
     if last and n:
         key[n - 1] = (np.inf, 2)
     order = sorted(range(n), key=lambda i: (-key[i][0], -key[i][1], i))

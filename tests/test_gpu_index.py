@@ -402,6 +402,24 @@ def test_select_long_rows(n):
         _select_both(s, [n], 2, True, 1, topk, bt, most)
 
 
+@pytest.mark.parametrize("n", [700, 2000, 9000, 20000, 131072])
+@pytest.mark.parametrize("kind", ["rising", "falling", "comb", "few", "plateau", "inf"])
+def test_select_uneven_rows(n, kind):
+    """Rows on which a sample of the scores says little about the rest, or whose threshold is shared by many."""
+    most = -(-n // PAGE)
+    bt = np.random.default_rng(n).permutation(most).reshape(1, most).astype(np.int32)
+    t = torch.arange(n, dtype=torch.float32)
+    s = {"rising": t / n - 0.5, "falling": 1e3 - t, "comb": torch.where(t % 64 < 62, t % 977, -t),
+         "few": torch.where(t > n - 40, t, torch.zeros(n)), "plateau": torch.where(t % 3 == 0, t * 1e-3, torch.full((n,), 5.0)),
+         "inf": torch.where(t % 5 == 0, float("inf"), torch.where(t % 7 == 0, -float("inf"), t))}[kind]
+    # every warp's and every block's first scores low, the others high
+    low = s.clone()
+    low[(torch.arange(n) % 160) < 80] = -1e30
+    for row in (s, low):
+        for topk in (1, 30, min(2048, n // 2), n - 1):
+            _select_both(row.view(1, 1, n), [n], 1, False, 1, topk, bt, most)
+
+
 # ---------------------------------------------------------------------------
 # a run of them together
 # ---------------------------------------------------------------------------

@@ -195,7 +195,8 @@ def test_oracle_selection_by_brute_force():
     assert oracle.select_topk(s, 8, 1).tolist() == [7]
     assert oracle.select_topk(s, 8, 2).tolist() == [1, 7]          # of two 3.0 the first
     assert oracle.select_topk(s, 8, 5).tolist() == [0, 1, 4, 6, 7]  # 0.0 and -0.0 are equal
-    assert oracle.select_topk(s, 8, 7).tolist() == [0, 1, 2, 4, 5, 6, 7]
+    assert oracle.select_topk(s, 8, 6).tolist() == [0, 1, 2, 4, 6, 7]
+    assert oracle.select_topk(s, 8, 7).tolist() == [0, 1, 2, 3, 4, 6, 7]   # NaN as -inf: the lower position
     assert oracle.select_topk(s, 6, 2, last=True).tolist() == [1, 5]
     assert oracle.select_topk(s, 4, 9).tolist() == [0, 1, 2, 3]
     assert oracle.select_topk(s, 0, 3).tolist() == []
