@@ -159,12 +159,11 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
       for (int k = 0; k < 2; ++k) probe[k] = held[k % (kKeys > 0 ? kKeys : 1)] == 0xFFFFFFFFu ? 0u : held[k % (kKeys > 0 ? kKeys : 1)];
     }
   }
-  // f(key, step) over the warp's steps
+  // f(key, step) over the warp's steps (and the padding behind them: no branches)
   auto for_keys = [&](auto&& f) {
     if (kKeys > 0) {
 #pragma unroll
-      for (int s = 0; s < kKeys; ++s)
-        if (s < steps) f(held[s], s);
+      for (int s = 0; s < kKeys; ++s) f(held[s], s);
     } else {
 #pragma unroll 4
       for (int s = 0; s < steps; ++s) f(key_of(s), s);
@@ -282,20 +281,30 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
       } else if (size <= kList) {
         // 3. the bin's keys, compared pairwise
         uint32_t* mine = p.cluster > 1 ? own_list : list;
-        for_keys([&](uint32_t key, int s) {
-          (void)s;
-          if (key >= first && key <= last) mine[atomicAdd(&list_count, 1)] = key;
-        });
+        const uint32_t span = last - first;
+        if (kKeys > 0) {
+          // few lanes have one: marked without a branch per step, then read again
+          uint32_t marks = 0;
+          for_keys([&](uint32_t key, int s) { marks |= key - first <= span ? 1u << s : 0u; });
+          while (marks) {
+            const int s = __ffs(marks) - 1;
+            marks &= marks - 1u;
+            mine[atomicAdd(&list_count, 1)] = key_of(s);
+          }
+        } else {
+          for_keys([&](uint32_t key, int s) {
+            (void)s;
+            if (key - first <= span) mine[atomicAdd(&list_count, 1)] = key;
+          });
+        }
         sync_row();
         if (p.cluster > 1) {
-          int before = 0;
-#pragma unroll 1
-          for (int q = 0; q < p.cluster; ++q) {
-            const int m = (int)ld_cluster_u32(mapa(smem_u32(&list_count), q));
-            for (int k = threadIdx.x; k < m; k += kThreads)
-              list[before + k] = ld_cluster_u32(mapa(smem_u32(own_list + k), q));
-            before += m;
-          }
+          // warp q copies block q's share behind those of the blocks before it
+          const int m = lane < p.cluster ? (int)ld_cluster_u32(mapa(smem_u32(&list_count), lane)) : 0;
+          const int upto = warp_inclusive(m), own = __shfl_sync(0xffffffffu, m, warp & 7);
+          const int before = __shfl_sync(0xffffffffu, upto, warp & 7) - own;
+          if (warp < p.cluster)
+            for (int k = lane; k < own; k += 32) list[before + k] = ld_cluster_u32(mapa(smem_u32(own_list + k), warp));
           __syncthreads();
         }
         for (int k = threadIdx.x; k < size; k += kThreads) {
@@ -306,8 +315,9 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
             same += list[o] == key;
           }
           if (more < need1 && need1 <= more + same) {  // every thread with this key writes the same
-            found[0] = (int)key;
-            found[1] = need1 - more;
+            const bool whole = need1 == more + same;
+            found[0] = (int)(whole ? key - 1u : key);
+            found[1] = whole ? 0 : need1 - more;
           }
         }
         __syncthreads();
@@ -379,22 +389,31 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
       emit(c1 - c >= 32 ? 0xFFFFFFFFu : (1u << (c1 - c)) - 1u, c, out, c);
   } else {
     uint32_t m_gt = 0, m_eq = 0;
-    int gt = 0, eq = 0;  // of this lane's bits, over all rounds
     auto vote = [&](uint32_t key, int s) {
       const uint32_t g = __ballot_sync(0xffffffffu, key > threshold);
-      const uint32_t q = __ballot_sync(0xffffffffu, key == threshold);
-      if (lane == (s & 31)) {
-        m_gt = g;
-        m_eq = q;
-        gt += __popc(g);
-        eq += __popc(q);
-      }
+      m_gt = lane == (s & 31) ? g : m_gt;
     };
-    for_keys(vote);
-    int gt_before = warp_inclusive(gt), eq_before = warp_inclusive(eq);
+    auto vote_equal = [&](uint32_t key, int s) {
+      const uint32_t q = __ballot_sync(0xffffffffu, key == threshold);
+      m_eq = lane == (s & 31) ? q : m_eq;
+    };
+    int gt = 0, eq = 0;  // selected and tied columns of this lane's
+    if (kKeys > 0) {
+      for_keys(vote);
+      if (ties > 0) for_keys(vote_equal);
+      gt = __popc(m_gt);
+      eq = __popc(m_eq);
+    } else {
+      for_keys([&](uint32_t key, int s) {
+        (void)s;
+        gt += key > threshold;
+        eq += key == threshold;
+      });
+    }
+    int gt_before = warp_inclusive(gt), eq_before = ties > 0 ? warp_inclusive(eq) : 0;
     if (lane == 31) warp_count[warp] = make_int2(gt_before, eq_before);
     gt_before -= gt;
-    eq_before -= eq;
+    eq_before -= ties > 0 ? eq : 0;
     __syncthreads();
     int2 block = make_int2(0, 0), lower = make_int2(0, 0);
 #pragma unroll
@@ -409,13 +428,9 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
     if (p.cluster > 1) {
       if (threadIdx.x == 0) block_count = block;
       sync_row();
-#pragma unroll
-      for (int k = 0; k < kMaxCluster - 1; ++k)
-        if (k < rank) {
-          const int2 c = ld_cluster_int2(mapa(smem_u32(&block_count), k));
-          ahead.x += c.x;
-          ahead.y += c.y;
-        }
+      const int2 c = lane < rank ? ld_cluster_int2(mapa(smem_u32(&block_count), lane)) : make_int2(0, 0);
+      ahead.x = (int)__reduce_add_sync(0xffffffffu, (unsigned)c.x);
+      ahead.y = (int)__reduce_add_sync(0xffffffffu, (unsigned)c.y);
     }
     auto selected_before = [&](int g, int q) { return g + (q < ties ? q : ties); };
     const int start = selected_before(ahead.x, ahead.y);
@@ -435,11 +450,15 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
     if (kKeys > 0) {
       write(c0 + 32 * lane, gt_before, eq_before);
     } else {
-      // lane by lane the counts above mix the rounds: take them again, round by round
+      // the warp's columns 1024 at a time
       int g0 = __shfl_sync(0xffffffffu, gt_before, 0), q0 = __shfl_sync(0xffffffffu, eq_before, 0);
       for (int s0 = 0; s0 < steps; s0 += 32) {
         m_gt = m_eq = 0;
-        for (int s = s0; s < min(s0 + 32, steps); ++s) vote(key_of(s), s);
+        for (int s = s0; s < min(s0 + 32, steps); ++s) {
+          const uint32_t key = key_of(s);
+          vote(key, s);
+          vote_equal(key, s);
+        }
         const int n_gt = __popc(m_gt), n_eq = __popc(m_eq);
         const int p_gt = warp_inclusive(n_gt), p_eq = warp_inclusive(n_eq);
         write(c0 + 32 * (s0 + lane), g0 + p_gt - n_gt, q0 + p_eq - n_eq);
