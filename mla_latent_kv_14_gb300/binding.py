@@ -6,6 +6,7 @@ the shared library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import Optional, Tuple
@@ -373,45 +374,25 @@ def mla_set_test_stall(cycles: int) -> None:
 ROPE_PAIRS, ROPE_HALVES = 0, 1        # rope_style: pairs (2i, 2i+1), or (i, i+32)
 INDEX_16BIT, INDEX_FP8 = 0, 1         # index_format
 INDEX_DIM, INDEX_FP8_PAGE_BYTES = 128, 8448
-_KV_ROW = {KV_16BIT: 576, KV_FP8_656: 656, KV_FP8_528: 528, KV_FP4_288: 288}
+_host = None
 
 
-# These calls take a few microseconds on the GPU for a decode step's sizes, so
-# the checks below are written for few interpreter steps: plain attribute reads
-# and comparisons, messages built only for a refusal, addresses and the raw
-# stream passed as integers.
-def _refuse(where: str, what: str):
-    raise MLAError(1, f"{where}: {what}")
-
-
-def _run(where: str, fn, dev: int, *args):
-    """Call a C entry point with the tensors' device current; its stream comes last."""
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream)
-    if st != MLA_OK:
-        raise MLAError(st, where)
-
-
-def _status_ptr(where: str, status: Optional[torch.Tensor], dev: int):
-    if status is None:
-        return None
-    if status.get_device() != dev or status.element_size() * status.numel() < 4:
-        _refuse(where, "status: a 4-byte word on the tensors' device")
-    return status.data_ptr()
-
-
-def _rope_check(where: str, positions: torch.Tensor, rope_table: torch.Tensor, tokens: int, dev: int):
-    if positions.dtype != torch.int32 or positions.shape != (tokens,) or not positions.is_contiguous():
-        _refuse(where, f"positions int32 [{tokens}]")
-    if (rope_table.dtype != torch.float32 or rope_table.dim() != 2 or rope_table.shape[1] != 64 or
-            not rope_table.is_contiguous()):
-        _refuse(where, "rope_table fp32 [positions, 64]")
-    if dev < 0 or positions.get_device() != dev or rope_table.get_device() != dev:
-        _refuse(where, "tensors of one cuda device")
+def _load_host():
+    """The extension module that checks and launches these calls (built with
+    libmla.so; their time on the GPU is a few microseconds)."""
+    global _host
+    load_library()
+    with _lib_lock:
+        if _host is None:
+            path = os.path.join(_HERE, "_host.so")
+            if not os.path.exists(path):
+                raise ImportError(f"_host.so not built at {path}: run `python -m mla_latent_kv_14_gb300.build`")
+            spec = importlib.util.spec_from_file_location("mla_latent_kv_14_gb300._host", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.set_error(MLAError)
+            _host = module
+    return _host
 
 
 def mla_rope_table(max_positions: int, base: float = 10000.0, inv_freq: Optional[torch.Tensor] = None,
@@ -423,7 +404,7 @@ def mla_rope_table(max_positions: int, base: float = 10000.0, inv_freq: Optional
     if inv_freq is None:
         inv_freq = base ** (-torch.arange(32, dtype=torch.float64) / 32)
     if tuple(inv_freq.shape) != (32,):
-        _refuse("mla_rope_table", "inv_freq [32]")
+        raise MLAError(1, "mla_rope_table: inv_freq [32]")
     angle = torch.arange(max_positions, dtype=torch.float64, device=dev)[:, None] * inv_freq.to(dev, torch.float64)
     return torch.cat((angle.cos() * scale, angle.sin() * scale), 1).float()
 
@@ -434,35 +415,8 @@ def mla_append_kv(c_kv: torch.Tensor, k_rope: torch.Tensor, kvcache: torch.Tenso
     """Append tokens to the paged cache in place: c_kv [n, 512] (V4.1 rows: 448)
     and k_rope [n, 64], which is rotated on the way; ``slots`` int32 [n] are cache
     rows (page * 64 + offset, negative: skip). Returns kvcache."""
-    lib, where = _lib or load_library(), "mla_append_kv"
-    row = _KV_ROW.get(kv_format)
-    if row is None:
-        _refuse(where, f"unknown kv_format {kv_format}")
-    dtype, dev, n = c_kv.dtype, c_kv.get_device(), c_kv.shape[0]
-    latent = 448 if kv_format >= KV_FP8_528 else 512
-    if (c_kv.shape != (n, latent) or k_rope.shape != (n, 64) or k_rope.dtype != dtype or c_kv.stride(1) != 1 or
-            k_rope.stride(1) != 1 or dtype not in DTYPE_CODES):
-        _refuse(where, f"c_kv [n, {latent}] and k_rope [n, 64], bf16 or fp16")
-    if slots.dtype != torch.int32 or slots.shape != (n,) or not slots.is_contiguous():
-        _refuse(where, "slots int32 [n]")
-    shape = kvcache.shape
-    if (kvcache.dtype != (torch.uint8 if kv_format else dtype) or len(shape) < 3 or shape[-1] != row or
-            not kvcache.is_contiguous() or kvcache.numel() != shape[0] * shape[1] * row):
-        _refuse(where, f"kvcache [num_blocks, page_block, 1, {row}] of {'uint8' if kv_format else dtype}")
-    _rope_check(where, positions, rope_table, n, dev)
-    if k_rope.get_device() != dev or kvcache.get_device() != dev or slots.get_device() != dev:
-        _refuse(where, "tensors of one cuda device")
-    _run(where, lib.mla_append_kv, dev, c_kv.data_ptr(), _stride(c_kv, 0, latent), k_rope.data_ptr(),
-         _stride(k_rope, 0, 64), DTYPE_CODES[dtype], slots.data_ptr(), positions.data_ptr(), rope_table.data_ptr(),
-         rope_table.shape[0], rope_style, n, kvcache.data_ptr(), shape[0], shape[1], kv_format,
-         _status_ptr(where, status, dev))
-    return kvcache
-
-
-def _stride(t: torch.Tensor, dim: int, dense: int) -> int:
-    """The stride of ``dim``; of a dim with at most one entry, which is never
-    stepped over, the dense one (PyTorch leaves any number there)."""
-    return t.stride(dim) if t.shape[dim] > 1 else dense
+    return (_host or _load_host()).mla_append_kv(c_kv, k_rope, kvcache, slots, positions, rope_table, kv_format,
+                                                 rope_style, status)
 
 
 def mla_rotate_q(x: torch.Tensor, positions: torch.Tensor, rope_table: torch.Tensor,
@@ -472,37 +426,7 @@ def mla_rotate_q(x: torch.Tensor, positions: torch.Tensor, rope_table: torch.Ten
     example ``q[..., 128:]`` of the projection) -> out, of the same shape
     (``q_abs[..., 512:]``, ``x`` itself, or allocated). Rows of tokens whose
     position is negative are not written."""
-    lib, where = _lib or load_library(), "mla_rotate_q"
-    dtype, dev = x.dtype, x.get_device()
-    if x.dim() != 3 or x.shape[2] != 64 or x.stride(2) != 1 or dtype not in DTYPE_CODES:
-        _refuse(where, "x [tokens, heads, 64], bf16 or fp16")
-    tokens, heads, _ = x.shape
-    if out is None:
-        out = x.new_empty((tokens, heads, 64))
-    elif out.shape != x.shape or out.dtype != dtype or out.stride(2) != 1:
-        _refuse(where, "out like x")
-    _rope_check(where, positions, rope_table, tokens, dev)
-    if out.get_device() != dev:
-        _refuse(where, "tensors of one cuda device")
-    _run(where, lib.mla_rotate_q, dev, x.data_ptr(), _stride(x, 0, 64 * heads), _stride(x, 1, 64), out.data_ptr(),
-         _stride(out, 0, 64 * heads), _stride(out, 1, 64), DTYPE_CODES[dtype], positions.data_ptr(),
-         rope_table.data_ptr(), rope_table.shape[0], rope_style, tokens, heads, _status_ptr(where, status, dev))
-    return out
-
-
-def _index_cache(where: str, cache: torch.Tensor, index_format: int, dtype: torch.dtype) -> Tuple[int, int]:
-    """(num_blocks, page_block) of an index cache."""
-    shape = cache.shape
-    if index_format == INDEX_FP8:
-        if len(shape) != 2 or shape[1] != INDEX_FP8_PAGE_BYTES or cache.dtype != torch.uint8 or not cache.is_contiguous():
-            _refuse(where, f"FP8 index cache uint8 [num_blocks, {INDEX_FP8_PAGE_BYTES}]")
-        return shape[0], 64
-    if index_format != INDEX_16BIT:
-        _refuse(where, f"unknown index_format {index_format}")
-    if (len(shape) < 3 or shape[-1] != INDEX_DIM or cache.dtype != dtype or not cache.is_contiguous() or
-            cache.numel() != shape[0] * shape[1] * INDEX_DIM):
-        _refuse(where, f"index cache [num_blocks, page_block, 1, {INDEX_DIM}] of {dtype}")
-    return shape[0], shape[1]
+    return (_host or _load_host()).mla_rotate_q(x, positions, rope_table, out, rope_style, status)
 
 
 def mla_append_index_k(k: torch.Tensor, index_cache: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor,
@@ -511,20 +435,8 @@ def mla_append_index_k(k: torch.Tensor, index_cache: torch.Tensor, slots: torch.
     """Append index keys k [n, 128] (dims [0, 64) are rotated) to the paged index
     cache in place: [num_blocks, 64, 1, 128] of k's type, or uint8 [num_blocks,
     8448] with INDEX_FP8. ``slots`` as in :func:`mla_append_kv`."""
-    lib, where = _lib or load_library(), "mla_append_index_k"
-    dtype, dev, n = k.dtype, k.get_device(), k.shape[0]
-    if k.shape != (n, INDEX_DIM) or k.stride(1) != 1 or dtype not in DTYPE_CODES:
-        _refuse(where, f"k [n, {INDEX_DIM}], bf16 or fp16")
-    if slots.dtype != torch.int32 or slots.shape != (n,) or not slots.is_contiguous():
-        _refuse(where, "slots int32 [n]")
-    blocks, page = _index_cache(where, index_cache, index_format, dtype)
-    _rope_check(where, positions, rope_table, n, dev)
-    if index_cache.get_device() != dev or slots.get_device() != dev:
-        _refuse(where, "tensors of one cuda device")
-    _run(where, lib.mla_append_index_k, dev, k.data_ptr(), _stride(k, 0, INDEX_DIM), DTYPE_CODES[dtype],
-         slots.data_ptr(), positions.data_ptr(), rope_table.data_ptr(), rope_table.shape[0], rope_style, n,
-         index_cache.data_ptr(), blocks, page, index_format, _status_ptr(where, status, dev))
-    return index_cache
+    return (_host or _load_host()).mla_append_index_k(k, index_cache, slots, positions, rope_table, index_format,
+                                                      rope_style, status)
 
 
 def mla_quantize_index_q(q: torch.Tensor, weights: torch.Tensor, positions: torch.Tensor, rope_table: torch.Tensor,
@@ -535,51 +447,8 @@ def mla_quantize_index_q(q: torch.Tensor, weights: torch.Tensor, positions: torc
     with each row's scale folded into ``weights`` fp32 [tokens, heads]. Returns
     (float8_e4m3fn [tokens, heads, 128], fp32 [tokens, heads]); rows of tokens
     whose position is negative are not written."""
-    lib, where = _lib or load_library(), "mla_quantize_index_q"
-    dtype, dev = q.dtype, q.get_device()
-    if q.dim() != 3 or q.shape[2] != INDEX_DIM or q.stride(2) != 1 or dtype not in DTYPE_CODES:
-        _refuse(where, f"q [tokens, heads, {INDEX_DIM}], bf16 or fp16")
-    tokens, heads, _ = q.shape
-    if weights.shape != (tokens, heads) or weights.dtype != torch.float32 or not weights.is_contiguous():
-        _refuse(where, "weights fp32 [tokens, heads]")
-    if q_out is None:
-        q_out = q.new_empty((tokens, heads, INDEX_DIM), dtype=torch.float8_e4m3fn)
-    elif q_out.shape != q.shape or not q_out.is_contiguous() or q_out.dtype not in (torch.float8_e4m3fn, torch.uint8):
-        _refuse(where, "q_out e4m3 like q")
-    if weights_out is None:
-        weights_out = weights.new_empty((tokens, heads))
-    elif weights_out.shape != (tokens, heads) or weights_out.dtype != torch.float32 or not weights_out.is_contiguous():
-        _refuse(where, "weights_out fp32 [tokens, heads]")
-    _rope_check(where, positions, rope_table, tokens, dev)
-    if weights.get_device() != dev or q_out.get_device() != dev or weights_out.get_device() != dev:
-        _refuse(where, "tensors of one cuda device")
-    _run(where, lib.mla_quantize_index_q, dev, q.data_ptr(), _stride(q, 0, INDEX_DIM * heads), _stride(q, 1, INDEX_DIM),
-         DTYPE_CODES[dtype], weights.data_ptr(), positions.data_ptr(), rope_table.data_ptr(), rope_table.shape[0],
-         rope_style, tokens, heads, q_out.data_ptr(), weights_out.data_ptr(), _status_ptr(where, status, dev))
-    return q_out, weights_out
-
-
-def _paged_check(where: str, block_table: torch.Tensor, cache_seqlens: torch.Tensor, batch: int, dev: int) -> int:
-    """max_blocks of a block table for `batch` requests."""
-    if (block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch or
-            not block_table.is_contiguous()):
-        _refuse(where, "block_table int32 [B, max_blocks]")
-    if cache_seqlens.dtype != torch.int32 or cache_seqlens.shape != (batch,) or not cache_seqlens.is_contiguous():
-        _refuse(where, "cache_seqlens int32 [B]")
-    if dev < 0 or block_table.get_device() != dev or cache_seqlens.get_device() != dev:
-        _refuse(where, "tensors of one cuda device")
-    return block_table.shape[1]
-
-
-def _score_stride(where: str, scores: torch.Tensor, width: int) -> int:
-    """Row stride of scores [B, s_q, width] (a column range of a wider buffer is fine)."""
-    if scores.is_contiguous():
-        return width
-    batch, s_q, _ = scores.shape
-    stride = scores.stride(1) if s_q > 1 else scores.stride(0) if batch > 1 else width
-    if (width > 1 and scores.stride(2) != 1) or (batch > 1 and s_q > 1 and scores.stride(0) != s_q * stride):
-        _refuse(where, "rows of scores dense and equally spaced")
-    return stride
+    return (_host or _load_host()).mla_quantize_index_q(q, weights, positions, rope_table, rope_style, q_out,
+                                                        weights_out, status)
 
 
 def mla_index_score(q: torch.Tensor, weights: torch.Tensor, index_cache: torch.Tensor, block_table: torch.Tensor,
@@ -590,36 +459,8 @@ def mla_index_score(q: torch.Tensor, weights: torch.Tensor, index_cache: torch.T
     (block=64): sum_h weights[b, i, h] * relu(q[b, i, h] . k_t), -inf where
     nothing is visible. q [B, s_q, heads, 128] of the index cache's type (e4m3
     with INDEX_FP8); ``width`` defaults to what the block table reaches."""
-    lib, where = _lib or load_library(), "mla_index_score"
-    dtype, dev, shape = q.dtype, q.get_device(), q.shape
-    if len(shape) != 4 or shape[3] != INDEX_DIM or not q.is_contiguous():
-        _refuse(where, f"q [B, s_q, heads, {INDEX_DIM}]")
-    batch, s_q, heads, _ = shape
-    code = DTYPE_CODES.get(dtype) if index_format != INDEX_FP8 else 0 if dtype in (torch.float8_e4m3fn, torch.uint8) else None
-    if code is None:
-        _refuse(where, "q's type: that of the index cache, e4m3 with an FP8 one")
-    if weights.dtype != torch.float32 or weights.shape != (batch, s_q, heads) or not weights.is_contiguous():
-        _refuse(where, "weights fp32 [B, s_q, heads]")
-    blocks, page = _index_cache(where, index_cache, index_format, dtype)
-    max_blocks = _paged_check(where, block_table, cache_seqlens, batch, dev)
-    if block != 1 and block != 64:
-        _refuse(where, "block 1 or 64")
-    if width is None:
-        width = scores.shape[-1] if scores is not None else max_blocks * (64 // block)
-    if not 1 <= width < 1 << 31:
-        _refuse(where, "1 <= width < 2^31")
-    if scores is None:
-        scores, stride = weights.new_empty((batch, s_q, width)), width
-    else:
-        if scores.dtype != torch.float32 or scores.shape != (batch, s_q, width):
-            _refuse(where, "scores fp32 [B, s_q, width]")
-        stride = _score_stride(where, scores, width)
-    if weights.get_device() != dev or index_cache.get_device() != dev or scores.get_device() != dev:
-        _refuse(where, "tensors of one cuda device")
-    _run(where, lib.mla_index_score, dev, q.data_ptr(), code, weights.data_ptr(), index_cache.data_ptr(), index_format,
-         blocks, page, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(), batch, s_q, heads, causal, block,
-         scores.data_ptr(), stride, width, _status_ptr(where, status, dev))
-    return scores
+    return (_host or _load_host()).mla_index_score(q, weights, index_cache, block_table, cache_seqlens, width, causal,
+                                                   block, index_format, scores, status)
 
 
 def mla_select_topk(scores: torch.Tensor, cache_seqlens: torch.Tensor, topk: int, block_table: torch.Tensor,
@@ -631,26 +472,5 @@ def mla_select_topk(scores: torch.Tensor, cache_seqlens: torch.Tensor, topk: int
     their number [B, s_q]); block=64: (pages [B, s_q, topk] and the tokens they
     hold [B, s_q]), the block table and lengths of a decode with B * s_q requests
     of one query. ``num_blocks``: pages of the cache that the rows index."""
-    lib, where = _lib or load_library(), "mla_select_topk"
-    dev, shape = scores.get_device(), scores.shape
-    if len(shape) != 3 or scores.dtype != torch.float32:
-        _refuse(where, "scores fp32 [B, s_q, width]")
-    batch, s_q, width = shape
-    stride = _score_stride(where, scores, width)
-    max_blocks = _paged_check(where, block_table, cache_seqlens, batch, dev)
-    if not 1 <= topk < 1 << 31 or width >= 1 << 31:
-        _refuse(where, "1 <= topk, width < 2^31")
-    if indices is None:
-        indices = block_table.new_empty((batch, s_q, topk))
-    elif indices.dtype != torch.int32 or indices.shape != (batch, s_q, topk) or not indices.is_contiguous():
-        _refuse(where, "indices int32 [B, s_q, topk]")
-    if lens is None:
-        lens = block_table.new_empty((batch, s_q))
-    elif lens.dtype != torch.int32 or lens.shape != (batch, s_q) or not lens.is_contiguous():
-        _refuse(where, "lens int32 [B, s_q]")
-    if indices.get_device() != dev or lens.get_device() != dev:
-        _refuse(where, "tensors of one cuda device")
-    _run(where, lib.mla_select_topk, dev, scores.data_ptr(), stride, width, cache_seqlens.data_ptr(), batch, s_q, causal,
-         block, topk, block_table.data_ptr(), max_blocks, num_blocks, 64, indices.data_ptr(), lens.data_ptr(),
-         _status_ptr(where, status, dev))
-    return indices, lens
+    return (_host or _load_host()).mla_select_topk(scores, cache_seqlens, topk, block_table, num_blocks, causal, block,
+                                                   indices, lens, status)

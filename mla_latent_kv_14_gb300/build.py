@@ -1,4 +1,5 @@
-"""Build libmla.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libmla.so (the C-ABI library) in-tree with nvcc for sm_103a, and _host.so,
+the extension module that the Python calls around the decode go through.
 
     python -m mla_latent_kv_14_gb300.build        # or build() from Python
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla.so")
+HOST = os.path.join(HERE, "_host.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["mla_api.cu", "cache_api.cu"]
 
@@ -37,6 +40,39 @@ def _flags():
                    "-DMLA_BUILD_SO"]
 
 
+def _run(cmd, what: str, verbose: bool = False):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout, r.stderr, flush=True)
+
+
+def _compile_host(verbose: bool = False) -> str:
+    """host_binding.cpp against the installed PyTorch's headers."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    obj = os.path.join(BUILD, "host_binding.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", os.path.join(CSRC, "host_binding.cpp"), "-o", obj,
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+          "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+          "-isystem", os.path.join(cuda, "include")], "g++", verbose)
+    return obj
+
+
+def _link_host(obj: str, verbose: bool = False):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = HOST + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-lc10_cuda"], "link of _host.so", verbose)
+    os.replace(tmp, HOST)
+
+
 def build(verbose: bool = False, extra_flags=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -45,23 +81,18 @@ def build(verbose: bool = False, extra_flags=None) -> str:
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         cmd = [nvcc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout, r.stderr, flush=True)
+        _run(cmd, f"nvcc for {src}", verbose)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(SOURCES), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        host = ex.submit(_compile_host, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        host = host.result()
     tmp = LIB + ".tmp"
-    cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static", "-lpthread", "-ldl", "-lrt"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xlinker", "-soname=libmla.so", "-cudart", "static", "-lpthread", "-ldl", "-lrt"],
+         "link", verbose)
     os.replace(tmp, LIB)
+    _link_host(host, verbose)
     return LIB
 
 
