@@ -13,6 +13,8 @@ using namespace mla;
 namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
+// rows of (token, head) from which a thread takes several heads of a token
+constexpr int64_t kManyRows = 32768;
 
 bool dtype_ok(int dtype) { return dtype == MLA_DTYPE_BF16 || dtype == MLA_DTYPE_FP16; }
 bool cache_ok(int64_t num_blocks, int page_block) {
@@ -119,12 +121,15 @@ mla_status mla_rotate_q(const void* x, int64_t x_token_stride, int64_t x_head_st
                        tokens, heads, 0};
   if (const mla_status v = check_positions(p.pos)) return v;
   constexpr int kU = 4;
-  p.heads_per_slot = (uint32_t)((heads + kU - 1) / kU);
+  const bool many = tokens * heads >= kManyRows;
+  p.heads_per_slot = (uint32_t)(many ? (heads + kU - 1) / kU : heads);
   const int64_t items = tokens * p.heads_per_slot * 4;
   const dim3 grid((unsigned)((items + rows::kRotateThreads - 1) / rows::kRotateThreads));
   if (dtype == MLA_DTYPE_FP16)
-    return launch(rows::mla_rotate_kernel<true, kU>, grid, rows::kRotateThreads, 0, stream, p);
-  return launch(rows::mla_rotate_kernel<false, kU>, grid, rows::kRotateThreads, 0, stream, p);
+    return many ? launch(rows::mla_rotate_kernel<true, kU>, grid, rows::kRotateThreads, 0, stream, p)
+                : launch(rows::mla_rotate_kernel<true, 1>, grid, rows::kRotateThreads, 0, stream, p);
+  return many ? launch(rows::mla_rotate_kernel<false, kU>, grid, rows::kRotateThreads, 0, stream, p)
+              : launch(rows::mla_rotate_kernel<false, 1>, grid, rows::kRotateThreads, 0, stream, p);
 }
 
 mla_status mla_append_index_k(const void* k, int64_t k_stride, int dtype, const int32_t* slots,
@@ -140,16 +145,16 @@ mla_status mla_append_index_k(const void* k, int64_t k_stride, int dtype, const 
     return MLA_ERR_INVALID_ARG;
   rows::IndexRowParams p{static_cast<const uint16_t*>(k), k_stride, 0, slots, nullptr,
                          {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
-                         n, 1, static_cast<uint8_t*>(index_cache), nullptr, num_blocks * kTile};
+                         n, 1, 1, static_cast<uint8_t*>(index_cache), nullptr, num_blocks * kTile};
   if (const mla_status v = check_positions(p.pos)) return v;
-  const int per = rows::kIndexThreads / 16;
+  const int per = rows::kIndexGroups;
   const dim3 grid((unsigned)((n + per - 1) / per));
   const bool fp16 = dtype == MLA_DTYPE_FP16;
   if (index_format == MLA_INDEX_FP8)
-    return fp16 ? launch(rows::mla_index_rows_kernel<true, true, true>, grid, rows::kIndexThreads, 0, stream, p)
-                : launch(rows::mla_index_rows_kernel<false, true, true>, grid, rows::kIndexThreads, 0, stream, p);
-  return fp16 ? launch(rows::mla_index_rows_kernel<true, false, true>, grid, rows::kIndexThreads, 0, stream, p)
-              : launch(rows::mla_index_rows_kernel<false, false, true>, grid, rows::kIndexThreads, 0, stream, p);
+    return fp16 ? launch(rows::mla_index_rows_kernel<true, true, true, 1>, grid, rows::kIndexThreads, 0, stream, p)
+                : launch(rows::mla_index_rows_kernel<false, true, true, 1>, grid, rows::kIndexThreads, 0, stream, p);
+  return fp16 ? launch(rows::mla_index_rows_kernel<true, false, true, 1>, grid, rows::kIndexThreads, 0, stream, p)
+              : launch(rows::mla_index_rows_kernel<false, false, true, 1>, grid, rows::kIndexThreads, 0, stream, p);
 }
 
 mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
@@ -166,13 +171,21 @@ mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q
     return MLA_ERR_INVALID_ARG;
   rows::IndexRowParams p{static_cast<const uint16_t*>(q), q_token_stride, q_head_stride, nullptr, weights,
                          {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
-                         tokens * heads, heads, q_out, weights_out, 0};
+                         tokens, heads, heads, q_out, weights_out, 0};
   if (const mla_status v = check_positions(p.pos)) return v;
-  const int per = rows::kIndexThreads / 16;
-  const dim3 grid((unsigned)((p.rows + per - 1) / per));
+  // four heads to a lane group share the table row and keep four loads in
+  // flight, once there are enough rows to fill the card that way
+  constexpr int kU = 4;
+  const bool many = tokens * heads >= kManyRows;
+  if (many) p.heads_per_slot = (heads + kU - 1) / kU;
+  const int64_t groups = tokens * p.heads_per_slot;
+  const int per = rows::kIndexGroups;
+  const dim3 grid((unsigned)((groups + per - 1) / per));
   if (dtype == MLA_DTYPE_FP16)
-    return launch(rows::mla_index_rows_kernel<true, true, false>, grid, rows::kIndexThreads, 0, stream, p);
-  return launch(rows::mla_index_rows_kernel<false, true, false>, grid, rows::kIndexThreads, 0, stream, p);
+    return many ? launch(rows::mla_index_rows_kernel<true, true, false, kU>, grid, rows::kIndexThreads, 0, stream, p)
+                : launch(rows::mla_index_rows_kernel<true, true, false, 1>, grid, rows::kIndexThreads, 0, stream, p);
+  return many ? launch(rows::mla_index_rows_kernel<false, true, false, kU>, grid, rows::kIndexThreads, 0, stream, p)
+              : launch(rows::mla_index_rows_kernel<false, true, false, 1>, grid, rows::kIndexThreads, 0, stream, p);
 }
 
 }  // extern "C"

@@ -21,6 +21,47 @@ MLA_DEV uint32_t e4m3x4_rn_sat(float a, float b, float c, float d) {
 // scale of a block whose largest magnitude is amax: fp32(amax / 448), 1 for zeros
 MLA_DEV float e4m3_scale(float amax) { return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f); }
 
+// Sixteen values over their block's scale, as e4m3 codes (value i in byte i).
+//
+// A quotient x / scale is formed as x * r, r = 1 / scale rounded to nearest,
+// corrected by its exact remainder (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990: with r correctly
+// rounded, so is the result, as long as the remainder does not underflow). For
+// scale >= 2^-60 only an |x| below 2^-102 could underflow one, and its quotient
+// is below 2^-42, zero in e4m3; smaller scales are divided by. On packed pairs
+// that is 1.5 operations a value and one for the sign of a zero, where a
+// division takes some ten.
+MLA_DEV void e4m3_codes16(const float* x, float scale, uint32_t* w) {
+  if (scale >= 0x1p-60f) {
+    const float inv = __frcp_rn(scale);
+    const uint64_t r = f2_pack(inv, inv), m = f2_pack(-scale, -scale);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float lo = x[4 * k + 2 * j], hi = x[4 * k + 2 * j + 1];
+        const uint64_t v = f2_pack(lo, hi), q = f2_mul(v, r);
+        const float2 c = f2_unpack(f2_fma(f2_fma(q, m, v), r, q));
+        y[2 * j] = __uint_as_float(__float_as_uint(c.x) | (__float_as_uint(lo) & 0x80000000u));
+        y[2 * j + 1] = __uint_as_float(__float_as_uint(c.y) | (__float_as_uint(hi) & 0x80000000u));
+      }
+      w[k] = e4m3x4_rn_sat(y[0], y[1], y[2], y[3]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = e4m3x4_rn_sat(__fdiv_rn(x[4 * k], scale), __fdiv_rn(x[4 * k + 1], scale), __fdiv_rn(x[4 * k + 2], scale),
+                           __fdiv_rn(x[4 * k + 3], scale));
+  }
+}
+MLA_DEV float amax16(const float* x) {
+  float m = fabsf(x[0]);
+#pragma unroll
+  for (int k = 1; k < 15; k += 2) m = max3(m, fabsf(x[k]), fabsf(x[k + 1]));
+  return fmaxf(m, fabsf(x[15]));
+}
+
 // UE8M0 exponent of a block: the smallest integer k >= -127 with
 // 448 * 2^k >= amax, found from amax's fp32 fields: amax = f * 2^e, f in
 // [1, 2), gives k = e - 8 when f <= 1.75 (448 = 1.75 * 2^8) and e - 7 above.

@@ -61,8 +61,8 @@ struct IndexRowParams {
   const int32_t* slots;      // keys: [tokens]
   const float* weights;      // queries: [tokens, heads]
   Positions pos;
-  int64_t rows;              // tokens * heads
-  int heads;
+  int64_t tokens;
+  int heads, heads_per_slot;  // head slots of a token: ceil(heads / kU)
   uint8_t* out;              // keys: the index cache; queries: [tokens, heads, 128] codes
   float* w_out;              // queries: [tokens, heads]
   int64_t num_rows;          // keys: rows of the index cache
@@ -121,16 +121,6 @@ MLA_DEV void load_row(const float* src, float* v) {
   }
 }
 
-// Table row of a token, or null (and the status bit) for a position outside it.
-MLA_DEV const float* table_row(const Positions& p, int64_t token, bool report) {
-  const int32_t at = __ldg(p.positions + token);
-  if (at < 0 || at >= p.max_positions) {
-    if (report) flag(p.status, STATUS_INDEX);
-    return nullptr;
-  }
-  return p.table + (int64_t)at * kRope;
-}
-
 // ---------------------------------------------------------------------------
 // The paged latent cache: one warp per token.
 // ---------------------------------------------------------------------------
@@ -144,52 +134,56 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kv_kernel(const 
   if (t >= p.n) return;
   const uint16_t* c = static_cast<const uint16_t*>(p.c_kv) + t * p.c_stride;
   const uint16_t* r = static_cast<const uint16_t*>(p.k_rope) + t * p.r_stride;
-  const int32_t slot = __ldg(p.slots + t);
+  // all that does not depend on the slot is on its way before the slot is
+  // looked at: one round trip to memory, then the table row
+  const int32_t slot = __ldg(p.slots + t), at = __ldg(p.pos.positions + t);
+  uint4 raw[2];  // 16-bit rows: two strips of 512 bytes, else values [16 lane, 16 lane + 16)
+  if (kFormat == 0) {
+    raw[0] = __ldg(reinterpret_cast<const uint4*>(c) + lane);
+    raw[1] = __ldg(reinterpret_cast<const uint4*>(c) + 32 + lane);
+  } else if (kFormat == 1 || lane < 28) {
+    raw[0] = __ldg(reinterpret_cast<const uint4*>(c) + 2 * lane);
+    raw[1] = __ldg(reinterpret_cast<const uint4*>(c) + 2 * lane + 1);
+  }
+  float a = 0.f, b = 0.f;  // pair `lane`
+  if (kFormat <= 1) {
+    if (p.pos.halves) {
+      a = to_f32<kFp16>(__ldg(r + lane));
+      b = to_f32<kFp16>(__ldg(r + lane + kPairs));
+    } else {
+      const float2 v = unpack2<kFp16>(__ldg(reinterpret_cast<const uint32_t*>(r) + lane));
+      a = v.x;
+      b = v.y;
+    }
+  }
   if (slot < 0) return;  // padding
-  const float* row = table_row(p.pos, t, lane == 0);
-  if (slot >= p.num_rows) {
+  if (slot >= p.num_rows || at < 0 || at >= p.pos.max_positions) {
     if (lane == 0) flag(p.pos.status, STATUS_INDEX);
     return;
   }
-  if (!row) return;
+  const float* row = p.pos.table + (int64_t)at * kRope;
 
   if (kFormat <= 1) {
     // lane l turns pair l
     constexpr int kRow = kFormat == 0 ? kDK * 2 : kRowBytesFp8;
     constexpr int kLatentBytes = kFormat == 0 ? 1024 : 528;
     uint8_t* dst = p.kv + (int64_t)slot * kRow;
-    float a, b;
-    if (p.pos.halves) {
-      a = to_f32<kFp16>(r[lane]);
-      b = to_f32<kFp16>(r[lane + kPairs]);
-    } else {
-      const float2 v = unpack2<kFp16>(reinterpret_cast<const uint32_t*>(r)[lane]);
-      a = v.x;
-      b = v.y;
-    }
     const float cs = __ldg(row + lane), sn = __ldg(row + kPairs + lane);
     if (kFormat == 0) {
-      const uint4 v0 = reinterpret_cast<const uint4*>(c)[lane], v1 = reinterpret_cast<const uint4*>(c)[32 + lane];
-      reinterpret_cast<uint4*>(dst)[lane] = v0;
-      reinterpret_cast<uint4*>(dst)[32 + lane] = v1;
+      reinterpret_cast<uint4*>(dst)[lane] = raw[0];
+      reinterpret_cast<uint4*>(dst)[32 + lane] = raw[1];
     } else {
-      // lane l owns values [4l, 4l + 4) of each block of 128
-      uint2 raw[4];
+      // lane l owns values [16l, 16l + 16): eight lanes to a block of 128
+      float x[16];
+      unpack<false, 16>(raw, x);
+      float amax = amax16(x);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) raw[j] = reinterpret_cast<const uint2*>(c)[32 * j + lane];
-      float scales[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 lo = unpack2<false>(raw[j].x), hi = unpack2<false>(raw[j].y);
-        float amax = fmaxf(fmaxf(fabsf(lo.x), fabsf(lo.y)), fmaxf(fabsf(hi.x), fabsf(hi.y)));
-#pragma unroll
-        for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float scale = e4m3_scale(amax);
-        scales[j] = scale;
-        reinterpret_cast<uint32_t*>(dst)[32 * j + lane] =
-            e4m3x4_rn_sat(__fdiv_rn(lo.x, scale), __fdiv_rn(lo.y, scale), __fdiv_rn(hi.x, scale), __fdiv_rn(hi.y, scale));
-      }
-      if (lane == 0) reinterpret_cast<float4*>(dst)[32] = make_float4(scales[0], scales[1], scales[2], scales[3]);
+      for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const float scale = e4m3_scale(amax);
+      uint32_t w[4];
+      e4m3_codes16(x, scale, w);
+      reinterpret_cast<uint4*>(dst)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+      if ((lane & 7) == 0) reinterpret_cast<float*>(dst)[128 + (lane >> 3)] = scale;
     }
     const uint32_t y = pack2<kFp16>(turn_lo(a, b, cs, sn), turn_hi(a, b, cs, sn));
     uint8_t* rd = dst + kLatentBytes;
@@ -204,7 +198,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kv_kernel(const 
     // 0..27, RoPE dims [16j, 16j + 16) in lane 28 + j
     float x[16];
     if (lane < 28) {
-      const uint4 raw[2] = {reinterpret_cast<const uint4*>(c)[2 * lane], reinterpret_cast<const uint4*>(c)[2 * lane + 1]};
       unpack<false, 16>(raw, x);
     } else {
       const int j = lane - 28;
@@ -281,12 +274,6 @@ __global__ void __launch_bounds__(kRotateThreads) mla_rotate_kernel(const Rotate
   const uint32_t t = group / p.heads_per_slot, h0 = group - t * p.heads_per_slot;
   if (t >= p.tokens) return;
   const int32_t at = __ldg(p.pos.positions + t);
-  if (at < 0) return;  // padding
-  if (at >= p.pos.max_positions) {
-    if (j == 0 && h0 == 0) flag(p.pos.status, STATUS_INDEX);
-    return;
-  }
-  const float* row = p.pos.table + (int64_t)at * kRope + 8 * j;
   // pairs [8j, 8j + 8): dims [16j, 16j + 16), or [8j, 8j + 8) and 32 behind
   const int d0 = p.pos.halves ? 8 * j : 16 * j, d1 = p.pos.halves ? 8 * j + 32 : 16 * j + 8;
   const uint16_t* src = p.x + t * p.x_token;
@@ -300,6 +287,12 @@ __global__ void __launch_bounds__(kRotateThreads) mla_rotate_kernel(const Rotate
       raw[u][1] = *reinterpret_cast<const uint4*>(src + h * p.x_head + d1);
     }
   }
+  if (at < 0) return;  // padding
+  if (at >= p.pos.max_positions) {
+    if (j == 0 && h0 == 0) flag(p.pos.status, STATUS_INDEX);
+    return;
+  }
+  const float* row = p.pos.table + (int64_t)at * kRope + 8 * j;
   float cs[8], sn[8];
   load_row<8>(row, cs);
   load_row<8>(row + kPairs, sn);
@@ -327,92 +320,105 @@ __global__ void __launch_bounds__(kRotateThreads) mla_rotate_kernel(const Rotate
 // ---------------------------------------------------------------------------
 // Index rows of 128 values, dims [0, 64) rotated: keys into the paged index
 // cache, queries as e4m3 with their scale folded into the head's weight.
-// Sixteen lanes per row, 8 values each.
+// Eight lanes per row: lane l holds dims [8l, 8l + 8) of the rotated half and
+// [64 + 8l, 64 + 8l + 8) of the other, so that every lane turns four pairs. A
+// lane group takes kU heads of one token, which share the position and the
+// table row.
 // ---------------------------------------------------------------------------
 constexpr int kIndexThreads = 256;
+constexpr int kIndexLanes = 8;
+constexpr int kIndexGroups = kIndexThreads / kIndexLanes;
 
-template <bool kFp16, bool kFp8, bool kKeys>
+template <bool kFp16, bool kFp8, bool kKeys, int kU>
 __global__ void __launch_bounds__(kIndexThreads) mla_index_rows_kernel(const IndexRowParams p) {
   pdl_wait();
-  const int l = threadIdx.x & 15;
-  const int64_t r = (int64_t)blockIdx.x * (kIndexThreads / 16) + (threadIdx.x >> 4);
+  const int l = threadIdx.x & (kIndexLanes - 1);
+  const uint32_t group = blockIdx.x * kIndexGroups + threadIdx.x / kIndexLanes;
+  const uint32_t slots = (uint32_t)p.heads_per_slot;
+  const uint32_t t = kKeys ? group : group / slots, h0 = kKeys ? 0u : group - t * slots;
   // every lane takes part in the shuffles below; rows past the end or to be
   // skipped work on zeros and store nothing
-  bool live = r < p.rows;
-  const int64_t t = kKeys ? r : (int64_t)((uint32_t)r / (uint32_t)p.heads);  // rows < 2^31 (checked on the host)
-  const int h = kKeys ? 0 : (int)(r - t * p.heads);
-  const float* row = nullptr;
-  int32_t slot = 0;
-  if (live) {
-    if (kKeys) {
-      slot = __ldg(p.slots + t);
-      live = slot >= 0;
-      if (live && slot >= p.num_rows) {
-        if (l == 0) flag(p.pos.status, STATUS_INDEX);
-        live = false;
-      }
-      if (live) row = table_row(p.pos, t, l == 0);
-    } else {
-      const int32_t at = __ldg(p.pos.positions + t);
-      if (at >= p.pos.max_positions) {
-        if (l == 0 && h == 0) flag(p.pos.status, STATUS_INDEX);
-      } else if (at >= 0) {
-        row = p.pos.table + (int64_t)at * kRope;
-      }
+  const bool inside = t < p.tokens;
+  const int32_t slot = kKeys && inside ? __ldg(p.slots + t) : 0, at = inside ? __ldg(p.pos.positions + t) : -1;
+  uint4 raw[kU][2];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const uint32_t h = h0 + u * slots;
+    raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+    if (inside && h < (uint32_t)p.heads) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.x + t * p.x_token + h * p.x_head);
+      raw[u][0] = __ldg(src + l);
+      raw[u][1] = __ldg(src + 8 + l);
     }
-    live = live && row != nullptr;
   }
-  float x[8] = {};
+  // padding: a negative slot, or for queries a negative position
+  bool live = inside && (kKeys ? slot >= 0 : at >= 0);
+  if (live && (at < 0 || at >= p.pos.max_positions || (kKeys && slot >= p.num_rows))) {
+    if (l == 0 && h0 == 0) flag(p.pos.status, STATUS_INDEX);
+    live = false;
+  }
+  const float* row = p.pos.table + (int64_t)at * kRope;  // read where live
+  // The lane's cosines and sines: of its four pairs, or, with halves, of its
+  // eight dims, each half of a pair (lanes 0..3 the first halves, 4..7 the
+  // second, whose partner's sine enters with the other sign).
+  float cs[8] = {}, sn[8] = {};
   if (live) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(p.x + t * p.x_token + h * p.x_head + 8 * l);
-    unpack<kFp16, 8>(&raw, x);
-  }
-  if (p.pos.halves) {
-    // lanes 0..3 hold the first members of the pairs, lanes 4..7 the second
-    float cs[8] = {}, sn[8] = {};
-    if (live && l < 8) {
+    if (p.pos.halves) {
       load_row<8>(row + 8 * (l & 3), cs);
       load_row<8>(row + kPairs + 8 * (l & 3), sn);
-    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float other = __shfl_xor_sync(0xffffffffu, x[k], 4);
-      if (l < 4) x[k] = turn_lo(x[k], other, cs[k], sn[k]);
-      else if (l < 8) x[k] = turn_hi(other, x[k], cs[k], sn[k]);
-    }
-  } else if (live && l < 8) {
-    float cs[4], sn[4];
-    load_row<4>(row + 4 * l, cs);
-    load_row<4>(row + kPairs + 4 * l, sn);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float a = x[2 * k], b = x[2 * k + 1];
-      x[2 * k] = turn_lo(a, b, cs[k], sn[k]);
-      x[2 * k + 1] = turn_hi(a, b, cs[k], sn[k]);
+      for (int k = 0; k < 8; ++k) sn[k] = l < 4 ? -sn[k] : sn[k];
+    } else {
+      load_row<4>(row + 4 * l, cs);
+      load_row<4>(row + kPairs + 4 * l, sn);
     }
   }
-  if (!kFp8) {
-    if (live) reinterpret_cast<uint4*>(p.out)[(int64_t)slot * 16 + l] = pack8<kFp16>(x);
-    return;
-  }
-  float amax = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
+  for (int u = 0; u < kU; ++u) {
+    const uint32_t h = h0 + u * slots;
+    const bool store = live && h < (uint32_t)p.heads;
+    float x[16];
+    unpack<kFp16, 16>(raw[u], x);
+    if (p.pos.halves) {
 #pragma unroll
-  for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (!live) return;
-  const float scale = e4m3_scale(amax);
+      for (int k = 0; k < 8; ++k)
+        x[k] = turn_hi(__shfl_xor_sync(0xffffffffu, x[k], 4), x[k], cs[k], sn[k]);  // other * sin + own * cos
+    } else {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = __fdiv_rn(x[k], scale);
-  const uint2 codes = make_uint2(e4m3x4_rn_sat(x[0], x[1], x[2], x[3]), e4m3x4_rn_sat(x[4], x[5], x[6], x[7]));
-  if (kKeys) {
-    uint8_t* page = p.out + (int64_t)(slot / kTile) * kIndexPageFp8;
-    const int in = slot % kTile;
-    reinterpret_cast<uint2*>(page)[in * 16 + l] = codes;
-    if (l == 0) reinterpret_cast<float*>(page + kTile * kIndexDim)[in] = scale;
-  } else {
-    reinterpret_cast<uint2*>(p.out)[r * 16 + l] = codes;
-    if (l == 0) p.w_out[r] = __fmul_rn(__ldg(p.weights + r), scale);
+      for (int k = 0; k < 4; ++k) {
+        const float a = x[2 * k], b = x[2 * k + 1];
+        x[2 * k] = turn_lo(a, b, cs[k], sn[k]);
+        x[2 * k + 1] = turn_hi(a, b, cs[k], sn[k]);
+      }
+    }
+    if (!kFp8) {
+      if (store) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out) + (int64_t)slot * 16;
+        dst[l] = pack8<kFp16>(x);
+        dst[8 + l] = raw[u][1];
+      }
+      continue;
+    }
+    float amax = amax16(x);
+#pragma unroll
+    for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (!store) continue;
+    const float scale = e4m3_scale(amax);
+    uint32_t w[4];
+    e4m3_codes16(x, scale, w);
+    uint2* dst;
+    if (kKeys) {
+      uint8_t* page = p.out + (int64_t)(slot / kTile) * kIndexPageFp8;
+      const int in = slot % kTile;
+      dst = reinterpret_cast<uint2*>(page) + in * 16;
+      if (l == 0) reinterpret_cast<float*>(page + kTile * kIndexDim)[in] = scale;
+    } else {
+      const int64_t at = (int64_t)t * p.heads + h;
+      dst = reinterpret_cast<uint2*>(p.out) + at * 16;
+      if (l == 0) p.w_out[at] = __fmul_rn(p.weights[at], scale);
+    }
+    dst[l] = make_uint2(w[0], w[1]);
+    dst[8 + l] = make_uint2(w[2], w[3]);
   }
 }
 
