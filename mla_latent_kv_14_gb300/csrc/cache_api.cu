@@ -173,9 +173,8 @@ mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q
                          {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
                          tokens, heads, heads, q_out, weights_out, 0};
   if (const mla_status v = check_positions(p.pos)) return v;
-  // four heads to a lane group share the table row and keep four loads in
-  // flight, once there are enough rows to fill the card that way
-  constexpr int kU = 4;
+  // two heads to a lane group share the position and the table row, once there are enough rows to fill the card that way
+  constexpr int kU = 2;
   const bool many = tokens * heads >= kManyRows;
   if (many) p.heads_per_slot = (heads + kU - 1) / kU;
   const int64_t groups = tokens * p.heads_per_slot;

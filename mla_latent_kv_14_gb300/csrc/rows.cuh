@@ -127,7 +127,7 @@ MLA_DEV void load_row(const float* src, float* v) {
 constexpr int kAppendWarps = 8;
 
 template <bool kFp16, int kFormat>  // kFormat: mla_kv_format
-__global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kv_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps, kFormat == 0 ? 8 : 6) mla_append_kv_kernel(const AppendParams p) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
@@ -330,7 +330,7 @@ constexpr int kIndexLanes = 8;
 constexpr int kIndexGroups = kIndexThreads / kIndexLanes;
 
 template <bool kFp16, bool kFp8, bool kKeys, int kU>
-__global__ void __launch_bounds__(kIndexThreads) mla_index_rows_kernel(const IndexRowParams p) {
+__global__ void __launch_bounds__(kIndexThreads, 4) mla_index_rows_kernel(const IndexRowParams p) {
   pdl_wait();
   const int l = threadIdx.x & (kIndexLanes - 1);
   const uint32_t group = blockIdx.x * kIndexGroups + threadIdx.x / kIndexLanes;
