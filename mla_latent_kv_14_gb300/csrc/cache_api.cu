@@ -231,24 +231,26 @@ mla_status launch_score(int dev, int grid, uint32_t smem, void* stream, const CU
 template <bool kPages>
 mla_status launch_select(select::SelectParams p, int64_t most, int sms, void* stream) {
   const int64_t rows = (int64_t)p.batch * p.s_q;
-  constexpr int kSmall = 4, kBlockSmall = select::kThreads * kSmall;
-  auto blocks = [](int64_t n, int per) {
+  auto blocks = [&](int keys) {  // of a row, at `keys` scores per thread
     int c = 1;
-    while (c < select::kMaxCluster && (int64_t)c * per < n) c *= 2;
+    while (c < select::kMaxCluster && (int64_t)c * select::kThreads * keys < most) c *= 2;
     return c;
   };
-  int keys = select::kMaxKeys;
-  const int small = blocks(most, kBlockSmall);
-  if ((int64_t)small * kBlockSmall >= most && rows * small <= 2 * sms) {
-    keys = kSmall;
-    p.cluster = small;
-  } else {
-    p.cluster = blocks(most, select::kBlockKeys);
-    if ((int64_t)p.cluster * select::kBlockKeys < most) keys = 0;
+  // The fewest scores per thread that hold the longest row; but a row is not
+  // cut into more blocks than run at once while fewer, fuller ones hold it.
+  int keys = 0;
+  for (const int k : {4, 16, 32}) {
+    const int c = blocks(k);
+    if ((int64_t)c * select::kThreads * k < most) continue;
+    keys = k;
+    p.cluster = c;
+    if (c == 1 || rows * c <= 2 * sms) break;
   }
-  auto kernel = keys == kSmall ? select::mla_select_topk_kernel<kPages, kSmall>
-                : keys         ? select::mla_select_topk_kernel<kPages, select::kMaxKeys>
-                               : select::mla_select_topk_kernel<kPages, 0>;
+  if (!keys) p.cluster = select::kMaxCluster;
+  auto kernel = keys == 4    ? select::mla_select_topk_kernel<kPages, 4>
+                : keys == 16 ? select::mla_select_topk_kernel<kPages, 16>
+                : keys       ? select::mla_select_topk_kernel<kPages, 32>
+                             : select::mla_select_topk_kernel<kPages, 0>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * p.cluster), 1, 1);
   cfg.blockDim = dim3(select::kThreads, 1, 1);
