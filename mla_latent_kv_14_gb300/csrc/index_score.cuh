@@ -223,7 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the warp's number as a value that the compiler knows to be the same in all
+  // its lanes: the roles' loops then run on the uniform registers that the
+  // copy and MMA instructions take their operands from
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int N = p.nq * kHp;
   const uint32_t q_chunk = (uint32_t)N * 128u, q_group = kChunks * q_chunk;
   const uint32_t off_ring = p.groups * q_group;          // a multiple of 1024 (N is one of 16)
@@ -323,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 && !it.done()) {
     // ---------------- producer: a unit's query groups, then key tiles ----------------
-    if (lane == 0) {
+    const bool leader = elect_one();
+    if (leader) {
       prefetch_tmap(&tm_q);
       prefetch_tmap(&tm_k);
     }
@@ -334,23 +338,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; !stop && !it.done(); it.next(p), ++units) {
       const int b = it.u / p.units;
       pages.start(p, b, it.t);
-      if (lane == 0) {
-        const int q0 = (it.u - b * p.units) * p.nq * p.groups;
+      const int q0 = (it.u - b * p.units) * p.nq * p.groups;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          // a last group behind the request's queries reads others (or the
-          // zero fill); its products are never stored
-          if (g >= p.groups || stop) break;
-          if (!wait_for(bar(B_QEMPTY + g), (units & 1) ^ 1, guard)) { stop = true; break; }
+      for (int g = 0; g < 2; ++g) {
+        // a last group behind the request's queries reads others (or the
+        // zero fill); its products are never stored
+        if (g >= p.groups || stop) break;
+        if (!__all_sync(0xffffffffu, wait_for(bar(B_QEMPTY + g), (units & 1) ^ 1, guard))) { stop = true; break; }
+        if (leader) {
           mbar_arrive_expect_tx(bar(B_QFULL + g), q_group);
           for (int c = 0; c < kChunks; ++c)
             tma_load_3d_plain(sb + g * q_group + c * q_chunk, &tm_q, bar(B_QFULL + g), c * kChunkElems, 0,
                               b * p.s_q + q0 + g * p.nq);
-          last_q[g] = units;
         }
+        last_q[g] = units;
       }
       const int t1 = it.t + it.m;
-      for (int t = it.t; t < t1; ++t) {
+      for (int t = it.t; t < t1 && !stop; ++t) {
         pages.advance(p, t);
         int page[2];
 #pragma unroll
@@ -358,21 +362,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           page[k] = pages.page(t, k);
           if (page[k] < 0 || page[k] >= p.num_blocks) page[k] = 0;  // a bad page's products are not stored
         }
-        if (lane == 0 && !stop) {
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (!wait_for(bar(B_KEMPTY + kr.slot), kr.phase ^ 1u, guard)) { stop = true; break; }
+        for (int c = 0; c < kChunks; ++c) {
+          if (!__all_sync(0xffffffffu, wait_for(bar(B_KEMPTY + kr.slot), kr.phase ^ 1u, guard))) { stop = true; break; }
+          if (leader) {
             mbar_arrive_expect_tx(bar(B_KFULL + kr.slot), kUnit);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               tma_load_3d_plain(sb + off_ring + kr.slot * kUnit + k * (kUnit / 2), &tm_k, bar(B_KFULL + kr.slot),
                                 c * kChunkElems, 0, page[k]);
-            kr.step(p.ring);
-            ++n;
           }
+          kr.step(p.ring);
+          ++n;
         }
       }
-      stop = __shfl_sync(0xffffffffu, (int)stop, 0) != 0;
     }
     // never leave with a copy in flight into this CTA's shared memory
     if (lane == 0) {
@@ -384,51 +387,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last_q[g] >= 0)
           while (!mbar_try_wait(bar(B_QFULL + g), last_q[g] & 1) && cycles() - t_0 < kDrainLimitCycles) {}
     }
-  } else if (warp == 1 && lane == 0 && !it.done()) {
+  } else if (warp == 1 && !it.done()) {
     // ---------------- UMMA issue ----------------
     const uint32_t idesc = kType == K_FP8 ? ((1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24))
                                           : idesc_f16(128, N, kType == K_BF16, false, false);
     const uint64_t d_ring = sdesc_sw128(sb + off_ring, 16, 1024), d_q = sdesc_sw128(sb, 16, 1024);
+    const bool leader = elect_one();  // issues every MMA and commit
+    auto ready = [&](uint32_t i, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar(i), parity, guard)) != 0; };
     int seq = 0, units = 0;
     bool failed = false;
     Ring kr;
     for (; !failed && !it.done(); it.next(p), ++units) {
-      if (!wait_for(bar(B_QFULL), units & 1, guard) ||
-          (p.groups == 2 && !wait_for(bar(B_QFULL + 1), units & 1, guard)))
-        break;
+      if (!ready(B_QFULL, units & 1) || (p.groups == 2 && !ready(B_QFULL + 1, units & 1))) break;
       for (int i = 0; i < it.m && !failed; ++i) {
         Ring at = kr;
         for (int g = 0; g < p.groups; ++g, ++seq) {
           at = kr;  // every group reads the tile's units
           const int acc = seq & (accs - 1);
           const uint32_t d = tmem + acc_cols * acc;
-          if (!wait_for(bar(B_AEMPTY + acc), ((seq >> acc_shift) & 1) ^ 1, guard)) { failed = true; break; }
+          if (!ready(B_AEMPTY + acc, ((seq >> acc_shift) & 1) ^ 1)) { failed = true; break; }
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            if (g == 0 && !wait_for(bar(B_KFULL + at.slot), at.phase, guard)) { failed = true; break; }
+            if (g == 0 && !ready(B_KFULL + at.slot, at.phase)) { failed = true; break; }
             tc_fence_after();
             const uint64_t da = d_ring + (uint32_t)at.slot * (kUnit >> 4);
             const uint64_t db = d_q + ((g * q_group + c * q_chunk) >> 4);
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the contraction each
-              if (kType == K_FP8)
-                umma_ss_f8(d, da + 2u * kk, db + 2u * kk, idesc, (c | kk) ? 1u : 0u);
-              else
-                umma_ss(d, da + 2u * kk, db + 2u * kk, idesc, (c | kk) ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the contraction each
+                if (kType == K_FP8)
+                  umma_ss_f8(d, da + 2u * kk, db + 2u * kk, idesc, (c | kk) ? 1u : 0u);
+                else
+                  umma_ss(d, da + 2u * kk, db + 2u * kk, idesc, (c | kk) ? 1u : 0u);
+              }
+              if (g == p.groups - 1) umma_commit(bar(B_KEMPTY + at.slot));
+              if (c == kChunks - 1) umma_commit(bar(B_AFULL + acc));
             }
-            if (g == p.groups - 1) umma_commit(bar(B_KEMPTY + at.slot));
             at.step(p.ring);
           }
           if (failed) break;
-          umma_commit(bar(B_AFULL + acc));
         }
         kr = at;
       }
-      umma_commit(bar(B_QEMPTY));
-      if (p.groups == 2) umma_commit(bar(B_QEMPTY + 1));
+      if (leader) {
+        umma_commit(bar(B_QEMPTY));
+        if (p.groups == 2) umma_commit(bar(B_QEMPTY + 1));
+      }
     }
     // every UMMA this thread issued has completed before TMEM is released
-    umma_commit(bar(B_DRAIN));
+    if (leader) umma_commit(bar(B_DRAIN));
     const uint64_t t_0 = cycles();
     while (!mbar_try_wait(bar(B_DRAIN), 0) && cycles() - t_0 < kDrainLimitCycles) {}
   } else if (warp == 2 && ok) {
