@@ -20,8 +20,13 @@ bool dtype_ok(int dtype) { return dtype == MLA_DTYPE_BF16 || dtype == MLA_DTYPE_
 bool cache_ok(int64_t num_blocks, int page_block) {
   return num_blocks > 0 && page_block == kTile && num_blocks < kMaxRows / kTile;
 }
-// strides in elements that keep 16-byte rows aligned
-bool stride_ok(int64_t s, int64_t least) { return s >= least && s % 8 == 0; }
+// strides in elements that keep 16-byte rows aligned, and `count` of them in
+// the range of addresses
+bool stride_ok(int64_t s, int64_t least, int64_t count) {
+  return s >= least && s % 8 == 0 && s <= (int64_t(1) << 46) / (count > 0 ? count : 1);
+}
+// tokens of a row and columns written: room for the kernels' strides in 31 bits
+constexpr int64_t kMaxColumns = kMaxRows - 65536;
 
 // Launched as a programmatic dependent: every kernel here waits for the grid
 // before it (griddepcontrol.wait) ahead of its first global access, so only
@@ -71,7 +76,7 @@ mla_status mla_append_kv(const void* c_kv, int64_t c_stride, const void* k_rope,
   if (!dtype_ok(dtype) || kv_format < MLA_KV_16BIT || kv_format > MLA_KV_FP4_288) return MLA_ERR_INVALID_ARG;
   if (rope_style != MLA_ROPE_PAIRS && rope_style != MLA_ROPE_HALVES) return MLA_ERR_INVALID_ARG;
   const int latent = kv_format >= MLA_KV_FP8_528 ? kDV41 - rows::kRope : kDV;
-  if (!stride_ok(c_stride, latent) || !stride_ok(r_stride, rows::kRope)) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(c_stride, latent, n) || !stride_ok(r_stride, rows::kRope, n)) return MLA_ERR_INVALID_ARG;
   if (status && !aligned(status, 4)) return MLA_ERR_INVALID_ARG;
   if (kv_format && dtype != MLA_DTYPE_BF16) return MLA_ERR_UNSUPPORTED;  // quantised rows pair with bf16
   if (n == 0) return MLA_OK;
@@ -102,7 +107,8 @@ mla_status mla_rotate_q(const void* x, int64_t x_token_stride, int64_t x_head_st
   if (tokens < 0 || heads < 1 || tokens >= kMaxRows / heads || max_positions <= 0) return MLA_ERR_INVALID_ARG;
   if (!dtype_ok(dtype) || (rope_style != MLA_ROPE_PAIRS && rope_style != MLA_ROPE_HALVES)) return MLA_ERR_INVALID_ARG;
   const int64_t xt = x_token_stride, xh = x_head_stride, ot = out_token_stride, oh = out_head_stride, w = rows::kRope;
-  if (!stride_ok(xt, 0) || !stride_ok(xh, 0) || !stride_ok(ot, w) || !stride_ok(oh, w)) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(xt, 0, tokens) || !stride_ok(xh, 0, heads) || !stride_ok(ot, w, tokens) || !stride_ok(oh, w, heads))
+    return MLA_ERR_INVALID_ARG;
   if (status && !aligned(status, 4)) return MLA_ERR_INVALID_ARG;
   if (tokens == 0) return MLA_OK;
   if (!x || !out || !aligned(x, 16) || !aligned(out, 16)) return MLA_ERR_INVALID_ARG;
@@ -139,7 +145,7 @@ mla_status mla_append_index_k(const void* k, int64_t k_stride, int dtype, const 
   if (n < 0 || n >= kMaxRows || max_positions <= 0 || !cache_ok(num_blocks, page_block)) return MLA_ERR_INVALID_ARG;
   if (!dtype_ok(dtype) || (index_format != MLA_INDEX_16BIT && index_format != MLA_INDEX_FP8)) return MLA_ERR_INVALID_ARG;
   if (rope_style != MLA_ROPE_PAIRS && rope_style != MLA_ROPE_HALVES) return MLA_ERR_INVALID_ARG;
-  if (!stride_ok(k_stride, rows::kIndexDim) || (status && !aligned(status, 4))) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(k_stride, rows::kIndexDim, n) || (status && !aligned(status, 4))) return MLA_ERR_INVALID_ARG;
   if (n == 0) return MLA_OK;
   if (!k || !slots || !index_cache || !aligned(k, 16) || !aligned(slots, 4) || !aligned(index_cache, 16))
     return MLA_ERR_INVALID_ARG;
@@ -163,7 +169,7 @@ mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q
                                 float* weights_out, uint32_t* status, void* stream) {
   if (tokens < 0 || heads < 1 || tokens >= kMaxRows / heads || max_positions <= 0) return MLA_ERR_INVALID_ARG;
   if (!dtype_ok(dtype) || (rope_style != MLA_ROPE_PAIRS && rope_style != MLA_ROPE_HALVES)) return MLA_ERR_INVALID_ARG;
-  if (!stride_ok(q_token_stride, 0) || !stride_ok(q_head_stride, 0) || (status && !aligned(status, 4)))
+  if (!stride_ok(q_token_stride, 0, tokens) || !stride_ok(q_head_stride, 0, heads) || (status && !aligned(status, 4)))
     return MLA_ERR_INVALID_ARG;
   if (tokens == 0) return MLA_OK;
   if (!q || !weights || !q_out || !weights_out || !aligned(q, 16) || !aligned(weights, 4) || !aligned(q_out, 16) ||
@@ -303,7 +309,7 @@ mla_status mla_index_score(const void* q, int q_dtype, const float* weights, con
     return MLA_ERR_INVALID_ARG;
   const int64_t columns = (int64_t)width * (pages ? kTile : 1), reach = (int64_t)max_blocks * kTile;
   const int64_t cover = columns < reach ? columns : reach;
-  if (cover >= kMaxRows - score::kTokens) return MLA_ERR_INVALID_ARG;
+  if (cover > kMaxColumns || width > kMaxColumns) return MLA_ERR_INVALID_ARG;
 
   score::ScoreParams p{};
   const int hp = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
@@ -362,7 +368,7 @@ mla_status mla_select_topk(const float* scores, int64_t score_stride, int width,
     return MLA_ERR_INVALID_ARG;
   if ((int64_t)batch * s_q >= kMaxRows) return MLA_ERR_INVALID_ARG;
   const int64_t columns = (int64_t)width * (pages ? kTile : 1), reach = (int64_t)max_blocks * kTile;
-  if ((columns < reach ? columns : reach) >= kMaxRows - kTile) return MLA_ERR_INVALID_ARG;
+  if ((columns < reach ? columns : reach) > kMaxColumns || topk > kMaxColumns) return MLA_ERR_INVALID_ARG;
   if ((int64_t)batch * s_q >= kMaxRows / select::kMaxCluster) return MLA_ERR_UNSUPPORTED;
   if (!scores || !cache_seqlens || !block_table || !indices || (pages && !lens) || !aligned(scores, 4) ||
       !aligned(cache_seqlens, 4) || !aligned(block_table, 4) || !aligned(indices, 4) || (lens && !aligned(lens, 4)) ||

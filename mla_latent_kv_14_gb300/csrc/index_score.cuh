@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(misc), 512);
     tmem_relinquish();
   }
+  pdl_launch_dependents();
   pdl_wait();  // nothing above reads global memory
 
   // ---- this CTA's range: scan of the units' tiles ----

@@ -258,6 +258,11 @@ def _check_scores(got, ref, err, what):
     ([513], 17, 33, False),                        # padded heads
     ([250, 900], 9, 20, True),
     ([190], 40, 7, True),                          # several units of 32 queries
+    ([300, 77], 2, 64, True),                      # 128 columns: the widest of four accumulators
+    ([140, 400], 8, 32, False),                    # 256 columns, one group
+    ([140], 16, 16, True),
+    ([500], 3, 16, False),                         # 48 columns: a batch that ends inside a load
+    ([260, 5], 13, 16, True),
 ])
 def test_index_score(lens, s_q, heads, causal, kind):
     q, w, cache, bt, qv, kv = _score_case(lens, s_q, heads, kind, seed=heads + s_q)
@@ -537,6 +542,76 @@ def test_captured_and_replayed_on_another_stream():
             chain(sc2, ix2, ct2)
         torch.cuda.synchronize()
         assert torch.equal(scores, sc2) and torch.equal(idx, ix2) and torch.equal(cnt, ct2)
+
+
+@pytest.mark.parametrize("n,topk", [(40000, 2048), (300, 7)])
+def test_selection_of_long_rows_captured(n, topk):
+    """Clusters (the long rows) in a graph; the graph and an eager call on another stream at once."""
+    most = -(-n // PAGE)
+    bt = torch.arange(2 * most, dtype=torch.int32, device=DEV).view(2, most)
+    sl = torch.tensor([n, n - 5], dtype=torch.int32, device=DEV)
+    s = torch.randn(2, 1, n, generator=_gen(n)).to(DEV)
+    idx, cnt = torch.empty(2, 1, topk, dtype=torch.int32, device=DEV), torch.empty(2, 1, dtype=torch.int32, device=DEV)
+    mla.mla_select_topk(s, sl, topk, bt, 2 * most, indices=idx, lens=cnt)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mla.mla_select_topk(s, sl, topk, bt, 2 * most, indices=idx, lens=cnt)
+    other = torch.cuda.Stream()
+    for step in range(3):
+        s.copy_(torch.randn(2, 1, n, generator=_gen(n + step)))
+        idx.fill_(-7)
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(other):
+            ix2, ct2 = mla.mla_select_topk(s, sl, topk, bt, 2 * most)
+        torch.cuda.synchronize()
+        ref, want = _select_ref(s.cpu().numpy(), [n, n - 5], 1, False, 1, topk, bt.cpu().numpy(), 2 * most)
+        assert (idx.cpu().numpy() == ref).all() and (cnt.cpu().numpy() == want).all()
+        assert torch.equal(idx, ix2) and torch.equal(cnt, ct2)
+
+
+def test_writers_on_a_side_stream_and_captured():
+    """Every writer in one graph, replayed with new tokens: the same bytes as eager calls."""
+    n, pages = 70, 3
+    table = _table()
+    g = _gen(99)
+    kv, k = torch.randn(n, 576, generator=g).to(BF).to(DEV), torch.randn(n, 128, generator=g).to(BF).to(DEV)
+    q, w = torch.randn(n, 4, 128, generator=g).to(BF).to(DEV), torch.randn(n, 4, generator=g).to(DEV)
+    slots = torch.randperm(pages * PAGE, generator=g)[:n].int().to(DEV)
+    pos = torch.randint(0, 5000, (n,), generator=g).int().to(DEV)
+
+    def buffers():
+        return dict(kv=torch.zeros(pages, PAGE, 1, 656, dtype=torch.uint8, device=DEV), ic=torch.zeros(pages, 8448, dtype=torch.uint8, device=DEV),
+                    rot=torch.zeros(n, 4, 64, dtype=BF, device=DEV), q8=torch.zeros(n, 4, 128, dtype=torch.uint8, device=DEV),
+                    w=torch.zeros(n, 4, device=DEV))
+
+    def write(o):
+        mla.mla_append_kv(kv[:, :512], kv[:, 512:], o["kv"], slots, pos, table, kv_format=mla.KV_FP8_656)
+        mla.mla_append_index_k(k, o["ic"], slots, pos, table, index_format=mla.INDEX_FP8)
+        mla.mla_rotate_q(q[..., :64], pos, table, out=o["rot"])
+        mla.mla_quantize_index_q(q, w, pos, table, q_out=o["q8"], weights_out=o["w"])
+
+    captured = buffers()
+    write(captured)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        write(captured)
+    side = torch.cuda.Stream()
+    for step in range(2):
+        kv.mul_(-1.5), k.mul_(0.75), q.mul_(2.0), w.add_(1.0)
+        pos.copy_((pos + 311) % 5000)
+        eager = buffers()
+        for o in captured.values():
+            o.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            write(eager)
+        torch.cuda.synchronize()
+        for name in eager:
+            assert torch.equal(eager[name], captured[name]), name
 
 
 def test_same_inputs_same_bits():

@@ -44,6 +44,7 @@ APPEND = dict(c=FAKE, cs=576, r=FAKE, rs=576, dtype=0, slots=FAKE, pos=FAKE, tab
     (dict(c=None), 1), (dict(r=None), 1), (dict(slots=None), 1), (dict(pos=None), 1), (dict(table=None), 1),
     (dict(kv=None), 1), (dict(c=ODD), 1), (dict(r=ODD), 1), (dict(kv=ODD), 1), (dict(table=ODD), 1),
     (dict(slots=ODD), 1), (dict(pos=ODD), 1), (dict(status=ODD), 1), (dict(n=0, c=None, kv=None), 0),
+    (dict(cs=1 << 50), 1), (dict(rs=1 << 62), 1),                 # beyond any address
 ])
 def test_append_kv_argument_checks(lib, kw, code):
     assert _call(lib, "mla_append_kv", APPEND, **kw) == code
@@ -59,6 +60,7 @@ ROTATE = dict(x=FAKE, xt=192 * 8, xh=192, out=FAR, ot=576 * 8, oh=576, dtype=0, 
     (dict(oh=64, ot=128), 1),                                     # rows of the output overlap one another
     (dict(x=ODD), 1), (dict(out=ODD), 1), (dict(x=None), 1), (dict(out=None), 1), (dict(pos=None), 1),
     (dict(table=None), 1), (dict(status=ODD), 1), (dict(tokens=0, x=None, out=None), 0),
+    (dict(xt=1 << 60), 1), (dict(oh=1 << 50), 1),
     (dict(out=FAKE), 1),                                          # overlaps x with other strides
     (dict(out=ctypes.c_void_p((1 << 20) + 64), ot=192 * 8, oh=192), 1),   # 32 elements into x's rows
     (dict(out=ctypes.c_void_p((1 << 20) + 320), ot=192 * 8, oh=192), 1),  # 160 of 192: into the next head's dims
@@ -106,6 +108,7 @@ SCORE = dict(q=FAKE, dtype=0, w=FAKE, cache=FAKE, fmt=0, blocks=8, page=64, bt=F
     (dict(bt=None), 1), (dict(sl=None), 1), (dict(scores=None), 1), (dict(q=ODD), 1), (dict(cache=ODD), 1),
     (dict(w=ODD), 1), (dict(scores=ODD), 1), (dict(status=ODD), 1), (dict(batch=1 << 20, s_q=1 << 10), 1),
     (dict(width=(1 << 31) - 1, stride=1 << 31, maxb=1 << 26), 1),
+    (dict(width=(1 << 31) - 1, stride=1 << 31), 1),               # columns behind the table's reach
     (dict(batch=1 << 16, width=1 << 24, stride=1 << 24, maxb=1 << 20), 2),   # more tiles than the list counts
 ])
 def test_index_score_argument_checks(lib, kw, code):
@@ -121,6 +124,8 @@ SELECT = dict(scores=FAKE, stride=512, width=512, sl=FAKE, batch=2, s_q=1, causa
     (dict(topk=0), 1), (dict(maxb=0), 1), (dict(blocks=0), 1), (dict(page=16), 1), (dict(scores=None), 1),
     (dict(sl=None), 1), (dict(bt=None), 1), (dict(idx=None), 1), (dict(block=64, lens=None), 1), (dict(idx=ODD), 1),
     (dict(lens=ODD), 1), (dict(scores=ODD), 1), (dict(status=ODD), 1), (dict(batch=1 << 16, s_q=1 << 16), 1),
+    (dict(topk=(1 << 31) - 1), 1), (dict(width=(1 << 31) - 1, stride=1 << 31, maxb=1 << 26), 1),
+    (dict(batch=1 << 14, s_q=1 << 14), 2),                        # rows beyond a launch's blocks
 ])
 def test_select_topk_argument_checks(lib, kw, code):
     assert _call(lib, "mla_select_topk", SELECT, **kw) == code
