@@ -527,12 +527,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int tok = t * kTokens + row;
         if (bad && lane == 0 && (tok & ~(kTile - 1)) < unit_seen) atomicOr(status, STATUS_INDEX);
-        float* out = out_unit;
-        int left = p.s_q - k0, seen = bad ? INT_MIN / 2 : seen0;
-#pragma unroll 1
-        for (int g = 0; g < p.groups; ++g) {
-          const int queries = min(most, left);                             // may be none in a request's last unit
-          const int batches = queries > 0 ? (queries * kHp + 63) / 64 : 0;  // of 64 columns, at most 2
+        const int seen_unit = bad ? INT_MIN / 2 : seen0;
+        // stores (or keeps for the page maximum) the score of query j of a group's share
+        auto finish = [&](int g, int j, float total) {
+          const float s = tok < min(seen_unit + later * (g * p.nq + j), p.cover) ? total * ks : -INFINITY;
+          if (!kPages) {
+            if (tok < p.width) out_unit[g * group_step + j * p.stride] = s;
+          } else {
+            float m = s;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane == 0) red[(done & 1) * 64 + q4 * 16 + j] = m;
+          }
+        };
+        float v0[2][kQ][4], v1[2][kQ][4];  // sums over the lane's columns: [group][query of the batch][row]
+        // sums of a group's share: over the four lanes of a row, for all of its queries together
+        auto totals = [&](int g, int queries) {
+          float total[2 * kQ];
+#pragma unroll
+          for (int j = 0; j < kQ; ++j) {
+            total[j] = reduce(v0[g][j]);
+            if (queries > kQ) total[kQ + j] = reduce(v1[g][j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 2 * kQ; ++j)
+            if (j < queries) finish(g, j, total[j]);
+        };
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (g >= p.groups) break;
+          const int queries = min(most, p.s_q - k0 - g * p.nq);  // may be none in a request's last unit
+          const bool two = queries > kQ;                        // batches of 64 columns
           const int seq = shared ? done : kGroups * done + e, acc = seq & (accs - 1);
           const uint32_t tl = tl0 + acc_cols * (uint32_t)acc;
           uint64_t wv[8];  // the lane's weights of a batch: columns 8k + 2 (lane % 4) + {0, 1}
@@ -562,7 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           // two register buffers of 16 rows: one is loaded while the other is summed
           uint32_t ra[32], rb[32];
-          float v0[kQ][4], v1[kQ][4];
           load_weights(0);
           if (!__all_sync(0xffffffffu, wait_for(bar(B_AFULL + acc), (seq >> acc_shift) & 1, guard))) {
             failed = true;
@@ -574,42 +598,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           pin_regs32(ra);
           pin_regs32(rb);
-          if (batches == 2) {
-            half(ra, v0, 0);
+          if (two) {
+            half(ra, v0[g], 0);
             tmem_ld_16x64(tl + 64, ra);
-            half(rb, v0, 2);
+            half(rb, v0[g], 2);
             load_weights(1);
             tmem_ld_16x64(tl + (16u << 16) + 64, rb);
             tmem_wait_ld();
             pin_regs32(ra);
             pin_regs32(rb);
             release();
-            half(ra, v1, 0);
-            half(rb, v1, 2);
+            half(ra, v1[g], 0);
+            half(rb, v1[g], 2);
           } else {
             release();
-            half(ra, v0, 0);
-            half(rb, v0, 2);
+            half(ra, v0[g], 0);
+            half(rb, v0[g], 2);
           }
-          float total[2 * kQ];
-#pragma unroll
-          for (int j = 0; j < kQ; ++j) {
-            total[j] = reduce(v0[j]);
-            if (batches == 2) total[kQ + j] = reduce(v1[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < 2 * kQ; ++j) {
-            if (j >= queries) break;
-            const float s = tok < min(seen + later * j, p.cover) ? total[j] * ks : -INFINITY;
-            if (!kPages) {
-              if (tok < p.width) out[j * p.stride] = s;
-            } else {
-              float m = s;
-#pragma unroll
-              for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-              if (lane == 0) red[(done & 1) * 64 + q4 * 16 + j] = m;
-            }
-          }
+          if (kPages || kHp < 64) totals(g, queries);
           if (kPages) {
             // the page's other warp; bounded like every wait, so that a warp that
             // gave up leaves no one behind
@@ -622,14 +628,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int x = 32 * q4 + lane, j = x >> 1, k = x & 1, page = 2 * t + k;
             if (j < queries && page < p.width) {
               const float* v = red + (done & 1) * 64 + 2 * k * 16 + j;
-              out[j * p.stride + page] = fmaxf(v[0], v[16]);
+              out_unit[g * group_step + j * p.stride + page] = fmaxf(v[0], v[16]);
             }
           }
           ++done;
-          // the unit's second group
-          out += group_step;
-          seen += later * p.nq;
-          left -= p.nq;
+        }
+        if (!kPages && kHp == 64 && !failed) {
+          // the scores of both groups at once: the shuffles' latencies overlap
+          totals(0, min(most, p.s_q - k0));
+          if (p.groups == 2) totals(1, min(most, p.s_q - k0 - p.nq));
         }
         if (failed) break;
       }
