@@ -112,16 +112,19 @@ def workload_seqlens(w):
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "dram_traffic.txt")
 
 
+# the sources of the kernels that the workloads time
+KERNEL_SOURCES = ("absorb.cuh", "decode_dense.cuh", "decode_fewheads.cuh", "params.h", "ptx.cuh", "sched.cuh")
+
+
 def kernel_source_digest() -> str:
-    """Digest of the CUDA sources the kernels are built from (so a stored
+    """Digest of the CUDA sources the timed kernels are built from (so a stored
     DRAM-traffic figure is used only for the kernels it was measured on)."""
     import hashlib
     csrc = os.path.join(ROOT, "mla_latent_kv_14_gb300", "csrc")
     h = hashlib.sha256()
-    for name in sorted(os.listdir(csrc)):
-        if name.endswith((".cu", ".cuh", ".h")):
-            with open(os.path.join(csrc, name), "rb") as f:
-                h.update(name.encode() + b"\0" + f.read())
+    for name in KERNEL_SOURCES:
+        with open(os.path.join(csrc, name), "rb") as f:
+            h.update(name.encode() + b"\0" + f.read())
     return h.hexdigest()[:16]
 
 

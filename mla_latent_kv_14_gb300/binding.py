@@ -377,7 +377,7 @@ INDEX_DIM, INDEX_FP8_PAGE_BYTES = 128, 8448
 _host = None
 
 
-def _load_host():
+def load_host():
     """The extension module that checks and launches these calls (built with
     libmla.so; their time on the GPU is a few microseconds)."""
     global _host
@@ -415,7 +415,7 @@ def mla_append_kv(c_kv: torch.Tensor, k_rope: torch.Tensor, kvcache: torch.Tenso
     """Append tokens to the paged cache in place: c_kv [n, 512] (V4.1 rows: 448)
     and k_rope [n, 64], which is rotated on the way; ``slots`` int32 [n] are cache
     rows (page * 64 + offset, negative: skip). Returns kvcache."""
-    return (_host or _load_host()).mla_append_kv(c_kv, k_rope, kvcache, slots, positions, rope_table, kv_format,
+    return (_host or load_host()).mla_append_kv(c_kv, k_rope, kvcache, slots, positions, rope_table, kv_format,
                                                  rope_style, status)
 
 
@@ -426,7 +426,7 @@ def mla_rotate_q(x: torch.Tensor, positions: torch.Tensor, rope_table: torch.Ten
     example ``q[..., 128:]`` of the projection) -> out, of the same shape
     (``q_abs[..., 512:]``, ``x`` itself, or allocated). Rows of tokens whose
     position is negative are not written."""
-    return (_host or _load_host()).mla_rotate_q(x, positions, rope_table, out, rope_style, status)
+    return (_host or load_host()).mla_rotate_q(x, positions, rope_table, out, rope_style, status)
 
 
 def mla_append_index_k(k: torch.Tensor, index_cache: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor,
@@ -435,7 +435,7 @@ def mla_append_index_k(k: torch.Tensor, index_cache: torch.Tensor, slots: torch.
     """Append index keys k [n, 128] (dims [0, 64) are rotated) to the paged index
     cache in place: [num_blocks, 64, 1, 128] of k's type, or uint8 [num_blocks,
     8448] with INDEX_FP8. ``slots`` as in :func:`mla_append_kv`."""
-    return (_host or _load_host()).mla_append_index_k(k, index_cache, slots, positions, rope_table, index_format,
+    return (_host or load_host()).mla_append_index_k(k, index_cache, slots, positions, rope_table, index_format,
                                                       rope_style, status)
 
 
@@ -447,7 +447,7 @@ def mla_quantize_index_q(q: torch.Tensor, weights: torch.Tensor, positions: torc
     with each row's scale folded into ``weights`` fp32 [tokens, heads]. Returns
     (float8_e4m3fn [tokens, heads, 128], fp32 [tokens, heads]); rows of tokens
     whose position is negative are not written."""
-    return (_host or _load_host()).mla_quantize_index_q(q, weights, positions, rope_table, rope_style, q_out,
+    return (_host or load_host()).mla_quantize_index_q(q, weights, positions, rope_table, rope_style, q_out,
                                                         weights_out, status)
 
 
@@ -459,7 +459,7 @@ def mla_index_score(q: torch.Tensor, weights: torch.Tensor, index_cache: torch.T
     (block=64): sum_h weights[b, i, h] * relu(q[b, i, h] . k_t), -inf where
     nothing is visible. q [B, s_q, heads, 128] of the index cache's type (e4m3
     with INDEX_FP8); ``width`` defaults to what the block table reaches."""
-    return (_host or _load_host()).mla_index_score(q, weights, index_cache, block_table, cache_seqlens, width, causal,
+    return (_host or load_host()).mla_index_score(q, weights, index_cache, block_table, cache_seqlens, width, causal,
                                                    block, index_format, scores, status)
 
 
@@ -472,5 +472,5 @@ def mla_select_topk(scores: torch.Tensor, cache_seqlens: torch.Tensor, topk: int
     their number [B, s_q]); block=64: (pages [B, s_q, topk] and the tokens they
     hold [B, s_q]), the block table and lengths of a decode with B * s_q requests
     of one query. ``num_blocks``: pages of the cache that the rows index."""
-    return (_host or _load_host()).mla_select_topk(scores, cache_seqlens, topk, block_table, num_blocks, causal, block,
+    return (_host or load_host()).mla_select_topk(scores, cache_seqlens, topk, block_table, num_blocks, causal, block,
                                                    indices, lens, status)

@@ -13,7 +13,11 @@ using namespace mla;
 namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
-// rows of (token, head) from which a thread takes several heads of a token
+// Rows of (token, head) from which a thread takes several heads of a token, so
+// that they share its table row (rotation, 4 heads: 256 x 128 rows 2.5 us
+// against 2.9 with one, 4095 x 128 22.9 against 29.9; 64 x 128, where one head a
+// thread fills the card better, 2.4 against 1.8. Index queries, 2 heads: 512 x
+// 64 rows 3.8 us against 4.2, 128 x 64 2.4 against 2.0).
 constexpr int64_t kManyRows = 32768;
 
 bool dtype_ok(int dtype) { return dtype == MLA_DTYPE_BF16 || dtype == MLA_DTYPE_FP16; }
@@ -242,15 +246,19 @@ mla_status launch_select(select::SelectParams p, int64_t most, int sms, void* st
     while (c < select::kMaxCluster && (int64_t)c * select::kThreads * keys < most) c *= 2;
     return c;
   };
-  // The fewest scores per thread that hold the longest row; but a row is not
-  // cut into more blocks than run at once while fewer, fuller ones hold it.
+  // One block a row where it holds the row, with the fewest scores per thread
+  // (32 rows of 12288: 7.8 us with 32 scores a thread, 10.4 in clusters of 8
+  // with 4; 64 rows of 8192: 6.5 with 16, 7.7 with 32). Longer rows go to
+  // clusters, of 16 scores per thread while all of them run at once (8 rows of
+  // 32768: 9.7 us, 10.8 with 32), else of 32.
   int keys = 0;
   for (const int k : {4, 16, 32}) {
     const int c = blocks(k);
-    if ((int64_t)c * select::kThreads * k < most) continue;
+    const bool holds = (int64_t)c * select::kThreads * k >= most, at_once = rows * c <= 2 * sms;
+    if (!holds || (c > 1 && (k == 4 || most <= select::kBlockKeys || (k == 16 && !at_once)))) continue;
     keys = k;
     p.cluster = c;
-    if (c == 1 || rows * c <= 2 * sms) break;
+    break;
   }
   if (!keys) p.cluster = select::kMaxCluster;
   auto kernel = keys == 4    ? select::mla_select_topk_kernel<kPages, 4>
