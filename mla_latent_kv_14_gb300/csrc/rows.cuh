@@ -11,7 +11,8 @@
 // rounded once, to the row's own type.
 //
 // All of these are bound by their bytes (under 1 FLOP per byte) and, for a few
-// tokens, by the latency of slot/position -> table row -> store.
+// tokens, by the latency of slot/position -> table row -> store. So each kernel
+// has every load that does not depend on another one in flight first.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -122,7 +123,14 @@ MLA_DEV void load_row(const float* src, float* v) {
 }
 
 // ---------------------------------------------------------------------------
-// The paged latent cache: one warp per token.
+// The paged latent cache: one warp per token, 32 contiguous bytes of latent
+// dims per lane (eight lanes to a block of 128, so that its scale is formed
+// once a lane and agreed on in three shuffles).
+// Measured (GB300): 64 tokens 1.4 us; 32768 tokens, 16-bit rows 14.3 us (0.87 of
+// the copy bandwidth), 656-byte rows 14.4 us (0.69; 16.9 at the 52 registers a
+// thread takes unlimited, which leave 40 warps an SM instead of 48), 528-byte
+// rows 15.1 us (0.58): the quantised rows wait for their loads between two
+// stretches of arithmetic, at half of the issue slots.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 8;
 
@@ -262,6 +270,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kFormat == 0 ? 8 : 6) mla_a
 // Rotation of query rows: a thread turns 8 pairs (32 bytes) of kU heads of one
 // token, four threads per row of 64 dims. The table row stays in registers for
 // the kU heads.
+// Measured (GB300): 64 tokens x 128 heads 1.8 us; 4095 x 128 22.9 us (0.87 of the
+// copy bandwidth).
 // ---------------------------------------------------------------------------
 constexpr int kRotateThreads = 256;
 
@@ -324,6 +334,9 @@ __global__ void __launch_bounds__(kRotateThreads) mla_rotate_kernel(const Rotate
 // [64 + 8l, 64 + 8l + 8) of the other, so that every lane turns four pairs. A
 // lane group takes kU heads of one token, which share the position and the
 // table row.
+// Measured (GB300): 4096 x 64 e4m3 queries 27 us (0.57 of the copy bandwidth; 42
+// with 16 lanes a row and a division per value): some 230 instructions for 16
+// values of a lane, the loads waited for in between. 32768 keys 4.2 us (0.75).
 // ---------------------------------------------------------------------------
 constexpr int kIndexThreads = 256;
 constexpr int kIndexLanes = 8;
