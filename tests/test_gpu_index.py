@@ -103,6 +103,66 @@ def test_append_equals_the_contiguous_quantisers():
         assert torch.equal(cache.view(n, -1), want)
 
 
+def _wide(n, width, seed):
+    """bf16 rows over the type's whole range: block maxima from subnormal to the
+    largest, zeros of both signs, infinities and NaN."""
+    g = _gen(seed)
+    kv = torch.randn(n, width, generator=g)
+    kv = (kv * torch.exp2(torch.linspace(-132.0, 124.0, n))[:, None]).to(BF)
+    kv[torch.rand(n, width, generator=g) < 0.02] = 0.0
+    kv[torch.rand(n, width, generator=g) < 0.02] = -0.0
+    kv[3, 5], kv[n // 3, 100], kv[n // 2, 7] = float("inf"), float("-inf"), float("nan")
+    kv[n - 9] = float("nan")
+    kv[n - 4, :128] = -0.0
+    return kv
+
+
+def test_append_of_any_value_equals_the_contiguous_quantisers():
+    n = 1024
+    for fmt, quant, w in ((1, mla.mla_quantize_kv_fp8, 576), (2, mla.mla_quantize_kv_fp8_528, 512),
+                          (3, mla.mla_quantize_kv_fp4_288, 512)):
+        kv = _wide(n, w, fmt)
+        kv[:, w - 64:] = kv[:, w - 64:].nan_to_num(1.0, 2.0, -2.0).clamp(-4, 4)    # rotated by cos 1, sin 0: kept
+        kv = kv.to(DEV)
+        want = quant(kv)
+        cache = torch.zeros(n // 64, 64, 1, want.shape[-1], dtype=torch.uint8, device=DEV)
+        zero = torch.zeros(n, dtype=torch.int32, device=DEV)
+        mla.mla_append_kv(kv[:, : w - 64], kv[:, w - 64:], cache, torch.arange(n, dtype=torch.int32, device=DEV), zero,
+                          _table(), kv_format=fmt)
+        got = cache.view(n, -1)
+        same = got == want
+        if fmt == 1:      # an fp32 NaN (the scale of a NaN block) may have any payload
+            same[:, 512:528] |= (got[:, 512:528].contiguous().view(torch.float32).isnan()
+                                 & want[:, 512:528].contiguous().view(torch.float32).isnan()).repeat_interleave(4, dim=1)
+            # adding 0 * sin turns a rope value of -0 into +0
+            rope, plain = got[:, 528:].contiguous().view(BF), want[:, 528:].contiguous().view(BF)
+            same[:, 528:] |= (rope == plain).repeat_interleave(2, dim=1)
+        else:             # the same -0, as a code's sign
+            per = 1 if fmt == 2 else 2
+            zero_code = (kv[:, 448:] == 0).view(n, -1, per).any(dim=2)
+            same[:, 448 // per:512 // per] |= zero_code
+        assert same.all(), (fmt, (~same).nonzero()[:8].tolist())
+
+
+def test_index_rows_of_any_value():
+    n = 1024
+    x = _wide(n, 128, 4)
+    x[:, :64] = x[:, :64].nan_to_num(0.0, 0.0, 0.0)              # the rotated half finite
+    x[:, :64] = x[:, :64].clamp(-1e30, 1e30)
+    pos = np.arange(n).astype(np.int32)
+    with np.errstate(invalid="ignore"):
+        _, codes, scale = oracle.index_row_codes(x, TABLE[:n], False)
+    whole = torch.isfinite(x.float()).all(dim=1).numpy()
+    q8, w = mla.mla_quantize_index_q(x[:, None].to(DEV), torch.ones(n, 1, device=DEV), torch.from_numpy(pos).to(DEV), _table())
+    q8, w = q8.view(torch.uint8).cpu().numpy()[:, 0], w.cpu().numpy()[:, 0]
+    assert (q8[whole] == codes[whole]).all() and (w[whole] == scale[whole]).all()
+    row = [i for i in np.flatnonzero(~whole) if not torch.isnan(x[i].float()).any()]
+    assert row
+    for i in row:                                                # an infinite scale: zeros, NaN for the infinities
+        inf = torch.isinf(x[i].float()).numpy()
+        assert np.isinf(w[i]) and ((q8[i] & 0x7F) == np.where(inf, 0x7F, 0)).all()
+
+
 @pytest.mark.parametrize("halves", [0, 1])
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("tokens,heads", [(1, 1), (3, 128), (65, 5), (7, 16), (40, 33)])

@@ -165,6 +165,38 @@ def test_binding_refuses_before_the_library():
         assert e.value.status == 1, k
 
 
+# ---- the quotient of the quantisers ----
+def _fma32(a, b, c):
+    """a * b + c of fp32 arrays, rounded once: the product is exact in 64 bits,
+    the sum is rounded to odd there, then to fp32."""
+    p, c = a.astype(np.float64) * b.astype(np.float64), c.astype(np.float64)
+    s = p + c
+    t = s - p
+    rest = (p - (s - t)) + (c - t)
+    beside = np.nextafter(s, np.where(rest > 0, np.inf, -np.inf))
+    return np.where((rest != 0) & (s.view(np.int64) % 2 == 0), beside, s).astype(np.float32)
+
+
+@pytest.mark.parametrize("kind", ["any", "midpoints", "ends"])
+def test_corrected_quotient_is_the_division(kind):
+    """q = x r, q + (x - q s) r with r = 1 / s: the steps by which the paged
+    writers divide by a block's scale, against the correctly rounded quotient."""
+    rng = np.random.default_rng(0)
+    n = 1 << 20
+    s = (1 + rng.integers(0, 1 << 23, n) * 2.0 ** -23).astype(np.float32)
+    x = (1 + rng.integers(0, 1 << 23, n) * 2.0 ** -23).astype(np.float32)
+    if kind == "midpoints":        # x / s within a few units of five-bit numbers, e4m3's values and midpoints
+        x = (rng.integers(16, 32, n) / 16 * s.astype(np.float64)).astype(np.float32)
+        x = (x.view(np.int32) + rng.integers(-2, 3, n).astype(np.int32)).view(np.float32)
+    if kind == "ends":             # scales just below a power of two
+        s = (2 - rng.integers(1, 1 << 12, n) * 2.0 ** -23).astype(np.float32)
+    r = (1 / s.astype(np.float64)).astype(np.float32)
+    q = x * r
+    got = _fma32(_fma32(q, -s, x), r, q)
+    # a quotient of two 24-bit numbers rounded to 53 bits, then to 24, is rounded correctly
+    assert (got == (x.astype(np.float64) / s.astype(np.float64)).astype(np.float32)).all()
+
+
 # ---- the oracle ----
 @pytest.mark.parametrize("halves", [False, True])
 def test_oracle_rotation_is_a_complex_product(halves):
