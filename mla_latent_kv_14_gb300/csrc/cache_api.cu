@@ -13,11 +13,10 @@ using namespace mla;
 namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
-// Rows of (token, head) from which a thread takes several heads of a token, so
-// that they share its table row (rotation, 4 heads: 256 x 128 rows 2.5 us
+// Rows of (token, head) from which a thread of the rotation takes four heads of
+// a token, which share its table row ( 256 x 128 rows 2.5 us
 // against 2.9 with one, 4095 x 128 22.9 against 29.9; 64 x 128, where one head a
-// thread fills the card better, 2.4 against 1.8. Index queries, 2 heads: 512 x
-// 64 rows 3.8 us against 4.2, 128 x 64 2.4 against 2.0).
+// thread fills the card better, 2.4 against 1.8).
 constexpr int64_t kManyRows = 32768;
 
 bool dtype_ok(int dtype) { return dtype == MLA_DTYPE_BF16 || dtype == MLA_DTYPE_FP16; }
@@ -155,16 +154,16 @@ mla_status mla_append_index_k(const void* k, int64_t k_stride, int dtype, const 
     return MLA_ERR_INVALID_ARG;
   rows::IndexRowParams p{static_cast<const uint16_t*>(k), k_stride, 0, slots, nullptr,
                          {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
-                         n, 1, 1, static_cast<uint8_t*>(index_cache), nullptr, num_blocks * kTile};
+                         n, 1, 1, 1, static_cast<uint8_t*>(index_cache), nullptr, num_blocks * kTile};
   if (const mla_status v = check_positions(p.pos)) return v;
   const int per = rows::kIndexGroups;
   const dim3 grid((unsigned)((n + per - 1) / per));
   const bool fp16 = dtype == MLA_DTYPE_FP16;
   if (index_format == MLA_INDEX_FP8)
-    return fp16 ? launch(rows::mla_index_rows_kernel<true, true, true, 1>, grid, rows::kIndexThreads, 0, stream, p)
-                : launch(rows::mla_index_rows_kernel<false, true, true, 1>, grid, rows::kIndexThreads, 0, stream, p);
-  return fp16 ? launch(rows::mla_index_rows_kernel<true, false, true, 1>, grid, rows::kIndexThreads, 0, stream, p)
-              : launch(rows::mla_index_rows_kernel<false, false, true, 1>, grid, rows::kIndexThreads, 0, stream, p);
+    return fp16 ? launch(rows::mla_index_rows_kernel<true, true, true>, grid, rows::kIndexThreads, 0, stream, p)
+                : launch(rows::mla_index_rows_kernel<false, true, true>, grid, rows::kIndexThreads, 0, stream, p);
+  return fp16 ? launch(rows::mla_index_rows_kernel<true, false, true>, grid, rows::kIndexThreads, 0, stream, p)
+              : launch(rows::mla_index_rows_kernel<false, false, true>, grid, rows::kIndexThreads, 0, stream, p);
 }
 
 mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype,
@@ -181,20 +180,20 @@ mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q
     return MLA_ERR_INVALID_ARG;
   rows::IndexRowParams p{static_cast<const uint16_t*>(q), q_token_stride, q_head_stride, nullptr, weights,
                          {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
-                         tokens, heads, heads, q_out, weights_out, 0};
+                         tokens, heads, heads, 1, q_out, weights_out, 0};
   if (const mla_status v = check_positions(p.pos)) return v;
-  // two heads to a lane group share the position and the table row, once there are enough rows to fill the card that way
-  constexpr int kU = 2;
-  const bool many = tokens * heads >= kManyRows;
-  if (many) p.heads_per_slot = (heads + kU - 1) / kU;
-  const int64_t groups = tokens * p.heads_per_slot;
+  // up to eight heads to a lane group, as long as that leaves kFewGroups of them: half the card's lanes. Measured with
+  // 64 heads (GB300): 512 tokens 4.0 us (two heads a group), 5.5 with eight; 4096 tokens 20.6 with eight, 24.5 with two
+  constexpr int64_t kFewGroups = 16384;
+  const int64_t steps = tokens * heads / kFewGroups;
+  p.steps = (int)(steps < 1 ? 1 : steps > 8 ? 8 : steps);
+  p.slots_per_token = (heads + p.steps - 1) / p.steps;
+  const int64_t groups = tokens * p.slots_per_token;
   const int per = rows::kIndexGroups;
   const dim3 grid((unsigned)((groups + per - 1) / per));
-  if (dtype == MLA_DTYPE_FP16)
-    return many ? launch(rows::mla_index_rows_kernel<true, true, false, kU>, grid, rows::kIndexThreads, 0, stream, p)
-                : launch(rows::mla_index_rows_kernel<true, true, false, 1>, grid, rows::kIndexThreads, 0, stream, p);
-  return many ? launch(rows::mla_index_rows_kernel<false, true, false, kU>, grid, rows::kIndexThreads, 0, stream, p)
-              : launch(rows::mla_index_rows_kernel<false, true, false, 1>, grid, rows::kIndexThreads, 0, stream, p);
+  return dtype == MLA_DTYPE_FP16
+             ? launch(rows::mla_index_rows_kernel<true, true, false>, grid, rows::kIndexThreads, 0, stream, p)
+             : launch(rows::mla_index_rows_kernel<false, true, false>, grid, rows::kIndexThreads, 0, stream, p);
 }
 
 }  // extern "C"

@@ -18,8 +18,17 @@ MLA_DEV uint32_t e4m3x4_rn_sat(float a, float b, float c, float d) {
   return (uint32_t)e4m3x2_rn_sat(a, b) | ((uint32_t)e4m3x2_rn_sat(c, d) << 16);
 }
 
-// scale of a block whose largest magnitude is amax: fp32(amax / 448), 1 for zeros
-MLA_DEV float e4m3_scale(float amax) { return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f); }
+// scale of a block whose largest magnitude is amax: fp32(amax / 448), 1 for
+// zeros; the quotient by the corrected reciprocal of e4m3_codes16, equal to the
+// division for every fp32 significand
+MLA_DEV float e4m3_scale(float amax) {
+  if (amax >= 0x1p-60f && amax < 0x1p127f) {
+    constexpr float r = 1.f / 448.f;
+    const float q = __fmul_rn(amax, r);
+    return __fmaf_rn(__fmaf_rn(q, -448.f, amax), r, q);
+  }
+  return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f);
+}
 
 // Sixteen values over their block's scale, as e4m3 codes (value i in byte i).
 //

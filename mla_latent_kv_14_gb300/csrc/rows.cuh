@@ -59,11 +59,13 @@ struct RotateParams {
 struct IndexRowParams {
   const uint16_t* x;         // [tokens, heads, 128]
   int64_t x_token, x_head;   // strides in elements
-  const int32_t* slots;      // keys: [tokens]
+  const int32_t* cache_slots;  // keys: [tokens]
   const float* weights;      // queries: [tokens, heads]
   Positions pos;
   int64_t tokens;
-  int heads, heads_per_slot;  // head slots of a token: ceil(heads / kU)
+  int heads;
+  int slots_per_token;       // queries: lane groups of a token, ceil(heads / steps)
+  int steps;                 // queries: heads a lane group takes
   uint8_t* out;              // keys: the index cache; queries: [tokens, heads, 128] codes
   float* w_out;              // queries: [tokens, heads]
   int64_t num_rows;          // keys: rows of the index cache
@@ -332,38 +334,42 @@ __global__ void __launch_bounds__(kRotateThreads) mla_rotate_kernel(const Rotate
 // cache, queries as e4m3 with their scale folded into the head's weight.
 // Eight lanes per row: lane l holds dims [8l, 8l + 8) of the rotated half and
 // [64 + 8l, 64 + 8l + 8) of the other, so that every lane turns four pairs. A
-// lane group takes kU heads of one token, which share the position and the
-// table row.
-// Measured (GB300): 4096 x 64 e4m3 queries 27 us (0.57 of the copy bandwidth; 42
-// with 16 lanes a row and a division per value): some 230 instructions for 16
-// values of a lane, the loads waited for in between. 32768 keys 4.2 us (0.75).
+// lane group takes `steps` query heads of one token, which share the position
+// and the table row, and loads a head ahead.
+// Measured (GB300): 4096 x 64 e4m3 queries 20.6 us (0.74 of the copy bandwidth; 27 with two heads a
+// group, their weight loaded where it is used and the scale divided; 42 with 16
+// lanes a row and a division per value as well): some 200 instructions for 16
+// values of a lane. 32768 keys 4.2 us (0.75).
 // ---------------------------------------------------------------------------
 constexpr int kIndexThreads = 256;
 constexpr int kIndexLanes = 8;
 constexpr int kIndexGroups = kIndexThreads / kIndexLanes;
 
-template <bool kFp16, bool kFp8, bool kKeys, int kU>
+template <bool kFp16, bool kFp8, bool kKeys>
 __global__ void __launch_bounds__(kIndexThreads, 4) mla_index_rows_kernel(const IndexRowParams p) {
   pdl_wait();
   const int l = threadIdx.x & (kIndexLanes - 1);
   const uint32_t group = blockIdx.x * kIndexGroups + threadIdx.x / kIndexLanes;
-  const uint32_t slots = (uint32_t)p.heads_per_slot;
+  const uint32_t slots = kKeys ? 1u : (uint32_t)p.slots_per_token;
   const uint32_t t = kKeys ? group : group / slots, h0 = kKeys ? 0u : group - t * slots;
+  const int steps = kKeys ? 1 : p.steps;
   // every lane takes part in the shuffles below; rows past the end or to be
   // skipped work on zeros and store nothing
   const bool inside = t < p.tokens;
-  const int32_t slot = kKeys && inside ? __ldg(p.slots + t) : 0, at = inside ? __ldg(p.pos.positions + t) : -1;
-  uint4 raw[kU][2];
-#pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const uint32_t h = h0 + u * slots;
-    raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+  const int32_t slot = kKeys && inside ? __ldg(p.cache_slots + t) : 0, at = inside ? __ldg(p.pos.positions + t) : -1;
+  uint4 raw[2];
+  float weight;
+  auto fetch = [&](uint32_t h) {
+    raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+    weight = 0.f;
     if (inside && h < (uint32_t)p.heads) {
       const uint4* src = reinterpret_cast<const uint4*>(p.x + t * p.x_token + h * p.x_head);
-      raw[u][0] = __ldg(src + l);
-      raw[u][1] = __ldg(src + 8 + l);
+      raw[0] = __ldg(src + l);
+      raw[1] = __ldg(src + 8 + l);
+      if (!kKeys && l == 0) weight = p.weights[(int64_t)t * p.heads + h];
     }
-  }
+  };
+  fetch(h0);
   // padding: a negative slot, or for queries a negative position
   bool live = inside && (kKeys ? slot >= 0 : at >= 0);
   if (live && (at < 0 || at >= p.pos.max_positions || (kKeys && slot >= p.num_rows))) {
@@ -386,12 +392,15 @@ __global__ void __launch_bounds__(kIndexThreads, 4) mla_index_rows_kernel(const 
       load_row<4>(row + kPairs + 4 * l, sn);
     }
   }
-#pragma unroll
-  for (int u = 0; u < kU; ++u) {
+#pragma unroll 1
+  for (int u = 0; u < steps; ++u) {
     const uint32_t h = h0 + u * slots;
     const bool store = live && h < (uint32_t)p.heads;
     float x[16];
-    unpack<kFp16, 16>(raw[u], x);
+    unpack<kFp16, 16>(raw, x);
+    const uint4 second = raw[1];
+    const float w_head = weight;
+    if (u + 1 < steps) fetch(h + slots);
     if (p.pos.halves) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -408,7 +417,7 @@ __global__ void __launch_bounds__(kIndexThreads, 4) mla_index_rows_kernel(const 
       if (store) {
         uint4* dst = reinterpret_cast<uint4*>(p.out) + (int64_t)slot * 16;
         dst[l] = pack8<kFp16>(x);
-        dst[8 + l] = raw[u][1];
+        dst[8 + l] = second;
       }
       continue;
     }
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(kIndexThreads, 4) mla_index_rows_kernel(const 
     } else {
       const int64_t at = (int64_t)t * p.heads + h;
       dst = reinterpret_cast<uint2*>(p.out) + at * 16;
-      if (l == 0) p.w_out[at] = __fmul_rn(p.weights[at], scale);
+      if (l == 0) p.w_out[at] = __fmul_rn(w_head, scale);
     }
     dst[l] = make_uint2(w[0], w[1]);
     dst[8 + l] = make_uint2(w[2], w[3]);

@@ -197,6 +197,16 @@ def test_corrected_quotient_is_the_division(kind):
     assert (got == (x.astype(np.float64) / s.astype(np.float64)).astype(np.float32)).all()
 
 
+def test_scale_quotient_for_every_significand():
+    """amax / 448 by the same steps, for all 2^23 significands."""
+    x = (1 + np.arange(1 << 23) * 2.0 ** -23).astype(np.float32)
+    s = np.full_like(x, 448.0)
+    r = (1 / s.astype(np.float64)).astype(np.float32)
+    q = x * r
+    got = _fma32(_fma32(q, -s, x), r, q)
+    assert (got == (x.astype(np.float64) / 448.0).astype(np.float32)).all()
+
+
 # ---- the oracle ----
 @pytest.mark.parametrize("halves", [False, True])
 def test_oracle_rotation_is_a_complex_product(halves):
