@@ -336,7 +336,8 @@ MLA_API mla_status mla_up_project(const void* o_lat, const void* w_uv, void* o_o
  * position out of range is skipped and recorded as an index error (bit 1) in
  * `status` (device, optional, 4-B aligned; read it with mla_read_status).
  * Values must be finite. Strides are in elements and multiples of 8, row
- * starts are 16-B aligned.
+ * starts are 16-B aligned. An output that shares memory with another argument
+ * is refused, but for the cases named below.
  */
 typedef enum { MLA_ROPE_PAIRS = 0, MLA_ROPE_HALVES = 1 } mla_rope_style;
 
@@ -408,7 +409,8 @@ MLA_API mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, i
  * The cheap score:
  *     s[b, i, t] = ks_t * sum_h weights[b, i, h] * max(0, q[b, i, h, :] . k_t)
  * over the visible tokens t of request b (L_b, or L_b - s_q + 1 + i when
- * causal), accumulated in fp32; ks_t is the scale of an e4m3 key, else 1.
+ * causal), accumulated in fp32; ks_t is the scale of an e4m3 key, else 1. A NaN
+ * dot counts as 0 (what stands behind the visible tokens does not matter).
  * q       (device) [batch, s_q, heads, 128] contiguous, 16-B aligned: `q_dtype`
  *         and a 16-bit index cache of the same type, or e4m3 (q_dtype is not
  *         read) with MLA_INDEX_FP8. heads is 1 to 64.
@@ -440,7 +442,8 @@ MLA_API mla_status mla_index_score(const void* q, int q_dtype, const float* weig
  *             the tokens they hold. The last visible page always takes part and
  *             comes last, so (indices, lens) are a block table [batch * s_q,
  *             topk] and the cache_seqlens of a paged decode with one query per
- *             request (batch * s_q requests, s_q = 1).
+ *             request (batch * s_q requests, s_q = 1; a decode takes up to 8192
+ *             requests).
  * A row with no visible token gets -1 everywhere and lens 0. An out-of-range
  * page yields -1 in its place and an index error in `status`.
  */

@@ -68,8 +68,8 @@ def _link_host(obj: str, verbose: bool = False):
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = HOST + ".tmp"
-    _run(["g++", "-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
-          "-lc10_cuda"], "link of _host.so", verbose)
+    _run(["g++", "-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu",
+          "-ltorch_cuda", "-lc10", "-lc10_cuda"], "link of _host.so", verbose)
     os.replace(tmp, HOST)
 
 

@@ -2,6 +2,8 @@
 // and choose what the sparse attention reads: rotary positions, appends to the
 // paged caches, index queries, the index score and the selection
 // (include/mla.h). Every argument check happens before anything is enqueued.
+#include <initializer_list>
+
 #include "host.h"
 #include "index_score.cuh"
 #include "params.h"
@@ -14,7 +16,7 @@ namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
 // Rows of (token, head) from which a thread of the rotation takes four heads of
-// a token, which share its table row ( 256 x 128 rows 2.5 us
+// a token, which share its table row (256 x 128 rows 2.5 us
 // against 2.9 with one, 4095 x 128 22.9 against 29.9; 64 x 128, where one head a
 // thread fills the card better, 2.4 against 1.8).
 constexpr int64_t kManyRows = 32768;
@@ -23,10 +25,24 @@ bool dtype_ok(int dtype) { return dtype == MLA_DTYPE_BF16 || dtype == MLA_DTYPE_
 bool cache_ok(int64_t num_blocks, int page_block) {
   return num_blocks > 0 && page_block == kTile && num_blocks < kMaxRows / kTile;
 }
-// strides in elements that keep 16-byte rows aligned, and `count` of them in
-// the range of addresses
-bool stride_ok(int64_t s, int64_t least, int64_t count) {
-  return s >= least && s % 8 == 0 && s <= (int64_t(1) << 46) / (count > 0 ? count : 1);
+// `count` strides in the range of addresses
+bool in_memory(int64_t stride, int64_t count) { return stride <= (int64_t(1) << 46) / (count > 0 ? count : 1); }
+// strides in elements that keep 16-byte rows aligned
+bool stride_ok(int64_t s, int64_t least, int64_t count) { return s >= least && s % 8 == 0 && in_memory(s, count); }
+// memory of a call: `bytes` from `at` on. An output must not share any with
+// another argument: blocks read what others have already written.
+struct Span {
+  const void* at;
+  int64_t bytes;
+  bool meets(const Span& o) const {
+    const intptr_t a = reinterpret_cast<intptr_t>(at), b = reinterpret_cast<intptr_t>(o.at);
+    return at && o.at && a < b + o.bytes && b < a + bytes;
+  }
+};
+bool apart(const Span& out, std::initializer_list<Span> others) {
+  for (const Span& o : others)
+    if (out.meets(o)) return false;
+  return true;
 }
 // tokens of a row and columns written: room for the kernels' strides in 31 bits
 constexpr int64_t kMaxColumns = kMaxRows - 65536;
@@ -90,6 +106,10 @@ mla_status mla_append_kv(const void* c_kv, int64_t c_stride, const void* k_rope,
                        {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
                        n, static_cast<uint8_t*>(kvcache), num_blocks * kTile};
   if (const mla_status v = check_positions(p.pos)) return v;
+  static constexpr int64_t row_bytes[4] = {kDK * 2, kRowBytesFp8, kRowBytesFp8_528, kRowBytesFp4_288};
+  if (!apart({kvcache, p.num_rows * row_bytes[kv_format]},
+             {{c_kv, 2 * ((n - 1) * c_stride + latent)}, {k_rope, 2 * ((n - 1) * r_stride + rows::kRope)}}))
+    return MLA_ERR_INVALID_ARG;
   const dim3 grid((unsigned)((n + rows::kAppendWarps - 1) / rows::kAppendWarps));
   const int threads = 32 * rows::kAppendWarps;
   if (kv_format == MLA_KV_FP8_656)
@@ -156,6 +176,8 @@ mla_status mla_append_index_k(const void* k, int64_t k_stride, int dtype, const 
                          {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
                          n, 1, 1, 1, static_cast<uint8_t*>(index_cache), nullptr, num_blocks * kTile};
   if (const mla_status v = check_positions(p.pos)) return v;
+  const int64_t page = index_format == MLA_INDEX_FP8 ? rows::kIndexPageFp8 : kTile * 2 * rows::kIndexDim;
+  if (!apart({index_cache, num_blocks * page}, {{k, 2 * ((n - 1) * k_stride + rows::kIndexDim)}})) return MLA_ERR_INVALID_ARG;
   const int per = rows::kIndexGroups;
   const dim3 grid((unsigned)((n + per - 1) / per));
   const bool fp16 = dtype == MLA_DTYPE_FP16;
@@ -182,6 +204,10 @@ mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q
                          {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
                          tokens, heads, heads, 1, q_out, weights_out, 0};
   if (const mla_status v = check_positions(p.pos)) return v;
+  const Span in{q, 2 * ((tokens - 1) * q_token_stride + (heads - 1) * q_head_stride + rows::kIndexDim)},
+      w_in{weights, 4 * tokens * heads}, w_to{weights_out, 4 * tokens * heads}, codes{q_out, rows::kIndexDim * tokens * heads};
+  if (!apart(codes, {in, w_in, w_to}) || in.meets(w_to) || (weights != weights_out && w_in.meets(w_to)))
+    return MLA_ERR_INVALID_ARG;
   // up to eight heads to a lane group, as long as that leaves kFewGroups of them: half the card's lanes. Measured with
   // 64 heads (GB300): 512 tokens 4.0 us (two heads a group), 5.5 with eight; 4096 tokens 20.6 with eight, 24.5 with two
   constexpr int64_t kFewGroups = 16384;
@@ -309,7 +335,8 @@ mla_status mla_index_score(const void* q, int q_dtype, const float* weights, con
     return MLA_ERR_INVALID_ARG;
   if (heads < 1) return MLA_ERR_INVALID_ARG;
   if (heads > 64) return MLA_ERR_UNSUPPORTED;
-  if ((int64_t)batch * s_q >= kMaxRows / heads) return MLA_ERR_INVALID_ARG;
+  if ((int64_t)batch * s_q >= kMaxRows / heads || !in_memory(score_stride, (int64_t)batch * s_q) || !in_memory(max_blocks, batch))
+    return MLA_ERR_INVALID_ARG;
   if (!q || !weights || !index_cache || !block_table || !cache_seqlens || !scores || !aligned(q, 16) ||
       !aligned(weights, 4) || !aligned(index_cache, 16) || !aligned(block_table, 4) || !aligned(cache_seqlens, 4) ||
       !aligned(scores, 4) || (status && !aligned(status, 4)))
@@ -326,6 +353,11 @@ mla_status mla_index_score(const void* q, int q_dtype, const float* weights, con
   p.units = (s_q + p.nq * p.groups - 1) / (p.nq * p.groups);
   const int64_t pairs = (int64_t)batch * p.units * ((cover + score::kTokens - 1) / score::kTokens);
   if (pairs >= kMaxRows) return MLA_ERR_UNSUPPORTED;
+  const int64_t queries = (int64_t)batch * s_q, row_bytes = fp8 ? 128 : 256;
+  if (!apart({scores, 4 * ((queries - 1) * score_stride + width)},
+             {{q, queries * heads * row_bytes}, {weights, 4 * queries * heads}, {block_table, 4 * (int64_t)batch * max_blocks},
+              {cache_seqlens, 4 * (int64_t)batch}, {index_cache, num_blocks * (fp8 ? rows::kIndexPageFp8 : kTile * 256)}}))
+    return MLA_ERR_INVALID_ARG;
   const uint32_t q_bytes = (uint32_t)(p.groups * p.nq * hp) * (fp8 ? 128u : 256u);
   uint32_t ring = (232448u - score::smem_bytes(q_bytes, 0)) / score::kUnit;
   ring = ring > score::kMaxRing ? score::kMaxRing : ring;
@@ -373,7 +405,8 @@ mla_status mla_select_topk(const float* scores, int64_t score_stride, int width,
   if (!cache_ok(num_blocks, page_block) || max_blocks <= 0 || batch <= 0 || s_q <= 0 || width <= 0 || topk <= 0 ||
       score_stride < width || (block != 1 && !pages))
     return MLA_ERR_INVALID_ARG;
-  if ((int64_t)batch * s_q >= kMaxRows) return MLA_ERR_INVALID_ARG;
+  if ((int64_t)batch * s_q >= kMaxRows || !in_memory(score_stride, (int64_t)batch * s_q) || !in_memory(max_blocks, batch))
+    return MLA_ERR_INVALID_ARG;
   const int64_t columns = (int64_t)width * (pages ? kTile : 1), reach = (int64_t)max_blocks * kTile;
   if ((columns < reach ? columns : reach) > kMaxColumns || topk > kMaxColumns) return MLA_ERR_INVALID_ARG;
   if ((int64_t)batch * s_q >= kMaxRows / select::kMaxCluster) return MLA_ERR_UNSUPPORTED;
@@ -381,6 +414,10 @@ mla_status mla_select_topk(const float* scores, int64_t score_stride, int width,
       !aligned(cache_seqlens, 4) || !aligned(block_table, 4) || !aligned(indices, 4) || (lens && !aligned(lens, 4)) ||
       (status && !aligned(status, 4)))
     return MLA_ERR_INVALID_ARG;
+  const int64_t queries = (int64_t)batch * s_q;
+  const Span in{scores, 4 * ((queries - 1) * score_stride + width)}, table{block_table, 4 * (int64_t)batch * max_blocks},
+      lengths{cache_seqlens, 4 * (int64_t)batch}, to{indices, 4 * queries * topk}, held{lens, 4 * queries};
+  if (!apart(to, {in, table, lengths, held}) || !apart(held, {in, table, lengths})) return MLA_ERR_INVALID_ARG;
   select::SelectParams p{scores, score_stride, width, cache_seqlens, block_table, num_blocks, max_blocks,
                          batch, s_q, causal ? 1 : 0, topk, 1, indices, lens, status};
   int dev = 0, sms = 0;

@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -17,6 +17,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <optional>
 
 #include "../../include/mla.h"
 
@@ -172,10 +173,16 @@ int64_t score_stride(const Call& c, const at::Tensor& t, int64_t width) {
   return stride;
 }
 
+// a new tensor, straight from the allocator (a dispatched empty takes twice as long, of the 4 us that a small call with
+// two outputs costs the host)
+at::Tensor fresh(c10::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
+  return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
+
 // an output: the caller's (None: a new one), of a type and shape
 at::Tensor output(Call& c, PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape,
                   const at::Tensor& like) {
-  if (o == Py_None) return at::empty(c10::IntArrayRef(shape), like.options().dtype(type));
+  if (o == Py_None) return fresh(c10::IntArrayRef(shape), type, like);
   const at::Tensor& t = c.tensor(o, name);
   if (t.scalar_type() != type || !is_shape(t, shape) || !t.is_contiguous())
     c.refuse("%s: contiguous %s of the result's shape", name, c10::toString(type));
@@ -226,7 +233,7 @@ PyObject* rotate_q(Call& c, PyObject* const* a) {
   const int64_t tokens = x.size(0), heads = x.size(1);
   if (heads > INT32_MAX) c.refuse("heads out of range");
   c.on_device(x);
-  const at::Tensor out = a[3] == Py_None ? at::empty(x.sizes(), x.options()) : c.tensor(a[3], "out");
+  const at::Tensor out = a[3] == Py_None ? fresh(x.sizes(), x.scalar_type(), x) : c.tensor(a[3], "out");
   if (out.sizes() != x.sizes() || out.scalar_type() != x.scalar_type() || out.stride(2) != 1) c.refuse("out like x");
   c.on_device(out);
   const Rope r(c, a[1], a[2], a[4], tokens);
@@ -309,7 +316,7 @@ PyObject* index_score(Call& c, PyObject* const* a) {
   if (a[5] != Py_None) width = c.integer(a[5], "width", 1);
   else if (given && c.tensor(a[9], "scores").dim()) width = c.tensor(a[9], "scores").size(-1);
   if (width < 1 || width > INT32_MAX) c.refuse("width out of range");
-  const at::Tensor scores = given ? c.tensor(a[9], "scores") : at::empty({batch, s_q, width}, w.options());
+  const at::Tensor scores = given ? c.tensor(a[9], "scores") : fresh({batch, s_q, width}, at::kFloat, w);
   int64_t stride = width;
   if (given) {
     if (scores.scalar_type() != at::kFloat || !is_shape(scores, {batch, s_q, width}))

@@ -16,6 +16,11 @@ ODD = ctypes.c_void_p((1 << 20) + 2)
 FAR = ctypes.c_void_p(1 << 40)
 
 
+def _at(k):
+    """The k-th of fake arrays that lie apart."""
+    return ctypes.c_void_p((k + 2) << 40)
+
+
 @pytest.fixture(scope="module")
 def lib():
     import mla_latent_kv_14_gb300 as m
@@ -32,8 +37,8 @@ def _call(lib, name, base, **kw):
     return getattr(lib, name)(*args.values())
 
 
-APPEND = dict(c=FAKE, cs=576, r=FAKE, rs=576, dtype=0, slots=FAKE, pos=FAKE, table=FAKE, maxp=4096, style=0, n=4,
-              kv=FAKE, blocks=8, page=64, fmt=0, status=None, stream=None)
+APPEND = dict(c=_at(0), cs=576, r=_at(1), rs=576, dtype=0, slots=_at(2), pos=_at(3), table=_at(4), maxp=4096, style=0, n=4,
+              kv=_at(5), blocks=8, page=64, fmt=0, status=None, stream=None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -45,6 +50,7 @@ APPEND = dict(c=FAKE, cs=576, r=FAKE, rs=576, dtype=0, slots=FAKE, pos=FAKE, tab
     (dict(kv=None), 1), (dict(c=ODD), 1), (dict(r=ODD), 1), (dict(kv=ODD), 1), (dict(table=ODD), 1),
     (dict(slots=ODD), 1), (dict(pos=ODD), 1), (dict(status=ODD), 1), (dict(n=0, c=None, kv=None), 0),
     (dict(cs=1 << 50), 1), (dict(rs=1 << 62), 1),                 # beyond any address
+    (dict(c=_at(5)), 1), (dict(r=ctypes.c_void_p((7 << 40) + 8 * 64 * 1152 - 16)), 1),   # in the cache
 ])
 def test_append_kv_argument_checks(lib, kw, code):
     assert _call(lib, "mla_append_kv", APPEND, **kw) == code
@@ -69,7 +75,7 @@ def test_rotate_q_argument_checks(lib, kw, code):
     assert _call(lib, "mla_rotate_q", ROTATE, **kw) == code
 
 
-INDEX_K = dict(k=FAKE, ks=128, dtype=0, slots=FAKE, pos=FAKE, table=FAKE, maxp=4096, style=0, n=4, cache=FAKE,
+INDEX_K = dict(k=_at(0), ks=128, dtype=0, slots=_at(1), pos=_at(2), table=_at(3), maxp=4096, style=0, n=4, cache=_at(4),
                blocks=8, page=64, fmt=0, status=None, stream=None)
 
 
@@ -77,14 +83,14 @@ INDEX_K = dict(k=FAKE, ks=128, dtype=0, slots=FAKE, pos=FAKE, table=FAKE, maxp=4
     (dict(n=-1), 1), (dict(ks=120), 1), (dict(ks=132), 1), (dict(fmt=2), 1), (dict(dtype=2), 1), (dict(page=128), 1),
     (dict(blocks=-1), 1), (dict(style=7), 1), (dict(maxp=-1), 1), (dict(k=ODD), 1), (dict(cache=ODD), 1),
     (dict(k=None), 1), (dict(slots=None), 1), (dict(pos=None), 1), (dict(table=None), 1), (dict(status=ODD), 1),
-    (dict(n=0, k=None), 0),
+    (dict(n=0, k=None), 0), (dict(k=_at(4)), 1),
 ])
 def test_append_index_k_argument_checks(lib, kw, code):
     assert _call(lib, "mla_append_index_k", INDEX_K, **kw) == code
 
 
-INDEX_Q = dict(q=FAKE, qt=64 * 128, qh=128, dtype=0, w=FAKE, pos=FAKE, table=FAKE, maxp=4096, style=0, tokens=4,
-               heads=64, out=FAKE, wout=FAKE, status=None, stream=None)
+INDEX_Q = dict(q=_at(0), qt=64 * 128, qh=128, dtype=0, w=_at(1), pos=_at(2), table=_at(3), maxp=4096, style=0, tokens=4,
+               heads=64, out=_at(4), wout=_at(5), status=None, stream=None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -92,13 +98,14 @@ INDEX_Q = dict(q=FAKE, qt=64 * 128, qh=128, dtype=0, w=FAKE, pos=FAKE, table=FAK
     (dict(dtype=2), 1), (dict(style=2), 1), (dict(q=None), 1), (dict(w=None), 1), (dict(out=None), 1),
     (dict(wout=None), 1), (dict(q=ODD), 1), (dict(out=ODD), 1), (dict(w=ODD), 1), (dict(pos=None), 1),
     (dict(status=ODD), 1), (dict(tokens=0, q=None), 0),
+    (dict(out=_at(0)), 1), (dict(wout=ctypes.c_void_p((3 << 40) + 4)), 1), (dict(out=_at(1)), 1), (dict(wout=_at(0)), 1),
 ])
 def test_quantize_index_q_argument_checks(lib, kw, code):
     assert _call(lib, "mla_quantize_index_q", INDEX_Q, **kw) == code
 
 
-SCORE = dict(q=FAKE, dtype=0, w=FAKE, cache=FAKE, fmt=0, blocks=8, page=64, bt=FAKE, maxb=8, sl=FAKE, batch=2, s_q=1,
-             heads=64, causal=0, block=1, scores=FAKE, stride=512, width=512, status=None, stream=None)
+SCORE = dict(q=_at(0), dtype=0, w=_at(1), cache=_at(2), fmt=0, blocks=8, page=64, bt=_at(3), maxb=8, sl=_at(4), batch=2,
+             s_q=1, heads=64, causal=0, block=1, scores=_at(5), stride=512, width=512, status=None, stream=None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -110,13 +117,15 @@ SCORE = dict(q=FAKE, dtype=0, w=FAKE, cache=FAKE, fmt=0, blocks=8, page=64, bt=F
     (dict(width=(1 << 31) - 1, stride=1 << 31, maxb=1 << 26), 1),
     (dict(width=(1 << 31) - 1, stride=1 << 31), 1),               # columns behind the table's reach
     (dict(batch=1 << 16, width=1 << 24, stride=1 << 24, maxb=1 << 20), 2),   # more tiles than the list counts
+    (dict(scores=_at(0)), 1), (dict(scores=_at(1)), 1), (dict(scores=_at(2)), 1), (dict(scores=_at(3)), 1),
+    (dict(scores=_at(4)), 1), (dict(stride=1 << 60), 1),
 ])
 def test_index_score_argument_checks(lib, kw, code):
     assert _call(lib, "mla_index_score", SCORE, **kw) == code
 
 
-SELECT = dict(scores=FAKE, stride=512, width=512, sl=FAKE, batch=2, s_q=1, causal=0, block=1, topk=64, bt=FAKE,
-              maxb=8, blocks=8, page=64, idx=FAKE, lens=FAKE, status=None, stream=None)
+SELECT = dict(scores=_at(0), stride=512, width=512, sl=_at(1), batch=2, s_q=1, causal=0, block=1, topk=64, bt=_at(2),
+              maxb=8, blocks=8, page=64, idx=_at(3), lens=_at(4), status=None, stream=None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -126,6 +135,7 @@ SELECT = dict(scores=FAKE, stride=512, width=512, sl=FAKE, batch=2, s_q=1, causa
     (dict(lens=ODD), 1), (dict(scores=ODD), 1), (dict(status=ODD), 1), (dict(batch=1 << 16, s_q=1 << 16), 1),
     (dict(topk=(1 << 31) - 1), 1), (dict(width=(1 << 31) - 1, stride=1 << 31, maxb=1 << 26), 1),
     (dict(batch=1 << 14, s_q=1 << 14), 2),                        # rows beyond a launch's blocks
+    (dict(idx=_at(0)), 1), (dict(idx=_at(2)), 1), (dict(lens=_at(1)), 1), (dict(lens=_at(3)), 1), (dict(stride=1 << 60), 1),
 ])
 def test_select_topk_argument_checks(lib, kw, code):
     assert _call(lib, "mla_select_topk", SELECT, **kw) == code
