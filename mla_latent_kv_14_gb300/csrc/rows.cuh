@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kFormat == 0 ? 8 : 6) mla_a
 // Rotation of query rows: a thread turns 8 pairs (32 bytes) of kU heads of one
 // token, four threads per row of 64 dims. The table row stays in registers for
 // the kU heads.
-// Measured (GB300): 64 tokens x 128 heads 1.8 us; 4095 x 128 22.9 us (0.87 of the
+// Measured (GB300): 64 tokens x 128 heads 1.8 us; 4095 x 128 22.3 us (0.89 of the
 // copy bandwidth).
 // ---------------------------------------------------------------------------
 constexpr int kRotateThreads = 256;
@@ -336,10 +336,10 @@ __global__ void __launch_bounds__(kRotateThreads) mla_rotate_kernel(const Rotate
 // [64 + 8l, 64 + 8l + 8) of the other, so that every lane turns four pairs. A
 // lane group takes `steps` query heads of one token, which share the position
 // and the table row, and loads a head ahead.
-// Measured (GB300): 4096 x 64 e4m3 queries 20.6 us (0.74 of the copy bandwidth; 27 with two heads a
-// group, their weight loaded where it is used and the scale divided; 42 with 16
-// lanes a row and a division per value as well): some 200 instructions for 16
-// values of a lane. 32768 keys 4.2 us (0.75).
+// Measured (GB300): 4096 x 64 e4m3 queries 20.6 us (0.74 of the copy bandwidth;
+// 27 with two heads a group, their weight loaded where it is used and the scale
+// divided; 42 with 16 lanes a row and a division per value as well): some 200
+// instructions for 16 values of a lane. 32768 keys 4.2 us (0.75).
 // ---------------------------------------------------------------------------
 constexpr int kIndexThreads = 256;
 constexpr int kIndexLanes = 8;
