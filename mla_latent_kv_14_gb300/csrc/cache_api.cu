@@ -276,33 +276,33 @@ mla_status launch_select(select::SelectParams p, int64_t most, int sms, void* st
   // with 4; 64 rows of 8192: 6.5 with 16, 7.7 with 32). Longer rows go to
   // clusters, of 16 scores per thread while all of them run at once (8 rows of
   // 32768: 9.7 us, 10.8 with 32), else of 32.
-  int keys = 0;
+  int keys = 0, cluster = select::kMaxCluster;
   for (const int k : {4, 16, 32}) {
     const int c = blocks(k);
     const bool holds = (int64_t)c * select::kThreads * k >= most, at_once = rows * c <= 2 * sms;
     if (!holds || (c > 1 && (k == 4 || most <= select::kBlockKeys || (k == 16 && !at_once)))) continue;
     keys = k;
-    p.cluster = c;
+    cluster = c;
     break;
   }
-  if (!keys) p.cluster = select::kMaxCluster;
+  while (1 << p.cluster_log2 < cluster) ++p.cluster_log2;
   auto kernel = keys == 4    ? select::mla_select_topk_kernel<kPages, 4>
                 : keys == 16 ? select::mla_select_topk_kernel<kPages, 16>
                 : keys       ? select::mla_select_topk_kernel<kPages, 32>
                              : select::mla_select_topk_kernel<kPages, 0>;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * p.cluster), 1, 1);
+  cfg.gridDim = dim3((unsigned)(rows * cluster), 1, 1);
   cfg.blockDim = dim3(select::kThreads, 1, 1);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)p.cluster;
+  at[1].val.clusterDim.x = (unsigned)cluster;
   at[1].val.clusterDim.y = 1;
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   MLA_CUDA(cudaLaunchKernelEx(&cfg, kernel, p));
   return MLA_OK;
 }
@@ -419,7 +419,7 @@ mla_status mla_select_topk(const float* scores, int64_t score_stride, int width,
       lengths{cache_seqlens, 4 * (int64_t)batch}, to{indices, 4 * queries * topk}, held{lens, 4 * queries};
   if (!apart(to, {in, table, lengths, held}) || !apart(held, {in, table, lengths})) return MLA_ERR_INVALID_ARG;
   select::SelectParams p{scores, score_stride, width, cache_seqlens, block_table, num_blocks, max_blocks,
-                         batch, s_q, causal ? 1 : 0, topk, 1, indices, lens, status};
+                         batch, s_q, causal ? 1 : 0, topk, 0, indices, lens, status};
   int dev = 0, sms = 0;
   if (const mla_status v = sm_count(&dev, &sms)) return v;
   const int64_t most = pages ? ((columns < reach ? columns : reach) + kTile - 1) / kTile : columns < reach ? columns : reach;

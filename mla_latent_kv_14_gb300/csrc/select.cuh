@@ -8,9 +8,9 @@
 // that may be partly filled) comes last. That page always takes part: it is
 // set apart, and topk - 1 are selected from the others.
 //
-// Measured (GB300): 4 x 1024 rows of up to 16384 scores, topk 2048, 135 us (the
-// read alone 43 us; 64 % of the issue slots and 48 % of the ALU pipe busy); 32
-// rows of 131072 15 us, 64 rows of up to 512 pages 5.5 us: there the steps'
+// Measured (GB300): 4 x 1024 rows of up to 16384 scores, topk 2048, 113 us (the
+// read alone 43 us; 66 % of the issue slots and 53 % of the ALU pipe busy); 32
+// rows of 131072 14 us, 64 rows of up to 512 pages 5.1 us: there the steps'
 // latencies, of 1 to 2 us for a cluster's barriers and remote reads.
 //
 // The floor is one read of the visible scores. A row is therefore loaded once
@@ -25,10 +25,10 @@
 //     steps of value; one fma gives a score's bin. Bins of equal steps spread
 //     the shared memory atomics, where the digits of a radix select do not (its
 //     first histogram has all scores in a few bins, and its atomics queue);
-//  3. sweep: the scores of the bin with the threshold, a handful, are listed
-//     and compared with one another;
-//  4. sweep: each warp's ballots of the selected scores; the columns are written
-//     through shared memory as whole lines.
+//  3. sweep: each lane marks its scores above the bin with the threshold and in
+//     it; the latter, a handful, are listed and compared with one another;
+//  4. the marks, transposed within a warp, are the selected columns in their
+//     order; they are written through shared memory as whole lines.
 // A sample that misled, or a bin of too many equal scores, falls back on a
 // radix select by digits of 11, 11 and 10 bits of the scores' ordered keys.
 #pragma once
@@ -40,8 +40,9 @@
 namespace mla {
 namespace select {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarpsLog2 = 4;
+constexpr int kWarps = 1 << kWarpsLog2;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kBins = 2048;                      // of a digit
 constexpr int kFine = 1024;                      // bins of the bracketed range
 constexpr int kList = 1024;                      // scores of one bin that are compared pairwise
@@ -58,7 +59,7 @@ struct SelectParams {
   const int32_t* block_table;  // [batch, max_blocks]
   int64_t num_blocks;
   int max_blocks, batch, s_q, causal, topk;
-  int cluster;                 // blocks of a row
+  int cluster_log2;            // blocks of a row
   int32_t* indices;            // [batch * s_q, topk]
   int32_t* lens;               // [batch * s_q], or null (tokens only)
   uint32_t* status;            // or null
@@ -85,6 +86,26 @@ MLA_DEV int2 ld_cluster_int2(uint32_t addr) {
   return v;
 }
 
+// adds 1 at a shared memory address if x >= least, as one predicated instruction
+// (an `if` around atomicAdd becomes a branch and a reconvergence in every step)
+MLA_DEV void red_shared_from(float x, float least, uint32_t addr) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], 1;\n\t}" ::"f"(x),
+               "f"(least), "r"(addr)
+               : "memory");
+}
+// bit k of lane l -> bit l of lane k
+MLA_DEV uint32_t warp_transpose(uint32_t x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 16; j; j >>= 1) {
+    const uint32_t low = 0xFFFFFFFFu / ((1u << j) + 1u);  // the lower j bits of every 2 j
+    const bool up = lane & j;
+    const uint32_t keep = up ? ~low : low, y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = (x & keep) | (__funnelshift_l(y, y, up ? 32 - j : j) & ~keep);
+  }
+  return x;
+}
+
 template <int kLanes = 32>
 MLA_DEV int warp_inclusive(int v) {
   const int lane = threadIdx.x & 31;
@@ -98,7 +119,7 @@ MLA_DEV int warp_inclusive(int v) {
 
 // kKeys: scores per thread held in registers; 0: read again in each sweep
 template <bool kPages, int kKeys>
-__global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const SelectParams p) {
   __shared__ __align__(16) int hist[3][kBins];   // digits; then the staged columns
   __shared__ __align__(16) int fine[kFine];
   __shared__ __align__(16) uint32_t list[kList];
@@ -110,8 +131,9 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
   __shared__ __align__(8) int2 warp_count[kWarps];
   __shared__ __align__(8) int2 block_count;      // scores above the threshold, scores equal to it
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
-  const int64_t r = p.cluster > 1 ? blockIdx.x / p.cluster : blockIdx.x;
+  const int cluster = 1 << p.cluster_log2;
+  const int rank = cluster > 1 ? (int)cluster_ctarank() : 0;
+  const uint32_t r = blockIdx.x >> p.cluster_log2;  // below 2^28 (checked on the host)
   for (int c = threadIdx.x; c < kFine / 4; c += kThreads) reinterpret_cast<int4*>(fine)[c] = make_int4(0, 0, 0, 0);
   for (int c = threadIdx.x; c < kList / 4; c += kThreads) reinterpret_cast<int4*>(list)[c] = make_int4(0, 0, 0, 0);
   for (int c = threadIdx.x; c < kBins / 4; c += kThreads) reinterpret_cast<int4*>(hist)[c] = make_int4(0, 0, 0, 0);
@@ -121,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
     bracket[0] = bracket[1] = -1;
   }
   pdl_wait();
-  const int b = (int)(r / p.s_q), i = (int)(r - (int64_t)b * p.s_q);
+  const int b = (int)(r / (uint32_t)p.s_q), i = (int)(r - (uint32_t)b * (uint32_t)p.s_q);
   const int len = __ldg(p.seqlens + b);
   int seen = p.causal ? len - (p.s_q - 1 - i) : len;
   seen = seen < 0 ? 0 : seen;
@@ -137,7 +159,8 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
   const int n = visible - apart, count = chosen_all - apart;
   const bool all = count == n, none = count == 0;
   // each warp owns a contiguous range of whole 32-column steps
-  const int per_warp = ((n + p.cluster * kWarps - 1) / (p.cluster * kWarps) + 31) & ~31;
+  const int ranges_log2 = p.cluster_log2 + kWarpsLog2;
+  const int per_warp = (((n - 1) >> ranges_log2) + 32) & ~31;  // ceil(n / ranges), in whole steps; 0 for none
   const int c0 = min((rank * kWarps + warp) * per_warp, n), c1 = min(c0 + per_warp, n);
   const int steps = (c1 - c0 + 31) >> 5;
   // the block-table entries of what this lane or block may select, on their way
@@ -151,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
   } else if (!kPages && kKeys > 0 && c0 + 32 * lane < c1) {
     lane_page = __ldg(table + (c0 + 32 * lane) / kTile);
   }
-  const float* first_score = p.scores + r * p.stride;
+  const float* first_score = p.scores + (int64_t)r * p.stride;
   const float* row = first_score + c0 + lane;
   const float kNan = __uint_as_float(0x7FFFFFFFu);
   const int mine = c1 - c0 - lane;  // step s is inside for this lane if 32 s < mine
@@ -176,9 +199,10 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
   uint32_t probe[2] = {0u, 0u};
   int samples = 2 * kThreads;
   if (!all && !none) {
-    if (kKeys > 0 && p.cluster == 1) {
+    if (kKeys > 0 && cluster == 1) {
       const int each = min(per_warp, 64);
-      samples = n / per_warp * each + min(n % per_warp, each);
+      const int full = (int)((uint32_t)n / (uint32_t)per_warp);
+      samples = full * each + min(n - full * per_warp, each);
 #pragma unroll
       for (int k = 0; k < 2; ++k) probe[k] = 32 * k < mine ? score_key(held[k % (kKeys > 0 ? kKeys : 1)]) : 0u;
     } else {
@@ -191,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
 
   auto sync_row = [&]() {  // all blocks of the row
     __syncwarp();
-    if (p.cluster > 1) cluster_sync();
+    if (cluster > 1) cluster_sync();
     else __syncthreads();
   };
   // exclusive prefix of v over the block's threads
@@ -210,14 +234,14 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
     int v[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) v[k] = 0;
-    if (p.cluster > 1) {
+    if (cluster > 1) {
       const uint32_t addr = smem_u32(h + top);
       int2 part[kMaxCluster][kPer / 2];
 #pragma unroll
       for (int q = 0; q < kMaxCluster; ++q)
 #pragma unroll
         for (int k = 0; k < kPer / 2; ++k)
-          part[q][k] = q < p.cluster ? ld_cluster_int2(mapa(addr + 8 * k, q)) : make_int2(0, 0);
+          part[q][k] = q < cluster ? ld_cluster_int2(mapa(addr + 8 * k, q)) : make_int2(0, 0);
 #pragma unroll
       for (int q = 0; q < kMaxCluster; ++q)
 #pragma unroll
@@ -251,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
   uint32_t threshold = 0;  // a key
   int ties = 0;
   bool by_value = false;   // found by value: no NaN and no padding is selected or tied
+  uint32_t above_marks = 0, in_marks = 0, lane_key = 0;  // held scores above the threshold's bin, in it; the last of those
   if (!all && !none) {
     // 1. the sample's histogram by the top digit of the keys
 #pragma unroll
@@ -261,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
       // Around the threshold's share of the sample: a quarter more and a few at
       // the lower end, about four standard deviations of that share at any
       // topk; half of it and a few fewer at the upper end.
-      const int share = (int)((int64_t)count * samples / n);
+      const int share = (int)(__fdividef((float)count, (float)n) * (float)samples);
       const int most = min(share + share / 4 + 8, samples), least = max(share / 2 - 8, 1);
       const int top = 4 * (kThreads - 1 - (int)threadIdx.x);
       const int4 h4 = *reinterpret_cast<const int4*>(hist[0] + top);
@@ -289,10 +314,11 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
     if (usable) {
       constexpr float kLast = kBase + (kFine - 1);
       // 2. the bins
+      const uint32_t fine_at = smem_u32(fine) - 4u * __float_as_uint(kBase);
       sweep([&](float x, int s) {
         (void)s;
         const float f = fmaf(x, scale, bias);
-        if (f >= kBase) atomicAdd(&fine[__float_as_uint(fminf(f, kLast)) - __float_as_uint(kBase)], 1);
+        red_shared_from(f, kBase, fine_at + 4u * __float_as_uint(fminf(f, kLast)));
       });
     }
     sync_row();
@@ -301,36 +327,44 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
     if (usable && bin >= 0 && bin < kFine - 1 && size <= kList) {
       // 3. the bin's scores, compared pairwise
       const float in_bin = kBase + (float)bin;
-      uint32_t* to = p.cluster > 1 ? own_list : list;
-      for (int s0 = 0; s0 < steps; s0 += 32) {  // one round where the scores are held
-        // few lanes have one: marked without a branch per step, then read again
-        uint32_t marks = 0;
-        if (kKeys > 0) {
-          sweep([&](float x, int s) { marks |= fmaf(x, scale, bias) == in_bin ? 1u << s : 0u; });
-        } else {
-#pragma unroll 4
-          for (int s = s0; s < min(s0 + 32, steps); ++s)
-            marks |= fmaf(score_at(s), scale, bias) == in_bin ? 1u << (s - s0) : 0u;
-        }
+      uint32_t* to = cluster > 1 ? own_list : list;
+      if (kKeys > 0) {
+        // bit s: the lane's score of step s lies above the bin, or in it
+        uint32_t from = 0;
+        sweep([&](float x, int s) {
+          const float f = fmaf(x, scale, bias);
+          from |= f >= in_bin ? 1u << s : 0u;
+          in_marks |= f == in_bin ? 1u << s : 0u;
+        });
+        above_marks = from & ~in_marks;
+        // few lanes have one in the bin: taken from the registers where that is no loop, else read again
         if (kKeys == 4) {
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            if (marks >> s & 1u) to[atomicAdd(&list_count, 1)] = score_key(held[s % (kKeys > 0 ? kKeys : 1)]);
+            if (in_marks >> s & 1u) to[atomicAdd(&list_count, 1)] = score_key(held[s % (kKeys > 0 ? kKeys : 1)]);
         } else {
-          while (marks) {
-            const int s = s0 + __ffs(marks) - 1;
-            marks &= marks - 1u;
-            to[atomicAdd(&list_count, 1)] = score_key(__ldg(row + 32 * s));
+          for (uint32_t marks = in_marks; marks; marks &= marks - 1u) {
+            lane_key = score_key(__ldg(row + 32 * (__ffs(marks) - 1)));
+            to[atomicAdd(&list_count, 1)] = lane_key;
           }
+        }
+      } else {
+        for (int s0 = 0; s0 < steps; s0 += 32) {
+          uint32_t marks = 0;
+#pragma unroll 4
+          for (int s = s0; s < min(s0 + 32, steps); ++s)
+            marks |= fmaf(score_at(s), scale, bias) == in_bin ? 1u << (s - s0) : 0u;
+          for (; marks; marks &= marks - 1u)
+            to[atomicAdd(&list_count, 1)] = score_key(__ldg(row + 32 * (s0 + __ffs(marks) - 1)));
         }
       }
       sync_row();
-      if (p.cluster > 1) {
+      if (cluster > 1) {
         // warp q copies block q's share behind those of the blocks before it
-        const int m = lane < p.cluster ? (int)ld_cluster_u32(mapa(smem_u32(&list_count), lane)) : 0;
+        const int m = lane < cluster ? (int)ld_cluster_u32(mapa(smem_u32(&list_count), lane)) : 0;
         const int upto = warp_inclusive(m), own = __shfl_sync(0xffffffffu, m, warp & 7);
         const int before = __shfl_sync(0xffffffffu, upto, warp & 7) - own;
-        if (warp < p.cluster)
+        if (warp < cluster)
           for (int k = lane; k < own; k += 32) list[before + k] = ld_cluster_u32(mapa(smem_u32(own_list + k), warp));
         __syncthreads();
       }
@@ -387,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
   // ---- compaction in ascending position ----
   // A step's ballots are the bits of 32 consecutive columns; lane l keeps those
   // of step l (and, where the scores are read again, l + 32, ... in later rounds).
-  int32_t* out = p.indices + r * p.topk;
+  int32_t* out = p.indices + (int64_t)r * p.topk;
   int* stage = &hist[0][0];
   // the columns first + (set bits), to dst[at ...]
   auto emit = [&](uint32_t bits, int first, int32_t* dst, int at) {
@@ -444,7 +478,36 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
     };
     int gt = 0, eq = 0;  // selected and tied columns of this lane's
     if (kKeys > 0) {
-      vote(sweep);
+      if (by_value) {
+        // the bin's own scores against the threshold
+        uint32_t equal_marks = 0;
+        const bool single = (in_marks & (in_marks - 1u)) == 0;
+        auto place = [&](uint32_t key, uint32_t bit) {
+          if (key > threshold || (key == threshold && ties < 0)) above_marks |= bit;
+          else if (key == threshold) equal_marks |= bit;
+        };
+        if (kKeys == 4) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            if (in_marks >> s & 1u) place(score_key(held[s % (kKeys > 0 ? kKeys : 1)]), 1u << s);
+        } else {
+          for (uint32_t marks = in_marks; marks; marks &= marks - 1u)
+            place(single ? lane_key : score_key(__ldg(row + 32 * (__ffs(marks) - 1))), marks & (0u - marks));
+        }
+        if (kKeys == 4) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t g = __ballot_sync(0xffffffffu, above_marks >> s & 1u), q = __ballot_sync(0xffffffffu, equal_marks >> s & 1u);
+            m_gt = lane == s ? g : m_gt;
+            m_eq = lane == s ? q : m_eq;
+          }
+        } else {
+          m_gt = warp_transpose(above_marks);
+          if (ties >= 0) m_eq = warp_transpose(equal_marks);
+        }
+      } else {
+        vote(sweep);
+      }
       gt = __popc(m_gt);
       eq = __popc(m_eq);
     } else {
@@ -467,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
     gt_before += __shfl_sync(0xffffffffu, upto_gt - per.x, warp);
     if (equal) eq_before += __shfl_sync(0xffffffffu, upto_eq - per.y, warp);
     int2 ahead = make_int2(0, 0);  // in the blocks before this one
-    if (p.cluster > 1) {
+    if (cluster > 1) {
       if (threadIdx.x == 0) block_count = block;
       sync_row();
       const int2 c = lane < rank ? ld_cluster_int2(mapa(smem_u32(&block_count), lane)) : make_int2(0, 0);
@@ -523,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, kKeys == 16 ? 3 : 2) mla_select_topk
       p.lens[r] = !kPages ? chosen_all : chosen_all > 0 ? (chosen_all - 1) * kTile + seen - (visible - 1) * kTile : 0;
   }
   __syncwarp();
-  if (p.cluster > 1) cluster_sync();  // no block leaves while another reads its shared memory
+  if (cluster > 1) cluster_sync();  // no block leaves while another reads its shared memory
 }
 
 }  // namespace select
