@@ -263,12 +263,15 @@ mla_status launch_score(int dev, int grid, uint32_t smem, void* stream, const CU
   return MLA_OK;
 }
 // `most`: columns of the longest possible row
+constexpr int64_t kManySelections = 304;
+
 template <bool kPages>
 mla_status launch_select(select::SelectParams p, int64_t most, int sms, void* stream) {
   const int64_t rows = (int64_t)p.batch * p.s_q;
+  constexpr int kWide = 32 * select::kMaxWarps;
   auto blocks = [&](int keys) {  // of a row, at `keys` scores per thread
     int c = 1;
-    while (c < select::kMaxCluster && (int64_t)c * select::kThreads * keys < most) c *= 2;
+    while (c < select::kMaxCluster && (int64_t)c * kWide * keys < most) c *= 2;
     return c;
   };
   // One block a row where it holds the row, with the fewest scores per thread
@@ -279,20 +282,30 @@ mla_status launch_select(select::SelectParams p, int64_t most, int sms, void* st
   int keys = 0, cluster = select::kMaxCluster;
   for (const int k : {4, 16, 32}) {
     const int c = blocks(k);
-    const bool holds = (int64_t)c * select::kThreads * k >= most, at_once = rows * c <= 2 * sms;
+    const bool holds = (int64_t)c * kWide * k >= most, at_once = rows * c <= 2 * sms;
     if (!holds || (c > 1 && (k == 4 || most <= select::kBlockKeys || (k == 16 && !at_once)))) continue;
     keys = k;
     cluster = c;
     break;
   }
   while (1 << p.cluster_log2 < cluster) ++p.cluster_log2;
-  auto kernel = keys == 4    ? select::mla_select_topk_kernel<kPages, 4>
-                : keys == 16 ? select::mla_select_topk_kernel<kPages, 16>
-                : keys       ? select::mla_select_topk_kernel<kPages, 32>
-                             : select::mla_select_topk_kernel<kPages, 0>;
+  // Many short rows: fewer warps with more scores each, since a warp's fixed
+  // part (scans, brackets, barriers) outweighs its sweeps
+  int threads = kWide;
+  const bool many = rows > kManySelections && most <= select::kBlockKeys / 2;
+  auto kernel = keys == 4    ? select::mla_select_topk_kernel<kPages, 4, 16>
+                : keys == 16 ? select::mla_select_topk_kernel<kPages, 16, 16>
+                : keys       ? select::mla_select_topk_kernel<kPages, 32, 16>
+                             : select::mla_select_topk_kernel<kPages, 0, 16>;
+  if (many) {
+    threads = most <= 4096 ? 128 : 256;
+    kernel = most <= 2048   ? select::mla_select_topk_kernel<kPages, 16, 4>
+             : most <= 4096 ? select::mla_select_topk_kernel<kPages, 32, 4>
+                            : select::mla_select_topk_kernel<kPages, 32, 8>;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * cluster), 1, 1);
-  cfg.blockDim = dim3(select::kThreads, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

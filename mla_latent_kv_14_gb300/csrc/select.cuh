@@ -40,15 +40,11 @@
 namespace mla {
 namespace select {
 
-constexpr int kWarpsLog2 = 4;
-constexpr int kWarps = 1 << kWarpsLog2;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxWarps = 16;                    // of a block
 constexpr int kBins = 2048;                      // of a digit
-constexpr int kFine = 1024;                      // bins of the bracketed range
-constexpr int kList = 1024;                      // scores of one bin that are compared pairwise
 constexpr int kStage = 3 * kBins;                // columns written through shared memory
 constexpr int kMaxKeys = 32;                     // scores per thread
-constexpr int kBlockKeys = kThreads * kMaxKeys;  // scores that one block holds
+constexpr int kBlockKeys = 32 * kMaxWarps * kMaxKeys;  // scores that one block holds
 constexpr int kMaxCluster = 8;
 
 struct SelectParams {
@@ -118,12 +114,18 @@ MLA_DEV int warp_inclusive(int v) {
 }
 
 // kKeys: scores per thread held in registers; 0: read again in each sweep
-template <bool kPages, int kKeys>
-__global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const SelectParams p) {
+// kWarps: of a block; clusters have 16
+template <bool kPages, int kKeys, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) mla_select_topk_kernel(const SelectParams p) {
+  constexpr int kThreads = 32 * kWarps, kWarpsLog2 = kWarps == 16 ? 4 : kWarps == 8 ? 3 : 2;
+  static_assert(kWarps == 1 << kWarpsLog2, "");
+  constexpr int kFine = 2 * kThreads;  // bins of the bracketed range
+  constexpr int kList = 2 * kThreads;  // scores of one bin that are compared pairwise
+  constexpr bool kClusters = kWarps == kMaxWarps && (kKeys == 0 || kKeys >= 16);
   __shared__ __align__(16) int hist[3][kBins];   // digits; then the staged columns
   __shared__ __align__(16) int fine[kFine];
   __shared__ __align__(16) uint32_t list[kList];
-  __shared__ uint32_t own_list[kList];           // this block's share of it (of a cluster)
+  __shared__ uint32_t own_list[kClusters ? kList : 1];  // this block's share of it (of a cluster)
   __shared__ int warp_sum[kWarps];
   __shared__ int found[3];                       // bin, how many of it are selected, its size
   __shared__ int list_count;
@@ -131,9 +133,9 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
   __shared__ __align__(8) int2 warp_count[kWarps];
   __shared__ __align__(8) int2 block_count;      // scores above the threshold, scores equal to it
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cluster = 1 << p.cluster_log2;
+  const int cluster_log2 = kClusters ? p.cluster_log2 : 0, cluster = 1 << cluster_log2;
   const int rank = cluster > 1 ? (int)cluster_ctarank() : 0;
-  const uint32_t r = blockIdx.x >> p.cluster_log2;  // below 2^28 (checked on the host)
+  const uint32_t r = blockIdx.x >> cluster_log2;  // below 2^28 (checked on the host)
   for (int c = threadIdx.x; c < kFine / 4; c += kThreads) reinterpret_cast<int4*>(fine)[c] = make_int4(0, 0, 0, 0);
   for (int c = threadIdx.x; c < kList / 4; c += kThreads) reinterpret_cast<int4*>(list)[c] = make_int4(0, 0, 0, 0);
   for (int c = threadIdx.x; c < kBins / 4; c += kThreads) reinterpret_cast<int4*>(hist)[c] = make_int4(0, 0, 0, 0);
@@ -159,15 +161,15 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
   const int n = visible - apart, count = chosen_all - apart;
   const bool all = count == n, none = count == 0;
   // each warp owns a contiguous range of whole 32-column steps
-  const int ranges_log2 = p.cluster_log2 + kWarpsLog2;
+  const int ranges_log2 = cluster_log2 + kWarpsLog2;
   const int per_warp = (((n - 1) >> ranges_log2) + 32) & ~31;  // ceil(n / ranges), in whole steps; 0 for none
   const int c0 = min((rank * kWarps + warp) * per_warp, n), c1 = min(c0 + per_warp, n);
   const int steps = (c1 - c0 + 31) >> 5;
   // the block-table entries of what this lane or block may select, on their way
   // before they are needed: the page of the lane's 32 columns, or all pages
   const int32_t* table = p.block_table + (int64_t)b * p.max_blocks;
-  constexpr bool kPagesHere = kPages && kKeys == 4;  // one block of up to 2048 pages
-  __shared__ int page_ids[kPagesHere ? kThreads * 4 : 1];
+  constexpr bool kPagesHere = kPages && kKeys > 0 && kThreads * kKeys <= 2048;  // one block of up to 2048 pages
+  __shared__ int page_ids[kPagesHere ? kThreads * kKeys : 1];
   int lane_page = 0;
   if (kPagesHere) {
     for (int c = threadIdx.x; c < n; c += kThreads) page_ids[c] = __ldg(table + c);
@@ -194,17 +196,18 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
       for (int s = 0; s < steps; ++s) f(score_at(s), s);
     }
   };
-  // The sample: the first 64 scores of each warp's range where the block has
-  // the whole row, else scores spread over the row, the same for every block.
+  // The sample: 32 scores from the start and 32 from the middle of each warp's
+  // range where the block has the whole row, else scores spread over the row,
+  // the same for every block.
   uint32_t probe[2] = {0u, 0u};
   int samples = 2 * kThreads;
   if (!all && !none) {
     if (kKeys > 0 && cluster == 1) {
-      const int each = min(per_warp, 64);
-      const int full = (int)((uint32_t)n / (uint32_t)per_warp);
-      samples = full * each + min(n - full * per_warp, each);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) probe[k] = 32 * k < mine ? score_key(held[k % (kKeys > 0 ? kKeys : 1)]) : 0u;
+      const int middle = per_warp >> 6 << 5;  // 0: a range of one step
+      if (middle > 0 && middle < mine) probe[1] = score_key(__ldg(row + middle));
+      if (0 < mine) probe[0] = score_key(held[0]);
+      const int full = (int)((uint32_t)n / (uint32_t)per_warp), rest = n - full * per_warp;
+      samples = full * (middle > 0 ? 64 : 32) + min(rest, 32) + (middle > 0 ? min(max(rest - middle, 0), 32) : 0);
     } else {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
     int v[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) v[k] = 0;
-    if (cluster > 1) {
+    if (kClusters && cluster > 1) {
       const uint32_t addr = smem_u32(h + top);
       int2 part[kMaxCluster][kPer / 2];
 #pragma unroll
@@ -288,14 +291,22 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
       // topk; half of it and a few fewer at the upper end.
       const int share = (int)(__fdividef((float)count, (float)n) * (float)samples);
       const int most = min(share + share / 4 + 8, samples), least = max(share / 2 - 8, 1);
-      const int top = 4 * (kThreads - 1 - (int)threadIdx.x);
-      const int4 h4 = *reinterpret_cast<const int4*>(hist[0] + top);
-      const int v[4] = {h4.x, h4.y, h4.z, h4.w};
-      const int sum = v[0] + v[1] + v[2] + v[3];
+      constexpr int kPer = kBins / kThreads;
+      const int top = kPer * (kThreads - 1 - (int)threadIdx.x);
+      int v[kPer], sum = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; k += 4) {
+        const int4 h4 = *reinterpret_cast<const int4*>(hist[0] + top + k);
+        v[k] = h4.x;
+        v[k + 1] = h4.y;
+        v[k + 2] = h4.z;
+        v[k + 3] = h4.w;
+        sum += h4.x + h4.y + h4.z + h4.w;
+      }
       int above = before_in_block(sum);
       if (sum > 0) {
 #pragma unroll
-        for (int k = 3; k >= 0; --k) {
+        for (int k = kPer - 1; k >= 0; --k) {
           if (above < most && most <= above + v[k]) bracket[0] = top + k;
           if (above < least && least <= above + v[k]) bracket[1] = top + k;
           above += v[k];
@@ -327,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_select_topk_kernel(const Sele
     if (usable && bin >= 0 && bin < kFine - 1 && size <= kList) {
       // 3. the bin's scores, compared pairwise
       const float in_bin = kBase + (float)bin;
-      uint32_t* to = cluster > 1 ? own_list : list;
+      uint32_t* to = kClusters && cluster > 1 ? own_list : list;
       if (kKeys > 0) {
         // bit s: the lane's score of step s lies above the bin, or in it
         uint32_t from = 0;

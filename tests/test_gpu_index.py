@@ -457,6 +457,39 @@ def test_select_bad_pages_and_hidden_columns():
     _select_both(s[..., :100].contiguous(), lens, 1, False, 1, 20, np.abs(bt) % 8, 8, bits=1)   # fewer columns than tokens
 
 
+@pytest.mark.parametrize("kind", ["normal", "ties", "special", "smooth", "low starts"])
+@pytest.mark.parametrize("n", [100, 2000, 2049, 4096, 5001, 8192])
+def test_select_many_rows(n, kind):
+    """Enough rows that each gets a narrow block; lengths down to one and none."""
+    rng = np.random.default_rng(n)
+    lens, s_q = [n, n - 1, n // 2 + 3, 70, 1, 0], 80
+    most = -(-n // PAGE)
+    bt = rng.permutation(6 * most).reshape(6, most).astype(np.int32)
+    s = torch.randn(6, s_q, n, generator=_gen(n))
+    if kind == "ties":
+        s = (s * 4).round() / 4
+    elif kind == "special":
+        r = torch.rand(s.shape, generator=_gen(1))
+        s[r < 0.2], s[r < 0.1], s[r < 0.03] = float("nan"), float("-inf"), float("inf")
+    elif kind == "smooth":
+        s = torch.sin(torch.arange(n) * (9.0 / n)).expand(6, s_q, n) + s * 1e-3
+    elif kind == "low starts":
+        s[..., (torch.arange(n) % 256) < 64] -= 1e4
+    for topk in (1, min(512, n // 3), n - 2):
+        _select_both(s, lens, s_q, True, 1, topk, bt, 6 * most)
+    pages = s[..., :most].contiguous()
+    _select_both(pages, lens, s_q, True, 64, max(1, most // 3), bt, 6 * most)
+
+
+@pytest.mark.parametrize("topk", [3, 200, 1500])
+def test_select_pages_of_many_long_rows(topk):
+    lens, s_q = [64 * 2100, 64 * 4100 + 5, 64 * 1000], 120
+    most = 4101
+    bt = np.random.default_rng(topk).permutation(3 * most).reshape(3, most).astype(np.int32)
+    s = torch.randn(3, s_q, most, generator=_gen(topk))
+    _select_both(s, lens, s_q, True, 64, topk, bt, 3 * most)
+
+
 @pytest.mark.parametrize("n", [5000, 40000, 131072, 300001])
 def test_select_long_rows(n):
     rng = np.random.default_rng(n)
