@@ -263,8 +263,6 @@ mla_status launch_score(int dev, int grid, uint32_t smem, void* stream, const CU
   return MLA_OK;
 }
 // `most`: columns of the longest possible row
-constexpr int64_t kManySelections = 304;
-
 template <bool kPages>
 mla_status launch_select(select::SelectParams p, int64_t most, int sms, void* stream) {
   const int64_t rows = (int64_t)p.batch * p.s_q;
@@ -289,10 +287,13 @@ mla_status launch_select(select::SelectParams p, int64_t most, int sms, void* st
     break;
   }
   while (1 << p.cluster_log2 < cluster) ++p.cluster_log2;
-  // Many short rows: fewer warps with more scores each, since a warp's fixed
-  // part (scans, brackets, barriers) outweighs its sweeps
+  // More rows than SMs: narrow blocks with more scores per thread, since a warp's
+  // scans, barriers and start cost as much as its sweeps (4096 rows of up to 2048
+  // scores, topk an eighth: 25 us, 65 in wide blocks; of 8192: 54, 88; 256 rows of
+  // 2048 4.6, 5.2, but 128 rows 4.3, 4.2). Rows beyond 8192 stay wide: 64 scores a
+  // thread halve the warps in flight (16384: 121 us, 113).
   int threads = kWide;
-  const bool many = rows > kManySelections && most <= select::kBlockKeys / 2;
+  const bool many = rows > sms && most <= select::kBlockKeys / 2;
   auto kernel = keys == 4    ? select::mla_select_topk_kernel<kPages, 4, 16>
                 : keys == 16 ? select::mla_select_topk_kernel<kPages, 16, 16>
                 : keys       ? select::mla_select_topk_kernel<kPages, 32, 16>

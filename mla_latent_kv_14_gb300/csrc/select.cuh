@@ -8,9 +8,9 @@
 // that may be partly filled) comes last. That page always takes part: it is
 // set apart, and topk - 1 are selected from the others.
 //
-// Measured (GB300): 4 x 1024 rows of up to 16384 scores, topk 2048, 113 us (the
-// read alone 43 us; 66 % of the issue slots and 53 % of the ALU pipe busy); 32
-// rows of 131072 14 us, 64 rows of up to 512 pages 5.1 us: there the steps'
+// Measured (GB300): 4 x 1024 rows of up to 16384 scores, topk 2048, 110 us (the
+// read alone 43 us; 61 % of the issue slots busy), of up to 8192 57, 2048 27; 32
+// rows of 131072 13.3 us, 64 rows of up to 512 pages 4.9 us: there the steps'
 // latencies, of 1 to 2 us for a cluster's barriers and remote reads.
 //
 // The floor is one read of the visible scores. A row is therefore loaded once
@@ -20,11 +20,14 @@
 // Beyond the read, the sweeps over the held scores bound the kernel (the ALU
 // pipe), so they are few and short, without branches or range tests (the
 // padding behind a row is NaN, which fails every comparison):
-//  1. a sample of 1024 scores brackets the threshold between two values;
-//  2. sweep: the scores from the lower value on are counted in 1024 bins, equal
-//     steps of value; one fma gives a score's bin. Bins of equal steps spread
-//     the shared memory atomics, where the digits of a radix select do not (its
-//     first histogram has all scores in a few bins, and its atomics queue);
+//  1. a sample of two scores a thread brackets the threshold between two values;
+//  2. sweep: the scores from the lower value on are counted in bins, equal steps
+//     of value (two a thread); one fma gives a score's bin. Bins of equal steps
+//     spread the shared memory atomics, where the digits of a radix select do
+//     not (its first histogram has all scores in a few bins, and its atomics
+//     queue). Scores below count in a bin of their lane's own: a condition on
+//     the atomic is a branch and a reconvergence in every step (110 us for the
+//     first case above, 113 with it; a loop over marked scores alone: 137);
 //  3. sweep: each lane marks its scores above the bin with the threshold and in
 //     it; the latter, a handful, are listed and compared with one another;
 //  4. the marks, transposed within a warp, are the selected columns in their
@@ -82,12 +85,9 @@ MLA_DEV int2 ld_cluster_int2(uint32_t addr) {
   return v;
 }
 
-// adds 1 at a shared memory address if x >= least, as one predicated instruction
-// (an `if` around atomicAdd becomes a branch and a reconvergence in every step)
-MLA_DEV void red_shared_from(float x, float least, uint32_t addr) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], 1;\n\t}" ::"f"(x),
-               "f"(least), "r"(addr)
-               : "memory");
+// adds 1 at a shared memory address
+MLA_DEV void red_shared(uint32_t addr) {
+  asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(addr) : "memory");
 }
 // bit k of lane l -> bit l of lane k
 MLA_DEV uint32_t warp_transpose(uint32_t x) {
@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) mla_select_topk_kern
   constexpr int kList = 2 * kThreads;  // scores of one bin that are compared pairwise
   constexpr bool kClusters = kWarps == kMaxWarps && (kKeys == 0 || kKeys >= 16);
   __shared__ __align__(16) int hist[3][kBins];   // digits; then the staged columns
-  __shared__ __align__(16) int fine[kFine];
+  __shared__ __align__(16) int fine_all[32 + kFine];  // a bin for each lane's scores below the bracket, then the bins
+  int* fine = fine_all + 32;
   __shared__ __align__(16) uint32_t list[kList];
   __shared__ uint32_t own_list[kClusters ? kList : 1];  // this block's share of it (of a cluster)
   __shared__ int warp_sum[kWarps];
@@ -326,10 +327,11 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) mla_select_topk_kern
       constexpr float kLast = kBase + (kFine - 1);
       // 2. the bins
       const uint32_t fine_at = smem_u32(fine) - 4u * __float_as_uint(kBase);
+      const float kBelow = kBase - 32.0f + (float)lane;
       sweep([&](float x, int s) {
         (void)s;
-        const float f = fmaf(x, scale, bias);
-        red_shared_from(f, kBase, fine_at + 4u * __float_as_uint(fminf(f, kLast)));
+        const float f = fminf(fmaxf(fmaf(x, scale, bias), kBelow), kLast);  // NaN: below
+        red_shared(fine_at + 4u * __float_as_uint(f));
       });
     }
     sync_row();
