@@ -273,10 +273,10 @@ mla_status launch_select(select::SelectParams p, int64_t most, int sms, void* st
     return c;
   };
   // One block a row where it holds the row, with the fewest scores per thread
-  // (32 rows of 12288: 7.8 us with 32 scores a thread, 10.4 in clusters of 8
-  // with 4; 64 rows of 8192: 6.5 with 16, 7.7 with 32). Longer rows go to
+  // (32 rows of 12288: 5.5 us in one block, 7.2 in clusters of 2 with 16 scores a
+  // thread; 64 rows of 8192: 4.8 with 16, 5.7 with 32). Longer rows go to
   // clusters, of 16 scores per thread while all of them run at once (8 rows of
-  // 32768: 9.7 us, 10.8 with 32), else of 32.
+  // 32768: 8.0 us, 8.8 with 32), else of 32.
   int keys = 0, cluster = select::kMaxCluster;
   for (const int k : {4, 16, 32}) {
     const int c = blocks(k);
