@@ -8,9 +8,9 @@
 // that may be partly filled) comes last. That page always takes part: it is
 // set apart, and topk - 1 are selected from the others.
 //
-// Measured (GB300): 4 x 1024 rows of up to 16384 scores, topk 2048, 110 us (the
-// read alone 43 us; 61 % of the issue slots busy), of up to 8192 57, 2048 27; 32
-// rows of 131072 13.3 us, 64 rows of up to 512 pages 4.9 us: there the steps'
+// Measured (GB300): 4 x 1024 rows of up to 16384 scores, topk 2048, 106 us (the
+// read alone 43 us; 62 % of the issue slots busy), of up to 8192 57, 2048 27; 32
+// rows of 131072 13.2 us, 64 rows of up to 512 pages 4.9 us: there the steps'
 // latencies, of 1 to 2 us for a cluster's barriers and remote reads.
 //
 // The floor is one read of the visible scores. A row is therefore loaded once
@@ -25,8 +25,8 @@
 //     of value (two a thread); one fma gives a score's bin. Bins of equal steps
 //     spread the shared memory atomics, where the digits of a radix select do
 //     not (its first histogram has all scores in a few bins, and its atomics
-//     queue). Scores below count in a bin of their lane's own: a condition on
-//     the atomic is a branch and a reconvergence in every step (110 us for the
+//     queue). Scores below count in bins that are not read: a condition on
+//     the atomic is a branch and a reconvergence in every step (106 us for the
 //     first case above, 113 with it; a loop over marked scores alone: 137);
 //  3. sweep: each lane marks its scores above the bin with the threshold and in
 //     it; the latter, a handful, are listed and compared with one another;
@@ -120,11 +120,12 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) mla_select_topk_kern
   constexpr int kThreads = 32 * kWarps, kWarpsLog2 = kWarps == 16 ? 4 : kWarps == 8 ? 3 : 2;
   static_assert(kWarps == 1 << kWarpsLog2, "");
   constexpr int kFine = 2 * kThreads;  // bins of the bracketed range
+  constexpr int kBelow = 32;           // counters before the first bin
   constexpr int kList = 2 * kThreads;  // scores of one bin that are compared pairwise
   constexpr bool kClusters = kWarps == kMaxWarps && (kKeys == 0 || kKeys >= 16);
   __shared__ __align__(16) int hist[3][kBins];   // digits; then the staged columns
-  __shared__ __align__(16) int fine_all[32 + kFine];  // a bin for each lane's scores below the bracket, then the bins
-  int* fine = fine_all + 32;
+  __shared__ __align__(16) int fine_all[kBelow + kFine];  // counts of scores below the bracket, then the bins
+  int* fine = fine_all + kBelow;
   __shared__ __align__(16) uint32_t list[kList];
   __shared__ uint32_t own_list[kClusters ? kList : 1];  // this block's share of it (of a cluster)
   __shared__ int warp_sum[kWarps];
@@ -327,10 +328,12 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) mla_select_topk_kern
       constexpr float kLast = kBase + (kFine - 1);
       // 2. the bins
       const uint32_t fine_at = smem_u32(fine) - 4u * __float_as_uint(kBase);
-      const float kBelow = kBase - 32.0f + (float)lane;
+      // below 2^23 fp32 steps by halves: lane l's scores there count from bin l - 32 on, in -1 at most
+      static_assert(__builtin_bit_cast(uint32_t, kBase) - __builtin_bit_cast(uint32_t, kBase - 0.5f * kBelow) == kBelow, "");
+      const float least = kBase - 0.5f * (float)(kBelow - lane);
       sweep([&](float x, int s) {
         (void)s;
-        const float f = fminf(fmaxf(fmaf(x, scale, bias), kBelow), kLast);  // NaN: below
+        const float f = fminf(fmaxf(fmaf(x, scale, bias), least), kLast);  // NaN: least
         red_shared(fine_at + 4u * __float_as_uint(f));
       });
     }
