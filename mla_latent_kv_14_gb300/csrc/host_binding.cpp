@@ -173,8 +173,8 @@ int64_t score_stride(const Call& c, const at::Tensor& t, int64_t width) {
   return stride;
 }
 
-// a new tensor, straight from the allocator (a dispatched empty takes twice as long, of the 4 us that a small call with
-// two outputs costs the host)
+// a new tensor, straight from the allocator (0.2 us less than a dispatched empty, where a call with two outputs takes
+// the host 3.9 us)
 at::Tensor fresh(c10::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
   return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
