@@ -142,8 +142,14 @@ mla_status mla_rotate_q(const void* x, int64_t x_token_stride, int64_t x_head_st
   const int64_t xspan = 2 * ((tokens - 1) * xt + (heads - 1) * xh + w), ospan = 2 * ((tokens - 1) * ot + (heads - 1) * oh + w);
   if (xb < ob + ospan && ob < xb + xspan) {
     const bool same = (xt == ot || tokens == 1) && (xh == oh || heads == 1);
-    const int64_t apart = (xb < ob ? ob - xb : xb - ob) / 2, pitch = heads > 1 && (oh < ot || tokens == 1) ? oh : ot;
-    if (!same || (apart != 0 && (apart < w || apart > pitch - w))) return MLA_ERR_INVALID_ARG;
+    // rows lie in runs of `inner`, `pitch` apart, and the runs `outer` apart: other columns of the same rows leave room
+    // for both in the pitch, and for the last row of a run before the next run
+    const bool heads_inside = heads > 1 && (oh < ot || tokens == 1);
+    const int64_t apart = (xb < ob ? ob - xb : xb - ob) / 2, pitch = heads_inside ? oh : ot, outer = heads_inside ? ot : oh;
+    const int64_t inner = heads_inside ? heads : tokens, runs = heads_inside ? tokens : heads;
+    const bool beside = apart >= w && (inner == 1 || apart <= pitch - w) &&
+                        (runs == 1 || (inner - 1) * pitch + apart + w <= outer);
+    if (!same || (apart != 0 && !beside)) return MLA_ERR_INVALID_ARG;
   }
   rows::RotateParams p{static_cast<const uint16_t*>(x), static_cast<uint16_t*>(out), xt, xh, ot, oh,
                        {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},

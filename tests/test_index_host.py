@@ -264,3 +264,42 @@ def test_oracle_score_of_one_head():
     q[0, 0, 5], k[0, 5], k[1, 5], k[2, 6] = 2.0, 3.0, -1.0, 9.0
     assert oracle.index_score(q, np.array([[0.5]]), k).tolist() == [[3.0, 0.0, 0.0]]
     assert oracle.page_max(np.arange(65.0)[None]).tolist() == [[63.0, 64.0]]
+
+
+# ---- memory that an output may not share ----
+def _row_starts(base, token, head, tokens, heads):
+    return {(t, h): base + t * token + h * head for t in range(tokens) for h in range(heads)}
+
+
+def _rows_race(x, out):
+    """True where a row of `out` touches another (token, head)'s row of `x`, or a part of its own."""
+    return any(abs(a - b) < 64 and not (i == j and a == b) for i, a in x.items() for j, b in out.items())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(tokens=2, heads=2, xt=192, xh=128, ot=192, oh=128, d=64),     # out[0, 1] is x[1, 0]
+    dict(tokens=2, heads=2, xt=320, xh=192, ot=320, oh=192, d=-128),   # x[0, 1] is out[1, 0]
+    dict(tokens=2, heads=2, xt=192, xh=320, ot=192, oh=320, d=-128),   # the same, heads outside
+])
+def test_rotate_q_refuses_rows_that_meet(lib, kw):
+    kw, d = dict(kw), kw["d"]
+    del kw["d"]
+    out = ctypes.c_void_p(FAKE.value + 2 * d)
+    assert _rows_race(_row_starts(0, kw["xt"], kw["xh"], 2, 2), _row_starts(d, kw["ot"], kw["oh"], 2, 2))
+    assert _call(lib, "mla_rotate_q", ROTATE, **dict(kw, out=out)) == 1
+
+
+def test_rotate_q_refuses_every_row_that_meets_another(lib):
+    """All small layouts in which one thread would write what another reads (only such layouts are called)."""
+    strides, meets = [64, 72, 128, 136, 192, 200, 256, 320, 384], 0
+    for tokens, heads in ((1, 2), (2, 1), (2, 2), (3, 2), (2, 3)):
+        for t in strides:
+            for h in strides:
+                x = _row_starts(0, t, h, tokens, heads)
+                for d in range(-512, 513, 8):
+                    if _rows_race(x, _row_starts(d, t, h, tokens, heads)):
+                        meets += 1
+                        out = ctypes.c_void_p(FAKE.value + 2 * d)
+                        got = _call(lib, "mla_rotate_q", ROTATE, xt=t, xh=h, ot=t, oh=h, out=out, tokens=tokens, heads=heads)
+                        assert got == 1, (tokens, heads, t, h, d)
+    assert meets > 10000
