@@ -336,8 +336,11 @@ MLA_API mla_status mla_up_project(const void* o_lat, const void* w_uv, void* o_o
  * position out of range is skipped and recorded as an index error (bit 1) in
  * `status` (device, optional, 4-B aligned; read it with mla_read_status).
  * Values must be finite. Strides are in elements and multiples of 8, row
- * starts are 16-B aligned. An output that shares memory with another argument
- * is refused, but for the cases named below.
+ * starts are 16-B aligned.
+ *
+ * Common to all six: an output (`status` is one) that shares memory with another
+ * argument is refused, but for the cases named below. An array's memory is all
+ * from its first to its last byte, gaps between its rows included.
  */
 typedef enum { MLA_ROPE_PAIRS = 0, MLA_ROPE_HALVES = 1 } mla_rope_style;
 

@@ -29,8 +29,9 @@ bool cache_ok(int64_t num_blocks, int page_block) {
 bool in_memory(int64_t stride, int64_t count) { return stride <= (int64_t(1) << 46) / (count > 0 ? count : 1); }
 // strides in elements that keep 16-byte rows aligned
 bool stride_ok(int64_t s, int64_t least, int64_t count) { return s >= least && s % 8 == 0 && in_memory(s, count); }
-// memory of a call: `bytes` from `at` on. An output must not share any with
-// another argument: blocks read what others have already written.
+// memory of a call: `bytes` from `at` on (gaps between rows included). An
+// output, the status word among them, must not share any with another argument:
+// blocks read what others have already written.
 struct Span {
   const void* at;
   int64_t bytes;
@@ -39,10 +40,21 @@ struct Span {
     return at && o.at && a < b + o.bytes && b < a + bytes;
   }
 };
-bool apart(const Span& out, std::initializer_list<Span> others) {
-  for (const Span& o : others)
-    if (out.meets(o)) return false;
+// every output apart from the inputs and from the other outputs
+bool apart(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span* other = outputs.begin(); other != o; ++other)
+      if (o->meets(*other)) return false;
+    for (const Span& i : inputs)
+      if (o->meets(i)) return false;
+  }
   return true;
+}
+Span int32_span(const int32_t* at, int64_t n) { return {at, 4 * n}; }
+Span status_span(const uint32_t* at) { return {at, 4}; }
+// the table's rows that an int32 position reaches
+Span table_span(const rows::Positions& p) {
+  return {p.table, 4 * rows::kRope * (p.max_positions < kMaxRows ? p.max_positions : kMaxRows)};
 }
 // tokens of a row and columns written: room for the kernels' strides in 31 bits
 constexpr int64_t kMaxColumns = kMaxRows - 65536;
@@ -107,8 +119,9 @@ mla_status mla_append_kv(const void* c_kv, int64_t c_stride, const void* k_rope,
                        n, static_cast<uint8_t*>(kvcache), num_blocks * kTile};
   if (const mla_status v = check_positions(p.pos)) return v;
   static constexpr int64_t row_bytes[4] = {kDK * 2, kRowBytesFp8, kRowBytesFp8_528, kRowBytesFp4_288};
-  if (!apart({kvcache, p.num_rows * row_bytes[kv_format]},
-             {{c_kv, 2 * ((n - 1) * c_stride + latent)}, {k_rope, 2 * ((n - 1) * r_stride + rows::kRope)}}))
+  if (!apart({{kvcache, p.num_rows * row_bytes[kv_format]}, status_span(status)},
+             {{c_kv, 2 * ((n - 1) * c_stride + latent)}, {k_rope, 2 * ((n - 1) * r_stride + rows::kRope)},
+              int32_span(slots, n), int32_span(positions, n), table_span(p.pos)}))
     return MLA_ERR_INVALID_ARG;
   const dim3 grid((unsigned)((n + rows::kAppendWarps - 1) / rows::kAppendWarps));
   const int threads = 32 * rows::kAppendWarps;
@@ -155,6 +168,9 @@ mla_status mla_rotate_q(const void* x, int64_t x_token_stride, int64_t x_head_st
                        {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
                        tokens, heads, 0};
   if (const mla_status v = check_positions(p.pos)) return v;
+  if (!apart({{out, ospan}, status_span(status)}, {int32_span(positions, tokens), table_span(p.pos)}) ||
+      status_span(status).meets({x, xspan}))
+    return MLA_ERR_INVALID_ARG;
   constexpr int kU = 4;
   const bool many = tokens * heads >= kManyRows;
   p.heads_per_slot = (uint32_t)(many ? (heads + kU - 1) / kU : heads);
@@ -183,7 +199,9 @@ mla_status mla_append_index_k(const void* k, int64_t k_stride, int dtype, const 
                          n, 1, 1, 1, static_cast<uint8_t*>(index_cache), nullptr, num_blocks * kTile};
   if (const mla_status v = check_positions(p.pos)) return v;
   const int64_t page = index_format == MLA_INDEX_FP8 ? rows::kIndexPageFp8 : kTile * 2 * rows::kIndexDim;
-  if (!apart({index_cache, num_blocks * page}, {{k, 2 * ((n - 1) * k_stride + rows::kIndexDim)}})) return MLA_ERR_INVALID_ARG;
+  if (!apart({{index_cache, num_blocks * page}, status_span(status)},
+             {{k, 2 * ((n - 1) * k_stride + rows::kIndexDim)}, int32_span(slots, n), int32_span(positions, n), table_span(p.pos)}))
+    return MLA_ERR_INVALID_ARG;
   const int per = rows::kIndexGroups;
   const dim3 grid((unsigned)((n + per - 1) / per));
   const bool fp16 = dtype == MLA_DTYPE_FP16;
@@ -211,8 +229,11 @@ mla_status mla_quantize_index_q(const void* q, int64_t q_token_stride, int64_t q
                          tokens, heads, heads, 1, q_out, weights_out, 0};
   if (const mla_status v = check_positions(p.pos)) return v;
   const Span in{q, 2 * ((tokens - 1) * q_token_stride + (heads - 1) * q_head_stride + rows::kIndexDim)},
-      w_in{weights, 4 * tokens * heads}, w_to{weights_out, 4 * tokens * heads}, codes{q_out, rows::kIndexDim * tokens * heads};
-  if (!apart(codes, {in, w_in, w_to}) || in.meets(w_to) || (weights != weights_out && w_in.meets(w_to)))
+      w_in{weights, 4 * tokens * heads}, w_to{weights_out, 4 * tokens * heads}, codes{q_out, rows::kIndexDim * tokens * heads},
+      flags = status_span(status);
+  // the weights may be scaled in place
+  if (!apart({codes, w_to, flags}, {in, int32_span(positions, tokens), table_span(p.pos)}) || codes.meets(w_in) || flags.meets(w_in) ||
+      (weights != weights_out && w_in.meets(w_to)))
     return MLA_ERR_INVALID_ARG;
   // up to eight heads to a lane group, as long as that leaves kFewGroups of them: half the card's lanes. Measured with
   // 64 heads (GB300): 512 tokens 4.0 us (two heads a group), 5.5 with eight; 4096 tokens 20.6 with eight, 24.5 with two
@@ -374,7 +395,7 @@ mla_status mla_index_score(const void* q, int q_dtype, const float* weights, con
   const int64_t pairs = (int64_t)batch * p.units * ((cover + score::kTokens - 1) / score::kTokens);
   if (pairs >= kMaxRows) return MLA_ERR_UNSUPPORTED;
   const int64_t queries = (int64_t)batch * s_q, row_bytes = fp8 ? 128 : 256;
-  if (!apart({scores, 4 * ((queries - 1) * score_stride + width)},
+  if (!apart({{scores, 4 * ((queries - 1) * score_stride + width)}, status_span(status)},
              {{q, queries * heads * row_bytes}, {weights, 4 * queries * heads}, {block_table, 4 * (int64_t)batch * max_blocks},
               {cache_seqlens, 4 * (int64_t)batch}, {index_cache, num_blocks * (fp8 ? rows::kIndexPageFp8 : kTile * 256)}}))
     return MLA_ERR_INVALID_ARG;
@@ -435,9 +456,10 @@ mla_status mla_select_topk(const float* scores, int64_t score_stride, int width,
       (status && !aligned(status, 4)))
     return MLA_ERR_INVALID_ARG;
   const int64_t queries = (int64_t)batch * s_q;
-  const Span in{scores, 4 * ((queries - 1) * score_stride + width)}, table{block_table, 4 * (int64_t)batch * max_blocks},
-      lengths{cache_seqlens, 4 * (int64_t)batch}, to{indices, 4 * queries * topk}, held{lens, 4 * queries};
-  if (!apart(to, {in, table, lengths, held}) || !apart(held, {in, table, lengths})) return MLA_ERR_INVALID_ARG;
+  if (!apart({int32_span(indices, queries * topk), int32_span(lens, queries), status_span(status)},
+             {{scores, 4 * ((queries - 1) * score_stride + width)}, int32_span(block_table, (int64_t)batch * max_blocks),
+              int32_span(cache_seqlens, batch)}))
+    return MLA_ERR_INVALID_ARG;
   select::SelectParams p{scores, score_stride, width, cache_seqlens, block_table, num_blocks, max_blocks,
                          batch, s_q, causal ? 1 : 0, topk, 0, indices, lens, status};
   int dev = 0, sms = 0;

@@ -303,3 +303,49 @@ def test_rotate_q_refuses_every_row_that_meets_another(lib):
                         got = _call(lib, "mla_rotate_q", ROTATE, xt=t, xh=h, ot=t, oh=h, out=out, tokens=tokens, heads=heads)
                         assert got == 1, (tokens, heads, t, h, d)
     assert meets > 10000
+
+
+def _before(k, gap):
+    """`gap` bytes before the k-th of the fake arrays."""
+    return ctypes.c_void_p(_at(k).value - gap)
+
+
+ROTATE_APART = dict(ROTATE, x=_at(0), pos=_at(1), table=_at(2), out=_at(3))
+_TABLE_BYTES = 256 * 4096
+
+
+@pytest.mark.parametrize("name,base,out,inputs", [
+    ("mla_append_kv", "APPEND", 5, ["slots", "pos", "table", "status"]),
+    ("mla_append_index_k", "INDEX_K", 4, ["slots", "pos", "table", "status"]),
+    ("mla_quantize_index_q", "INDEX_Q", 4, ["pos", "table", "status"]),
+    ("mla_quantize_index_q", "INDEX_Q", 5, ["pos", "table", "status"]),
+    ("mla_rotate_q", "ROTATE_APART", 3, ["pos", "table", "status"]),
+    ("mla_index_score", "SCORE", 5, ["status"]),
+    ("mla_select_topk", "SELECT", 3, ["status"]),
+    ("mla_select_topk", "SELECT", 4, ["status"]),
+])
+def test_outputs_that_share_memory_are_refused(lib, name, base, out, inputs):
+    args = globals()[base]
+    for key in inputs:
+        assert _call(lib, name, args, **{key: _at(out)}) == 1, key
+    if "table" in inputs:                            # a table that ends inside the output; more rows than positions reach
+        assert _call(lib, name, args, table=_before(out, _TABLE_BYTES - 16)) == 1
+        assert _call(lib, name, args, table=_before(out, _TABLE_BYTES - 16), maxp=(1 << 63) - 1) == 1
+    if "slots" in inputs:                            # an array that ends inside the output
+        assert _call(lib, name, args, slots=_before(out, 4)) == 1
+    if "pos" in inputs:
+        assert _call(lib, name, args, pos=_before(out, 4)) == 1
+
+
+@pytest.mark.parametrize("name,base,inputs", [
+    ("mla_append_kv", "APPEND", ["c", "r", "slots", "pos", "table"]),
+    ("mla_append_index_k", "INDEX_K", ["k", "slots", "pos", "table"]),
+    ("mla_quantize_index_q", "INDEX_Q", ["q", "w", "pos", "table"]),
+    ("mla_rotate_q", "ROTATE_APART", ["x", "pos", "table"]),
+    ("mla_index_score", "SCORE", ["q", "w", "cache", "bt", "sl"]),
+    ("mla_select_topk", "SELECT", ["scores", "bt", "sl"]),
+])
+def test_a_status_word_inside_an_input_is_refused(lib, name, base, inputs):
+    for key in inputs:
+        args = globals()[base]
+        assert _call(lib, name, args, status=ctypes.c_void_p(args[key].value + 4)) == 1, key
