@@ -38,6 +38,16 @@ struct Raised {};  // a Python error is set
   throw Raised();
 }
 
+// the interpreter's lock given up for a scope
+class Unlocked {
+  PyThreadState* state_ = PyEval_SaveThread();
+
+ public:
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+};
+
 // One call: its name, for messages, and the device that its tensors are on.
 struct Call {
   const char* where;
@@ -75,10 +85,16 @@ struct Call {
     if (t.nbytes() < 4) refuse("status: a 4-byte word");
     return t.data_ptr();
   }
+  // The launch runs without the interpreter's lock: one into a full queue waits for the GPU, and the other Python
+  // threads must not wait with it. `f` touches no Python object; the caller's arguments outlive the call.
   template <typename F>
   void run(F&& f) const {
-    const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)));
-    const int st = f(static_cast<void*>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream()));
+    int st;
+    {
+      const Unlocked unlocked;
+      const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+      st = f(static_cast<void*>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream()));
+    }
     if (st != MLA_OK) raise(st, where);
   }
 };

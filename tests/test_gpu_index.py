@@ -5,6 +5,9 @@ oracle; and a run of them together, as a serving step uses them.
 Rows are compared bit for bit (the rotation's roundings are part of its
 definition). Scores carry the oracle's own bound of an fp32 evaluation.
 """
+import threading
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -714,3 +717,33 @@ def test_same_inputs_same_bits():
     first = mla.mla_index_score(*args, causal=True)
     for _ in range(3):
         assert torch.equal(first, mla.mla_index_score(*args, causal=True))
+
+
+def test_a_full_launch_queue_leaves_other_threads_running():
+    """Calls behind a spinning kernel fill the launch queue; the thread that makes them waits, the others do not."""
+    x = torch.randn(4, 2, 64, generator=_gen(1)).to(BF).to(DEV)
+    out, pos, table = torch.empty_like(x), torch.zeros(4, dtype=torch.int32, device=DEV), _table()
+    side = torch.cuda.Stream()
+    calls, longest = 5000, [0.0]
+
+    def work():
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_500_000_000)           # cycles: three quarters of a second
+            for _ in range(calls):
+                t = time.perf_counter()
+                mla.mla_rotate_q(x, pos, table, out=out)
+                longest[0] = max(longest[0], time.perf_counter() - t)
+
+    mla.mla_rotate_q(x, pos, table, out=out)
+    torch.cuda.synchronize()
+    thread = threading.Thread(target=work)
+    gap, last = 0.0, time.perf_counter()
+    thread.start()
+    while thread.is_alive():
+        time.sleep(0.001)
+        now = time.perf_counter()
+        gap, last = max(gap, now - last), now
+    thread.join()
+    torch.cuda.synchronize()
+    assert longest[0] > 0.2, "the queue never filled"
+    assert gap < longest[0] / 2
