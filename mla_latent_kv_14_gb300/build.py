@@ -87,12 +87,12 @@ def build(verbose: bool = False, extra_flags=None) -> str:
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         host = ex.submit(_compile_host, verbose)
         objs = list(ex.map(compile_one, SOURCES))
-        host = host.result()
-    tmp = LIB + ".tmp"
-    _run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xlinker", "-soname=libmla.so", "-cudart", "static", "-lpthread", "-ldl", "-lrt"],
-         "link", verbose)
-    os.replace(tmp, LIB)
-    _link_host(host, verbose)
+        tmp = LIB + ".tmp"
+        _run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xlinker", "-soname=libmla.so", "-cudart", "static", "-lpthread", "-ldl", "-lrt"],
+             "link", verbose)
+        os.replace(tmp, LIB)
+        # after the library, which needs neither g++ nor the headers of Python and PyTorch
+        _link_host(host.result(), verbose)
     return LIB
 
 

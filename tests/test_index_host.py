@@ -349,3 +349,24 @@ def test_a_status_word_inside_an_input_is_refused(lib, name, base, inputs):
     for key in inputs:
         args = globals()[base]
         assert _call(lib, name, args, status=ctypes.c_void_p(args[key].value + 4)) == 1, key
+
+
+def test_the_library_is_built_without_the_extension(monkeypatch, tmp_path):
+    """No Python or PyTorch headers: the extension's compilation fails, libmla.so is there all the same."""
+    from mla_latent_kv_14_gb300 import build as b
+    ran = []
+
+    def run(cmd, what, verbose=False):
+        ran.append(what)
+        if what == "g++":
+            raise RuntimeError("g++ failed: Python.h: No such file or directory")
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write(what)
+
+    monkeypatch.setattr(b, "_run", run)
+    monkeypatch.setattr(b, "BUILD", str(tmp_path / "objects"))
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "libmla.so"))
+    monkeypatch.setattr(b, "HOST", str(tmp_path / "_host.so"))
+    with pytest.raises(RuntimeError, match="Python.h"):
+        b.build()
+    assert (tmp_path / "libmla.so").read_text() == "link" and not (tmp_path / "_host.so").exists()
