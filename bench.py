@@ -112,19 +112,30 @@ def workload_seqlens(w):
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "dram_traffic.txt")
 
 
-# the sources of the kernels that the workloads time
-KERNEL_SOURCES = ("absorb.cuh", "decode_dense.cuh", "decode_fewheads.cuh", "params.h", "ptx.cuh", "sched.cuh")
+def kernel_sources() -> list:
+    """The files that the timed kernels and their launches are built from:
+    mla_api.cu and every file of its folder that it includes, at any depth."""
+    import re
+    csrc = os.path.join(ROOT, "mla_latent_kv_14_gb300", "csrc")
+    found, left = set(), ["mla_api.cu"]
+    while left:
+        name = left.pop()
+        if name in found or not os.path.exists(os.path.join(csrc, name)):
+            continue
+        found.add(name)
+        with open(os.path.join(csrc, name)) as f:
+            left += re.findall(r'^\s*#\s*include\s+"([^"/]+)"', f.read(), re.M)
+    return [os.path.join(csrc, name) for name in sorted(found)]
 
 
 def kernel_source_digest() -> str:
     """Digest of the CUDA sources the timed kernels are built from (so a stored
     DRAM-traffic figure is used only for the kernels it was measured on)."""
     import hashlib
-    csrc = os.path.join(ROOT, "mla_latent_kv_14_gb300", "csrc")
     h = hashlib.sha256()
-    for name in KERNEL_SOURCES:
-        with open(os.path.join(csrc, name), "rb") as f:
-            h.update(name.encode() + b"\0" + f.read())
+    for path in kernel_sources():
+        with open(path, "rb") as f:
+            h.update(os.path.basename(path).encode() + b"\0" + f.read())
     return h.hexdigest()[:16]
 
 

@@ -4,6 +4,7 @@ Every rank times its own replica; the job time is the slowest rank's
 (max over ranks) and the whole-job rate counts the work of all ranks.
 """
 import os
+import shutil
 import socket
 
 import pytest
@@ -69,3 +70,25 @@ def test_few_heads_sweep_rotates_sets_until_twice_the_l2():
             if n > 1:
                 assert (n - 1) * per_set < 2 * bench.L2_BYTES     # no more sets than needed
                 assert (n - 1) * per_set >= bench.L2_BYTES        # a set is gone from L2 when it returns
+
+
+def test_kernel_digest_covers_every_source_of_the_timed_launches(tmp_path, monkeypatch):
+    """A change in any file that mla_api.cu is built from, itself included, makes a stored DRAM figure stale; one in the
+    calls around the decode does not."""
+    csrc = os.path.join("mla_latent_kv_14_gb300", "csrc")
+    shutil.copytree(os.path.join(bench.ROOT, csrc), tmp_path / csrc)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    first = bench.kernel_source_digest()
+    names = ["mla_api.cu", "absorb.cuh", "codes.cuh", "decode_dense.cuh", "decode_fewheads.cuh", "host.h", "params.h",
+             "ptx.cuh", "quant.cuh", "sched.cuh"]
+    for name in names + ["select.cuh", "host_binding.cpp"]:
+        file = tmp_path / csrc / name
+        text = file.read_text()
+        file.write_text(text + "// changed\n")
+        assert (bench.kernel_source_digest() != first) == (name in names), name
+        file.write_text(text)
+    (tmp_path / csrc / "more.cuh").write_text("#pragma once\n")
+    (tmp_path / csrc / "sched.cuh").write_text((tmp_path / csrc / "sched.cuh").read_text() + '#include "more.cuh"\n')
+    second = bench.kernel_source_digest()
+    (tmp_path / csrc / "more.cuh").write_text("#pragma once\n// changed\n")
+    assert len({first, second, bench.kernel_source_digest()}) == 3
