@@ -747,3 +747,110 @@ def test_a_full_launch_queue_leaves_other_threads_running():
     torch.cuda.synchronize()
     assert longest[0] > 0.2, "the queue never filled"
     assert gap < longest[0] / 2
+
+
+# ---------------------------------------------------------------------------
+# the forms that many rows and long caches take
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("halves", [0, 1])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("tokens,heads", [(255, 128), (256, 128), (1100, 33), (32768, 1), (6600, 5), (259, 127)])
+def test_rotate_q_of_many_rows(tokens, heads, dtype, halves):
+    """Below 32768 rows a thread takes one head, from there four heads of a token (33, 5, 127: not all of them have one)."""
+    test_rotate_q(tokens, heads, dtype, halves)
+
+
+@pytest.mark.parametrize("halves", [0, 1])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("tokens,heads", [(511, 64), (512, 64), (5000, 7), (1500, 33), (2000, 33), (2100, 64), (131073, 1)])
+def test_quantize_index_q_of_many_rows(tokens, heads, dtype, halves):
+    """A lane group takes 1, 2, 2 (of 7 heads), 3, 4 (of 33), 8 and 8 (of one) heads of a token."""
+    test_quantize_index_q(tokens, heads, dtype, halves)
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2, 3])
+@pytest.mark.parametrize("halves", [0, 1])
+def test_appends_of_many_tokens(fmt, halves):
+    """Prompts of a few thousand tokens, into every format and both index formats."""
+    n, pages, latent = 3001, 50, (448 if fmt >= 2 else 512)
+    kv = torch.randn(n, latent + 64, generator=_gen(fmt)).to(BF)
+    slots, pos, keep, bad = _new(n, 40 + fmt, pages)
+    width = {0: 1152, 1: 656, 2: 528, 3: 288}[fmt]
+    want = torch.zeros(pages * PAGE, width, dtype=torch.uint8)
+    rows = oracle.append_rows(kv[:, :latent], kv[:, latent:], TABLE[np.clip(pos, 0, 4999)], bool(halves), fmt)
+    want[torch.from_numpy(slots[keep]).long()] = rows[torch.from_numpy(keep)]
+    got = torch.zeros(pages, PAGE, 1, width, dtype=torch.uint8, device=DEV)
+    dev, st = kv.to(DEV), _status()
+    sd, pd = torch.from_numpy(slots).to(DEV), torch.from_numpy(pos).to(DEV)
+    mla.mla_append_kv(dev[:, :latent], dev[:, latent:], got.view(BF) if fmt == 0 else got, sd, pd, _table(), kv_format=fmt,
+                      rope_style=halves, status=st)
+    assert _bits(st) == bad and torch.equal(got.cpu().view(pages * PAGE, width), want)
+
+
+def _long_ref(lens, s_q, causal, bt, qv, w, kv, width):
+    """_score_ref by matrix products, request by request, on long caches."""
+    ref, err = np.full((len(lens), s_q, width), -np.inf), np.zeros((len(lens), s_q, width))
+    wv, u = oracle.to_f64(w), 2.0 ** -24
+    for b, n in enumerate(lens):
+        keys = kv[bt[b]].reshape(-1, 128)[:min(n, width)]
+        heads = qv.shape[2]
+        for i in range(s_q):
+            v = max(0, min(n - (s_q - 1 - i if causal else 0), len(keys)))
+            if v:
+                ref[b, i, :v] = wv[b, i] @ np.maximum(qv[b, i] @ keys[:v].T, 0.0)
+                # the bound of oracle.index_score_error
+                err[b, i, :v] = (2 * 128 + heads + 2) * u * (np.abs(keys[:v]) @ (np.abs(wv[b, i]) @ np.abs(qv[b, i])))
+    return ref, err
+
+
+def test_the_long_reference_is_the_oracle():
+    lens = [150, 0, 64]
+    q, w, cache, bt, qv, kv = _score_case(lens, 3, 5, "bf16", seed=2)
+    a, b = _score_ref(lens, 3, True, bt, qv, w, kv, 160), _long_ref(lens, 3, True, bt, qv, w, kv, 160)
+    for x, y in zip(a, b):
+        assert (np.isneginf(x) == np.isneginf(y)).all()
+        assert np.allclose(np.where(np.isneginf(x), 0, x), np.where(np.isneginf(y), 0, y), rtol=1e-12, atol=1e-12)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("lens,s_q,heads,causal", [
+    ([200000, 30000, 0, 130, 25000], 1, 64, False),   # 64 columns, 13 tiles a block: a ring of 12 wraps, both epilogue groups
+    ([70001, 9000, 0, 130, 20000], 2, 64, True),      # 128 columns
+    ([40000, 1, 33333], 1, 16, False),                # 16 columns
+    ([60000, 129], 3, 32, True),                      # 96 columns
+    ([50000, 700, 5000], 8, 13, False),               # 128 columns of padded heads
+    ([30000, 4000, 130], 11, 64, True),               # two groups of 256 columns
+    ([26000, 3], 40, 9, True),                        # several units
+])
+def test_index_score_of_long_caches(lens, s_q, heads, causal, kind):
+    """Several tiles a block, by tokens and by pages."""
+    q, w, cache, _, qv, kv = _score_case([1] * len(lens), s_q, heads, kind, seed=heads, spare=400)
+    # requests share the pages of a small cache
+    bt = np.random.default_rng(heads).integers(0, len(kv), (len(lens), -(-max(lens) // PAGE))).astype(np.int32)
+    fmt = mla.INDEX_FP8 if kind == "fp8" else mla.INDEX_16BIT
+    args = (q.to(DEV), w.to(DEV), cache.to(DEV), torch.from_numpy(bt).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV))
+    width = bt.shape[1] * PAGE
+    ref, err = _long_ref(lens, s_q, causal, bt, qv, w, kv, width)
+    st = _status()
+    got = mla.mla_index_score(*args, causal=causal, index_format=fmt, status=st)
+    _check_scores(got, ref, err, f"{kind} tokens")
+    pages = mla.mla_index_score(*args, causal=causal, index_format=fmt, block=64, status=st)
+    _check_scores(pages, oracle.page_max(ref), oracle.page_max(err), f"{kind} pages")
+    assert _bits(st) == 0
+
+
+@pytest.mark.parametrize("n", [20000, 140001])
+def test_select_pages_of_rows_beyond_a_block(n):
+    """Pages in a cluster, and rows that are read again."""
+    bt = np.random.default_rng(n).permutation(n).reshape(1, n).astype(np.int32)
+    s = torch.randn(1, 2, n, generator=_gen(n))
+    for topk in (1, 500, n - 3, n + 1):
+        _select_both(s, [64 * n - 3], 2, True, 64, topk, bt, n)
+
+
+def test_select_tokens_of_many_long_rows():
+    """More clusters than run at once: 32 scores a thread."""
+    n, s_q = 20000, 80
+    most = -(-n // PAGE)
+    bt = np.random.default_rng(1).permutation(2 * most).reshape(2, most).astype(np.int32)
+    _select_both(torch.randn(2, s_q, n, generator=_gen(3)), [n, 17000], s_q, True, 1, 2048, bt, 2 * most)
