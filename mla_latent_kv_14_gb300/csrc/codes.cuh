@@ -34,15 +34,17 @@ MLA_DEV float e4m3_scale(float amax) {
 //
 // A quotient x / scale is formed as q = x * r, r = 1 / scale rounded to nearest,
 // corrected by its remainder: q + (x - q * scale) * r, each step one fused
-// operation (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990: the result is rounded correctly if q is within
-// one unit of the last place). Two roundings put q up to 1.5 units off, so the
-// theorem alone does not cover every q; of 63 million pairs, two thirds of them
-// beside e4m3's midpoints or at the ends of the binade, none came out other
-// than the division. For scale >= 2^-60 only an |x| below 2^-102 could underflow
-// a remainder, and its quotient is below 2^-42, zero in e4m3; smaller scales,
-// and an infinite one, are divided by. On packed pairs that is 1.5 operations a
-// value and one for the sign of a zero, where a division takes some ten.
+// operation (after P. Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990). Two roundings put q up to 1.5 units
+// off, where the correction may miss the rounded quotient by one fp32 step: only
+// if x / scale lies within 2^-45.9 of itself of the middle between two fp32
+// numbers. A code can change there only beside one of the five-bit numbers at
+// which e4m3's rounding turns, and few pairs fit both: all of them give the
+// division's code (the host tests derive and run through them). For scale >=
+// 2^-60 only an |x| below 2^-102 could underflow a remainder, and its quotient is
+// below 2^-42, zero in e4m3; smaller scales, and an infinite one, are divided by.
+// On packed pairs that is 1.5 operations a value and one for the sign of a zero,
+// where a division takes some ten.
 MLA_DEV void e4m3_codes16(const float* x, float scale, uint32_t* w) {
   if (scale >= 0x1p-60f && scale < 0x1p127f) {
     const float inv = __frcp_rn(scale);

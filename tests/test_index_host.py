@@ -370,3 +370,37 @@ def test_the_library_is_built_without_the_extension(monkeypatch, tmp_path):
     with pytest.raises(RuntimeError, match="Python.h"):
         b.build()
     assert (tmp_path / "libmla.so").read_text() == "link" and not (tmp_path / "_host.so").exists()
+
+
+def test_corrected_quotient_gives_the_codes_of_the_division():
+    """Every pair on which an e4m3 code could differ from that of the rounded quotient.
+
+    With u = 2^-24: r = (1/s)(1 + a), |a| <= u, and q = (x/s)(1 + e), |e| <= 2u + u^2. The remainder x - q s = -x e is
+    rounded by a factor 1 + b, |b| <= u, so what the last step rounds is (x/s)(1 - e (a + b + a b)): off by at most
+    2^-45.9 of the quotient. The result therefore is the rounded quotient unless a midpoint m of two fp32 neighbours lies
+    that close to x/s, and its code can differ only if one of the two neighbours is a number t at which e4m3's rounding
+    changes, which has five bits: t = T / 16 for T in 16..31, m = t +- 2^-24 (below t = 1: t - 2^-25), for quotients
+    scaled to [1, 2). With s = S 2^-23 and x = A 2^-27, |x - m s| <= 2^-45.9 x says |A - S T -+ S 2^-20| < 2^-16.9: S lies
+    within 8.6 of a multiple of 2^20 (2^21 below t = 1), and A = S T +- that multiple. All of those, with a margin:"""
+    s, x = [], []
+    for T in range(16, 32):
+        for sign, shift in ((1, 20), (-1, 20 if T > 16 else 21)):
+            for k in range((1 << 23) >> shift, ((1 << 24) >> shift) + 1):
+                for S in range((k << shift) - 64, (k << shift) + 65):
+                    if not (1 << 23) <= S < (1 << 24):
+                        continue
+                    for A in range(S * T + sign * k - 1, S * T + sign * k + 2):
+                        unit = 16 if A < 1 << 28 else 32           # x of [1, 2), of [2, 4)
+                        if A % unit == 0:
+                            s.append(S * 2.0 ** -23)
+                            x.append(A * 2.0 ** -27)
+    s, x = np.array(s), np.array(x)
+    assert len(s) > 1000 and (s.astype(np.float32) == s).all() and (x.astype(np.float32) == x).all()
+    q64 = x / s
+    s, x = s.astype(np.float32), x.astype(np.float32)
+    r = (1 / s.astype(np.float64)).astype(np.float32)
+    q = x * r
+    got, want = _fma32(_fma32(q, -s, x), r, q), q64.astype(np.float32)
+    for scale in range(-12, 9):                                    # codes from below the smallest to the saturated ones
+        f = np.float32(2.0 ** scale)
+        assert (oracle.e4m3_encode_rne(got * f) == oracle.e4m3_encode_rne(want * f)).all()
