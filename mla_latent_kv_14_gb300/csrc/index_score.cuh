@@ -26,9 +26,12 @@
 // Measured (GB300): 32 requests of 131072 e4m3 keys, 64 heads, 99.9 us (5.7
 // TB/s of keys and scores, 0.84 of the copy bandwidth); in bf16 174 us (0.92).
 // 4 x 1024 causal queries over 16384 bf16 keys 675 us at full clocks (1.60
-// PFLOP/s, 0.83 of the cuBLAS burst) and 728 us back to back, where power lowers
-// the clock; e4m3 686 us: there the epilogue bounds (without its sums the
-// kernel took 389 us, in bf16 558).
+// PFLOP/s, 0.83 of the cuBLAS burst) and 728 us in long runs, where power lowers
+// the clock; e4m3 687 us: there the epilogue bounds (without its sums the
+// kernel took 389 us, in bf16 558) by the latency of its steps, with the issue
+// slots (0.46) and the ALU pipe (46 %) half used. Page scores of the same
+// queries 884 us: a maximum over 32 lanes for every query of a tile. A single
+// tile takes 4.2 us, start to end.
 //
 // The (unit, tile) pairs of all requests form one list, cut into equal
 // contiguous ranges, one per CTA (one CTA per SM): ragged lengths balance, and
@@ -181,9 +184,10 @@ MLA_DEV void tma_load_3d_plain(uint32_t dst, const CUtensorMap* m, uint32_t bar,
       : "memory");
 }
 
-// acc += w * max(0, (x0, x1)) on packed pairs. One asm block: the maxima are
-// written where the packed fma reads them (built from separate expressions,
-// a third of the loop was register moves).
+// acc += w * max(0, (x0, x1)) on packed pairs. One asm block, so that the maxima
+// are written as the pair that the packed fma reads: 785 us where separate
+// expressions took 868 (4 x 1024 causal queries over 16384 bf16 keys, with one
+// row of an accumulator per lane).
 MLA_DEV void fma_positive(uint64_t& acc, uint32_t x0, uint32_t x1, uint64_t w) {
   asm("{\n\t.reg .f32 lo, hi;\n\t.reg .b64 x;\n\tmax.f32 lo, %1, 0f00000000;\n\tmax.f32 hi, %2, 0f00000000;\n\t"
       "mov.b64 x, {lo, hi};\n\tfma.rn.f32x2 %0, x, %3, %0;\n\t}"

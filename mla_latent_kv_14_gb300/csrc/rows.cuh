@@ -12,7 +12,9 @@
 //
 // All of these are bound by their bytes (under 1 FLOP per byte) and, for a few
 // tokens, by the latency of slot/position -> table row -> store. So each kernel
-// has every load that does not depend on another one in flight first.
+// has every load that does not depend on another one in flight first; only the
+// append of 528- and 288-byte rows loads its RoPE dims behind the slot's test, in
+// the four lanes that turn them.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -131,8 +133,9 @@ MLA_DEV void load_row(const float* src, float* v) {
 // Measured (GB300): 64 tokens 1.4 us; 32768 tokens, 16-bit rows 14.3 us (0.87 of
 // the copy bandwidth), 656-byte rows 14.4 us (0.69; 16.9 at the 52 registers a
 // thread takes unlimited, which leave 40 warps an SM instead of 48), 528-byte
-// rows 15.1 us (0.58): the quantised rows wait for their loads between two
-// stretches of arithmetic, at half of the issue slots.
+// rows 15.0 us (0.58): these wait for their loads between two stretches of
+// arithmetic, at half of the issue slots. 288-byte rows 24.5 us (0.31) are bound
+// by the ALU pipe (82 %): seven two-sided comparisons a value choose its code.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 8;
 
