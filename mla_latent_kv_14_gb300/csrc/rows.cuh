@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kFormat == 0 ? 8 : 6) mla_a
 // Rotation of query rows: a thread turns 8 pairs (32 bytes) of kU heads of one
 // token, four threads per row of 64 dims. The table row stays in registers for
 // the kU heads.
-// Measured (GB300): 64 tokens x 128 heads 1.8 us; 4095 x 128 22.3 us (0.89 of the
-// copy bandwidth).
+// Measured (GB300): 64 tokens x 128 heads 1.8 us; 4095 x 128 22.3 to 22.9 us (0.89
+// to 0.87 of the copy bandwidth).
 // ---------------------------------------------------------------------------
 constexpr int kRotateThreads = 256;
 

@@ -8,9 +8,10 @@
 // that may be partly filled) comes last. That page always takes part: it is
 // set apart, and topk - 1 are selected from the others.
 //
-// Measured (GB300): 4 x 1024 rows of up to 16384 scores, topk 2048, 106 us (the
-// read alone 43 us; 62 % of the issue slots busy), of up to 8192 57, 2048 27; 32
-// rows of 131072 13.2 us, 64 rows of up to 512 pages 4.9 us: there the steps'
+// Measured (GB300): 4 x 1024 rows of up to 16384 scores, topk an eighth, 106 us
+// (the read alone 43 us; 64 % of the issue slots busy), of up to 8192 51, 2048 25,
+// 4096 rows of 512 21; 32 rows of 131072, topk 2048, 13.2 us, 64 rows of up to 512
+// pages 4.9 us: there, and in the short rows, the steps'
 // latencies, of 1 to 2 us for a cluster's barriers and remote reads.
 //
 // The floor is one read of the visible scores. A row is therefore loaded once
