@@ -369,8 +369,9 @@ MLA_API mla_status mla_append_kv(const void* c_kv, int64_t c_stride, const void*
  * Rotate the RoPE dims of queries: out[t, h, :] = R(x[t, h, :]) over rows of 64.
  * x, out (device) [tokens, heads, 64] with token and head strides; a typical
  * call reads a slice of the query projection and writes dims [512, 576) of the
- * decode's query (the ones mla_absorb_q leaves). out may be x (in place) or
- * other columns of the same rows; any other overlap is refused.
+ * decode's query (the ones mla_absorb_q leaves). out may be x (in place) or, with
+ * x's strides, lie between its rows (other columns, other heads of the same
+ * tokens); any other overlap, gaps between rows included, is refused.
  */
 MLA_API mla_status mla_rotate_q(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
                                 int64_t out_token_stride, int64_t out_head_stride, int dtype,

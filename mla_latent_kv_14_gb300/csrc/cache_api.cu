@@ -56,6 +56,21 @@ Span status_span(const uint32_t* at) { return {at, 4}; }
 Span table_span(const rows::Positions& p) {
   return {p.table, 4 * rows::kRope * (p.max_positions < kMaxRows ? p.max_positions : kMaxRows)};
 }
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); }
+// Rows of `w` elements in runs of `inner` rows `pitch` apart (at least w), the
+// `runs` starting `outer` apart (a run's length at least). True if the same rows
+// `d` elements further on meet any of them: if d is less than w off some
+// a outer + b pitch. Only two values of a, and two of b for each, come that near.
+bool rows_meet(int64_t d, int64_t outer, int64_t runs, int64_t pitch, int64_t inner, int64_t w) {
+  const int64_t a0 = runs > 1 ? floor_div(d, outer) : 0;
+  for (int64_t a = a0; a <= a0 + 1; ++a) {
+    if (a <= -runs || a >= runs) continue;
+    const int64_t rest = d - a * outer, b0 = floor_div(rest, pitch);
+    for (int64_t b = b0; b <= b0 + 1; ++b)
+      if (b > -inner && b < inner && rest - b * pitch < w && b * pitch - rest < w) return true;
+  }
+  return false;
+}
 // tokens of a row and columns written: room for the kernels' strides in 31 bits
 constexpr int64_t kMaxColumns = kMaxRows - 65536;
 
@@ -150,19 +165,15 @@ mla_status mla_rotate_q(const void* x, int64_t x_token_stride, int64_t x_head_st
   if (!x || !out || !aligned(x, 16) || !aligned(out, 16)) return MLA_ERR_INVALID_ARG;
   // rows of the output must not overlap one another
   if (tokens > 1 && heads > 1 && ot < (heads - 1) * oh + w && oh < (tokens - 1) * ot + w) return MLA_ERR_INVALID_ARG;
-  // in place (the same rows), in other columns of the same rows, or apart
+  // in place (the same rows), between the rows of x, or apart
   const intptr_t xb = reinterpret_cast<intptr_t>(x), ob = reinterpret_cast<intptr_t>(out);
   const int64_t xspan = 2 * ((tokens - 1) * xt + (heads - 1) * xh + w), ospan = 2 * ((tokens - 1) * ot + (heads - 1) * oh + w);
   if (xb < ob + ospan && ob < xb + xspan) {
     const bool same = (xt == ot || tokens == 1) && (xh == oh || heads == 1);
-    // rows lie in runs of `inner`, `pitch` apart, and the runs `outer` apart: other columns of the same rows leave room
-    // for both in the pitch, and for the last row of a run before the next run
     const bool heads_inside = heads > 1 && (oh < ot || tokens == 1);
-    const int64_t apart = (xb < ob ? ob - xb : xb - ob) / 2, pitch = heads_inside ? oh : ot, outer = heads_inside ? ot : oh;
-    const int64_t inner = heads_inside ? heads : tokens, runs = heads_inside ? tokens : heads;
-    const bool beside = apart >= w && (inner == 1 || apart <= pitch - w) &&
-                        (runs == 1 || (inner - 1) * pitch + apart + w <= outer);
-    if (!same || (apart != 0 && !beside)) return MLA_ERR_INVALID_ARG;
+    if (!same || (xb != ob && (heads_inside ? rows_meet((ob - xb) / 2, ot, tokens, oh, heads, w)
+                                            : rows_meet((ob - xb) / 2, oh, heads, ot, tokens, w))))
+      return MLA_ERR_INVALID_ARG;
   }
   rows::RotateParams p{static_cast<const uint16_t*>(x), static_cast<uint16_t*>(out), xt, xh, ot, oh,
                        {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},

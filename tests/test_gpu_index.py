@@ -854,3 +854,20 @@ def test_select_tokens_of_many_long_rows():
     most = -(-n // PAGE)
     bt = np.random.default_rng(1).permutation(2 * most).reshape(2, most).astype(np.int32)
     _select_both(torch.randn(2, s_q, n, generator=_gen(3)), [n, 17000], s_q, True, 1, 2048, bt, 2 * most)
+
+
+@pytest.mark.parametrize("strides,beside", [((1088, 1024), 512), ((1024, 1088), 512), ((4 * 192, 192), 128), ((192, 40 * 192), 64)])
+def test_rotate_q_between_rows_of_one_buffer(strides, beside):
+    """Views whose rows interleave without meeting, tokens or heads outside: rows written, everything else as it was."""
+    tokens, heads = 2, 2
+    buf = torch.randn(20000, generator=_gen(beside)).to(BF)
+    pos = np.array([3, 4000], dtype=np.int32)
+    rows = (tokens, heads, 64)
+    for src, dst in ((0, beside), (beside, 0)):
+        x = buf.as_strided(rows, strides + (1,), src)
+        want = buf.clone()
+        want.as_strided(rows, strides + (1,), dst).copy_(oracle.round_to(oracle.rotate(x, TABLE[pos][:, None], False), BF))
+        dev = buf.to(DEV)
+        mla.mla_rotate_q(dev.as_strided(rows, strides + (1,), src), torch.from_numpy(pos).to(DEV), _table(),
+                         out=dev.as_strided(rows, strides + (1,), dst))
+        assert torch.equal(dev.cpu(), want)
