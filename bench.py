@@ -123,7 +123,7 @@ def kernel_sources() -> list:
         if name in found or not os.path.exists(os.path.join(csrc, name)):
             continue
         found.add(name)
-        with open(os.path.join(csrc, name)) as f:
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
             left += re.findall(r'^\s*#\s*include\s+"([^"/]+)"', f.read(), re.M)
     return [os.path.join(csrc, name) for name in sorted(found)]
 
