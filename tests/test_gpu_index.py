@@ -871,3 +871,113 @@ def test_rotate_q_between_rows_of_one_buffer(strides, beside):
         mla.mla_rotate_q(dev.as_strided(rows, strides + (1,), src), torch.from_numpy(pos).to(DEV), _table(),
                          out=dev.as_strided(rows, strides + (1,), dst))
         assert torch.equal(dev.cpu(), want)
+
+
+# ---------------------------------------------------------------------------
+# caches and rows beyond 4 GB
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt,row", [(0, 1152), (1, 656), (2, 528), (3, 288)])
+def test_append_behind_4_gb(fmt, row):
+    pages, latent, n = 2 ** 32 // (PAGE * row) + 40, (448 if fmt >= 2 else 512), 70
+    kv = torch.randn(n, latent + 64, generator=_gen(row)).to(BF)
+    first = pages * PAGE - n
+    cache = torch.empty(pages, PAGE, 1, row, dtype=torch.uint8, device=DEV)
+    flat = cache.view(-1, row)
+    flat[:n], flat[first - 3:] = 7, 7
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    dev = kv.to(DEV)
+    mla.mla_append_kv(dev[:, :latent], dev[:, latent:], cache.view(BF) if fmt == 0 else cache, pos + first, pos, _table(),
+                      kv_format=fmt)
+    rows = oracle.append_rows(kv[:, :latent], kv[:, latent:], TABLE[:n], False, fmt)
+    assert torch.equal(flat[first:].cpu(), rows)
+    assert (flat[:n] == 7).all() and (flat[first - 3:first] == 7).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_index_cache_and_scores_behind_4_gb(fp8):
+    """Keys written and scored on the last pages of a large index cache, into rows of scores 4 GB apart, and selected."""
+    page = 8448 if fp8 else PAGE * 256
+    pages, n, heads = 2 ** 32 // page + 40, 130, 16
+    g = _gen(page)
+    k, q = torch.randn(n, 128, generator=g).to(BF), torch.randn(2, heads, 128, generator=g).to(BF)
+    w = torch.randn(2, heads, generator=g)
+    cache = torch.empty(pages, page, dtype=torch.uint8, device=DEV)
+    cache[:3], cache[-3:] = 0, 0
+    ic = cache if fp8 else cache.view(BF).view(pages, PAGE, 1, 128)
+    fmt = mla.INDEX_FP8 if fp8 else mla.INDEX_16BIT
+    bt = torch.tensor([[pages - 1, pages - 3, pages - 2]] * 2, dtype=torch.int32)
+    t = torch.arange(n)
+    slots = (bt[0, t // PAGE] * PAGE + t % PAGE).int()
+    zero = torch.zeros(n, dtype=torch.int32, device=DEV)
+    mla.mla_append_index_k(k.to(DEV), ic, slots.to(DEV), zero, _table(), index_format=fmt)
+    assert not cache[:3].any()
+    if fp8:
+        _, codes, scale = oracle.index_row_codes(k, TABLE[:1], False)
+        kv = oracle.e4m3_value_table()[codes] * scale.astype(np.float64)[:, None]
+        _, codes, scale = oracle.index_row_codes(q, TABLE[:1], False)
+        qv, w = oracle.e4m3_value_table()[codes], w * torch.from_numpy(scale)
+        qd = torch.from_numpy(codes).view(torch.float8_e4m3fn).to(DEV)
+    else:
+        kv, qv, qd = oracle.to_f64(k), oracle.to_f64(q), q.to(DEV)
+    wide = torch.empty(2, 1, 2 ** 30 + 64, device=DEV)
+    scores = wide[..., :PAGE * 3]
+    sl = torch.tensor([n, 70], dtype=torch.int32, device=DEV)
+    mla.mla_index_score(qd[:, None], w[:, None].contiguous().to(DEV), ic, bt.to(DEV), sl, index_format=fmt, scores=scores)
+    for b, seen in enumerate((n, 70)):
+        ref, err = np.full((1, PAGE * 3), -np.inf), np.zeros((1, PAGE * 3))
+        ref[:, :seen] = oracle.index_score(qv[b:b + 1], oracle.to_f64(w[b:b + 1]), kv[:seen])
+        err[:, :seen] = oracle.index_score_error(qv[b:b + 1], oracle.to_f64(w[b:b + 1]), kv[:seen])
+        _check_scores(scores[b], ref, err, f"request {b}")
+    idx, cnt = mla.mla_select_topk(scores, sl, 50, bt.to(DEV), pages)
+    ref, want = _select_ref(scores.cpu().numpy(), [n, 70], 1, False, 1, 50, bt.numpy(), pages)
+    assert (idx.cpu().numpy() == ref).all() and (cnt.cpu().numpy() == want).all()
+
+
+def test_rotate_q_of_rows_4_gb_apart():
+    far = 2 ** 31 + 64
+    buf = torch.empty(far + 256, dtype=BF, device=DEV)
+    x = torch.randn(2, 2, 64, generator=_gen(8)).to(BF)
+    src, dst = (buf.as_strided((2, 2, 64), (far, 64, 1), at) for at in (0, 128))
+    src.copy_(x)
+    pos = torch.tensor([9, 4999], dtype=torch.int32, device=DEV)
+    mla.mla_rotate_q(src, pos, _table(), out=dst)
+    assert torch.equal(dst.cpu(), oracle.round_to(oracle.rotate(x, TABLE[[9, 4999]][:, None], False), BF))
+    assert torch.equal(src.cpu(), x)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("s_q,heads", [(1, 64), (3, 16), (11, 64)])
+def test_index_score_of_poisoned_keys(s_q, heads, kind):
+    """NaN and infinities behind the visible tokens, in pages that no table names and in their scales change nothing; a
+    visible key of NaN counts as 0."""
+    lens = [100, 0, 129, 64]
+    q, w, cache, bt, qv, kv = _score_case(lens, s_q, heads, kind, seed=s_q + heads, spare=3)
+    fp8 = kind == "fp8"
+    nan, inf = float("nan"), float("inf")
+    seen = {}
+    for b, n in enumerate(lens):
+        for t in range(n):
+            seen[(int(bt[b, t // PAGE]), t % PAGE)] = b
+    for p in range(len(cache)):
+        for r in range(PAGE):
+            if (p, r) not in seen:
+                if fp8:
+                    cache[p, r * 128:(r + 1) * 128] = 0x7F
+                    cache[p, 8192:].view(torch.float32)[r] = nan if r % 2 else inf
+                else:
+                    cache[p, r] = nan if r % 2 else inf
+    blind = (int(bt[0, 0]), 5)                                   # token 5 of request 0
+    if fp8:
+        cache[blind[0], 5 * 128:6 * 128] = 0x7F
+    else:
+        cache[blind] = nan
+    kv[blind] = 0.0
+    kv[~np.isfinite(kv)] = 0.0
+    fmt = mla.INDEX_FP8 if fp8 else mla.INDEX_16BIT
+    st = _status()
+    args = (q.to(DEV), w.to(DEV), cache.to(DEV), torch.from_numpy(bt).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV))
+    ref, err = _score_ref(lens, s_q, True, bt, qv, w, kv, bt.shape[1] * PAGE)
+    _check_scores(mla.mla_index_score(*args, causal=True, index_format=fmt, status=st), ref, err, "tokens")
+    pages = mla.mla_index_score(*args, causal=True, index_format=fmt, block=64, status=st)
+    _check_scores(pages, oracle.page_max(ref), oracle.page_max(err), "pages")
+    assert _bits(st) == 0
