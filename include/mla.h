@@ -457,6 +457,107 @@ MLA_API mla_status mla_select_topk(const float* scores, int64_t score_stride, in
                                    int32_t* indices, int32_t* lens, uint32_t* status, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Prompts over the paged latent cache: the norms of the projections with the
+ * rotary positions in the same pass, the normalised append, cached rows read
+ * back in 16 bits, and the attention of many new tokens. The pages stop at the
+ * decode; these calls are this library's own. The conventions of the calls
+ * above hold (positions and table, slots, status, strides, no shared memory
+ * between an output and another argument but where it is named).
+ *
+ * RMS norm of a row of d values: y = x * (1 / sqrt(mean(x^2) + eps)) * weight, in
+ * fp32 (the sum of squares too), with weight (device, 16-B aligned) of the row's
+ * type or NULL for ones. y stays in fp32 through the rotation or quantisation
+ * that follows and is rounded once, to the type it is stored in. eps >= 0.
+ */
+
+/*
+ * Norm and rotation of queries or keys for each head: x (device) [tokens, heads,
+ * dim] with token and head strides, dim a multiple of 8 from 64 to 576 (above:
+ * MLA_ERR_UNSUPPORTED); the norm is over all dim values, then dims [rope_at,
+ * rope_at + 64) are turned (rope_at a multiple of 8).
+ * out (device) [tokens, heads, dim], or, with rope_out, the dim - 64 other values
+ * of each row side by side, rope_out [tokens, heads, 64] taking the turned ones:
+ * a decode's query wants the others dense for mla_absorb_q and the turned ones
+ * in dims [512, 576) of its own rows. out may be x itself (in place, without
+ * rope_out); with dim 64 and rope_out, out is not read and may be NULL.
+ */
+MLA_API mla_status mla_norm_rotate(const void* x, int64_t x_token_stride, int64_t x_head_stride, const void* weight,
+                                   float eps, int dim, int rope_at, void* out, int64_t out_token_stride,
+                                   int64_t out_head_stride, void* rope_out, int64_t rope_token_stride,
+                                   int64_t rope_head_stride, int dtype, const int32_t* positions,
+                                   const float* rope_table, int64_t max_positions, int rope_style, int64_t tokens,
+                                   int heads, uint32_t* status, void* stream);
+
+/*
+ * mla_append_kv with the latent dims normalised on the way (the norm is over the
+ * 512 latent dims of a token, 448 for V4.1 rows; the RoPE dims take no part).
+ * Quantised rows are formed from the norm's fp32 values.
+ * rows_out (device, optional) [n, 576] (V4.1 rows: 512) of `dtype`, rows
+ *          rows_stride apart: the same rows as a 16-bit cache would hold them,
+ *          for the prompt's own attention; skipped tokens leave theirs as it was.
+ */
+MLA_API mla_status mla_norm_append_kv(const void* c_kv, int64_t c_stride, const void* k_rope, int64_t r_stride,
+                                      const void* weight, float eps, int dtype, const int32_t* slots,
+                                      const int32_t* positions, const float* rope_table, int64_t max_positions,
+                                      int rope_style, int64_t n, void* kvcache, int64_t num_blocks, int page_block,
+                                      int kv_format, void* rows_out, int64_t rows_stride, uint32_t* status,
+                                      void* stream);
+
+/*
+ * Rows of the cache read back in 16 bits, packed: row o of out, offsets[b] <= o <
+ * offsets[b + 1], is token starts[b] + o - offsets[b] of request b (starts NULL:
+ * 0). Values are code x scale, formed in fp32 and rounded once to `dtype`; 16-bit
+ * rows are copied (`dtype` is the cache's type then).
+ * offsets (device) int32 [batch + 1], ascending; starts (device) int32 [batch].
+ * out     (device) [total, 576] (V4.1 rows: 512, the last 64 of them RoPE dims),
+ *         rows out_stride apart. Rows behind offsets[batch] are left as they were;
+ *         offsets behind `total` are not written.
+ * A token whose page is out of range, or lies behind its block-table row, reads
+ * as zeros and is recorded as an index error in `status`.
+ */
+MLA_API mla_status mla_read_kv(const void* kvcache, int64_t num_blocks, int page_block, int kv_format,
+                               const int32_t* block_table, int max_blocks, const int32_t* offsets,
+                               const int32_t* starts, int batch, int64_t total, void* out, int64_t out_stride,
+                               int dtype, uint32_t* status, void* stream);
+
+/*
+ * Attention of many new tokens in the expanded form: documents b of packed rows
+ * cu_seqlens_q[b] .. cu_seqlens_q[b + 1] (n_q queries) and cu_seqlens_k[b] ..
+ * cu_seqlens_k[b + 1] (n_k keys). For query i of document b and head h:
+ *     s_j = softmax_scale (q[i, h, 0:128] . k_nope[j, h] + q[i, h, 128:192] . k_rope[j])
+ *     out[i, h] = sum_j softmax(s)_j v[j, h],   lse[i, h] = ln sum_j exp s_j
+ * over its visible keys j: all n_k, or with `causal` those below n_k - n_q + i + 1
+ * (the last query sees all keys), but at least the first prefix_lens[b] (a prefix
+ * that all queries see). A query that sees no key gets out = 0, lse = -inf.
+ * Per (query, key) pair 640 FLOP a head, where the decode's absorbed form takes
+ * 2176: the form for prompts and their chunks; keys and values come from the
+ * latent rows by the model's up-projections.
+ * q      (device) [tokens_q, heads, 192], `dtype`, any token and head strides of at
+ *        least a row (a head stride of 0, shared heads, is refused).
+ * k_nope, v (device) [tokens_k, heads, 128] likewise (column ranges of one
+ *        projection are fine); k_rope (device) [tokens_k, 64], rotated, shared by
+ *        the heads. Keys and values of a document must be finite as far as its
+ *        queries' tiles of 128 reach; what stands behind a document's keys does not matter.
+ * cu_seqlens_q, cu_seqlens_k (device) int32 [batch + 1], ascending; prefix_lens
+ *        (device, optional) int32 [batch], kept within [0, n_k]; not read unless
+ *        causal. A document whose offsets descend or leave the tensors is skipped
+ *        and recorded as an index error in `status`.
+ * out    (device) [tokens_q, heads, 128] with strides; lse (device) fp32 [tokens_q,
+ *        heads]. Rows of no document are left as they were.
+ * workspace (device, 16-B aligned) of mla_prefill_workspace_size() bytes (0: none
+ *        needed), for the call alone until it has run; its contents do not matter.
+ */
+MLA_API size_t mla_prefill_workspace_size(int64_t tokens_q, int64_t tokens_k, int batch, int heads);
+MLA_API mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_nope,
+                               int64_t k_token_stride, int64_t k_head_stride, const void* k_rope, int64_t rope_stride,
+                               const void* v, int64_t v_token_stride, int64_t v_head_stride, int dtype,
+                               const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, const int32_t* prefix_lens,
+                               int batch, int64_t tokens_q, int64_t tokens_k, int heads, float softmax_scale,
+                               int causal, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                               void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+
+/*
  * Synchronise `stream`, read and clear the status word of `workspace` (or of
  * any 4-B status word, e.g. the one given to mla_absorb_q), and return the
  * first error it records, in the order timeout, stale metadata, index, range

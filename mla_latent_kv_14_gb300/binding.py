@@ -86,8 +86,19 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.mla_index_score.argtypes = [vp, i32, vp, vp, i32, i64, i32, vp, i32, vp, i32, i32, i32, i32, i32, vp,
                                         i64, i32, vp, vp]
         lib.mla_select_topk.argtypes = [vp, i64, i32, vp, i32, i32, i32, i32, i32, vp, i32, i64, i32, vp, vp, vp, vp]
+        f32, size = c.c_float, c.c_size_t
+        lib.mla_norm_rotate.argtypes = [vp, i64, i64, vp, f32, i32, i32, vp, i64, i64, vp, i64, i64, i32] + rope + [
+            i64, i32, vp, vp]
+        lib.mla_norm_append_kv.argtypes = [vp, i64, vp, i64, vp, f32, i32, vp] + rope + [
+            i64, vp, i64, i32, i32, vp, i64, vp, vp]
+        lib.mla_read_kv.argtypes = [vp, i64, i32, i32, vp, i32, vp, vp, i32, i64, vp, i64, i32, vp, vp]
+        lib.mla_prefill.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, i32, vp, vp, vp, i32, i64, i64, i32,
+                                    f32, i32, vp, i64, i64, vp, vp, size, vp, vp]
+        lib.mla_prefill_workspace_size.restype = size
+        lib.mla_prefill_workspace_size.argtypes = [i64, i64, i32, i32]
         for name in ("mla_append_kv", "mla_rotate_q", "mla_append_index_k", "mla_quantize_index_q",
-                     "mla_index_score", "mla_select_topk"):
+                     "mla_index_score", "mla_select_topk", "mla_norm_rotate", "mla_norm_append_kv", "mla_read_kv",
+                     "mla_prefill"):
             getattr(lib, name).restype = c.c_int
         lib.mla_set_test_stall.restype = None
         lib.mla_set_test_stall.argtypes = [c.c_uint32]
@@ -474,3 +485,63 @@ def mla_select_topk(scores: torch.Tensor, cache_seqlens: torch.Tensor, topk: int
     of one query. ``num_blocks``: pages of the cache that the rows index."""
     return (_host or load_host()).mla_select_topk(scores, cache_seqlens, topk, block_table, num_blocks, causal, block,
                                                    indices, lens, status)
+
+
+# ---------------------------------------------------------------------------
+# Prompts over the latent cache
+# ---------------------------------------------------------------------------
+def mla_norm_rotate(x: torch.Tensor, positions: torch.Tensor, rope_table: torch.Tensor,
+                    weight: Optional[torch.Tensor] = None, eps: float = 1e-6, rope_at: Optional[int] = None,
+                    out: Optional[torch.Tensor] = None, rope_out: Optional[torch.Tensor] = None,
+                    rope_style: int = ROPE_PAIRS, status: Optional[torch.Tensor] = None):
+    """RMS norm of queries or keys for each head, with the rotation of dims
+    [rope_at, rope_at + 64) in the same pass (the last 64 unless given): x [tokens,
+    heads, dim] of any token and head strides -> out of the same shape (``x``
+    itself, or allocated). With ``rope_out`` [tokens, heads, 64] (for example
+    ``q_abs[..., 512:]``) the turned dims go there and out [tokens, heads, dim - 64]
+    takes the others; returns (out, rope_out) then. ``weight`` [dim] of x's type.
+    Rows of tokens whose position is negative are not written."""
+    return (_host or load_host()).mla_norm_rotate(x, positions, rope_table, weight, eps, rope_at, out, rope_out,
+                                                   rope_style, status)
+
+
+def mla_norm_append_kv(c_kv: torch.Tensor, k_rope: torch.Tensor, weight: Optional[torch.Tensor], kvcache: torch.Tensor,
+                       slots: torch.Tensor, positions: torch.Tensor, rope_table: torch.Tensor, eps: float = 1e-6,
+                       kv_format: int = KV_16BIT, rope_style: int = ROPE_PAIRS, rows: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """:func:`mla_append_kv` with the latent dims RMS-normalised on the way
+    (``weight`` [512], V4.1 rows [448], of c_kv's type, or None). ``rows`` [n, 576]
+    (V4.1 rows: 512) optionally takes the same rows in 16 bits, for the prompt's
+    own attention. Returns kvcache."""
+    return (_host or load_host()).mla_norm_append_kv(c_kv, k_rope, weight, kvcache, slots, positions, rope_table, eps,
+                                                      kv_format, rope_style, rows, status)
+
+
+def mla_read_kv(kvcache: torch.Tensor, block_table: torch.Tensor, offsets: torch.Tensor, total: Optional[int] = None,
+                starts: Optional[torch.Tensor] = None, kv_format: int = KV_16BIT, dtype: Optional[torch.dtype] = None,
+                out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows of the paged cache read back in 16 bits and packed: rows offsets[b] ..
+    offsets[b + 1] of the result [total, 576] (V4.1 rows: 512) are the tokens of
+    request b from ``starts[b]`` (0) on; the last 64 dims are the rotated ones.
+    ``total`` or ``out`` gives the number of rows (offsets stay on the device).
+    ``dtype`` of quantised rows: bf16 (default) or fp16."""
+    code = -1 if dtype is None else DTYPE_CODES.get(dtype)
+    if code is None:
+        raise MLAError(1, f"mla_read_kv: dtype {dtype}")
+    return (_host or load_host()).mla_read_kv(kvcache, block_table, offsets, total, starts, kv_format, code, out, status)
+
+
+def mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                cu_seqlens_k: torch.Tensor, softmax_scale: float, causal: bool = True,
+                prefix_lens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                lse: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of many new tokens in the expanded form, over packed documents:
+    q [tokens_q, heads, 192] (128 plain dims, 64 rotated), k_nope and v [tokens_k,
+    heads, 128], k_rope [tokens_k, 64] shared by the heads; rows cu_seqlens_q[b] ..
+    cu_seqlens_q[b + 1] attend to keys cu_seqlens_k[b] .. cu_seqlens_k[b + 1]. Causal:
+    the last query sees all keys, each before it one fewer, and every query at least
+    the first ``prefix_lens[b]``. Returns (out [tokens_q, heads, 128], lse fp32
+    [tokens_q, heads]); a query that sees nothing gets 0 and -inf."""
+    return (_host or load_host()).mla_prefill(q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, softmax_scale, causal,
+                                               prefix_lens, out, lse, status)

@@ -24,7 +24,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla.so")
 HOST = os.path.join(HERE, "_host.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["mla_api.cu", "cache_api.cu"]
+SOURCES = ["mla_api.cu", "cache_api.cu", "prompt_api.cu"]
 
 
 def _nvcc() -> str:

@@ -1,5 +1,6 @@
 // host_binding.cpp -- the Python side of the calls around the decode (appends,
-// rotation, index rows, index score, selection): checks of the tensors, their
+// rotation, norms, index rows, index score, selection, rows read back, the
+// attention of prompts): checks of the tensors, their
 // device and stream, allocation of outputs, and the call of the C entry point.
 //
 // These calls take one to a few microseconds on the GPU at a decode step's
@@ -15,6 +16,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <optional>
@@ -375,6 +377,189 @@ PyObject* select_topk(Call& c, PyObject* const* a) {
   return pair(indices, lens);
 }
 
+// a number that fits fp32
+float real(const Call& c, PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised();
+  const float f = static_cast<float>(v);
+  if (!std::isfinite(f)) c.refuse("%s: a finite number", name);
+  return f;
+}
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised();
+  return v != 0;
+}
+// the weights of a norm: [dim] like x, or None
+const void* gain(Call& c, PyObject* o, int64_t dim, const at::Tensor& x) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = c.tensor(o, "weight");
+  if (t.scalar_type() != x.scalar_type() || !is_shape(t, {dim}) || !t.is_contiguous())
+    c.refuse("weight: contiguous [%lld] of the rows' type", (long long)dim);
+  c.on_device(t);
+  return t.data_ptr();
+}
+// rows of heads that the caller gives for an output
+void check_rows(Call& c, const at::Tensor& t, const char* name, int64_t tokens, int64_t heads, int64_t dim, const at::Tensor& like) {
+  if (!is_shape(t, {tokens, heads, dim}) || t.scalar_type() != like.scalar_type() || (dim > 1 && t.stride(2) != 1))
+    c.refuse("%s: [tokens, heads, %lld] of the input's type, dense rows", name, (long long)dim);
+  c.on_device(t);
+}
+
+// (x, positions, rope_table, weight, eps, rope_at, out, rope_out, rope_style, status)
+PyObject* norm_rotate(Call& c, PyObject* const* a) {
+  const at::Tensor& x = c.tensor(a[0], "x");
+  const int code = dtype_code(x);
+  if (code < 0 || x.dim() != 3 || x.size(2) < 64 || x.stride(2) != 1) c.refuse("x [tokens, heads, dim], bf16 or fp16, dim of at least 64");
+  const int64_t tokens = x.size(0), heads = x.size(1), dim = x.size(2);
+  if (heads > INT32_MAX || dim > INT32_MAX) c.refuse("x's sizes out of range");
+  c.on_device(x);
+  const void* weight = gain(c, a[3], dim, x);
+  const float eps = real(c, a[4], "eps");
+  const int64_t at = a[5] == Py_None ? dim - 64 : c.integer(a[5], "rope_at");
+  const bool split = a[7] != Py_None;
+  const int64_t width = split ? dim - 64 : dim;
+  const at::Tensor out = a[6] == Py_None ? fresh({tokens, heads, width}, x.scalar_type(), x) : c.tensor(a[6], "out");
+  check_rows(c, out, "out", tokens, heads, width, x);
+  const at::Tensor rope = split ? c.tensor(a[7], "rope_out") : at::Tensor();
+  if (split) check_rows(c, rope, "rope_out", tokens, heads, 64, x);
+  const Rope r(c, a[1], a[2], a[8], tokens);
+  auto* st = static_cast<uint32_t*>(c.status(a[9]));
+  c.run([&](void* stream) {
+    return mla_norm_rotate(x.data_ptr(), stride_of(x, 0, dim * heads), stride_of(x, 1, dim), weight, eps, (int)dim, (int)at,
+                           width ? out.data_ptr() : nullptr, stride_of(out, 0, width * heads), stride_of(out, 1, width),
+                           split ? rope.data_ptr() : nullptr, split ? stride_of(rope, 0, 64 * heads) : 0,
+                           split ? stride_of(rope, 1, 64) : 0, code, r.positions, r.table, r.rows, r.style, tokens,
+                           (int)heads, st, stream);
+  });
+  if (split) return pair(out, rope);
+  return THPVariable_Wrap(out);
+}
+
+// (c_kv, k_rope, weight, kvcache, slots, positions, rope_table, eps, kv_format, rope_style, rows, status)
+PyObject* norm_append_kv(Call& c, PyObject* const* a) {
+  const int64_t format = c.integer(a[8], "kv_format");
+  static constexpr int64_t widths[4] = {MLA_HEAD_DIM_K, MLA_FP8_ROW_BYTES, MLA_FP8_528_ROW_BYTES, MLA_FP4_288_ROW_BYTES};
+  if (format < 0 || format > 3) c.refuse("unknown kv_format %lld", (long long)format);
+  const at::Tensor &kv = c.tensor(a[0], "c_kv"), &kr = c.tensor(a[1], "k_rope");
+  const int64_t latent = format >= MLA_KV_FP8_528 ? 448 : 512, n = kv.dim() ? kv.size(0) : 0;
+  const int code = dtype_code(kv);
+  if (code < 0 || !is_shape(kv, {n, latent}) || !is_shape(kr, {n, 64}) || kr.scalar_type() != kv.scalar_type() ||
+      kv.stride(1) != 1 || kr.stride(1) != 1)
+    c.refuse("c_kv [n, %lld] and k_rope [n, 64], bf16 or fp16", (long long)latent);
+  c.on_device(kv);
+  c.on_device(kr);
+  const void* weight = gain(c, a[2], latent, kv);
+  const float eps = real(c, a[7], "eps");
+  const Cache cache(c, a[3], "kvcache", widths[format], format ? at::kByte : kv.scalar_type());
+  const int32_t* slots = int32_vector(c, a[4], "slots", n);
+  const Rope r(c, a[5], a[6], a[9], n);
+  void* rows = nullptr;
+  int64_t rows_stride = latent + 64;
+  if (a[10] != Py_None) {
+    const at::Tensor& t = c.tensor(a[10], "rows");
+    if (t.scalar_type() != kv.scalar_type() || !is_shape(t, {n, latent + 64}) || t.stride(1) != 1)
+      c.refuse("rows [n, %lld] of c_kv's type", (long long)latent + 64);
+    c.on_device(t);
+    rows = t.data_ptr();
+    rows_stride = stride_of(t, 0, latent + 64);
+  }
+  auto* st = static_cast<uint32_t*>(c.status(a[11]));
+  c.run([&](void* stream) {
+    return mla_norm_append_kv(kv.data_ptr(), stride_of(kv, 0, latent), kr.data_ptr(), stride_of(kr, 0, 64), weight, eps,
+                              code, slots, r.positions, r.table, r.rows, r.style, n, cache.data, cache.blocks, cache.page,
+                              (int)format, rows, rows_stride, st, stream);
+  });
+  Py_INCREF(a[3]);
+  return a[3];
+}
+
+// (kvcache, block_table, offsets, total, starts, kv_format, dtype code, out, status); the code -1: the cache's own type,
+// of quantised rows that of `out`, or bf16
+PyObject* read_kv(Call& c, PyObject* const* a) {
+  const int64_t format = c.integer(a[5], "kv_format");
+  static constexpr int64_t widths[4] = {MLA_HEAD_DIM_K, MLA_FP8_ROW_BYTES, MLA_FP8_528_ROW_BYTES, MLA_FP4_288_ROW_BYTES};
+  if (format < 0 || format > 3) c.refuse("unknown kv_format %lld", (long long)format);
+  const at::Tensor& kv = c.tensor(a[0], "kvcache");
+  int64_t code = c.integer(a[6], "dtype");
+  if (format == 0) {
+    if (dtype_code(kv) < 0 || (code >= 0 && code != dtype_code(kv))) c.refuse("a 16-bit cache is read in its own type");
+    code = dtype_code(kv);
+  } else if (code < 0) {
+    code = a[7] != Py_None && dtype_code(c.tensor(a[7], "out")) == MLA_DTYPE_FP16 ? MLA_DTYPE_FP16 : MLA_DTYPE_BF16;
+  }
+  const Cache cache(c, a[0], "kvcache", widths[format], format ? at::kByte : kv.scalar_type());
+  const at::Tensor& table = c.tensor(a[1], "block_table");
+  const int64_t batch = table.dim() == 2 ? table.size(0) : -1;
+  if (table.scalar_type() != at::kInt || batch < 0 || batch > INT32_MAX || table.size(1) > INT32_MAX || !table.is_contiguous())
+    c.refuse("block_table: int32 [batch, max_blocks]");
+  c.on_device(table);
+  const int32_t* offsets = int32_vector(c, a[2], "offsets", batch + 1);
+  const int32_t* starts = a[4] == Py_None ? nullptr : int32_vector(c, a[4], "starts", batch);
+  const int64_t width = format >= MLA_KV_FP8_528 ? 512 : 576;
+  const at::ScalarType type = code == MLA_DTYPE_FP16 ? at::kHalf : at::kBFloat16;
+  const bool given = a[7] != Py_None;
+  int64_t total;
+  if (given) {
+    const at::Tensor& t = c.tensor(a[7], "out");
+    if (t.dim() != 2 || t.size(1) != width || t.scalar_type() != type || t.stride(1) != 1)
+      c.refuse("out [total, %lld] of the type read", (long long)width);
+    c.on_device(t);
+    total = t.size(0);
+    if (a[3] != Py_None && c.integer(a[3], "total") != total) c.refuse("out has another number of rows than total");
+  } else {
+    if (a[3] == Py_None) c.refuse("total (the rows that offsets name), or out");
+    total = c.integer(a[3], "total", 0);
+  }
+  const at::Tensor out = given ? c.tensor(a[7], "out") : fresh({total, width}, type, kv);
+  auto* st = static_cast<uint32_t*>(c.status(a[8]));
+  c.run([&](void* stream) {
+    return mla_read_kv(cache.data, cache.blocks, cache.page, (int)format, static_cast<const int32_t*>(table.data_ptr()),
+                       (int)table.size(1), offsets, starts, (int)batch, total, out.data_ptr(), stride_of(out, 0, width),
+                       (int)code, st, stream);
+  });
+  return THPVariable_Wrap(out);
+}
+
+// (q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, softmax_scale, causal, prefix_lens, out, lse, status)
+PyObject* prefill(Call& c, PyObject* const* a) {
+  const at::Tensor &q = c.tensor(a[0], "q"), &k = c.tensor(a[1], "k_nope"), &kr = c.tensor(a[2], "k_rope"), &v = c.tensor(a[3], "v");
+  const int code = dtype_code(q);
+  if (code < 0 || q.dim() != 3 || q.size(2) != 192 || q.stride(2) != 1) c.refuse("q [tokens, heads, 192], bf16 or fp16");
+  const int64_t tq = q.size(0), heads = q.size(1), tk = k.dim() ? k.size(0) : 0;
+  if (heads > INT32_MAX) c.refuse("heads out of range");
+  for (const at::Tensor* t : {&k, &kr, &v})
+    if (t->scalar_type() != q.scalar_type()) c.refuse("k_nope, k_rope and v of q's type");
+  if (!is_shape(k, {tk, heads, 128}) || !is_shape(v, {tk, heads, 128}) || !is_shape(kr, {tk, 64}) || k.stride(2) != 1 ||
+      v.stride(2) != 1 || kr.stride(1) != 1)
+    c.refuse("k_nope and v [tokens, heads, 128], k_rope [tokens, 64], dense rows");
+  for (const at::Tensor* t : {&q, &k, &kr, &v}) c.on_device(*t);
+  const at::Tensor& cu = c.tensor(a[4], "cu_seqlens_q");
+  const int64_t batch = cu.dim() == 1 ? cu.size(0) - 1 : -1;
+  if (batch < 0 || batch >= INT32_MAX) c.refuse("cu_seqlens_q: int32 [batch + 1]");
+  const int32_t* cu_q = int32_vector(c, a[4], "cu_seqlens_q", batch + 1);
+  const int32_t* cu_k = int32_vector(c, a[5], "cu_seqlens_k", batch + 1);
+  const float scale = real(c, a[6], "softmax_scale");
+  const bool causal = truth(a[7]);
+  const int32_t* prefix = a[8] == Py_None ? nullptr : int32_vector(c, a[8], "prefix_lens", batch);
+  const at::Tensor out = a[9] == Py_None ? fresh({tq, heads, 128}, q.scalar_type(), q) : c.tensor(a[9], "out");
+  check_rows(c, out, "out", tq, heads, 128, q);
+  const at::Tensor lse = output(c, a[10], "lse", at::kFloat, {tq, heads}, q);
+  auto* st = static_cast<uint32_t*>(c.status(a[11]));
+  // partial results of cut units, from the stream's own memory
+  const size_t bytes = mla_prefill_workspace_size(tq, tk, (int)batch, (int)heads);
+  at::Tensor space;
+  if (bytes) space = fresh({(int64_t)bytes}, at::kByte, q);
+  c.run([&](void* stream) {
+    return mla_prefill(q.data_ptr(), stride_of(q, 0, 192 * heads), stride_of(q, 1, 192), k.data_ptr(),
+                       stride_of(k, 0, 128 * heads), stride_of(k, 1, 128), kr.data_ptr(), stride_of(kr, 0, 64), v.data_ptr(),
+                       stride_of(v, 0, 128 * heads), stride_of(v, 1, 128), code, cu_q, cu_k, prefix, (int)batch, tq, tk,
+                       (int)heads, scale, causal, out.data_ptr(), stride_of(out, 0, 128 * heads), stride_of(out, 1, 128),
+                       static_cast<float*>(lse.data_ptr()), bytes ? space.data_ptr() : nullptr, bytes, st, stream);
+  });
+  return pair(out, lse);
+}
+
 template <PyObject* (*kBody)(Call&, PyObject* const*), int kArgs, const char* const& kName>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -404,6 +589,10 @@ constexpr const char* kAppendIndexK = "mla_append_index_k";
 constexpr const char* kQuantizeIndexQ = "mla_quantize_index_q";
 constexpr const char* kIndexScore = "mla_index_score";
 constexpr const char* kSelectTopk = "mla_select_topk";
+constexpr const char* kNormRotate = "mla_norm_rotate";
+constexpr const char* kNormAppendKv = "mla_norm_append_kv";
+constexpr const char* kReadKv = "mla_read_kv";
+constexpr const char* kPrefill = "mla_prefill";
 
 #define MLA_METHOD(name, body, args) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<body, args, name>)), METH_FASTCALL, nullptr}
@@ -415,6 +604,10 @@ PyMethodDef g_methods[] = {
     MLA_METHOD(kQuantizeIndexQ, quantize_index_q, 8),
     MLA_METHOD(kIndexScore, index_score, 11),
     MLA_METHOD(kSelectTopk, select_topk, 10),
+    MLA_METHOD(kNormRotate, norm_rotate, 10),
+    MLA_METHOD(kNormAppendKv, norm_append_kv, 12),
+    MLA_METHOD(kReadKv, read_kv, 9),
+    MLA_METHOD(kPrefill, prefill, 12),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

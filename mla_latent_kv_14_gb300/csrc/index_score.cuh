@@ -51,6 +51,7 @@
 #include <cuda.h>
 
 #include "params.h"
+#include "pipe.cuh"
 #include "ptx.cuh"
 
 namespace mla {
@@ -161,13 +162,6 @@ struct Pages {
   }
 };
 
-// The wait's slow path stands apart from the loops of the issuing threads:
-// what they run per tile has to stay in the instruction cache.
-static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Guard g) { return wait(bar, parity, g); }
-MLA_DEV bool wait_for(uint32_t bar, uint32_t parity, const Guard& g) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, g);
-}
-
 // D[tmem] (+)= A[smem] * B[smem], e4m3 operands, fp32 accumulation
 MLA_DEV void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -176,14 +170,6 @@ MLA_DEV void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint3
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-MLA_DEV void tma_load_3d_plain(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 // acc += w * max(0, (x0, x1)) on packed pairs. One asm block, so that the maxima
 // are written as the pair that the packed fma reads: 785 us where separate
 // expressions took 868 (4 x 1024 causal queries over 16384 bf16 keys, with one
@@ -212,20 +198,6 @@ MLA_DEV void tmem_ld_16x64(uint32_t taddr, uint32_t* r) {
         "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-
-// position in a ring whose length only the host knows: slot and phase are
-// stepped, since a division per tile (some 150 cycles) is what the issuing
-// threads would spend most of their time on
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  MLA_DEV void step(int length) {
-    if (++slot == length) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
-};
 
 enum : int { K_BF16 = 0, K_FP16 = 1, K_FP8 = 2 };
 

@@ -1,0 +1,300 @@
+// prompt_api.cu -- the C entry points of prompts over the paged latent cache:
+// norms with the rotary positions, the normalised append, rows read back, and
+// the attention of many new tokens (include/mla.h). Every argument check
+// happens before anything is enqueued.
+#include <cmath>
+
+#include "checks.h"
+#include "norms.cuh"
+#include "prefill.cuh"
+#include "read.cuh"
+
+using namespace mla;
+
+namespace {
+
+// rows of `inner` heads and `outer` tokens do not overlap one another
+bool rows_apart(int64_t tokens, int64_t token_stride, int64_t heads, int64_t head_stride, int64_t w) {
+  return tokens <= 1 || heads <= 1 || token_stride >= (heads - 1) * head_stride + w || head_stride >= (tokens - 1) * token_stride + w;
+}
+bool style_ok(int s) { return s == MLA_ROPE_PAIRS || s == MLA_ROPE_HALVES; }
+bool eps_ok(float e) { return e >= 0.f && std::isfinite(e); }
+
+template <bool kFp16, int kLanes, int kChunks, int kU>
+mla_status launch_norm(norms::NormRotateParams p, void* stream) {
+  p.groups_per_token = (uint32_t)((p.heads + kU - 1) / kU);
+  constexpr int per = norms::kNormThreads / kLanes;
+  const int64_t groups = p.tokens * p.groups_per_token;
+  return launch(norms::mla_norm_rotate_kernel<kFp16, kLanes, kChunks, kU>, dim3((unsigned)((groups + per - 1) / per)),
+                norms::kNormThreads, 0, stream, p);
+}
+template <bool kFp16>
+mla_status launch_norm_dim(const norms::NormRotateParams& p, void* stream) {
+  const int rest = (p.dim - rows::kRope) / 8;
+  if (rest <= 8) return launch_norm<kFp16, 8, 1, 1>(p, stream);
+  if (rest <= 16) return launch_norm<kFp16, 8, 2, 1>(p, stream);
+  if (rest <= 24) return launch_norm<kFp16, 8, 3, 1>(p, stream);
+  return launch_norm<kFp16, 32, 2, 1>(p, stream);
+}
+
+template <int kFormat, bool kFp16>
+mla_status launch_read(const read::ReadParams& p, void* stream) {
+  constexpr int kRows = 4;
+  const int64_t per = read::kReadWarps * kRows;
+  return launch(read::mla_read_kv_kernel<kFormat, kFp16, kRows>, dim3((unsigned)((p.total + per - 1) / per)),
+                32 * read::kReadWarps, 0, stream, p);
+}
+
+constexpr int kCardSms = 152;
+constexpr int kMostPieces = 16;
+// blocks of 256 queries that `batch` documents of tq rows can have
+int64_t blocks_of(int64_t tq, int64_t batch) {
+  const int64_t some = batch < tq ? batch : tq;     // documents with a row
+  return (tq + (prefill::kBlock - 1) * some) / prefill::kBlock;
+}
+// pieces that the key tiles of a unit are cut into: units that do not fill the card twice are cut until they would three times
+int pieces_of(int64_t tq, int64_t tk, int64_t batch, int64_t heads) {
+  const int64_t units = blocks_of(tq, batch) * heads;
+  if (units == 0 || units >= 2 * kCardSms) return 1;
+  const int64_t want = (3 * kCardSms + units - 1) / units, most = tk / (prefill::kPieceTiles * prefill::kKeys);
+  const int64_t n = want < most ? want : most;
+  return (int)(n < 1 ? 1 : n > kMostPieces ? kMostPieces : n);
+}
+size_t piece_bytes(int64_t tq, int64_t heads) { return (size_t)tq * (size_t)heads * (prefill::kV + 1) * 4; }
+
+// rows of `dim` elements of [rows, heads]: box of 64 elements by 128 rows of a head
+bool make_map_heads(CUtensorMap* m, const void* base, bool fp16, int dim, int64_t heads, int64_t rows, int64_t head_stride,
+                    int64_t row_stride) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
+  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kFp16>
+mla_status launch_prefill(int dev, int64_t grid, void* stream, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& r,
+                          const CUtensorMap& v, const prefill::PrefillParams& p) {
+  static std::atomic<bool> set[kMaxDevices];
+  auto kernel = prefill::mla_prefill_kernel<kFp16>;
+  if (!set[dev].load(std::memory_order_relaxed)) {
+    // the softmax warps wait for the registers that the launch gave the others: without them they would wait for good
+    cudaFuncAttributes at;
+    MLA_CUDA(cudaFuncGetAttributes(&at, kernel));
+    if (at.numRegs < prefill::kRegsLaunch) return MLA_ERR_UNSUPPORTED;
+    MLA_CUDA(set_smem(kernel, prefill::kSmem));
+    set[dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(prefill::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = prefill::kSmem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  MLA_CUDA(cudaLaunchKernelEx(&cfg, kernel, q, k, r, v, p));
+  if (p.splits == 1) return MLA_OK;
+  const int64_t warps = prefill::kCombineThreads / 32, items = p.tq * p.heads;
+  return launch(prefill::mla_prefill_combine_kernel<kFp16>, dim3((unsigned)((items + warps - 1) / warps)),
+                prefill::kCombineThreads, 0, stream, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_norm_rotate(const void* x, int64_t x_token_stride, int64_t x_head_stride, const void* weight, float eps,
+                           int dim, int rope_at, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                           void* rope_out, int64_t rope_token_stride, int64_t rope_head_stride, int dtype,
+                           const int32_t* positions, const float* rope_table, int64_t max_positions, int rope_style,
+                           int64_t tokens, int heads, uint32_t* status, void* stream) {
+  if (tokens < 0 || heads < 1 || tokens >= kMaxRows / heads || max_positions <= 0) return MLA_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || !style_ok(rope_style) || !eps_ok(eps)) return MLA_ERR_INVALID_ARG;
+  if (dim < rows::kRope || dim % 8 || rope_at < 0 || rope_at % 8 || rope_at > dim - rows::kRope) return MLA_ERR_INVALID_ARG;
+  if (dim > norms::kMaxDim) return MLA_ERR_UNSUPPORTED;
+  const int64_t w = rope_out ? dim - rows::kRope : dim;   // values of a row of out
+  const int64_t xt = x_token_stride, xh = x_head_stride, ot = out_token_stride, oh = out_head_stride;
+  if (!stride_ok(xt, 0, tokens) || !stride_ok(xh, 0, heads)) return MLA_ERR_INVALID_ARG;
+  if (w && (!stride_ok(ot, w, tokens) || !stride_ok(oh, w, heads))) return MLA_ERR_INVALID_ARG;
+  if (rope_out && (!stride_ok(rope_token_stride, rows::kRope, tokens) || !stride_ok(rope_head_stride, rows::kRope, heads)))
+    return MLA_ERR_INVALID_ARG;
+  if (status && !aligned(status, 4)) return MLA_ERR_INVALID_ARG;
+  if (tokens == 0) return MLA_OK;
+  if (!x || (w && !out) || !aligned(x, 16) || !aligned(out, 16) || !aligned(rope_out, 16) || !aligned(weight, 16))
+    return MLA_ERR_INVALID_ARG;
+  if (w && !rows_apart(tokens, ot, heads, oh, w)) return MLA_ERR_INVALID_ARG;
+  if (rope_out && !rows_apart(tokens, rope_token_stride, heads, rope_head_stride, rows::kRope)) return MLA_ERR_INVALID_ARG;
+  norms::NormRotateParams p{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(out),
+                            static_cast<uint16_t*>(rope_out), xt, xh, ot, oh, rope_token_stride, rope_head_stride,
+                            {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
+                            tokens, heads, dim, rope_at, eps, 0};
+  if (const mla_status v = check_positions(p.pos)) return v;
+  auto span = [&](const void* at, int64_t ts, int64_t hs, int64_t width) {
+    return Span{at, 2 * ((tokens - 1) * ts + (heads - 1) * hs + width)};
+  };
+  const Span sx = span(x, xt, xh, dim), so = w ? span(out, ot, oh, w) : Span{nullptr, 0},
+             sr = rope_out ? span(rope_out, rope_token_stride, rope_head_stride, rows::kRope) : Span{nullptr, 0};
+  // in place: the same rows, each read as a whole before it is written
+  const bool in_place = !rope_out && out == x && (xt == ot || tokens == 1) && (xh == oh || heads == 1);
+  if (!apart({so, sr, status_span(status)}, {{weight, 2 * (int64_t)dim}, int32_span(positions, tokens), table_span(p.pos)}) ||
+      (!in_place && so.meets(sx)) || sr.meets(sx) || status_span(status).meets(sx))
+    return MLA_ERR_INVALID_ARG;
+  return dtype == MLA_DTYPE_FP16 ? launch_norm_dim<true>(p, stream) : launch_norm_dim<false>(p, stream);
+}
+
+mla_status mla_norm_append_kv(const void* c_kv, int64_t c_stride, const void* k_rope, int64_t r_stride, const void* weight,
+                              float eps, int dtype, const int32_t* slots, const int32_t* positions,
+                              const float* rope_table, int64_t max_positions, int rope_style, int64_t n, void* kvcache,
+                              int64_t num_blocks, int page_block, int kv_format, void* rows_out, int64_t rows_stride,
+                              uint32_t* status, void* stream) {
+  if (n < 0 || n >= kMaxRows || max_positions <= 0 || !cache_ok(num_blocks, page_block)) return MLA_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || kv_format < MLA_KV_16BIT || kv_format > MLA_KV_FP4_288) return MLA_ERR_INVALID_ARG;
+  if (!style_ok(rope_style) || !eps_ok(eps)) return MLA_ERR_INVALID_ARG;
+  const int latent = kv_format >= MLA_KV_FP8_528 ? kDV41 - rows::kRope : kDV, width = latent + rows::kRope;
+  if (!stride_ok(c_stride, latent, n) || !stride_ok(r_stride, rows::kRope, n)) return MLA_ERR_INVALID_ARG;
+  if (rows_out && !stride_ok(rows_stride, width, n)) return MLA_ERR_INVALID_ARG;
+  if (status && !aligned(status, 4)) return MLA_ERR_INVALID_ARG;
+  if (kv_format && dtype != MLA_DTYPE_BF16) return MLA_ERR_UNSUPPORTED;  // quantised rows pair with bf16
+  if (n == 0) return MLA_OK;
+  if (!c_kv || !k_rope || !slots || !kvcache || !aligned(c_kv, 16) || !aligned(k_rope, 16) || !aligned(slots, 4) ||
+      !aligned(kvcache, 16) || !aligned(weight, 16) || !aligned(rows_out, 16))
+    return MLA_ERR_INVALID_ARG;
+  norms::NormAppendParams p{{c_kv, k_rope, c_stride, r_stride, slots,
+                             {positions, rope_table, max_positions, rope_style == MLA_ROPE_HALVES, status},
+                             n, static_cast<uint8_t*>(kvcache), num_blocks * kTile},
+                            static_cast<const uint16_t*>(weight), eps, static_cast<uint16_t*>(rows_out), rows_stride};
+  if (const mla_status v = check_positions(p.a.pos)) return v;
+  static constexpr int64_t row_bytes[4] = {kDK * 2, kRowBytesFp8, kRowBytesFp8_528, kRowBytesFp4_288};
+  if (!apart({{kvcache, p.a.num_rows * row_bytes[kv_format]}, {rows_out, 2 * ((n - 1) * rows_stride + width)}, status_span(status)},
+             {{c_kv, 2 * ((n - 1) * c_stride + latent)}, {k_rope, 2 * ((n - 1) * r_stride + rows::kRope)},
+              {weight, 2 * (int64_t)latent}, int32_span(slots, n), int32_span(positions, n), table_span(p.a.pos)}))
+    return MLA_ERR_INVALID_ARG;
+  const dim3 grid((unsigned)((n + rows::kAppendWarps - 1) / rows::kAppendWarps));
+  const int threads = 32 * rows::kAppendWarps;
+  if (kv_format == MLA_KV_FP8_656) return launch(norms::mla_norm_append_kv_kernel<false, MLA_KV_FP8_656>, grid, threads, 0, stream, p);
+  if (kv_format == MLA_KV_FP8_528) return launch(norms::mla_norm_append_kv_kernel<false, MLA_KV_FP8_528>, grid, threads, 0, stream, p);
+  if (kv_format == MLA_KV_FP4_288) return launch(norms::mla_norm_append_kv_kernel<false, MLA_KV_FP4_288>, grid, threads, 0, stream, p);
+  if (dtype == MLA_DTYPE_FP16) return launch(norms::mla_norm_append_kv_kernel<true, MLA_KV_16BIT>, grid, threads, 0, stream, p);
+  return launch(norms::mla_norm_append_kv_kernel<false, MLA_KV_16BIT>, grid, threads, 0, stream, p);
+}
+
+mla_status mla_read_kv(const void* kvcache, int64_t num_blocks, int page_block, int kv_format, const int32_t* block_table,
+                       int max_blocks, const int32_t* offsets, const int32_t* starts, int batch, int64_t total, void* out,
+                       int64_t out_stride, int dtype, uint32_t* status, void* stream) {
+  if (!cache_ok(num_blocks, page_block) || kv_format < MLA_KV_16BIT || kv_format > MLA_KV_FP4_288 || !dtype_ok(dtype))
+    return MLA_ERR_INVALID_ARG;
+  if (batch < 0 || max_blocks <= 0 || !in_memory(max_blocks, batch) || total < 0 || total >= kMaxRows) return MLA_ERR_INVALID_ARG;
+  const int width = kv_format >= MLA_KV_FP8_528 ? kDV41 : kDK;
+  if (!stride_ok(out_stride, width, total) || (status && !aligned(status, 4))) return MLA_ERR_INVALID_ARG;
+  if (total == 0 || batch == 0) return MLA_OK;
+  if (!kvcache || !block_table || !offsets || !out || !aligned(kvcache, 16) || !aligned(block_table, 4) || !aligned(offsets, 4) ||
+      !aligned(starts, 4) || !aligned(out, 16))
+    return MLA_ERR_INVALID_ARG;
+  static constexpr int64_t row_bytes[4] = {kDK * 2, kRowBytesFp8, kRowBytesFp8_528, kRowBytesFp4_288};
+  if (!apart({{out, 2 * ((total - 1) * out_stride + width)}, status_span(status)},
+             {{kvcache, num_blocks * kTile * row_bytes[kv_format]}, int32_span(block_table, (int64_t)batch * max_blocks),
+              int32_span(offsets, (int64_t)batch + 1), int32_span(starts, batch)}))
+    return MLA_ERR_INVALID_ARG;
+  const read::ReadParams p{static_cast<const uint8_t*>(kvcache), block_table, offsets, starts, num_blocks, batch, max_blocks,
+                           total, static_cast<uint16_t*>(out), out_stride, status};
+  const bool fp16 = dtype == MLA_DTYPE_FP16;
+  if (kv_format == MLA_KV_16BIT) return launch_read<MLA_KV_16BIT, false>(p, stream);   // copied, whatever the type
+  if (kv_format == MLA_KV_FP8_656) return fp16 ? launch_read<MLA_KV_FP8_656, true>(p, stream) : launch_read<MLA_KV_FP8_656, false>(p, stream);
+  if (kv_format == MLA_KV_FP8_528) return fp16 ? launch_read<MLA_KV_FP8_528, true>(p, stream) : launch_read<MLA_KV_FP8_528, false>(p, stream);
+  return fp16 ? launch_read<MLA_KV_FP4_288, true>(p, stream) : launch_read<MLA_KV_FP4_288, false>(p, stream);
+}
+
+size_t mla_prefill_workspace_size(int64_t tokens_q, int64_t tokens_k, int batch, int heads) {
+  if (tokens_q <= 0 || tokens_k < 0 || batch <= 0 || heads <= 0 || tokens_q >= kMaxRows || tokens_k >= kMaxRows) return 0;
+  const int n = pieces_of(tokens_q, tokens_k, batch, heads);
+  return n > 1 ? n * piece_bytes(tokens_q, heads) : 0;
+}
+
+mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_nope,
+                       int64_t k_token_stride, int64_t k_head_stride, const void* k_rope, int64_t rope_stride,
+                       const void* v, int64_t v_token_stride, int64_t v_head_stride, int dtype, const int32_t* cu_seqlens_q,
+                       const int32_t* cu_seqlens_k, const int32_t* prefix_lens, int batch, int64_t tokens_q,
+                       int64_t tokens_k, int heads, float softmax_scale, int causal, void* out, int64_t out_token_stride,
+                       int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes, uint32_t* status,
+                       void* stream) {
+  namespace pf = prefill;
+  const int64_t tq = tokens_q, tk = tokens_k;
+  if (tq < 0 || tk < 0 || batch < 0 || heads < 1 || tq >= kMaxRows - 512 || tk >= kMaxRows - 512 || !dtype_ok(dtype))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
+  if (tq >= (int64_t(1) << 44) / heads || tk >= (int64_t(1) << 44) / heads) return MLA_ERR_INVALID_ARG;
+  // TMA strides lie below 2^40 bytes
+  constexpr int64_t kStride = int64_t(1) << 39;
+  auto strides_ok = [&](int64_t token, int64_t head, int64_t rows, int64_t w) {
+    return stride_ok(token, w, rows) && stride_ok(head, w, heads) && token < kStride && head < kStride;
+  };
+  if (!strides_ok(q_token_stride, q_head_stride, tq, pf::kQk) || !strides_ok(k_token_stride, k_head_stride, tk, pf::kNope) ||
+      !strides_ok(v_token_stride, v_head_stride, tk, pf::kV) || !stride_ok(rope_stride, pf::kRopeDim, tk) || rope_stride >= kStride ||
+      !stride_ok(out_token_stride, pf::kV, tq) || !stride_ok(out_head_stride, pf::kV, heads))
+    return MLA_ERR_INVALID_ARG;
+  if (status && !aligned(status, 4)) return MLA_ERR_INVALID_ARG;
+  if (tq == 0 || batch == 0) return MLA_OK;
+  if (!q || !out || !lse || !cu_seqlens_q || !cu_seqlens_k || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) || !aligned(prefix_lens, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (tk > 0 && (!k_nope || !k_rope || !v || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16))) return MLA_ERR_INVALID_ARG;
+  if (!rows_apart(tq, out_token_stride, heads, out_head_stride, pf::kV)) return MLA_ERR_INVALID_ARG;
+  const int splits = pieces_of(tq, tk, batch, heads);
+  const int64_t grid = blocks_of(tq, batch) * heads * splits;
+  if (grid >= kMaxRows || tq * heads >= (kMaxRows - 1) * (pf::kCombineThreads / 32)) return MLA_ERR_UNSUPPORTED;
+  const size_t need = splits > 1 ? splits * piece_bytes(tq, heads) : 0;
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return MLA_ERR_INVALID_ARG;
+  auto span = [&](const void* at, int64_t ts, int64_t hs, int64_t rows, int64_t width) {
+    return rows ? Span{at, 2 * ((rows - 1) * ts + (heads - 1) * hs + width)} : Span{nullptr, 0};
+  };
+  if (!apart({span(out, out_token_stride, out_head_stride, tq, pf::kV), {lse, 4 * tq * heads},
+              {need ? workspace : nullptr, (int64_t)need}, status_span(status)},
+             {span(q, q_token_stride, q_head_stride, tq, pf::kQk), span(k_nope, k_token_stride, k_head_stride, tk, pf::kNope),
+              span(v, v_token_stride, v_head_stride, tk, pf::kV), {tk ? k_rope : nullptr, 2 * ((tk - 1) * rope_stride + pf::kRopeDim)},
+              int32_span(cu_seqlens_q, (int64_t)batch + 1), int32_span(cu_seqlens_k, (int64_t)batch + 1), int32_span(prefix_lens, batch)}))
+    return MLA_ERR_INVALID_ARG;
+
+  pf::PrefillParams p{};
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.prefix = prefix_lens;
+  p.tq = tq;
+  p.tk = tk;
+  p.batch = batch;
+  p.heads = heads;
+  p.causal = causal ? 1 : 0;
+  p.splits = splits;
+  p.scale = softmax_scale;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = out;
+  p.out_token = out_token_stride;
+  p.out_head = out_head_stride;
+  p.lse = lse;
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = need ? p.o_part + (int64_t)splits * tq * heads * pf::kV : nullptr;
+  p.status = status;
+  p.stall_cycles = g_test_stall.load(std::memory_order_relaxed);
+  int dev = 0, sms = 0;
+  if (const mla_status v = sm_count(&dev, &sms)) return v;
+  const bool fp16 = dtype == MLA_DTYPE_FP16;
+  CUtensorMap mq, mk, mr, mv;
+  // without keys nothing is copied through the last three
+  const bool some = tk > 0;
+  if (!make_map_heads(&mq, q, fp16, pf::kQk, heads, tq, q_head_stride, q_token_stride) ||
+      !make_map_heads(&mk, some ? k_nope : q, fp16, pf::kNope, some ? heads : 1, some ? tk : 1, some ? k_head_stride : pf::kNope,
+                      some ? k_token_stride : pf::kNope) ||
+      !make_map_heads(&mr, some ? k_rope : q, fp16, pf::kRopeDim, 1, some ? tk : 1, pf::kRopeDim, some ? rope_stride : pf::kRopeDim) ||
+      !make_map_heads(&mv, some ? v : q, fp16, pf::kV, some ? heads : 1, some ? tk : 1, some ? v_head_stride : pf::kV,
+                      some ? v_token_stride : pf::kV))
+    return MLA_ERR_CUDA;
+  return fp16 ? launch_prefill<true>(dev, grid, stream, mq, mk, mr, mv, p) : launch_prefill<false>(dev, grid, stream, mq, mk, mr, mv, p);
+}
+
+}  // extern "C"

@@ -18,3 +18,6 @@ from .mla_oracle import (  # noqa: F401
 from .index_oracle import (  # noqa: F401
     rope_table, rotate, round_to, append_rows, index_row_codes, index_score, index_score_error, page_max, select_topk,
 )
+from .prompt_oracle import (  # noqa: F401
+    rms_norm, norm_rotate, norm_rotate_error, cached_rows, visible, prefill, prefill_error,
+)
