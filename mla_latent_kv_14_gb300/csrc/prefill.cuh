@@ -24,9 +24,10 @@
 // Few rows over long keys: a unit's key tiles are cut into pieces (p.splits at
 // most), whose partial outputs mla_prefill_combine_kernel joins.
 //
-// Warp roles (384 threads): warp 0 issues the copies, warp 1 owns TMEM and
-// issues the MMAs, warp 2 finds the units, warps 4-7 and 8-11 are the softmax
-// of the two query tiles, one row a thread. Every wait is bounded; a wait that
+// Warp roles (384 threads): warp 0 issues the copies, warps 1 and 3 the MMAs of
+// the first and the second query tile (warp 1 owns TMEM), warp 2 finds the
+// units, warps 4-7 and 8-11 are the softmax of the two query tiles, one row a
+// thread. Every wait is bounded; a wait that
 // gives up sets the status word and the CTA unwinds.
 #pragma once
 #include <cuda.h>
@@ -52,12 +53,12 @@ constexpr uint32_t kOffBar = kOffRing + kRing * kChunk;
 enum : uint32_t {
   B_FULL = 0, B_EMPTY = B_FULL + kRing, B_QFULL = B_EMPTY + kRing, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
   B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 2, B_OEMPTY = B_OFULL + 2, B_UFULL = B_OEMPTY + 2, B_UEMPTY = B_UFULL + 2,
-  B_NEXT = B_UEMPTY + 2, B_DRAIN = B_NEXT + 1, B_STALL = B_DRAIN + 1, B_COUNT = B_STALL + 1
+  B_NEXT = B_UEMPTY + 2, B_DRAIN = B_NEXT + 1, B_STALL = B_DRAIN + 2, B_COUNT = B_STALL + 1
 };
 constexpr uint32_t kOffMisc = (kOffBar + 8 * B_COUNT + 15) / 16 * 16;
 constexpr uint32_t kSmem = kOffMisc + 256 + 1024;
 constexpr uint32_t kColO = 256;            // TMEM: S_w at 128 w (P_w over it), O_w at 256 + 128 w
-constexpr int kUnitReaders = 10;           // producer, MMA and eight softmax warps
+constexpr int kUnitReaders = 11;           // producer, two MMA and eight softmax warps
 
 struct PrefillParams {
   const int32_t* cu_q;         // [batch + 1]
@@ -99,6 +100,18 @@ MLA_DEV int visible(const PrefillParams& p, const Span& s, int i) {
 MLA_DEV int pieces_of(const PrefillParams& p, int tiles) {
   return max(1, min(p.splits, tiles / kPieceTiles));
 }
+
+// Ring positions: tile number `tile` of the CTA takes five consecutive chunks, three of keys and two of values; the two
+// of values stand side by side (one descriptor covers both).
+struct Slots {
+  uint32_t first;    // chunks before this tile
+  bool late;         // the values would wrap around: they come before the last chunk of keys
+  MLA_DEV explicit Slots(uint32_t tile) : first(5u * tile), late((first + 3u) % kRing == kRing - 1u) {}
+  MLA_DEV uint32_t key(int c) const { return first + (c < 2 ? c : late ? 4 : 2); }
+  MLA_DEV uint32_t value(int c) const { return first + (late ? 2 : 3) + c; }
+};
+MLA_DEV uint32_t slot_of(uint32_t chunk) { return chunk % kRing; }
+MLA_DEV uint32_t phase_of(uint32_t chunk) { return chunk / kRing & 1u; }
 
 // A unit as its readers see it (one piece of 256 queries of a head).
 struct Unit {
@@ -256,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRing; ++s) {
       mbar_init(bar(B_FULL + s), 1);
-      mbar_init(bar(B_EMPTY + s), 1);
+      mbar_init(bar(B_EMPTY + s), 2);   // both query tiles' products
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(B_QFULL + w), 1);
@@ -270,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(B_NEXT), 1);
     mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_DRAIN + 1), 1);
     mbar_init(bar(B_STALL), 1);
     *abort_flag = 0u;
     *ok_flag = 1u;
@@ -295,16 +309,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const bool ok = *ok_flag != 0u;
 
-  // the readers' side of the units: the n-th one, into registers
-  auto take = [&](int n, Unit& u) {
+  // the readers' side of the units: the n-th one, into registers; one lane reads for a role of a single thread
+  auto take_one = [&](int n, Unit& u) {
     const int s = n & 1;
-    if (!__all_sync(0xffffffffu, wait_inline(bar(B_UFULL + s), (n >> 1) & 1, guard))) return false;
-    int* at = units + 16 * s;
+    if (!wait_inline(bar(B_UFULL + s), (n >> 1) & 1, guard)) return false;
+    const volatile int* at = units + 16 * s;
     u.head = at[0]; u.row = at[1]; u.rows = at[2]; u.k0 = at[3]; u.nk = at[4]; u.seen = at[5]; u.prefix = at[6];
     u.t0 = at[7]; u.t1 = at[8]; u.piece = at[9]; u.pieces = at[10];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(B_UEMPTY + s));
-    return u.head >= 0;
+    return true;
+  };
+  auto take = [&](int n, Unit& u) {
+    const bool got = __all_sync(0xffffffffu, take_one(n, u));
+    if (got && lane == 0) mbar_arrive(bar(B_UEMPTY + (n & 1)));
+    return got && u.head >= 0;
   };
 
   if (warp < 4) {
@@ -366,12 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tm_r);
         prefetch_tmap(&tm_v);
       }
-      int n = 0, loads = 0, q_loads[2] = {0, 0};
-      uint32_t slot = 0, phase = 0;
+      int n = 0, q_loads[2] = {0, 0};
+      uint32_t loads = 0, tile = 0;
       bool stop = false;
       Unit u;
       auto chunk = [&](const CUtensorMap* m, int x, int y, int z) {
-        if (!__all_sync(0xffffffffu, wait_inline(bar(B_EMPTY + slot), phase ^ 1u, guard))) {
+        const uint32_t slot = slot_of(loads);
+        if (stop || !__all_sync(0xffffffffu, wait_inline(bar(B_EMPTY + slot), phase_of(loads) ^ 1u, guard))) {
           stop = true;
           return;
         }
@@ -380,171 +398,118 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d_plain(sb + kOffRing + slot * kChunk, m, bar(B_FULL + slot), x, y, z);
         }
         ++loads;
-        if (++slot == kRing) {
-          slot = 0;
-          phase ^= 1u;
+      };
+      auto queries = [&](int w) {
+        if (stop || !__all_sync(0xffffffffu, wait_inline(bar(B_QEMPTY + w), (q_loads[w] & 1) ^ 1, guard))) {
+          stop = true;
+          return;
         }
+        if (leader) {
+          mbar_arrive_expect_tx(bar(B_QFULL + w), kQTile);
+          for (int c = 0; c < 3; ++c)
+            tma_load_3d_plain(sb + w * kQTile + c * kChunk, &tm_q, bar(B_QFULL + w), 64 * c, u.head, u.row + kRows * w);
+        }
+        ++q_loads[w];
       };
       for (; !stop && take(n, u); ++n) {
         const int e0 = u.end(0, p.causal), e1 = u.end(1, p.causal), e = max(e0, e1);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (stop || (w ? e1 : e0) <= u.t0) continue;
-          if (!__all_sync(0xffffffffu, wait_inline(bar(B_QEMPTY + w), (q_loads[w] & 1) ^ 1, guard))) {
-            stop = true;
-            break;
-          }
-          if (leader) {
-            mbar_arrive_expect_tx(bar(B_QFULL + w), kQTile);
-            for (int c = 0; c < 3; ++c)
-              tma_load_3d_plain(sb + w * kQTile + c * kChunk, &tm_q, bar(B_QFULL + w), 64 * c, u.head, u.row + kRows * w);
-          }
-          ++q_loads[w];
-        }
-        for (int t = u.t0; t < e && !stop; ++t) {
+        if (e0 > u.t0) queries(0);
+        for (int t = u.t0; t < e && !stop; ++t, ++tile) {
           const int at = u.k0 + t * kKeys;
+          const bool late = Slots(tile).late;
           chunk(&tm_k, 0, u.head, at);
-          if (!stop) chunk(&tm_k, 64, u.head, at);
-          if (!stop) chunk(&tm_r, 0, 0, at);
-          if (!stop) chunk(&tm_v, 0, u.head, at);
-          if (!stop) chunk(&tm_v, 64, u.head, at);
+          chunk(&tm_k, 64, u.head, at);
+          if (!late) chunk(&tm_r, 0, 0, at);
+          // the second query tile is wanted after the first one's scores
+          if (t == u.t0 && e1 > u.t0) queries(1);
+          chunk(&tm_v, 0, u.head, at);
+          chunk(&tm_v, 64, u.head, at);
+          if (late) chunk(&tm_r, 0, 0, at);
         }
       }
       // never leave with a copy in flight into this CTA's shared memory
       if (lane == 0) {
         const uint64_t t_0 = cycles();
-        for (int k = loads < kRing ? 0 : loads - kRing; k < loads; ++k)
-          while (!mbar_try_wait(bar(B_FULL + k % kRing), (k / kRing) & 1) && cycles() - t_0 < kDrainLimitCycles) {}
+        for (uint32_t k = loads < kRing ? 0u : loads - kRing; k < loads; ++k)
+          while (!mbar_try_wait(bar(B_FULL + slot_of(k)), phase_of(k)) && cycles() - t_0 < kDrainLimitCycles) {}
         for (int w = 0; w < 2; ++w)
           if (q_loads[w])
             while (!mbar_try_wait(bar(B_QFULL + w), (q_loads[w] - 1) & 1) && cycles() - t_0 < kDrainLimitCycles) {}
       }
-    } else if (warp == 1 && ok) {
-      // ---------------- UMMA issue ----------------
-      constexpr uint32_t idesc_qk = idesc_f16(128, kKeys, !kFp16, false, false);
-      constexpr uint32_t idesc_pv = idesc_f16(128, kV, !kFp16, false, true);
-      const bool leader = elect_one();
-      const uint64_t d_q = sdesc_sw128(sb, 16, 1024), d_ring = sdesc_sw128(sb + kOffRing, 16, 1024);
-      auto ready = [&](uint32_t i, uint32_t parity) { return __all_sync(0xffffffffu, wait_inline(bar(i), parity, guard)) != 0; };
-      int n = 0;
-      uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0}, o_used[2] = {0, 0};
-      uint32_t k_slot = 0, k_phase = 0;      // ring position of the next tile's keys
-      bool failed = false;
-      Unit u;
-      for (; !failed && take(n, u); ++n) {
-        const int end[2] = {u.end(0, p.causal), u.end(1, p.causal)}, e = max(end[0], end[1]);
-        if (e <= u.t0) continue;
-        uint32_t v_slot = 0, v_phase = 0;    // of this tile's values
-        // S_w = Q_w K^T of tile t, whose keys start at k_slot; `last`: no other query tile reads them after
-        auto scores = [&](int w, bool first, bool last) {
-          const uint32_t d = tmem + 128u * w;
+    } else if ((warp & 1) && ok) {
+      // ---------------- UMMA issue for query tile w: one thread ----------------
+      // The pipe takes an instruction about when it starts it, so a wait between two of them idles it, but for the
+      // other tile's: all that can be waited for while the softmax runs (the next keys, the values) is, and the
+      // products of a tile and the scores of the next follow in one go.
+      const int w = warp >> 1;
+      if (elect_one()) {
+        constexpr uint32_t idesc_qk = idesc_f16(128, kKeys, !kFp16, false, false);
+        constexpr uint32_t idesc_pv = idesc_f16(128, kV, !kFp16, false, true);
+        const uint64_t d_q = sdesc_sw128(sb + w * kQTile, 16, 1024), d_ring = sdesc_sw128(sb + kOffRing, 16, 1024),
+                       d_v = sdesc_sw128(sb + kOffRing, kChunk, 1024);
+        const uint32_t t_s = tmem + 128u * w, t_o = tmem + kColO + 128u * w;
+        uint32_t tile = 0, q_used = 0, p_used = 0, o_used = 0;
+        auto ready = [&](uint32_t i, uint32_t parity) { return wait_inline(bar(i), parity & 1u, guard); };
+        auto keys_ready = [&](const Slots& s) {
+          return ready(B_FULL + slot_of(s.key(0)), phase_of(s.key(0))) && ready(B_FULL + slot_of(s.key(1)), phase_of(s.key(1))) &&
+                 ready(B_FULL + slot_of(s.key(2)), phase_of(s.key(2)));
+        };
+        // a chunk is free once both tiles' products that read it are done; `alone`: the other tile has none here
+        auto release = [&](uint32_t chunk, bool alone) {
+          umma_commit(bar(B_EMPTY + slot_of(chunk)));
+          if (alone) umma_commit(bar(B_EMPTY + slot_of(chunk)));
+        };
+        auto scores = [&](const Slots& s, bool alone, bool last) {   // S = Q K^T
 #pragma unroll
           for (int c = 0; c < 3; ++c) {
-            uint32_t s = k_slot + c, ph = k_phase;
-            if (s >= kRing) {
-              s -= kRing;
-              ph ^= 1u;
-            }
-            if (first && !ready(B_FULL + s, ph)) return false;
+            const uint64_t a = d_q + c * (kChunk >> 4), b = d_ring + slot_of(s.key(c)) * (kChunk >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_ss(t_s, a + 2u * k, b + 2u * k, idesc_qk, (c | k) ? 1u : 0u);
+          }
+          umma_commit(bar(B_SFULL + w));
+#pragma unroll
+          for (int c = 0; c < 3; ++c) release(s.key(c), alone);
+          if (last) umma_commit(bar(B_QEMPTY + w));
+        };
+        Unit u;
+        bool failed = false;
+        for (int n = 0; !failed && take_one(n, u); ++n) {
+          mbar_arrive(bar(B_UEMPTY + (n & 1)));
+          if (u.head < 0) break;
+          const int end = u.end(w, p.causal), other = u.end(w ^ 1, p.causal);
+          if (end > u.t0) {
+            const Slots s(tile);
+            if (!ready(B_QFULL + w, q_used++) || !keys_ready(s)) break;
             tc_fence_after();
-            if (leader) {
-              const uint64_t a = d_q + ((w * kQTile + c * kChunk) >> 4), b = d_ring + s * (kChunk >> 4);
+            scores(s, u.t0 >= other, u.t0 + 1 == end);
+          }
+          for (int t = u.t0; t < end; ++t) {
+            const Slots s(tile + (t - u.t0)), next(tile + (t - u.t0) + 1);
+            const uint32_t v0 = s.value(0), v1 = s.value(1);
+            if (!ready(B_FULL + slot_of(v0), phase_of(v0)) || !ready(B_FULL + slot_of(v1), phase_of(v1)) ||
+                (t + 1 < end && !keys_ready(next)) || (t == u.t0 && !ready(B_OEMPTY + w, o_used++ ^ 1u)) ||
+                !ready(B_PFULL + w, p_used++)) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t b = d_v + slot_of(v0) * (kChunk >> 4);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) umma_ss(d, a + 2u * k, b + 2u * k, idesc_qk, (c | k) ? 1u : 0u);
-              if (last) umma_commit(bar(B_EMPTY + s));
-            }
+            for (int k = 0; k < 8; ++k)   // O (+)= P V
+              umma_ts(t_o, t_s + 8u * k, b + 128u * k, idesc_pv, (t == u.t0 && k == 0) ? 0u : 1u);
+            release(v0, t >= other);
+            release(v1, t >= other);
+            if (t + 1 < end) scores(next, t + 1 >= other, t + 2 == end);
+            else umma_commit(bar(B_OFULL + w));
           }
-          if (leader) umma_commit(bar(B_SFULL + w));
-          return true;
-        };
-        auto step = [&](uint32_t& slot, uint32_t& phase, uint32_t by) {
-          slot += by;
-          if (slot >= kRing) {
-            slot -= kRing;
-            phase ^= 1u;
-          }
-        };
-        // O_w (+)= P_w V of tile t
-        auto values = [&](int w, int t, bool first, bool last) {
-          if (!ready(B_PFULL + w, p_used[w] & 1)) return false;
-          ++p_used[w];
-          uint32_t s[2] = {v_slot, v_slot + 1}, ph[2] = {v_phase, v_phase};
-          if (s[1] >= kRing) {
-            s[1] -= kRing;
-            ph[1] ^= 1u;
-          }
-          if (first) {
-            if (!ready(B_FULL + s[0], ph[0]) || !ready(B_FULL + s[1], ph[1])) return false;
-            const int left = u.nk - t * kKeys;
-            if (left < kKeys) {
-              // rows behind the document's keys may hold anything: P is zero there, but not its product with NaN
-              for (int i = left * 8 + lane; i < kKeys * 8; i += 32) {
-                st_shared_v4(sb + kOffRing + s[0] * kChunk + 16u * i, 0u, 0u, 0u, 0u);
-                st_shared_v4(sb + kOffRing + s[1] * kChunk + 16u * i, 0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
-          const bool fresh = t == u.t0;
-          if (fresh) {
-            if (!ready(B_OEMPTY + w, (o_used[w] & 1) ^ 1)) return false;
-            ++o_used[w];
-          }
-          tc_fence_after();
-          if (leader) {
-            // the two chunks of 64 dims may wrap around the ring: one product of N = 64 each then
-            const uint32_t d = tmem + kColO + 128u * w, a = tmem + 128u * w;
-            const uint64_t b0 = sdesc_sw128(sb + kOffRing + s[0] * kChunk, kChunk, 1024);
-            if (s[1] > s[0]) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) umma_ts(d, a + 8u * k, b0 + 128u * k, idesc_pv, (fresh && k == 0) ? 0u : 1u);
-            } else {
-              constexpr uint32_t idesc_half = idesc_f16(128, 64, !kFp16, false, true);
-              const uint64_t b1 = sdesc_sw128(sb + kOffRing + s[1] * kChunk, kChunk, 1024);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                umma_ts(d, a + 8u * k, b0 + 128u * k, idesc_half, (fresh && k == 0) ? 0u : 1u);
-                umma_ts(d + 64u, a + 8u * k, b1 + 128u * k, idesc_half, (fresh && k == 0) ? 0u : 1u);
-              }
-            }
-            if (last) {
-              umma_commit(bar(B_EMPTY + s[0]));
-              umma_commit(bar(B_EMPTY + s[1]));
-            }
-            if (t + 1 == end[w]) umma_commit(bar(B_OFULL + w));
-          }
-          return true;
-        };
-        for (int w = 0; w < 2; ++w)
-          if (end[w] > u.t0) {
-            if (!ready(B_QFULL + w, q_used[w] & 1)) { failed = true; break; }
-            ++q_used[w];
-          }
-        // a tile's first and last reader among the query tiles
-        auto lead = [&](int t) { return t < end[0] ? 0 : 1; };
-        auto trail = [&](int t) { return t < end[1] ? 1 : 0; };
-        for (int t = u.t0 - 1; t < e && !failed; ++t) {
-          // the ring holds tile t's values behind its keys, then tile t + 1
-          if (t >= u.t0) {
-            v_slot = k_slot;
-            v_phase = k_phase;
-            step(v_slot, v_phase, 3);
-            step(k_slot, k_phase, 5);
-          }
-          for (int w = 0; w < 2 && !failed; ++w) {
-            if (t >= u.t0 && t < end[w] && !values(w, t, w == lead(t), w == trail(t))) failed = true;
-            if (!failed && t + 1 < end[w]) {
-              if (!scores(w, w == lead(t + 1), w == trail(t + 1))) failed = true;
-              else if (t + 2 >= end[w] && leader) umma_commit(bar(B_QEMPTY + w));
-            }
-          }
+          tile += max(end, other) - u.t0;
         }
+        // every UMMA this thread issued has completed before TMEM is released
+        umma_commit(bar(B_DRAIN + w));
+        const uint64_t t_0 = cycles();
+        while (!mbar_try_wait(bar(B_DRAIN + w), 0) && cycles() - t_0 < kDrainLimitCycles) {}
       }
-      // every UMMA this thread issued has completed before TMEM is released
-      if (leader) umma_commit(bar(B_DRAIN));
-      const uint64_t t_0 = cycles();
-      while (!mbar_try_wait(bar(B_DRAIN), 0) && cycles() - t_0 < kDrainLimitCycles) {}
+      __syncwarp();
     }
   } else {
     set_registers_up<kRegsMany>();
@@ -554,11 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = tmem + tl + 128u * w, t_o = tmem + tl + kColO + 128u * w;
     const float sl2 = p.scale_log2;
     const float slack = 8.f / sl2;        // raw score units
-    uint32_t s_used = 0, o_used = 0;
+    uint32_t s_used = 0, o_used = 0, tile = 0;
     bool failed = !ok;
     Unit u;
     for (int n = 0; !failed && take(n, u); ++n) {
-      const int end = u.end(w, p.causal), row = kRows * w + r;
+      const int end = u.end(w, p.causal), other = u.end(w ^ 1, p.causal), row = kRows * w + r;
       const int seen = row < u.rows ? u.visible(row, p.causal) : u.nk;
       const int least = kRows * w < u.rows ? u.visible(kRows * w, p.causal) : 0;  // keys that all rows see
       float m = -INFINITY, l = 0.f;
@@ -577,6 +542,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 128; ++k)
             if (k >= left) s[k] = 0xFF800000u;  // -inf
+          const int rest = u.nk - t * kKeys;
+          if (rest < kKeys) {
+            // The value rows behind the document's keys may hold anything, and zero times NaN is NaN: they are cleared
+            // before this tile's P is handed over (by both query tiles, with the same zeros).
+            const Slots at(tile + (t - u.t0));
+            const uint32_t v0 = at.value(0), v1 = at.value(1);
+            if (!__all_sync(0xffffffffu, wait_inline(bar(B_FULL + slot_of(v0)), phase_of(v0), guard) &&
+                                             wait_inline(bar(B_FULL + slot_of(v1)), phase_of(v1), guard))) {
+              failed = true;
+              break;
+            }
+            const uint32_t to = sb + kOffRing + slot_of(v0) * kChunk;   // v1 stands behind v0
+            for (int i = rest * 8 + r; i < kKeys * 8; i += kRows) {
+              st_shared_v4(to + 16u * i, 0u, 0u, 0u, 0u);
+              st_shared_v4(to + kChunk + 16u * i, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
         }
         const float top = fmaxf(tree_max64([&](int k) { return __uint_as_float(s[k]); }),
                                 tree_max64([&](int k) { return __uint_as_float(s[64 + k]); }));
@@ -627,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += x.x + x.y;
       }
       if (failed) break;
+      tile += max(end, other) - u.t0;
       const bool live = row < u.rows;
       const int64_t at = (int64_t)u.row + row;
       const float inv = l > 0.f ? 1.f / l : l;   // NaN stays
