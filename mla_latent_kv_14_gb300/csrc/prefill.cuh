@@ -1,4 +1,6 @@
-// prefill.cuh -- attention of many new tokens in MLA's expanded form, sm_103a.
+// prefill.cuh -- attention of many new tokens in MLA's expanded form, sm_103a:
+// what its two kernels (prefill_pair.cuh, prefill_few.cuh) share, and the join
+// of cut units.
 //
 // For document b, head h and its query i of n_q, over the keys j < vis(i):
 //     s_j = scale (q^C . k^C_j + q^R . k^R_j)          (128 + 64 dims; k^R is shared by the heads)
@@ -7,11 +9,12 @@
 // least prefix_b (a prefix that every query sees). 640 FLOP a visible pair and
 // head, where the decode's absorbed form takes 2176.
 //
-// A unit is 256 consecutive queries of one (document, head): two query tiles of
-// 128 rows, which share every tile of 128 keys and values and take turns on the
+// A unit is a block of consecutive queries of one (document, head), in two query
+// tiles that share every tile of 128 keys and values and take turns on the
 // tensor pipe: while one tile's scores go through the softmax, the pipe
-// multiplies for the other. S (fp32) and P (16 bits, over the S that it comes
-// from) and both accumulators fill TMEM: 2 x 128 + 2 x 128 columns.
+// multiplies for the other. Per 128 rows, S (fp32) and P (16 bits, over the S
+// that it comes from) and the accumulator take 256 columns of TMEM: two tiles
+// fill it.
 //
 // The softmax is online with a lazy reference: the reference maximum of a row
 // moves only when a score passes it by more than 2^8 (P and its sum stay far
@@ -23,12 +26,6 @@
 //
 // Few rows over long keys: a unit's key tiles are cut into pieces (p.splits at
 // most), whose partial outputs mla_prefill_combine_kernel joins.
-//
-// Warp roles (384 threads): warp 0 issues the copies, warps 1 and 3 the MMAs of
-// the first and the second query tile (warp 1 owns TMEM), warp 2 finds the
-// units, warps 4-7 and 8-11 are the softmax of the two query tiles, one row a
-// thread. Every wait is bounded; a wait that
-// gives up sets the status word and the CTA unwinds.
 #pragma once
 #include <cuda.h>
 
@@ -40,25 +37,13 @@ namespace mla {
 namespace prefill {
 
 constexpr int kThreads = 384;
-constexpr int kRows = 128;                 // queries of a tile (UMMA M)
-constexpr int kBlock = 2 * kRows;          // queries of a unit
+constexpr int kRows = 128;                 // rows of a CTA in a query tile (TMEM lanes)
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kNope = 128, kRopeDim = 64, kQk = kNope + kRopeDim, kV = 128;
 constexpr int kPieceTiles = 8;             // key tiles that a piece of a cut unit has at least
 constexpr uint32_t kChunk = 128 * 128;     // 128 rows x 128 bytes (64 dims)
 constexpr uint32_t kQTile = 3 * kChunk;
-constexpr int kRing = 8;                   // chunks: three of K, two of V a tile
-constexpr uint32_t kOffRing = 2 * kQTile;
-constexpr uint32_t kOffBar = kOffRing + kRing * kChunk;
-enum : uint32_t {
-  B_FULL = 0, B_EMPTY = B_FULL + kRing, B_QFULL = B_EMPTY + kRing, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
-  B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 2, B_OEMPTY = B_OFULL + 2, B_UFULL = B_OEMPTY + 2, B_UEMPTY = B_UFULL + 2,
-  B_NEXT = B_UEMPTY + 2, B_DRAIN = B_NEXT + 1, B_STALL = B_DRAIN + 2, B_COUNT = B_STALL + 1
-};
-constexpr uint32_t kOffMisc = (kOffBar + 8 * B_COUNT + 15) / 16 * 16;
-constexpr uint32_t kSmem = kOffMisc + 256 + 1024;
 constexpr uint32_t kColO = 256;            // TMEM: S_w at 128 w (P_w over it), O_w at 256 + 128 w
-constexpr int kUnitReaders = 11;           // producer, two MMA and eight softmax warps
 
 struct PrefillParams {
   const int32_t* cu_q;         // [batch + 1]
@@ -70,6 +55,7 @@ struct PrefillParams {
   float scale, scale_log2;
   void* out;                   // [tq, heads, 128]
   int64_t out_token, out_head; // strides in elements
+  int out_v8;                  // rows of out are 32-B aligned
   float* lse;                  // [tq, heads]
   float* o_part;               // [splits][tq][heads][128], splits > 1
   float* lse_part;             // [splits][tq][heads]
@@ -101,19 +87,8 @@ MLA_DEV int pieces_of(const PrefillParams& p, int tiles) {
   return max(1, min(p.splits, tiles / kPieceTiles));
 }
 
-// Ring positions: tile number `tile` of the CTA takes five consecutive chunks, three of keys and two of values; the two
-// of values stand side by side (one descriptor covers both).
-struct Slots {
-  uint32_t first;    // chunks before this tile
-  bool late;         // the values would wrap around: they come before the last chunk of keys
-  MLA_DEV explicit Slots(uint32_t tile) : first(5u * tile), late((first + 3u) % kRing == kRing - 1u) {}
-  MLA_DEV uint32_t key(int c) const { return first + (c < 2 ? c : late ? 4 : 2); }
-  MLA_DEV uint32_t value(int c) const { return first + (late ? 2 : 3) + c; }
-};
-MLA_DEV uint32_t slot_of(uint32_t chunk) { return chunk % kRing; }
-MLA_DEV uint32_t phase_of(uint32_t chunk) { return chunk / kRing & 1u; }
-
-// A unit as its readers see it (one piece of 256 queries of a head).
+// A unit as its readers see it: one piece of a block of queries of a head, whose two query tiles have kTileRows rows.
+template <int kTileRows>
 struct Unit {
   int head;       // < 0: no more units
   int row;        // first row of q and out
@@ -123,18 +98,29 @@ struct Unit {
   int prefix;
   int t0, t1;     // key tiles of this piece
   int piece, pieces;
+  static constexpr int kWords = 11;
   // keys that row r sees
   MLA_DEV int visible(int r, int causal) const { return causal ? min(max(seen + r, prefix), nk) : nk; }
   // end of the piece's key tiles for query tile w
   MLA_DEV int end(int w, int causal) const {
-    const int last = min(rows, kRows * (w + 1)) - 1;
-    return last < kRows * w ? t0 : max(t0, min(t1, (visible(last, causal) + kKeys - 1) / kKeys));
+    const int last = min(rows, kTileRows * (w + 1)) - 1;
+    return last < kTileRows * w ? t0 : max(t0, min(t1, (visible(last, causal) + kKeys - 1) / kKeys));
+  }
+  MLA_DEV void read(const volatile int* at) {
+    head = at[0]; row = at[1]; rows = at[2]; k0 = at[3]; nk = at[4]; seen = at[5]; prefix = at[6];
+    t0 = at[7]; t1 = at[8]; piece = at[9]; pieces = at[10];
+  }
+  MLA_DEV int word(int k) const {
+    return k == 0 ? head : k == 1 ? row : k == 2 ? rows : k == 3 ? k0 : k == 4 ? nk : k == 5 ? seen : k == 6 ? prefix
+         : k == 7 ? t0 : k == 8 ? t1 : k == 9 ? piece : pieces;
   }
 };
 
-// Units in the order of the grid: documents, heads, blocks of 256 queries (those that see most first), pieces. The
-// warp holds 32 documents' counts and moves on only.
+// Units in the order of the grid: documents, heads, blocks of queries (those that see most first), pieces. The warp
+// holds 32 documents' counts and moves on only.
+template <int kTileRows>
 struct Finder {
+  static constexpr int kBlock = 2 * kTileRows;
   int base;            // first of the 32 documents
   int64_t before;      // blocks (of one head) times heads before them
   int blocks;          // of this lane's document
@@ -163,7 +149,7 @@ struct Finder {
     load(p);
   }
   // the unit of block `id` of the grid; false if there is none (a piece that its unit does not have)
-  MLA_DEV bool find(const PrefillParams& p, int64_t id, Unit& u, bool& past) {
+  MLA_DEV bool find(const PrefillParams& p, int64_t id, Unit<kTileRows>& u, bool& past) {
     const int64_t block = id / p.splits;
     const int piece = (int)(id - block * p.splits);
     past = false;
@@ -219,11 +205,13 @@ MLA_DEV int64_t answer_next(uint32_t src) {
 }
 
 // A bounded wait without a call (a kernel that moves registers between its warps makes none).
+template <bool kCluster>
 MLA_DEV bool wait_inline(uint32_t bar, uint32_t parity, const Guard& g) {
-  if (mbar_try_wait(bar, parity)) return true;
+  auto done = [&]() { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   const uint64_t t0 = cycles();
   while (!*g.abort) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (done()) return true;
     if (cycles() - t0 > g.limit) {
       *g.abort = 1u;
       atomicOr(g.status, STATUS_TIMEOUT);
@@ -245,428 +233,134 @@ MLA_DEV uint32_t pack_p(float lo, float hi) {
   return kFp16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
-// tm_q: dims {192, heads, tq}; tm_k: {128, heads, tk}; tm_r: {64, 1, tk}; tm_v: {128, heads, tk}; boxes {64, 1, 128},
-// 128-byte swizzled.
-template <bool kFp16>
-__global__ void __launch_bounds__(kThreads, 1)
-    mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
-                       const PrefillParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sb = smem_u32(smem);
-  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + kOffMisc);  // 16-B aligned
-  // misc: [0, 4) the answer of ask_next, 4 TMEM base, 5 abort, 6 ok, 7 status where none is given, [16, 48) two units
-  volatile uint32_t* tmem_slot = misc + 4;
-  volatile uint32_t* abort_flag = misc + 5;
-  volatile uint32_t* ok_flag = misc + 6;
-  int* units = reinterpret_cast<int*>(misc + 16);
-  auto bar = [&](uint32_t i) { return sb + kOffBar + 8u * i; };
-  uint32_t* status = p.status ? p.status : misc + 7;
-  const Guard guard{abort_flag, status, kWaitLimitCycles};
+// A thread's row in the softmax of one query tile.
+struct Row {
+  float m, l;                  // reference (raw score) and sum of the weights
+};
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kRing; ++s) {
-      mbar_init(bar(B_FULL + s), 1);
-      mbar_init(bar(B_EMPTY + s), 2);   // both query tiles' products
-    }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(bar(B_QFULL + w), 1);
-      mbar_init(bar(B_QEMPTY + w), 1);
-      mbar_init(bar(B_SFULL + w), 1);
-      mbar_init(bar(B_PFULL + w), 4);
-      mbar_init(bar(B_OFULL + w), 1);
-      mbar_init(bar(B_OEMPTY + w), 4);
-      mbar_init(bar(B_UFULL + w), 1);
-      mbar_init(bar(B_UEMPTY + w), kUnitReaders);
-    }
-    mbar_init(bar(B_NEXT), 1);
-    mbar_init(bar(B_DRAIN), 1);
-    mbar_init(bar(B_DRAIN + 1), 1);
-    mbar_init(bar(B_STALL), 1);
-    *abort_flag = 0u;
-    *ok_flag = 1u;
-    misc[7] = 0u;
-    fence_mbar_init();
-    if (p.stall_cycles) {
-      // test hook: a bounded wait on a barrier nothing arrives at gives up and reports STATUS_TIMEOUT before
-      // anything is issued
-      const Guard g_stall{abort_flag, status, p.stall_cycles};
-      pdl_wait();
-      if (!wait(bar(B_STALL), 0, g_stall)) *ok_flag = 0u;
-    }
+// S of one key tile -> P over it, for the thread's row (its TMEM lane): keys from `left` on are masked where `masked`.
+// hand_over(h) gives keys [64 h, 64 h + 64) of P to the products. `first`: the unit's first tile, whose accumulator
+// holds nothing yet.
+template <bool kFp16, class F>
+MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2, bool masked, int left, bool first, F hand_over) {
+  uint32_t s[128];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32u * c, s + 32 * c);
+  tmem_wait_ld();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) pin_regs32(s + 32 * c);
+  if (masked) {
+#pragma unroll
+    for (int k = 0; k < 128; ++k)
+      if (k >= left) s[k] = 0xFF800000u;  // -inf
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(misc + 4), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  pdl_launch_dependents();
-  pdl_wait();  // nothing above reads global memory
-  const uint32_t tmem = *tmem_slot;
-  const bool ok = *ok_flag != 0u;
-
-  // the readers' side of the units: the n-th one, into registers; one lane reads for a role of a single thread
-  auto take_one = [&](int n, Unit& u) {
-    const int s = n & 1;
-    if (!wait_inline(bar(B_UFULL + s), (n >> 1) & 1, guard)) return false;
-    const volatile int* at = units + 16 * s;
-    u.head = at[0]; u.row = at[1]; u.rows = at[2]; u.k0 = at[3]; u.nk = at[4]; u.seen = at[5]; u.prefix = at[6];
-    u.t0 = at[7]; u.t1 = at[8]; u.piece = at[9]; u.pieces = at[10];
-    return true;
-  };
-  auto take = [&](int n, Unit& u) {
-    const bool got = __all_sync(0xffffffffu, take_one(n, u));
-    if (got && lane == 0) mbar_arrive(bar(B_UEMPTY + (n & 1)));
-    return got && u.head >= 0;
-  };
-
-  if (warp < 4) {
-    set_registers_down<kRegsFew>();
-    if (warp == 2 && ok) {
-      // ---------------- the units ----------------
-      Finder finder;
-      finder.start(p);
-      int64_t id = blockIdx.x;
-      bool more = true, asking = false;
-      int n = 0, asked = 0;
-      while (true) {
-        // the next block's number travels while this one is looked up
-        if (more) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(B_NEXT), 16);
-            ask_next(smem_u32(misc), bar(B_NEXT));
-          }
-          asking = true;
-        }
-        Unit u;
-        u.head = -1;
-        bool past = false;
-        const bool found = more && finder.find(p, id, u, past);
-        if (found || !more) {
-          if (!__all_sync(0xffffffffu, wait_inline(bar(B_UEMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, guard))) break;
-          if (lane == 0) {
-            int* at = units + 16 * (n & 1);
-            at[0] = u.head;
-            if (found) {
-              at[1] = u.row; at[2] = u.rows; at[3] = u.k0; at[4] = u.nk; at[5] = u.seen; at[6] = u.prefix;
-              at[7] = u.t0; at[8] = u.t1; at[9] = u.piece; at[10] = u.pieces;
-            }
-            mbar_arrive(bar(B_UFULL + (n & 1)));
-          }
-          __syncwarp();
-          ++n;
-        }
-        if (!more) break;
-        if (!__all_sync(0xffffffffu, wait_inline(bar(B_NEXT), asked & 1, guard))) break;
-        asking = false;
-        ++asked;
-        id = answer_next(smem_u32(misc));
-        more = id >= 0;
-        // read before the next answer is written over it
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (asking && lane == 0) {   // a wait gave up: the answer is still to be written
-        const uint64_t t_0 = cycles();
-        while (!mbar_try_wait(bar(B_NEXT), asked & 1) && cycles() - t_0 < kDrainLimitCycles) {}
-      }
-    } else if (warp == 0 && ok) {
-      // ---------------- copies: a unit's query tiles, then its keys and values ----------------
-      const bool leader = elect_one();
-      if (leader) {
-        prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_r);
-        prefetch_tmap(&tm_v);
-      }
-      int n = 0, q_loads[2] = {0, 0};
-      uint32_t loads = 0, tile = 0;
-      bool stop = false;
-      Unit u;
-      auto chunk = [&](const CUtensorMap* m, int x, int y, int z) {
-        const uint32_t slot = slot_of(loads);
-        if (stop || !__all_sync(0xffffffffu, wait_inline(bar(B_EMPTY + slot), phase_of(loads) ^ 1u, guard))) {
-          stop = true;
-          return;
-        }
-        if (leader) {
-          mbar_arrive_expect_tx(bar(B_FULL + slot), kChunk);
-          tma_load_3d_plain(sb + kOffRing + slot * kChunk, m, bar(B_FULL + slot), x, y, z);
-        }
-        ++loads;
-      };
-      auto queries = [&](int w) {
-        if (stop || !__all_sync(0xffffffffu, wait_inline(bar(B_QEMPTY + w), (q_loads[w] & 1) ^ 1, guard))) {
-          stop = true;
-          return;
-        }
-        if (leader) {
-          mbar_arrive_expect_tx(bar(B_QFULL + w), kQTile);
-          for (int c = 0; c < 3; ++c)
-            tma_load_3d_plain(sb + w * kQTile + c * kChunk, &tm_q, bar(B_QFULL + w), 64 * c, u.head, u.row + kRows * w);
-        }
-        ++q_loads[w];
-      };
-      for (; !stop && take(n, u); ++n) {
-        const int e0 = u.end(0, p.causal), e1 = u.end(1, p.causal), e = max(e0, e1);
-        if (e0 > u.t0) queries(0);
-        for (int t = u.t0; t < e && !stop; ++t, ++tile) {
-          const int at = u.k0 + t * kKeys;
-          const bool late = Slots(tile).late;
-          chunk(&tm_k, 0, u.head, at);
-          chunk(&tm_k, 64, u.head, at);
-          if (!late) chunk(&tm_r, 0, 0, at);
-          // the second query tile is wanted after the first one's scores
-          if (t == u.t0 && e1 > u.t0) queries(1);
-          chunk(&tm_v, 0, u.head, at);
-          chunk(&tm_v, 64, u.head, at);
-          if (late) chunk(&tm_r, 0, 0, at);
-        }
-      }
-      // never leave with a copy in flight into this CTA's shared memory
-      if (lane == 0) {
-        const uint64_t t_0 = cycles();
-        for (uint32_t k = loads < kRing ? 0u : loads - kRing; k < loads; ++k)
-          while (!mbar_try_wait(bar(B_FULL + slot_of(k)), phase_of(k)) && cycles() - t_0 < kDrainLimitCycles) {}
-        for (int w = 0; w < 2; ++w)
-          if (q_loads[w])
-            while (!mbar_try_wait(bar(B_QFULL + w), (q_loads[w] - 1) & 1) && cycles() - t_0 < kDrainLimitCycles) {}
-      }
-    } else if ((warp & 1) && ok) {
-      // ---------------- UMMA issue for query tile w: one thread ----------------
-      // The pipe takes an instruction about when it starts it, so a wait between two of them idles it, but for the
-      // other tile's: all that can be waited for while the softmax runs (the next keys, the values) is, and the
-      // products of a tile and the scores of the next follow in one go.
-      const int w = warp >> 1;
-      if (elect_one()) {
-        constexpr uint32_t idesc_qk = idesc_f16(128, kKeys, !kFp16, false, false);
-        constexpr uint32_t idesc_pv = idesc_f16(128, kV, !kFp16, false, true);
-        const uint64_t d_q = sdesc_sw128(sb + w * kQTile, 16, 1024), d_ring = sdesc_sw128(sb + kOffRing, 16, 1024),
-                       d_v = sdesc_sw128(sb + kOffRing, kChunk, 1024);
-        const uint32_t t_s = tmem + 128u * w, t_o = tmem + kColO + 128u * w;
-        uint32_t tile = 0, q_used = 0, p_used = 0, o_used = 0;
-        auto ready = [&](uint32_t i, uint32_t parity) { return wait_inline(bar(i), parity & 1u, guard); };
-        auto keys_ready = [&](const Slots& s) {
-          return ready(B_FULL + slot_of(s.key(0)), phase_of(s.key(0))) && ready(B_FULL + slot_of(s.key(1)), phase_of(s.key(1))) &&
-                 ready(B_FULL + slot_of(s.key(2)), phase_of(s.key(2)));
-        };
-        // a chunk is free once both tiles' products that read it are done; `alone`: the other tile has none here
-        auto release = [&](uint32_t chunk, bool alone) {
-          umma_commit(bar(B_EMPTY + slot_of(chunk)));
-          if (alone) umma_commit(bar(B_EMPTY + slot_of(chunk)));
-        };
-        auto scores = [&](const Slots& s, bool alone, bool last) {   // S = Q K^T
+  uint64_t sum[2];
+  const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
+  // 2^(s - m) of keys [32 c, 32 c + 32), packed
+  auto weights = [&](int c, uint32_t* q) {
+    const float ref = row.m == -INFINITY ? 0.f : -row.m * scale_log2;
+    const uint64_t ref2 = f2_pack(ref, ref);
 #pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const uint64_t a = d_q + c * (kChunk >> 4), b = d_ring + slot_of(s.key(c)) * (kChunk >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_ss(t_s, a + 2u * k, b + 2u * k, idesc_qk, (c | k) ? 1u : 0u);
-          }
-          umma_commit(bar(B_SFULL + w));
-#pragma unroll
-          for (int c = 0; c < 3; ++c) release(s.key(c), alone);
-          if (last) umma_commit(bar(B_QEMPTY + w));
-        };
-        Unit u;
-        bool failed = false;
-        for (int n = 0; !failed && take_one(n, u); ++n) {
-          mbar_arrive(bar(B_UEMPTY + (n & 1)));
-          if (u.head < 0) break;
-          const int end = u.end(w, p.causal), other = u.end(w ^ 1, p.causal);
-          if (end > u.t0) {
-            const Slots s(tile);
-            if (!ready(B_QFULL + w, q_used++) || !keys_ready(s)) break;
-            tc_fence_after();
-            scores(s, u.t0 >= other, u.t0 + 1 == end);
-          }
-          for (int t = u.t0; t < end; ++t) {
-            const Slots s(tile + (t - u.t0)), next(tile + (t - u.t0) + 1);
-            const uint32_t v0 = s.value(0), v1 = s.value(1);
-            if (!ready(B_FULL + slot_of(v0), phase_of(v0)) || !ready(B_FULL + slot_of(v1), phase_of(v1)) ||
-                (t + 1 < end && !keys_ready(next)) || (t == u.t0 && !ready(B_OEMPTY + w, o_used++ ^ 1u)) ||
-                !ready(B_PFULL + w, p_used++)) {
-              failed = true;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t b = d_v + slot_of(v0) * (kChunk >> 4);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)   // O (+)= P V
-              umma_ts(t_o, t_s + 8u * k, b + 128u * k, idesc_pv, (t == u.t0 && k == 0) ? 0u : 1u);
-            release(v0, t >= other);
-            release(v1, t >= other);
-            if (t + 1 < end) scores(next, t + 1 >= other, t + 2 == end);
-            else umma_commit(bar(B_OFULL + w));
-          }
-          tile += max(end, other) - u.t0;
-        }
-        // every UMMA this thread issued has completed before TMEM is released
-        umma_commit(bar(B_DRAIN + w));
-        const uint64_t t_0 = cycles();
-        while (!mbar_try_wait(bar(B_DRAIN + w), 0) && cycles() - t_0 < kDrainLimitCycles) {}
-      }
-      __syncwarp();
+    for (int k = 0; k < 16; ++k) {
+      const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1])), scale2, ref2));
+      const float a = exp2_approx(x.x), b = exp2_approx(x.y);
+      sum[k & 1] = f2_add(sum[k & 1], f2_pack(a, b));
+      q[k] = pack_p<kFp16>(a, b);
     }
-  } else {
-    set_registers_up<kRegsMany>();
-    // ---------------- softmax: row `r` of query tile w ----------------
-    const int w = (warp - 4) >> 2, r = 32 * (warp & 3) + lane;
-    const uint32_t tl = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t t_s = tmem + tl + 128u * w, t_o = tmem + tl + kColO + 128u * w;
-    const float sl2 = p.scale_log2;
-    const float slack = 8.f / sl2;        // raw score units
-    uint32_t s_used = 0, o_used = 0, tile = 0;
-    bool failed = !ok;
-    Unit u;
-    for (int n = 0; !failed && take(n, u); ++n) {
-      const int end = u.end(w, p.causal), other = u.end(w ^ 1, p.causal), row = kRows * w + r;
-      const int seen = row < u.rows ? u.visible(row, p.causal) : u.nk;
-      const int least = kRows * w < u.rows ? u.visible(kRows * w, p.causal) : 0;  // keys that all rows see
-      float m = -INFINITY, l = 0.f;
-      for (int t = u.t0; t < end; ++t) {
-        if (!__all_sync(0xffffffffu, wait_inline(bar(B_SFULL + w), s_used & 1, guard))) { failed = true; break; }
-        ++s_used;
-        tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32u * c, s + 32 * c);
+  };
+  // The first weights are formed with the reference as it stands, beside the search for the row's maximum; only where
+  // that passes the reference by too much (in a document's first tiles, hardly ever later) are they formed again.
+  uint32_t q[16];
+  sum[0] = sum[1] = 0;
+  weights(0, q);
+  const float top = fmaxf(tree_max64([&](int k) { return __uint_as_float(s[k]); }),
+                          tree_max64([&](int k) { return __uint_as_float(s[64 + k]); }));
+  const bool move = top > row.m + 8.f / scale_log2;   // from -inf with the first key that it sees
+  if (__any_sync(0xffffffffu, move)) {
+    const float next = move ? top : row.m;
+    // rows that have seen nothing keep l = 0 and O = 0
+    const float f = move ? exp2_approx((row.m - next) * scale_log2) : 1.f;
+    row.m = next;
+    row.l *= f;
+    if (!first) {
+      // S of this tile is complete, and with it every product issued before: O holds still until this tile's P is
+      // handed over
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tmem_ld16(t_o + 16u * c, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) pin_regs32(s + 32 * c);
-        if ((t + 1) * kKeys > least) {
-          const int left = seen - t * kKeys;
-#pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k >= left) s[k] = 0xFF800000u;  // -inf
-          const int rest = u.nk - t * kKeys;
-          if (rest < kKeys) {
-            // The value rows behind the document's keys may hold anything, and zero times NaN is NaN: they are cleared
-            // before this tile's P is handed over (by both query tiles, with the same zeros).
-            const Slots at(tile + (t - u.t0));
-            const uint32_t v0 = at.value(0), v1 = at.value(1);
-            if (!__all_sync(0xffffffffu, wait_inline(bar(B_FULL + slot_of(v0)), phase_of(v0), guard) &&
-                                             wait_inline(bar(B_FULL + slot_of(v1)), phase_of(v1), guard))) {
-              failed = true;
-              break;
-            }
-            const uint32_t to = sb + kOffRing + slot_of(v0) * kChunk;   // v1 stands behind v0
-            for (int i = rest * 8 + r; i < kKeys * 8; i += kRows) {
-              st_shared_v4(to + 16u * i, 0u, 0u, 0u, 0u);
-              st_shared_v4(to + kChunk + 16u * i, 0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-          }
+        for (int k = 0; k < 16; ++k) {
+          asm volatile("" : "+r"(o[k]));
+          o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
         }
-        const float top = fmaxf(tree_max64([&](int k) { return __uint_as_float(s[k]); }),
-                                tree_max64([&](int k) { return __uint_as_float(s[64 + k]); }));
-        const bool move = top > m + slack;   // from -inf with the first key that it sees
-        if (__any_sync(0xffffffffu, move)) {
-          const float next = move ? top : m;
-          // rows that have seen nothing keep l = 0 and O = 0
-          const float f = move ? exp2_approx((m - next) * sl2) : 1.f;
-          m = next;
-          l *= f;
-          if (t > u.t0) {
-            // S of this tile is complete, and with it every product issued before: O holds still until this
-            // tile's P is handed over
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t o[16];
-              tmem_ld16(t_o + 16u * c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                asm volatile("" : "+r"(o[k]));
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              }
-              tmem_st16(t_o + 16u * c, o);
-            }
-          }
-        }
-        const float ref = m == -INFINITY ? 0.f : -m * sl2;
-        const uint64_t scale2 = f2_pack(sl2, sl2), ref2 = f2_pack(ref, ref);
-        uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t q[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1])), scale2, ref2));
-            const float a = exp2_approx(x.x), b = exp2_approx(x.y);
-            sum[k & 3] = f2_add(sum[k & 3], f2_pack(a, b));
-            q[k] = pack_p<kFp16>(a, b);
-          }
-          tmem_st16(t_s + 16u * c, q);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_PFULL + w));
-        const float2 x = f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])));
-        l += x.x + x.y;
-      }
-      if (failed) break;
-      tile += max(end, other) - u.t0;
-      const bool live = row < u.rows;
-      const int64_t at = (int64_t)u.row + row;
-      const float inv = l > 0.f ? 1.f / l : l;   // NaN stays
-      const bool whole = u.pieces == 1;
-      if (end > u.t0) {
-        if (!__all_sync(0xffffffffu, wait_inline(bar(B_OFULL + w), o_used & 1, guard))) { failed = true; break; }
-        ++o_used;
-        tc_fence_after();
-      }
-      if (live) {
-        const float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
-        if (whole) p.lse[at * p.heads + u.head] = lse;
-        else p.lse_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = lse;
-      }
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * p.out_token + u.head * p.out_head);
-      float4* part = reinterpret_cast<float4*>(p.o_part + (((int64_t)u.piece * p.tq + at) * p.heads + u.head) * kV);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        if (end > u.t0) {
-          tmem_ld32(t_o + 32u * c, o);
-          tmem_wait_ld();
-          pin_regs32(o);
-          if (c == 3) {   // O is read: the next unit may write it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_OEMPTY + w));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
-        }
-        if (live) {
-          // a row that sees nothing has l = 0 and gets zeros
-          float v[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]) * inv;
-          if (whole) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[4 * c + k] = make_uint4(pack_p<kFp16>(v[8 * k], v[8 * k + 1]), pack_p<kFp16>(v[8 * k + 2], v[8 * k + 3]),
-                                          pack_p<kFp16>(v[8 * k + 4], v[8 * k + 5]), pack_p<kFp16>(v[8 * k + 6], v[8 * k + 7]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) part[8 * c + k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          }
-        }
+        tmem_st16(t_o + 16u * c, o);
       }
     }
+    sum[0] = sum[1] = 0;
+    weights(0, q);
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
+  tmem_st16(t_s, q);
+  weights(1, q);
+  tmem_st16(t_s + 16u, q);
+  tmem_wait_st();
+  hand_over(0);
+  weights(2, q);
+  tmem_st16(t_s + 32u, q);
+  weights(3, q);
+  tmem_st16(t_s + 48u, q);
+  tmem_wait_st();
+  hand_over(1);
+  const float2 x = f2_unpack(f2_add(sum[0], sum[1]));
+  row.l += x.x + x.y;
+}
+
+// The row's result: O / l and lse, or a piece's share of them. `some`: the accumulator holds something; read() is called
+// when it has been read.
+template <bool kFp16, class U, class F>
+MLA_DEV void store_row(const PrefillParams& p, const U& u, const Row& row, uint32_t t_o, bool some, bool live, int64_t at, F read) {
+  const float inv = row.l > 0.f ? 1.f / row.l : row.l;   // a row that sees nothing has l = 0 and gets zeros; NaN stays
+  const bool whole = u.pieces == 1;
+  if (live) {
+    const float lse = row.l == 0.f ? -INFINITY : row.m * p.scale + logf(row.l);
+    if (whole) p.lse[at * p.heads + u.head] = lse;
+    else p.lse_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = lse;
+  }
+  uint16_t* dst = static_cast<uint16_t*>(p.out) + at * p.out_token + u.head * p.out_head;
+  float4* part = reinterpret_cast<float4*>(p.o_part + (((int64_t)u.piece * p.tq + at) * p.heads + u.head) * kV);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t o[32];
+    if (some) {
+      tmem_ld32(t_o + 32u * c, o);
+      tmem_wait_ld();
+      pin_regs32(o);
+      if (c == 3) read();
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = 0u;
+    }
+    if (!live) continue;
+    float v[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]) * inv;
+    if (whole) {
+      uint32_t y[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) y[k] = pack_p<kFp16>(v[2 * k], v[2 * k + 1]);
+      if (p.out_v8) {
+        st_global_v8(dst + 32 * c, y);
+        st_global_v8(dst + 32 * c + 16, y + 8);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          reinterpret_cast<uint4*>(dst + 32 * c)[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) part[8 * c + k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
   }
 }
 
@@ -674,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // (row, head), four dims a lane; rows whose unit was not cut are left as they are.
 constexpr int kCombineThreads = 256;
 
-template <bool kFp16>
+template <bool kFp16, int kTileRows>
 __global__ void __launch_bounds__(kCombineThreads) mla_prefill_combine_kernel(const PrefillParams p) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -691,7 +385,7 @@ __global__ void __launch_bounds__(kCombineThreads) mla_prefill_combine_kernel(co
   }
   const Span s = span_of(p, lo);
   if (row < s.q0 || row >= (int64_t)s.q0 + s.nq) return;   // behind the last document
-  const int i = (int)(row - s.q0), last = min((i / kBlock + 1) * kBlock, s.nq) - 1;
+  const int i = (int)(row - s.q0), block = 2 * kTileRows, last = min((i / block + 1) * block, s.nq) - 1;
   const int pieces = pieces_of(p, (visible(p, s, last) + kKeys - 1) / kKeys);
   if (pieces == 1) return;
   float m = -INFINITY;

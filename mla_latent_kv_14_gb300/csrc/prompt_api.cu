@@ -6,7 +6,8 @@
 
 #include "checks.h"
 #include "norms.cuh"
-#include "prefill.cuh"
+#include "prefill_few.cuh"
+#include "prefill_pair.cuh"
 #include "read.cuh"
 
 using namespace mla;
@@ -47,63 +48,80 @@ mla_status launch_read(const read::ReadParams& p, void* stream) {
 
 constexpr int kCardSms = 152;
 constexpr int kMostPieces = 16;
-// blocks of 256 queries that `batch` documents of tq rows can have
-int64_t blocks_of(int64_t tq, int64_t batch) {
+// How the attention is launched, from sizes that the host knows.
+struct PrefillPlan {
+  bool pair;         // two CTAs to a unit of 512 queries, or one to a unit of 256
+  int64_t units;     // most units there can be
+  int pieces;        // most pieces of a unit
+};
+// blocks of `rows` queries that `batch` documents of tq rows can have
+int64_t blocks_of(int64_t tq, int64_t batch, int64_t rows) {
   const int64_t some = batch < tq ? batch : tq;     // documents with a row
-  return (tq + (prefill::kBlock - 1) * some) / prefill::kBlock;
+  return (tq + (rows - 1) * some) / rows;
 }
-// pieces that the key tiles of a unit are cut into: units that do not fill the card twice are cut until they would three times
-int pieces_of(int64_t tq, int64_t tk, int64_t batch, int64_t heads) {
-  const int64_t units = blocks_of(tq, batch) * heads;
-  if (units == 0 || units >= 2 * kCardSms) return 1;
-  const int64_t want = (3 * kCardSms + units - 1) / units, most = tk / (prefill::kPieceTiles * prefill::kKeys);
+PrefillPlan plan_prefill(int64_t tq, int64_t tk, int64_t batch, int64_t heads) {
+  PrefillPlan plan{};
+  plan.pair = batch > 0 && tq / batch > prefill::kRows;
+  plan.units = blocks_of(tq, batch, 2 * (plan.pair ? prefill::pair::kTileRows : prefill::kRows)) * heads;
+  plan.pieces = 1;
+  // units that do not fill the card twice are cut until they would three times
+  const int64_t places = plan.pair ? kCardSms / 2 : kCardSms;
+  if (plan.units == 0 || plan.units >= 2 * places) return plan;
+  const int64_t want = (3 * places + plan.units - 1) / plan.units, most = tk / (prefill::kPieceTiles * prefill::kKeys);
   const int64_t n = want < most ? want : most;
-  return (int)(n < 1 ? 1 : n > kMostPieces ? kMostPieces : n);
+  plan.pieces = (int)(n < 1 ? 1 : n > kMostPieces ? kMostPieces : n);
+  return plan;
 }
 size_t piece_bytes(int64_t tq, int64_t heads) { return (size_t)tq * (size_t)heads * (prefill::kV + 1) * 4; }
 
-// rows of `dim` elements of [rows, heads]: box of 64 elements by 128 rows of a head
+// rows of `dim` elements of [rows, heads]: box of 64 elements by `box_rows` rows of a head
 bool make_map_heads(CUtensorMap* m, const void* base, bool fp16, int dim, int64_t heads, int64_t rows, int64_t head_stride,
-                    int64_t row_stride) {
+                    int64_t row_stride, uint32_t box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
-  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t box[3] = {64, 1, box_rows};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kFp16>
-mla_status launch_prefill(int dev, int64_t grid, void* stream, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& r,
+template <bool kFp16, bool kPair>
+mla_status launch_prefill(int dev, int64_t units, void* stream, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& r,
                           const CUtensorMap& v, const prefill::PrefillParams& p) {
+  namespace pf = prefill;
   static std::atomic<bool> set[kMaxDevices];
-  auto kernel = prefill::mla_prefill_kernel<kFp16>;
+  auto kernel = kPair ? pf::pair::mla_prefill_pair_kernel<kFp16> : pf::few::mla_prefill_few_kernel<kFp16>;
+  constexpr uint32_t smem = kPair ? pf::pair::kSmem : pf::few::kSmem;
   if (!set[dev].load(std::memory_order_relaxed)) {
     // the softmax warps wait for the registers that the launch gave the others: without them they would wait for good
     cudaFuncAttributes at;
     MLA_CUDA(cudaFuncGetAttributes(&at, kernel));
-    if (at.numRegs < prefill::kRegsLaunch) return MLA_ERR_UNSUPPORTED;
-    MLA_CUDA(set_smem(kernel, prefill::kSmem));
+    if (at.numRegs < pf::kRegsLaunch) return MLA_ERR_UNSUPPORTED;
+    MLA_CUDA(set_smem(kernel, smem));
     set[dev].store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(prefill::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = prefill::kSmem;
+  cfg.gridDim = dim3((unsigned)(units * p.splits * (kPair ? 2 : 1)), 1, 1);
+  cfg.blockDim = dim3(pf::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = kPair ? 2 : 1;
   MLA_CUDA(cudaLaunchKernelEx(&cfg, kernel, q, k, r, v, p));
   if (p.splits == 1) return MLA_OK;
-  const int64_t warps = prefill::kCombineThreads / 32, items = p.tq * p.heads;
-  return launch(prefill::mla_prefill_combine_kernel<kFp16>, dim3((unsigned)((items + warps - 1) / warps)),
-                prefill::kCombineThreads, 0, stream, p);
+  const int64_t warps = pf::kCombineThreads / 32, items = p.tq * p.heads;
+  return launch(pf::mla_prefill_combine_kernel<kFp16, kPair ? pf::pair::kTileRows : pf::kRows>,
+                dim3((unsigned)((items + warps - 1) / warps)), pf::kCombineThreads, 0, stream, p);
 }
 
 }  // namespace
@@ -213,7 +231,7 @@ mla_status mla_read_kv(const void* kvcache, int64_t num_blocks, int page_block, 
 
 size_t mla_prefill_workspace_size(int64_t tokens_q, int64_t tokens_k, int batch, int heads) {
   if (tokens_q <= 0 || tokens_k < 0 || batch <= 0 || heads <= 0 || tokens_q >= kMaxRows || tokens_k >= kMaxRows) return 0;
-  const int n = pieces_of(tokens_q, tokens_k, batch, heads);
+  const int n = plan_prefill(tokens_q, tokens_k, batch, heads).pieces;
   return n > 1 ? n * piece_bytes(tokens_q, heads) : 0;
 }
 
@@ -246,9 +264,9 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
     return MLA_ERR_INVALID_ARG;
   if (tk > 0 && (!k_nope || !k_rope || !v || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16))) return MLA_ERR_INVALID_ARG;
   if (!rows_apart(tq, out_token_stride, heads, out_head_stride, pf::kV)) return MLA_ERR_INVALID_ARG;
-  const int splits = pieces_of(tq, tk, batch, heads);
-  const int64_t grid = blocks_of(tq, batch) * heads * splits;
-  if (grid >= kMaxRows || tq * heads >= (kMaxRows - 1) * (pf::kCombineThreads / 32)) return MLA_ERR_UNSUPPORTED;
+  const PrefillPlan plan = plan_prefill(tq, tk, batch, heads);
+  const int splits = plan.pieces;
+  if (plan.units * splits >= kMaxRows / 2 || tq * heads >= (kMaxRows - 1) * (pf::kCombineThreads / 32)) return MLA_ERR_UNSUPPORTED;
   const size_t need = splits > 1 ? splits * piece_bytes(tq, heads) : 0;
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return MLA_ERR_INVALID_ARG;
   auto span = [&](const void* at, int64_t ts, int64_t hs, int64_t rows, int64_t width) {
@@ -276,6 +294,7 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   p.out = out;
   p.out_token = out_token_stride;
   p.out_head = out_head_stride;
+  p.out_v8 = aligned(out, 32) && out_token_stride % 16 == 0 && out_head_stride % 16 == 0;
   p.lse = lse;
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = need ? p.o_part + (int64_t)splits * tq * heads * pf::kV : nullptr;
@@ -287,14 +306,20 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   CUtensorMap mq, mk, mr, mv;
   // without keys nothing is copied through the last three
   const bool some = tk > 0;
-  if (!make_map_heads(&mq, q, fp16, pf::kQk, heads, tq, q_head_stride, q_token_stride) ||
+  const uint32_t key_rows = plan.pair ? pf::kKeys / 2 : pf::kKeys;   // a CTA of a pair copies half of the keys
+  if (!make_map_heads(&mq, q, fp16, pf::kQk, heads, tq, q_head_stride, q_token_stride, pf::kRows) ||
       !make_map_heads(&mk, some ? k_nope : q, fp16, pf::kNope, some ? heads : 1, some ? tk : 1, some ? k_head_stride : pf::kNope,
-                      some ? k_token_stride : pf::kNope) ||
-      !make_map_heads(&mr, some ? k_rope : q, fp16, pf::kRopeDim, 1, some ? tk : 1, pf::kRopeDim, some ? rope_stride : pf::kRopeDim) ||
+                      some ? k_token_stride : pf::kNope, key_rows) ||
+      !make_map_heads(&mr, some ? k_rope : q, fp16, pf::kRopeDim, 1, some ? tk : 1, pf::kRopeDim, some ? rope_stride : pf::kRopeDim,
+                      key_rows) ||
       !make_map_heads(&mv, some ? v : q, fp16, pf::kV, some ? heads : 1, some ? tk : 1, some ? v_head_stride : pf::kV,
-                      some ? v_token_stride : pf::kV))
+                      some ? v_token_stride : pf::kV, pf::kKeys))
     return MLA_ERR_CUDA;
-  return fp16 ? launch_prefill<true>(dev, grid, stream, mq, mk, mr, mv, p) : launch_prefill<false>(dev, grid, stream, mq, mk, mr, mv, p);
+  if (plan.pair)
+    return fp16 ? launch_prefill<true, true>(dev, plan.units, stream, mq, mk, mr, mv, p)
+                : launch_prefill<false, true>(dev, plan.units, stream, mq, mk, mr, mv, p);
+  return fp16 ? launch_prefill<true, false>(dev, plan.units, stream, mq, mk, mr, mv, p)
+              : launch_prefill<false, false>(dev, plan.units, stream, mq, mk, mr, mv, p);
 }
 
 }  // extern "C"
