@@ -9,12 +9,12 @@
 // least prefix_b (a prefix that every query sees). 640 FLOP a visible pair and
 // head, where the decode's absorbed form takes 2176.
 //
-// A unit is a block of consecutive queries of one (document, head), in two query
-// tiles that share every tile of 128 keys and values and take turns on the
-// tensor pipe: while one tile's scores go through the softmax, the pipe
-// multiplies for the other. Per 128 rows, S (fp32) and P (16 bits, over the S
-// that it comes from) and the accumulator take 256 columns of TMEM: two tiles
-// fill it.
+// A unit is a block of consecutive queries of one (document, head). Two chains
+// of score tile -> softmax -> product take turns on the tensor pipe: while one
+// goes through the softmax, the pipe multiplies for the other. They are two query
+// tiles over the same keys (prefill_pair.cuh) or every other key tile of the same
+// queries (prefill_few.cuh). A chain's S (fp32), P (16 bits, over the S that it
+// comes from) and accumulator take 256 columns of TMEM: two fill it.
 //
 // The softmax is online with a lazy reference: the reference maximum of a row
 // moves only when a score passes it by more than 2^8 (P and its sum stay far
@@ -43,7 +43,7 @@ constexpr int kNope = 128, kRopeDim = 64, kQk = kNope + kRopeDim, kV = 128;
 constexpr int kPieceTiles = 8;             // key tiles that a piece of a cut unit has at least
 constexpr uint32_t kChunk = 128 * 128;     // 128 rows x 128 bytes (64 dims)
 constexpr uint32_t kQTile = 3 * kChunk;
-constexpr uint32_t kColO = 256;            // TMEM: S_w at 128 w (P_w over it), O_w at 256 + 128 w
+constexpr uint32_t kColO = 256;            // TMEM: S of chain w at 128 w (P over it), its accumulator at 256 + 128 w
 
 struct PrefillParams {
   const int32_t* cu_q;         // [batch + 1]
@@ -55,7 +55,6 @@ struct PrefillParams {
   float scale, scale_log2;
   void* out;                   // [tq, heads, 128]
   int64_t out_token, out_head; // strides in elements
-  int out_v8;                  // rows of out are 32-B aligned
   float* lse;                  // [tq, heads]
   float* o_part;               // [splits][tq][heads][128], splits > 1
   float* lse_part;             // [splits][tq][heads]
@@ -87,9 +86,10 @@ MLA_DEV int pieces_of(const PrefillParams& p, int tiles) {
   return max(1, min(p.splits, tiles / kPieceTiles));
 }
 
-// A unit as its readers see it: one piece of a block of queries of a head, whose two query tiles have kTileRows rows.
-template <int kTileRows>
+// A unit as its readers see it: one piece of a block of queries of a head, in kTiles query tiles of kTileRows rows.
+template <int kTileRows, int kTiles>
 struct Unit {
+  static constexpr int kBlock = kTileRows * kTiles;
   int head;       // < 0: no more units
   int row;        // first row of q and out
   int rows;       // queries of the unit
@@ -118,9 +118,9 @@ struct Unit {
 
 // Units in the order of the grid: documents, heads, blocks of queries (those that see most first), pieces. The warp
 // holds 32 documents' counts and moves on only.
-template <int kTileRows>
+template <class U>
 struct Finder {
-  static constexpr int kBlock = 2 * kTileRows;
+  static constexpr int kBlock = U::kBlock;
   int base;            // first of the 32 documents
   int64_t before;      // blocks (of one head) times heads before them
   int blocks;          // of this lane's document
@@ -149,7 +149,7 @@ struct Finder {
     load(p);
   }
   // the unit of block `id` of the grid; false if there is none (a piece that its unit does not have)
-  MLA_DEV bool find(const PrefillParams& p, int64_t id, Unit<kTileRows>& u, bool& past) {
+  MLA_DEV bool find(const PrefillParams& p, int64_t id, U& u, bool& past) {
     const int64_t block = id / p.splits;
     const int piece = (int)(id - block * p.splits);
     past = false;
@@ -316,51 +316,77 @@ MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2
   row.l += x.x + x.y;
 }
 
-// The row's result: O / l and lse, or a piece's share of them. `some`: the accumulator holds something; read() is called
-// when it has been read.
+// 32 rows of 64 dims of the output from shared memory (128-byte swizzled), rows and dims all inside the tensor
+MLA_DEV void store_rows64(const CUtensorMap* m, uint32_t src, int x, int head, int row) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)), "r"(src), "r"(x), "r"(head), "r"(row)
+               : "memory");
+}
+MLA_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+MLA_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+MLA_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+constexpr uint32_t kStage = 32 * 128;   // a warp's 32 rows x 64 dims on their way out
+
+// The warp's 32 results: O / l and lse, or a piece's share of them. `some`: the accumulators hold something; read() is
+// called when they have been read. Rows of a warp that all belong to the unit leave through shared memory (`stage`) and
+// the copy engine: the plain stores of 32 rows touch 32 lines each and kept the SM's load/store path, and with it every
+// wait on a barrier, busy for some 3400 cycles a unit.
 template <bool kFp16, class U, class F>
-MLA_DEV void store_row(const PrefillParams& p, const U& u, const Row& row, uint32_t t_o, bool some, bool live, int64_t at, F read) {
+MLA_DEV void store_rows(const PrefillParams& p, const CUtensorMap* tm_out, uint32_t stage, const U& u, const Row& row, uint32_t t_o,
+                        bool some, int first, F read) {
+  const int lane = threadIdx.x & 31;
   const float inv = row.l > 0.f ? 1.f / row.l : row.l;   // a row that sees nothing has l = 0 and gets zeros; NaN stays
-  const bool whole = u.pieces == 1;
+  const bool whole = u.pieces == 1, live = first + lane < u.rows;
+  const int64_t at = (int64_t)u.row + first + lane;
+  uint32_t o[128];
+  if (some) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32(t_o + 32u * c, o + 32 * c);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) pin_regs32(o + 32 * c);
+    read();
+  } else {
+#pragma unroll
+    for (int k = 0; k < 128; ++k) o[k] = 0u;
+  }
   if (live) {
     const float lse = row.l == 0.f ? -INFINITY : row.m * p.scale + logf(row.l);
     if (whole) p.lse[at * p.heads + u.head] = lse;
     else p.lse_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = lse;
   }
-  uint16_t* dst = static_cast<uint16_t*>(p.out) + at * p.out_token + u.head * p.out_head;
-  float4* part = reinterpret_cast<float4*>(p.o_part + (((int64_t)u.piece * p.tq + at) * p.heads + u.head) * kV);
+  if (!whole) {
+    float4* part = reinterpret_cast<float4*>(p.o_part + (((int64_t)u.piece * p.tq + at) * p.heads + u.head) * kV);
+    if (!live) return;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t o[32];
-    if (some) {
-      tmem_ld32(t_o + 32u * c, o);
-      tmem_wait_ld();
-      pin_regs32(o);
-      if (c == 3) read();
-    } else {
+    for (int k = 0; k < 32; ++k)
+      part[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                            __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+    return;
+  }
+  uint32_t y[64];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] = 0u;
-    }
-    if (!live) continue;
-    float v[32];
+  for (int k = 0; k < 64; ++k) y[k] = pack_p<kFp16>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+  if (first + 32 <= u.rows) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]) * inv;
-    if (whole) {
-      uint32_t y[16];
+    for (int h = 0; h < 2; ++h) {
+      if (lane == 0) bulk_wait_read();   // the stage's last rows are out of it
+      __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) y[k] = pack_p<kFp16>(v[2 * k], v[2 * k + 1]);
-      if (p.out_v8) {
-        st_global_v8(dst + 32 * c, y);
-        st_global_v8(dst + 32 * c + 16, y + 8);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          reinterpret_cast<uint4*>(dst + 32 * c)[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+      for (int k = 0; k < 8; ++k)
+        st_shared_v4(stage + 128u * lane + 16u * (k ^ (lane & 7)), y[32 * h + 4 * k], y[32 * h + 4 * k + 1], y[32 * h + 4 * k + 2],
+                     y[32 * h + 4 * k + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        store_rows64(tm_out, stage, 64 * h, u.head, (int)at);
+        bulk_commit();
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) part[8 * c + k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     }
+  } else if (live) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * p.out_token + u.head * p.out_head);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
   }
 }
 
@@ -368,7 +394,7 @@ MLA_DEV void store_row(const PrefillParams& p, const U& u, const Row& row, uint3
 // (row, head), four dims a lane; rows whose unit was not cut are left as they are.
 constexpr int kCombineThreads = 256;
 
-template <bool kFp16, int kTileRows>
+template <bool kFp16, int kBlock>
 __global__ void __launch_bounds__(kCombineThreads) mla_prefill_combine_kernel(const PrefillParams p) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -385,7 +411,7 @@ __global__ void __launch_bounds__(kCombineThreads) mla_prefill_combine_kernel(co
   }
   const Span s = span_of(p, lo);
   if (row < s.q0 || row >= (int64_t)s.q0 + s.nq) return;   // behind the last document
-  const int i = (int)(row - s.q0), block = 2 * kTileRows, last = min((i / block + 1) * block, s.nq) - 1;
+  const int i = (int)(row - s.q0), last = min((i / kBlock + 1) * kBlock, s.nq) - 1;
   const int pieces = pieces_of(p, (visible(p, s, last) + kKeys - 1) / kKeys);
   if (pieces == 1) return;
   float m = -INFINITY;

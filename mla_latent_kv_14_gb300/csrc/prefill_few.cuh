@@ -1,14 +1,18 @@
 // prefill_few.cuh -- the attention of prefill.cuh for documents of few new
-// tokens, one CTA to a unit of 256 queries.
+// tokens, one CTA to a unit of 128 queries.
 //
-// Both query tiles read each chunk of 128 rows x 128 bytes of keys (three a
-// tile) and values (two) from one ring.
+// Few rows over long keys are bound by the keys' and values' bytes, so what
+// counts is how much of them is on its way: the queries take 48 KB, the rest of
+// shared memory is a ring of chunks of 128 rows x 128 bytes (three of keys, two
+// of values a tile), 2.2 tiles. The two chains take every other key tile of the
+// same queries, each with an accumulator and a reference of its own; the first
+// one's warps join them at the unit's end. Warps none of whose 32 rows is a query
+// only pass the tiles on.
 //
 // Warp roles (384 threads): warp 0 issues the copies, warps 1 and 3 the MMAs of
-// the first and the second query tile (warp 1 owns TMEM), warp 2 finds the
-// units, warps 4-7 and 8-11 are the softmax of the two query tiles, one row a
-// thread. Every wait is bounded; a wait that gives up sets the status word and
-// the CTA unwinds.
+// the first and the second chain (warp 1 owns TMEM), warp 2 finds the units,
+// warps 4-7 and 8-11 are the softmax of the two chains, one row a thread. Every
+// wait is bounded; a wait that gives up sets the status word and the CTA unwinds.
 #pragma once
 #include "prefill.cuh"
 
@@ -16,17 +20,22 @@ namespace mla {
 namespace prefill {
 namespace few {
 
-constexpr int kRing = 8;                   // chunks: three of K, two of V a tile
-constexpr uint32_t kOffRing = 2 * kQTile;
+using UnitF = Unit<kRows, 1>;
+constexpr int kRing = 11;                  // chunks
+constexpr int kUnits = 4;                  // units looked up ahead of the slowest reader
+constexpr uint32_t kOffRing = kQTile;
 constexpr uint32_t kOffBar = kOffRing + kRing * kChunk;
 enum : uint32_t {
-  B_FULL = 0, B_EMPTY = B_FULL + kRing, B_QFULL = B_EMPTY + kRing, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
-  B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 4, B_OEMPTY = B_OFULL + 2, B_UFULL = B_OEMPTY + 2, B_UEMPTY = B_UFULL + 2,
-  B_NEXT = B_UEMPTY + 2, B_DRAIN = B_NEXT + 1, B_STALL = B_DRAIN + 2, B_COUNT = B_STALL + 1
+  B_FULL = 0, B_EMPTY = B_FULL + kRing, B_QFULL = B_EMPTY + kRing, B_QEMPTY = B_QFULL + 1, B_SFULL = B_QEMPTY + 1,
+  B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 4, B_OEMPTY = B_OFULL + 2, B_LFULL = B_OEMPTY + 2, B_LEMPTY = B_LFULL + 1,
+  B_UFULL = B_LEMPTY + 1, B_UEMPTY = B_UFULL + kUnits, B_NEXT = B_UEMPTY + kUnits, B_DRAIN = B_NEXT + 1, B_STALL = B_DRAIN + 2,
+  B_COUNT = B_STALL + 1
 };
 constexpr uint32_t kOffMisc = (kOffBar + 8 * B_COUNT + 15) / 16 * 16;
-constexpr uint32_t kSmem = kOffMisc + 256 + 1024;
-constexpr int kUnitReaders = 11;           // producer, two MMA and eight softmax warps
+constexpr uint32_t kOffState = kOffMisc + 64 + 64 * kUnits;   // the second chain's reference and sum of each row
+constexpr uint32_t kSmem = kOffState + 8 * kRows + 1024;
+static_assert(kSmem <= 232448);
+constexpr int kUnitReaders = 11;           // producer, two issuing threads and eight softmax warps
 
 // Ring positions: tile number `tile` of the CTA takes five consecutive chunks, three of keys and two of values; the two
 // of values stand side by side (one descriptor covers both).
@@ -52,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + kOffMisc);  // 16-B aligned
-  // misc: [0, 4) the answer of ask_next, 4 TMEM base, 5 abort, 6 ok, 7 status where none is given, [16, 48) two units
+  // misc: [0, 4) the answer of ask_next, 4 TMEM base, 5 abort, 6 ok, 7 status where none is given, from 16 on the units
   volatile uint32_t* tmem_slot = misc + 4;
   volatile uint32_t* abort_flag = misc + 5;
   volatile uint32_t* ok_flag = misc + 6;
@@ -64,18 +73,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRing; ++s) {
       mbar_init(bar(B_FULL + s), 1);
-      mbar_init(bar(B_EMPTY + s), 2);   // both query tiles' products
+      mbar_init(bar(B_EMPTY + s), 1);
     }
+    mbar_init(bar(B_QFULL), 1);
+    mbar_init(bar(B_QEMPTY), 2);   // both chains
+    mbar_init(bar(B_LFULL), 4);
+    mbar_init(bar(B_LEMPTY), 4);
     for (int w = 0; w < 2; ++w) {
-      mbar_init(bar(B_QFULL + w), 1);
-      mbar_init(bar(B_QEMPTY + w), 1);
       mbar_init(bar(B_SFULL + w), 1);
       mbar_init(bar(B_PFULL + w), 4);
       mbar_init(bar(B_PFULL + 2 + w), 4);
       mbar_init(bar(B_OFULL + w), 1);
       mbar_init(bar(B_OEMPTY + w), 4);
-      mbar_init(bar(B_UFULL + w), 1);
-      mbar_init(bar(B_UEMPTY + w), kUnitReaders);
+    }
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(bar(B_UFULL + s), 1);
+      mbar_init(bar(B_UEMPTY + s), kUnitReaders);
     }
     mbar_init(bar(B_NEXT), 1);
     mbar_init(bar(B_DRAIN), 1);
@@ -105,16 +118,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const bool ok = *ok_flag != 0u;
 
+  auto ready = [&](uint32_t i, uint32_t parity) { return wait_inline<false>(bar(i), parity & 1u, guard); };
+  auto ready_all = [&](uint32_t i, uint32_t parity) { return __all_sync(0xffffffffu, ready(i, parity)) != 0; };
   // the readers' side of the units: the n-th one, into registers; one lane reads for a role of a single thread
-  auto take_one = [&](int n, Unit<kRows>& u) {
-    const int s = n & 1;
-    if (!wait_inline<false>(bar(B_UFULL + s), (n >> 1) & 1, guard)) return false;
-    u.read(units + 16 * s);
+  auto take_one = [&](int n, UnitF& u) {
+    if (!ready(B_UFULL + n % kUnits, n / kUnits)) return false;
+    u.read(units + 16 * (n % kUnits));
     return true;
   };
-  auto take = [&](int n, Unit<kRows>& u) {
+  auto take = [&](int n, UnitF& u) {
     const bool got = __all_sync(0xffffffffu, take_one(n, u));
-    if (got && lane == 0) mbar_arrive(bar(B_UEMPTY + (n & 1)));
+    if (got && lane == 0) mbar_arrive(bar(B_UEMPTY + n % kUnits));
     return got && u.head >= 0;
   };
 
@@ -122,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     set_registers_down<kRegsFew>();
     if (warp == 2 && ok) {
       // ---------------- the units ----------------
-      Finder<kRows> finder;
+      Finder<UnitF> finder;
       finder.start(p);
       int64_t id = blockIdx.x;
       bool more = true, asking = false;
@@ -136,22 +150,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           asking = true;
         }
-        Unit<kRows> u{};
+        UnitF u{};
         u.head = -1;
         bool past = false;
         const bool found = more && finder.find(p, id, u, past);
         if (found || !more) {
-          if (!__all_sync(0xffffffffu, wait_inline<false>(bar(B_UEMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, guard))) break;
+          const int s = n % kUnits;
+          if (!ready_all(B_UEMPTY + s, (n / kUnits) ^ 1)) break;
           if (lane == 0) {
 #pragma unroll
-            for (int i = 0; i < Unit<kRows>::kWords; ++i) units[16 * (n & 1) + i] = u.word(i);
-            mbar_arrive(bar(B_UFULL + (n & 1)));
+            for (int i = 0; i < UnitF::kWords; ++i) units[16 * s + i] = u.word(i);
+            mbar_arrive(bar(B_UFULL + s));
           }
           __syncwarp();
           ++n;
         }
         if (!more) break;
-        if (!__all_sync(0xffffffffu, wait_inline<false>(bar(B_NEXT), asked & 1, guard))) break;
+        if (!ready_all(B_NEXT, asked)) break;
         asking = false;
         ++asked;
         id = answer_next(smem_u32(misc));
@@ -165,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (!mbar_try_wait(bar(B_NEXT), asked & 1) && cycles() - t_0 < kDrainLimitCycles) {}
       }
     } else if (warp == 0 && ok) {
-      // ---------------- copies: a unit's query tiles, then its keys and values ----------------
+      // ---------------- copies: a unit's queries, then its keys and values ----------------
       const bool leader = elect_one();
       if (leader) {
         prefetch_tmap(&tm_q);
@@ -173,13 +188,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tm_r);
         prefetch_tmap(&tm_v);
       }
-      int n = 0, q_loads[2] = {0, 0};
-      uint32_t loads = 0, tile = 0;
+      uint32_t loads = 0, tile = 0, q_loads = 0;
       bool stop = false;
-      Unit<kRows> u;
+      UnitF u;
       auto chunk = [&](const CUtensorMap* m, int x, int y, int z) {
         const uint32_t slot = slot_of(loads);
-        if (stop || !__all_sync(0xffffffffu, wait_inline<false>(bar(B_EMPTY + slot), phase_of(loads) ^ 1u, guard))) {
+        if (stop || !ready_all(B_EMPTY + slot, phase_of(loads) ^ 1u)) {
           stop = true;
           return;
         }
@@ -189,29 +203,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++loads;
       };
-      auto queries = [&](int w) {
-        if (stop || !__all_sync(0xffffffffu, wait_inline<false>(bar(B_QEMPTY + w), (q_loads[w] & 1) ^ 1, guard))) {
-          stop = true;
-          return;
-        }
+      for (int n = 0; !stop && take(n, u); ++n) {
+        const int e = u.end(0, p.causal);
+        if (e <= u.t0) continue;
+        if (!ready_all(B_QEMPTY, q_loads ^ 1u)) break;
         if (leader) {
-          mbar_arrive_expect_tx(bar(B_QFULL + w), kQTile);
-          for (int c = 0; c < 3; ++c)
-            tma_load_3d_plain(sb + w * kQTile + c * kChunk, &tm_q, bar(B_QFULL + w), 64 * c, u.head, u.row + kRows * w);
+          mbar_arrive_expect_tx(bar(B_QFULL), kQTile);
+          for (int c = 0; c < 3; ++c) tma_load_3d_plain(sb + c * kChunk, &tm_q, bar(B_QFULL), 64 * c, u.head, u.row);
         }
-        ++q_loads[w];
-      };
-      for (; !stop && take(n, u); ++n) {
-        const int e0 = u.end(0, p.causal), e1 = u.end(1, p.causal), e = max(e0, e1);
-        if (e0 > u.t0) queries(0);
+        ++q_loads;
         for (int t = u.t0; t < e && !stop; ++t, ++tile) {
           const int at = u.k0 + t * kKeys;
           const bool late = Slots(tile).late;
           chunk(&tm_k, 0, u.head, at);
           chunk(&tm_k, 64, u.head, at);
           if (!late) chunk(&tm_r, 0, 0, at);
-          // the second query tile is wanted after the first one's scores
-          if (t == u.t0 && e1 > u.t0) queries(1);
           chunk(&tm_v, 0, u.head, at);
           chunk(&tm_v, 64, u.head, at);
           if (late) chunk(&tm_r, 0, 0, at);
@@ -222,34 +228,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t t_0 = cycles();
         for (uint32_t k = loads < kRing ? 0u : loads - kRing; k < loads; ++k)
           while (!mbar_try_wait(bar(B_FULL + slot_of(k)), phase_of(k)) && cycles() - t_0 < kDrainLimitCycles) {}
-        for (int w = 0; w < 2; ++w)
-          if (q_loads[w])
-            while (!mbar_try_wait(bar(B_QFULL + w), (q_loads[w] - 1) & 1) && cycles() - t_0 < kDrainLimitCycles) {}
+        if (q_loads)
+          while (!mbar_try_wait(bar(B_QFULL), (q_loads - 1u) & 1u) && cycles() - t_0 < kDrainLimitCycles) {}
       }
     } else if ((warp & 1) && ok) {
-      // ---------------- UMMA issue for query tile w: one thread ----------------
-      // The pipe takes an instruction about when it starts it, so a wait between two of them idles it, but for the
-      // other tile's: all that can be waited for while the softmax runs (the next keys, the values) is, and the
-      // products of a tile and the scores of the next follow in one go.
+      // ---------------- UMMA issue for chain w: one thread ----------------
       const int w = warp >> 1;
       if (elect_one()) {
         constexpr uint32_t idesc_qk = idesc_f16(128, kKeys, !kFp16, false, false);
         constexpr uint32_t idesc_pv = idesc_f16(128, kV, !kFp16, false, true);
-        const uint64_t d_q = sdesc_sw128(sb + w * kQTile, 16, 1024), d_ring = sdesc_sw128(sb + kOffRing, 16, 1024),
+        const uint64_t d_q = sdesc_sw128(sb, 16, 1024), d_ring = sdesc_sw128(sb + kOffRing, 16, 1024),
                        d_v = sdesc_sw128(sb + kOffRing, kChunk, 1024);
         const uint32_t t_s = tmem + 128u * w, t_o = tmem + kColO + 128u * w;
         uint32_t tile = 0, q_used = 0, p_used = 0, o_used = 0;
-        auto ready = [&](uint32_t i, uint32_t parity) { return wait_inline<false>(bar(i), parity & 1u, guard); };
-        auto keys_ready = [&](const Slots& s) {
-          return ready(B_FULL + slot_of(s.key(0)), phase_of(s.key(0))) && ready(B_FULL + slot_of(s.key(1)), phase_of(s.key(1))) &&
-                 ready(B_FULL + slot_of(s.key(2)), phase_of(s.key(2)));
-        };
-        // a chunk is free once both tiles' products that read it are done; `alone`: the other tile has none here
-        auto release = [&](uint32_t chunk, bool alone) {
-          umma_commit(bar(B_EMPTY + slot_of(chunk)));
-          if (alone) umma_commit(bar(B_EMPTY + slot_of(chunk)));
-        };
-        auto scores = [&](const Slots& s, bool alone, bool last) {   // S = Q K^T
+        auto landed = [&](uint32_t chunk) { return ready(B_FULL + slot_of(chunk), phase_of(chunk)); };
+        auto scores = [&](const Slots& s, bool last) {   // S = Q K^T
+          if (!landed(s.key(0)) || !landed(s.key(1)) || !landed(s.key(2))) return false;
+          tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 3; ++c) {
             const uint64_t a = d_q + c * (kChunk >> 4), b = d_ring + slot_of(s.key(c)) * (kChunk >> 4);
@@ -258,27 +253,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           umma_commit(bar(B_SFULL + w));
 #pragma unroll
-          for (int c = 0; c < 3; ++c) release(s.key(c), alone);
-          if (last) umma_commit(bar(B_QEMPTY + w));
+          for (int c = 0; c < 3; ++c) umma_commit(bar(B_EMPTY + slot_of(s.key(c))));
+          if (last) umma_commit(bar(B_QEMPTY));
+          return true;
         };
-        Unit<kRows> u;
+        UnitF u;
         bool failed = false;
         for (int n = 0; !failed && take_one(n, u); ++n) {
-          mbar_arrive(bar(B_UEMPTY + (n & 1)));
+          mbar_arrive(bar(B_UEMPTY + n % kUnits));
           if (u.head < 0) break;
-          const int end = u.end(w, p.causal), other = u.end(w ^ 1, p.causal);
-          if (end > u.t0) {
-            const Slots s(tile);
-            if (!ready(B_QFULL + w, q_used++) || !keys_ready(s)) break;
-            tc_fence_after();
-            scores(s, u.t0 >= other, u.t0 + 1 == end);
-          }
-          for (int t = u.t0; t < end; ++t) {
-            const Slots s(tile + (t - u.t0)), next(tile + (t - u.t0) + 1);
+          const int e = u.end(0, p.causal), first = u.t0 + w;
+          if (e <= u.t0) continue;
+          if (!ready(B_QFULL, q_used++)) break;
+          if (first >= e) mbar_arrive(bar(B_QEMPTY));   // no tile for this chain
+          else if (!scores(Slots(tile + w), first + 2 >= e)) break;
+          for (int t = first; t < e; t += 2) {
+            const Slots s(tile + (uint32_t)(t - u.t0));
             const uint32_t v0 = s.value(0), v1 = s.value(1);
-            if (!ready(B_FULL + slot_of(v0), phase_of(v0)) || !ready(B_FULL + slot_of(v1), phase_of(v1)) ||
-                (t + 1 < end && !keys_ready(next)) || (t == u.t0 && !ready(B_OEMPTY + w, o_used++ ^ 1u)) ||
-                !ready(B_PFULL + w, p_used)) {
+            if (!landed(v0) || !landed(v1) || (t == first && !ready(B_OEMPTY + w, o_used++ ^ 1u)) || !ready(B_PFULL + w, p_used)) {
               failed = true;
               break;
             }
@@ -286,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O (+)= P V, 16 keys at a time; the first half while the second is still formed
             const uint64_t b = d_v + slot_of(v0) * (kChunk >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) umma_ts(t_o, t_s + 8u * k, b + 128u * k, idesc_pv, (t == u.t0 && k == 0) ? 0u : 1u);
+            for (int k = 0; k < 4; ++k) umma_ts(t_o, t_s + 8u * k, b + 128u * k, idesc_pv, (t == first && k == 0) ? 0u : 1u);
             if (!ready(B_PFULL + 2 + w, p_used++)) {
               failed = true;
               break;
@@ -294,12 +286,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int k = 4; k < 8; ++k) umma_ts(t_o, t_s + 8u * k, b + 128u * k, idesc_pv, 1u);
-            release(v0, t >= other);
-            release(v1, t >= other);
-            if (t + 1 < end) scores(next, t + 1 >= other, t + 2 == end);
-            else umma_commit(bar(B_OFULL + w));
+            umma_commit(bar(B_EMPTY + slot_of(v0)));
+            umma_commit(bar(B_EMPTY + slot_of(v1)));
+            // the next keys may wait for these values' place in the ring
+            if (t + 2 >= e) umma_commit(bar(B_OFULL + w));
+            else if (!scores(Slots(tile + (uint32_t)(t - u.t0) + 2), t + 4 >= e)) {
+              failed = true;
+              break;
+            }
           }
-          tile += max(end, other) - u.t0;
+          tile += e - u.t0;
         }
         // every UMMA this thread issued has completed before TMEM is released
         umma_commit(bar(B_DRAIN + w));
@@ -310,29 +306,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     set_registers_up<kRegsMany>();
-    // ---------------- softmax: row `r` of query tile w ----------------
+    // ---------------- softmax of chain w: row `r` ----------------
     const int w = (warp - 4) >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t tl = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t t_s = tmem + tl + 128u * w, t_o = tmem + tl + kColO + 128u * w;
-    uint32_t s_used = 0, o_used = 0, tile = 0;
+    const uint32_t t_s = tmem + tl + 128u * w, t_o = tmem + tl + kColO;
+    float2* states = reinterpret_cast<float2*>(smem + kOffState);
+    auto arrive = [&](uint32_t i) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(i));
+    };
+    uint32_t s_used = 0, o_used[2] = {0, 0}, l_used = 0, tile = 0;
     bool failed = !ok;
-    Unit<kRows> u;
+    UnitF u;
     for (int n = 0; !failed && take(n, u); ++n) {
-      const int end = u.end(w, p.causal), other = u.end(w ^ 1, p.causal), row = kRows * w + r;
-      const int seen = row < u.rows ? u.visible(row, p.causal) : u.nk;
-      const int least = kRows * w < u.rows ? u.visible(kRows * w, p.causal) : 0;  // keys that all rows see
+      const int e = u.end(0, p.causal);
+      const bool idle = r - lane >= u.rows;          // none of the warp's rows is a query
+      const int seen = r < u.rows ? u.visible(r, p.causal) : u.nk, least = u.visible(0, p.causal);   // of the row; of all rows
       Row state{-INFINITY, 0.f};
-      for (int t = u.t0; t < end; ++t) {
-        if (!__all_sync(0xffffffffu, wait_inline<false>(bar(B_SFULL + w), s_used++ & 1, guard))) { failed = true; break; }
+      for (int t = u.t0 + w; t < e; t += 2) {
+        if (!ready_all(B_SFULL + w, s_used++)) { failed = true; break; }
         tc_fence_after();
         const int rest = u.nk - t * kKeys;
         if (rest < kKeys) {
           // The value rows behind the document's keys may hold anything, and zero times NaN is NaN: they are cleared
-          // before this tile's P is handed over (by both query tiles, with the same zeros).
-          const Slots at(tile + (t - u.t0));
+          // before this tile's P is handed over.
+          const Slots at(tile + (uint32_t)(t - u.t0));
           const uint32_t v0 = at.value(0), v1 = at.value(1);
-          if (!__all_sync(0xffffffffu, wait_inline<false>(bar(B_FULL + slot_of(v0)), phase_of(v0), guard) &&
-                                           wait_inline<false>(bar(B_FULL + slot_of(v1)), phase_of(v1), guard))) {
+          if (!ready_all(B_FULL + slot_of(v0), phase_of(v0)) || !ready_all(B_FULL + slot_of(v1), phase_of(v1))) {
             failed = true;
             break;
           }
@@ -343,23 +344,70 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        softmax_tile<kFp16>(state, t_s, t_o, p.scale_log2, (t + 1) * kKeys > least, seen - t * kKeys, t == u.t0, [&](int h) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_PFULL + 2 * h + w));
-        });
+        if (idle) {        // the rows' products are of no query: any P will do
+          arrive(B_PFULL + w);
+          arrive(B_PFULL + 2 + w);
+          continue;
+        }
+        softmax_tile<kFp16>(state, t_s, t_o + 128u * w, p.scale_log2, (t + 1) * kKeys > least, seen - t * kKeys, t == u.t0 + w,
+                            [&](int h) { arrive(B_PFULL + 2 * h + w); });
       }
       if (failed) break;
-      tile += max(end, other) - u.t0;
-      if (end > u.t0) {
-        if (!__all_sync(0xffffffffu, wait_inline<false>(bar(B_OFULL + w), o_used++ & 1, guard))) break;
-        tc_fence_after();
+      tile += max(e - u.t0, 0);
+      if (w == 1) {
+        if (!ready_all(B_LEMPTY, l_used++ ^ 1u)) break;
+        states[r] = make_float2(state.m, state.l);
+        arrive(B_LFULL);
+        continue;
       }
-      store_row<kFp16>(p, u, state, t_o, end > u.t0, row < u.rows, (int64_t)u.row + row, [&]() {
-        tc_fence_before();   // O is read: the next unit may write it
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_OEMPTY + w));
-      });
+      // the first chain's warps write the unit: both chains' shares, at the larger of their references
+      if (!ready_all(B_LFULL, l_used++)) break;
+      const float2 other = states[r];
+      arrive(B_LEMPTY);
+      const bool some = e > u.t0, both = e > u.t0 + 1;
+      if ((some && !ready_all(B_OFULL, o_used[0]++)) || (both && !ready_all(B_OFULL + 1, o_used[1]++))) break;
+      tc_fence_after();
+      const float m = fmaxf(state.m, other.x), ref = m == -INFINITY ? 0.f : m;
+      const float f0 = exp2_approx((state.m - ref) * p.scale_log2), f1 = exp2_approx((other.x - ref) * p.scale_log2);
+      const float l = f0 * state.l + f1 * other.y;
+      const float inv = l > 0.f ? 1.f / l : l;       // a row that sees nothing has l = 0 and gets zeros; NaN stays
+      const bool whole = u.pieces == 1, live = r < u.rows;
+      const int64_t at = (int64_t)u.row + r;
+      if (live) {
+        const float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+        if (whole) p.lse[at * p.heads + u.head] = lse;
+        else p.lse_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = lse;
+      }
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * p.out_token + u.head * p.out_head);
+      float4* part = reinterpret_cast<float4*>(p.o_part + (((int64_t)u.piece * p.tq + at) * p.heads + u.head) * kV);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t a[32], b[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) a[k] = b[k] = 0u;
+        if (some) tmem_ld32(t_o + 32u * c, a);
+        if (both) tmem_ld32(t_o + 128u + 32u * c, b);
+        tmem_wait_ld();
+        pin_regs32(a);
+        pin_regs32(b);
+        if (c == 3) {      // both are read: the next unit may write them
+          if (some) arrive(B_OEMPTY);
+          if (both) arrive(B_OEMPTY + 1);
+        }
+        if (!live) continue;
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = (f0 * __uint_as_float(a[k]) + f1 * __uint_as_float(b[k])) * inv;
+        if (whole) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[4 * c + k] = make_uint4(pack_p<kFp16>(v[8 * k], v[8 * k + 1]), pack_p<kFp16>(v[8 * k + 2], v[8 * k + 3]),
+                                        pack_p<kFp16>(v[8 * k + 4], v[8 * k + 5]), pack_p<kFp16>(v[8 * k + 6], v[8 * k + 7]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) part[8 * c + k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+      }
     }
   }
   __syncwarp();

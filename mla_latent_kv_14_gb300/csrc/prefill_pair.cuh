@@ -5,9 +5,10 @@
 // the pair holds rows [128 r, 128 r + 128) of either query tile of 256, keys [64
 // r, 64 r + 64) of a tile's K and dims [64 r, 64 r + 64) of its V, and the
 // hardware brings the halves of K and V together. So an SM copies and keeps 40 KB
-// of a tile of 128 keys where a CTA alone needs 80: rings of three tiles fit
-// beside the queries, and the L2 gives half the bytes (a CTA to 256 queries asked
-// it for 7.5 TB/s and its ring of 1.6 tiles ran dry under that load).
+// of a tile of 128 keys where a CTA alone needs 80: two tiles fit beside the
+// queries and the outputs on their way, and the L2 gives half the bytes (a CTA to
+// 256 queries asked it for 7.5 TB/s and its ring of 1.6 tiles ran dry under that
+// load).
 //
 // Warp roles (384 threads a CTA): warp 0 copies this CTA's halves; in CTA 0 warps
 // 1 and 3 issue the products of the first and the second query tile for both
@@ -25,12 +26,13 @@ namespace prefill {
 namespace pair {
 
 constexpr int kTileRows = 2 * kRows;       // queries of a tile, of both CTAs
-constexpr int kStages = 3;                 // tiles of K and of V held
+constexpr int kStages = 2;                 // tiles of K and of V held
 constexpr uint32_t kKStage = kQTile / 2;   // 64 keys x 192 dims
 constexpr uint32_t kVStage = kChunk;       // 128 keys x 64 dims
-constexpr uint32_t kOffK = 2 * kQTile, kOffV = kOffK + kStages * kKStage, kOffBar = kOffV + kStages * kVStage;
+constexpr uint32_t kOffK = 2 * kQTile, kOffV = kOffK + kStages * kKStage, kOffOut = kOffV + kStages * kVStage,
+                   kOffBar = kOffOut + 8 * kStage;
 constexpr int kUnits = 4;                  // units looked up ahead of the slowest reader
-using UnitP = Unit<kTileRows>;
+using UnitP = Unit<kTileRows, 2>;
 // Barriers of CTA 0: K, V, Q (from both CTAs' copies), P, O read, units read. Of each CTA: the others.
 enum : uint32_t {
   B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages, B_VEMPTY = B_VFULL + kStages,
@@ -90,12 +92,12 @@ MLA_DEV void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
 }
 
 // tm_q: dims {192, heads, tq}, tm_v: {128, heads, tk}: boxes {64, 1, 128}; tm_k: {128, heads, tk}, tm_r: {64, 1, tk}:
-// boxes {64, 1, 64}; 128-byte swizzled.
+// boxes {64, 1, 64}; tm_out: {128, heads, tq}, box {64, 1, 32}; 128-byte swizzled.
 template <bool kFp16>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
-                            const PrefillParams p) {
+                            const __grid_constant__ CUtensorMap tm_out, const PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
   // the same offset in both CTAs: the operands' descriptors and the barriers' addresses serve both
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     set_registers_down<kRegsFew>();
     if (warp == 2 && rank == 0 && ok) {
       // ---------------- the units, for both CTAs ----------------
-      Finder<kTileRows> finder;
+      Finder<UnitP> finder;
       finder.start(p);
       int64_t id = blockIdx.x >> 1;
       bool more = true, asking = false;
@@ -425,8 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // O is read: the next unit may write it
-      store_row<kFp16>(p, u, state, t_o, end > u.t0, row < u.rows, (int64_t)u.row + row, [&]() { arrive(B_OEMPTY + w); });
+      store_rows<kFp16>(p, &tm_out, sb + kOffOut + (warp - 4) * kStage, u, state, t_o, end > u.t0, first_row + 32 * (warp & 3),
+                        [&]() { arrive(B_OEMPTY + w); });
     }
+    if (lane == 0) bulk_wait();
   }
   __syncwarp();
   tc_fence_before();

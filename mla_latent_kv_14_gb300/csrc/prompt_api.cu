@@ -50,7 +50,7 @@ constexpr int kCardSms = 152;
 constexpr int kMostPieces = 16;
 // How the attention is launched, from sizes that the host knows.
 struct PrefillPlan {
-  bool pair;         // two CTAs to a unit of 512 queries, or one to a unit of 256
+  bool pair;         // two CTAs to a unit of 512 queries, or one to a unit of 128
   int64_t units;     // most units there can be
   int pieces;        // most pieces of a unit
 };
@@ -62,7 +62,7 @@ int64_t blocks_of(int64_t tq, int64_t batch, int64_t rows) {
 PrefillPlan plan_prefill(int64_t tq, int64_t tk, int64_t batch, int64_t heads) {
   PrefillPlan plan{};
   plan.pair = batch > 0 && tq / batch > prefill::kRows;
-  plan.units = blocks_of(tq, batch, 2 * (plan.pair ? prefill::pair::kTileRows : prefill::kRows)) * heads;
+  plan.units = blocks_of(tq, batch, plan.pair ? prefill::pair::UnitP::kBlock : prefill::few::UnitF::kBlock) * heads;
   plan.pieces = 1;
   // units that do not fill the card twice are cut until they would three times
   const int64_t places = plan.pair ? kCardSms / 2 : kCardSms;
@@ -88,13 +88,17 @@ bool make_map_heads(CUtensorMap* m, const void* base, bool fp16, int dim, int64_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kFp16, bool kPair>
-mla_status launch_prefill(int dev, int64_t units, void* stream, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& r,
-                          const CUtensorMap& v, const prefill::PrefillParams& p) {
+// `maps`: of the queries, keys, rotated keys, values, and for a pair of the outputs
+template <bool kFp16, bool kPair, typename... M>
+mla_status launch_prefill(int dev, int64_t units, void* stream, const prefill::PrefillParams& p, const M&... maps) {
   namespace pf = prefill;
   static std::atomic<bool> set[kMaxDevices];
-  auto kernel = kPair ? pf::pair::mla_prefill_pair_kernel<kFp16> : pf::few::mla_prefill_few_kernel<kFp16>;
+  auto kernel = [] {
+    if constexpr (kPair) return pf::pair::mla_prefill_pair_kernel<kFp16>;
+    else return pf::few::mla_prefill_few_kernel<kFp16>;
+  }();
   constexpr uint32_t smem = kPair ? pf::pair::kSmem : pf::few::kSmem;
+  constexpr int block = kPair ? pf::pair::UnitP::kBlock : pf::few::UnitF::kBlock;
   if (!set[dev].load(std::memory_order_relaxed)) {
     // the softmax warps wait for the registers that the launch gave the others: without them they would wait for good
     cudaFuncAttributes at;
@@ -117,10 +121,10 @@ mla_status launch_prefill(int dev, int64_t units, void* stream, const CUtensorMa
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = kPair ? 2 : 1;
-  MLA_CUDA(cudaLaunchKernelEx(&cfg, kernel, q, k, r, v, p));
+  MLA_CUDA(cudaLaunchKernelEx(&cfg, kernel, maps..., p));
   if (p.splits == 1) return MLA_OK;
   const int64_t warps = pf::kCombineThreads / 32, items = p.tq * p.heads;
-  return launch(pf::mla_prefill_combine_kernel<kFp16, kPair ? pf::pair::kTileRows : pf::kRows>,
+  return launch(pf::mla_prefill_combine_kernel<kFp16, block>,
                 dim3((unsigned)((items + warps - 1) / warps)), pf::kCombineThreads, 0, stream, p);
 }
 
@@ -253,7 +257,7 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   auto strides_ok = [&](int64_t token, int64_t head, int64_t rows, int64_t w) {
     return stride_ok(token, w, rows) && stride_ok(head, w, heads) && token < kStride && head < kStride;
   };
-  if (!strides_ok(q_token_stride, q_head_stride, tq, pf::kQk) || !strides_ok(k_token_stride, k_head_stride, tk, pf::kNope) ||
+  if (out_token_stride >= kStride || out_head_stride >= kStride || !strides_ok(q_token_stride, q_head_stride, tq, pf::kQk) || !strides_ok(k_token_stride, k_head_stride, tk, pf::kNope) ||
       !strides_ok(v_token_stride, v_head_stride, tk, pf::kV) || !stride_ok(rope_stride, pf::kRopeDim, tk) || rope_stride >= kStride ||
       !stride_ok(out_token_stride, pf::kV, tq) || !stride_ok(out_head_stride, pf::kV, heads))
     return MLA_ERR_INVALID_ARG;
@@ -294,7 +298,6 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   p.out = out;
   p.out_token = out_token_stride;
   p.out_head = out_head_stride;
-  p.out_v8 = aligned(out, 32) && out_token_stride % 16 == 0 && out_head_stride % 16 == 0;
   p.lse = lse;
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = need ? p.o_part + (int64_t)splits * tq * heads * pf::kV : nullptr;
@@ -315,11 +318,14 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
       !make_map_heads(&mv, some ? v : q, fp16, pf::kV, some ? heads : 1, some ? tk : 1, some ? v_head_stride : pf::kV,
                       some ? v_token_stride : pf::kV, pf::kKeys))
     return MLA_ERR_CUDA;
-  if (plan.pair)
-    return fp16 ? launch_prefill<true, true>(dev, plan.units, stream, mq, mk, mr, mv, p)
-                : launch_prefill<false, true>(dev, plan.units, stream, mq, mk, mr, mv, p);
-  return fp16 ? launch_prefill<true, false>(dev, plan.units, stream, mq, mk, mr, mv, p)
-              : launch_prefill<false, false>(dev, plan.units, stream, mq, mk, mr, mv, p);
+  if (plan.pair) {
+    CUtensorMap mo;
+    if (!make_map_heads(&mo, out, fp16, pf::kV, heads, tq, out_head_stride, out_token_stride, 32)) return MLA_ERR_CUDA;
+    return fp16 ? launch_prefill<true, true>(dev, plan.units, stream, p, mq, mk, mr, mv, mo)
+                : launch_prefill<false, true>(dev, plan.units, stream, p, mq, mk, mr, mv, mo);
+  }
+  return fp16 ? launch_prefill<true, false>(dev, plan.units, stream, p, mq, mk, mr, mv)
+              : launch_prefill<false, false>(dev, plan.units, stream, p, mq, mk, mr, mv);
 }
 
 }  // extern "C"
