@@ -40,7 +40,7 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;                 // rows of a CTA in a query tile (TMEM lanes)
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kNope = 128, kRopeDim = 64, kQk = kNope + kRopeDim, kV = 128;
-constexpr int kPieceTiles = 8;             // key tiles that a piece of a cut unit has at least
+constexpr int kPieceTiles = 8;             // key tiles that a piece of an average unit has at least
 constexpr uint32_t kChunk = 128 * 128;     // 128 rows x 128 bytes (64 dims)
 constexpr uint32_t kQTile = 3 * kChunk;
 constexpr uint32_t kColO = 256;            // TMEM: S of chain w at 128 w (P over it), its accumulator at 256 + 128 w
@@ -52,6 +52,7 @@ struct PrefillParams {
   int64_t tq, tk;              // rows of q and of k, v
   int batch, heads, causal;
   int splits;                  // most pieces of a unit
+  int piece_tiles;             // key tiles of a piece
   float scale, scale_log2;
   void* out;                   // [tq, heads, 128]
   int64_t out_token, out_head; // strides in elements
@@ -83,7 +84,7 @@ MLA_DEV int visible(const PrefillParams& p, const Span& s, int i) {
   return p.causal ? min(max(s.nk - s.nq + i + 1, s.prefix), s.nk) : s.nk;
 }
 MLA_DEV int pieces_of(const PrefillParams& p, int tiles) {
-  return max(1, min(p.splits, tiles / kPieceTiles));
+  return max(1, min(p.splits, (tiles + p.piece_tiles - 1) / p.piece_tiles));
 }
 
 // A unit as its readers see it: one piece of a block of queries of a head, in kTiles query tiles of kTileRows rows.

@@ -28,7 +28,7 @@ constexpr uint32_t kOffBar = kOffRing + kRing * kChunk;
 enum : uint32_t {
   B_FULL = 0, B_EMPTY = B_FULL + kRing, B_QFULL = B_EMPTY + kRing, B_QEMPTY = B_QFULL + 1, B_SFULL = B_QEMPTY + 1,
   B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 4, B_OEMPTY = B_OFULL + 2, B_LFULL = B_OEMPTY + 2, B_LEMPTY = B_LFULL + 1,
-  B_UFULL = B_LEMPTY + 1, B_UEMPTY = B_UFULL + kUnits, B_NEXT = B_UEMPTY + kUnits, B_DRAIN = B_NEXT + 1, B_STALL = B_DRAIN + 2,
+  B_UFULL = B_LEMPTY + 1, B_UEMPTY = B_UFULL + kUnits, B_WANT = B_UEMPTY + kUnits, B_NEXT = B_WANT + 1, B_DRAIN = B_NEXT + 1, B_STALL = B_DRAIN + 2,
   B_COUNT = B_STALL + 1
 };
 constexpr uint32_t kOffMisc = (kOffBar + 8 * B_COUNT + 15) / 16 * 16;
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_UFULL + s), 1);
       mbar_init(bar(B_UEMPTY + s), kUnitReaders);
     }
+    mbar_init(bar(B_WANT), 1);
     mbar_init(bar(B_NEXT), 1);
     mbar_init(bar(B_DRAIN), 1);
     mbar_init(bar(B_DRAIN + 1), 1);
@@ -139,22 +140,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       Finder<UnitF> finder;
       finder.start(p);
       int64_t id = blockIdx.x;
-      bool more = true, asking = false;
+      // A unit is taken only when the copies of the one before it come to their end: one taken early could not go to a
+      // block that is free sooner.
+      bool asking = false;
       int n = 0, asked = 0;
       while (true) {
-        // the next block's number travels while this one is looked up
-        if (more) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(B_NEXT), 16);
-            ask_next(smem_u32(misc), bar(B_NEXT));
-          }
-          asking = true;
-        }
         UnitF u{};
         u.head = -1;
         bool past = false;
-        const bool found = more && finder.find(p, id, u, past);
-        if (found || !more) {
+        const bool found = id >= 0 && finder.find(p, id, u, past);
+        if (found || id < 0) {
           const int s = n % kUnits;
           if (!ready_all(B_UEMPTY + s, (n / kUnits) ^ 1)) break;
           if (lane == 0) {
@@ -163,14 +158,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(bar(B_UFULL + s));
           }
           __syncwarp();
-          ++n;
+          if (id < 0 || !ready_all(B_WANT, n++)) break;
         }
-        if (!more) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(B_NEXT), 16);
+          ask_next(smem_u32(misc), bar(B_NEXT));
+        }
+        asking = true;
         if (!ready_all(B_NEXT, asked)) break;
         asking = false;
         ++asked;
         id = answer_next(smem_u32(misc));
-        more = id >= 0;
         // read before the next answer is written over it
         fence_proxy_async_smem();
         __syncwarp();
@@ -203,8 +201,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++loads;
       };
+      auto want_next = [&]() {
+        if (leader) mbar_arrive(bar(B_WANT));
+      };
       for (int n = 0; !stop && take(n, u); ++n) {
         const int e = u.end(0, p.causal);
+        if (e - u.t0 < 4) want_next();
         if (e <= u.t0) continue;
         if (!ready_all(B_QEMPTY, q_loads ^ 1u)) break;
         if (leader) {
@@ -213,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++q_loads;
         for (int t = u.t0; t < e && !stop; ++t, ++tile) {
+          if (t == e - 4) want_next();
           const int at = u.k0 + t * kKeys;
           const bool late = Slots(tile).late;
           chunk(&tm_k, 0, u.head, at);

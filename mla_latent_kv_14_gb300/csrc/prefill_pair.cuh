@@ -37,7 +37,7 @@ using UnitP = Unit<kTileRows, 2>;
 enum : uint32_t {
   B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages, B_VEMPTY = B_VFULL + kStages,
   B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2, B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 4,
-  B_OEMPTY = B_OFULL + 2, B_UFULL = B_OEMPTY + 2, B_UEMPTY = B_UFULL + kUnits, B_NEXT = B_UEMPTY + kUnits,
+  B_OEMPTY = B_OFULL + 2, B_UFULL = B_OEMPTY + 2, B_UEMPTY = B_UFULL + kUnits, B_WANT = B_UEMPTY + kUnits, B_NEXT = B_WANT + 1,
   B_VTAIL = B_NEXT + 1, B_DRAIN = B_VTAIL + 1, B_STALL = B_DRAIN + 2, B_COUNT = B_STALL + 1
 };
 constexpr uint32_t kOffMisc = (kOffBar + 8 * B_COUNT + 15) / 16 * 16;
@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_UFULL + s), 1);
       mbar_init(bar(B_UEMPTY + s), kUnitReaders);
     }
+    mbar_init(bar(B_WANT), 1);
     mbar_init(bar(B_NEXT), 1);
     mbar_init(bar(B_VTAIL), 1);
     mbar_init(bar(B_STALL), 1);
@@ -184,23 +185,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       Finder<UnitP> finder;
       finder.start(p);
       int64_t id = blockIdx.x >> 1;
-      bool more = true, asking = false;
+      // A unit is taken only when the copies of the one before it come to their end: one taken early could not go to a
+      // block that is free sooner.
+      bool asking = false;
       int n = 0, asked = 0;
       const uint32_t peer_units = mapa(smem_u32(units), 1);
       while (true) {
-        // the next pair's number travels while this one is looked up
-        if (more) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(B_NEXT), 16);
-            ask_next(smem_u32(misc), bar(B_NEXT));
-          }
-          asking = true;
-        }
         UnitP u{};
         u.head = -1;
         bool past = false;
-        const bool found = more && finder.find(p, id, u, past);
-        if (found || !more) {
+        const bool found = id >= 0 && finder.find(p, id, u, past);
+        if (found || id < 0) {
           const int s = n % kUnits;
           if (!ready_all(B_UEMPTY + s, (n / kUnits) ^ 1)) break;
           if (lane == 0) {
@@ -213,15 +208,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_remote(mapa(bar(B_UFULL + s), 1));
           }
           __syncwarp();
-          ++n;
+          if (id < 0 || !ready_all(B_WANT, n++)) break;
         }
-        if (!more) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(B_NEXT), 16);
+          ask_next(smem_u32(misc), bar(B_NEXT));
+        }
+        asking = true;
         if (!ready_all(B_NEXT, asked)) break;
         asking = false;
         ++asked;
         id = answer_next(smem_u32(misc));
-        more = id >= 0;
-        id >>= 1;
+        id = id < 0 ? id : id >> 1;
         // read before the next answer is written over it
         fence_proxy_async_smem();
         __syncwarp();
@@ -255,10 +253,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d_pair(sb + w * kQTile + c * kChunk, &tm_q, b, 64 * c, u.head, u.row + kTileRows * w + kRows * rank);
         }
       };
+      auto want_next = [&]() {
+        if (leader && rank == 0) mbar_arrive(bar(B_WANT));
+      };
       for (; !stop && take(n, u); ++n) {
         const int e0 = u.end(0, p.causal), e1 = u.end(1, p.causal), e = max(e0, e1);
         if (e0 > u.t0) queries(0);
+        if (e - u.t0 < 2) want_next();
         for (int t = u.t0; t < e && !stop; ++t, ++tile) {
+          if (t == e - 2) want_next();
           const uint32_t s = tile % kStages, round = tile / kStages;
           const int at = u.k0 + t * kKeys, rest = u.nk - t * kKeys;
           if (!ready_all(B_KEMPTY + s, round ^ 1u)) { stop = true; break; }

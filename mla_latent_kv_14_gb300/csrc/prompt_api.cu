@@ -53,23 +53,30 @@ struct PrefillPlan {
   bool pair;         // two CTAs to a unit of 512 queries, or one to a unit of 128
   int64_t units;     // most units there can be
   int pieces;        // most pieces of a unit
+  int piece_tiles;   // key tiles of a piece
 };
-// blocks of `rows` queries that `batch` documents of tq rows can have
-int64_t blocks_of(int64_t tq, int64_t batch, int64_t rows) {
-  const int64_t some = batch < tq ? batch : tq;     // documents with a row
-  return (tq + (rows - 1) * some) / rows;
-}
+// A unit's key tiles are cut where the units would fill the card's places less than twice: into as many pieces as fill
+// them twice if the documents are alike, and of one length, so that long documents get more of them (up to twice as
+// many). Measured (GB300, us): 16 units of 512 tiles 102 in 16 pieces each, 138 in 10, which leave a second round of 8
+// pieces; 128 units of 43 to 128 tiles 131 to 140 in 2 to 4 pieces, 154 uncut; but 256 units of 64 tiles 172 uncut, 187
+// in 2 pieces. A piece costs some 4 tiles more than its own (the pipeline's start, its share of the output to memory and
+// back), so that 8 units of 256 tiles take 36 in 16 pieces and 43 in 32.
 PrefillPlan plan_prefill(int64_t tq, int64_t tk, int64_t batch, int64_t heads) {
   PrefillPlan plan{};
-  plan.pair = batch > 0 && tq / batch > prefill::kRows;
-  plan.units = blocks_of(tq, batch, plan.pair ? prefill::pair::UnitP::kBlock : prefill::few::UnitF::kBlock) * heads;
-  plan.pieces = 1;
-  // units that do not fill the card twice are cut until they would three times
-  const int64_t places = plan.pair ? kCardSms / 2 : kCardSms;
-  if (plan.units == 0 || plan.units >= 2 * places) return plan;
-  const int64_t want = (3 * places + plan.units - 1) / plan.units, most = tk / (prefill::kPieceTiles * prefill::kKeys);
-  const int64_t n = want < most ? want : most;
-  plan.pieces = (int)(n < 1 ? 1 : n > kMostPieces ? kMostPieces : n);
+  plan.pieces = plan.piece_tiles = 1;
+  if (batch <= 0 || tq <= 0) return plan;
+  plan.pair = tq / batch > prefill::kRows;
+  const int64_t block = plan.pair ? prefill::pair::UnitP::kBlock : prefill::few::UnitF::kBlock, places = plan.pair ? kCardSms / 2 : kCardSms;
+  const int64_t some = batch < tq ? batch : tq;     // documents with a query, at most
+  plan.units = (tq + (block - 1) * some) / block * heads;
+  const int64_t alike = some * ((tq / some + block - 1) / block) * heads;   // units of documents of one length
+  const int64_t tiles = (tk / batch + prefill::kKeys - 1) / prefill::kKeys;
+  int64_t want = 2 * places / alike, most = tiles / prefill::kPieceTiles;
+  if (want < 1 || most < 1) return plan;
+  want = want < most ? want : most;
+  want = want < kMostPieces ? want : kMostPieces;
+  plan.piece_tiles = (int)((tiles + want - 1) / want);
+  plan.pieces = (int)(2 * want < kMostPieces ? 2 * want : kMostPieces);
   return plan;
 }
 size_t piece_bytes(int64_t tq, int64_t heads) { return (size_t)tq * (size_t)heads * (prefill::kV + 1) * 4; }
@@ -293,6 +300,7 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   p.heads = heads;
   p.causal = causal ? 1 : 0;
   p.splits = splits;
+  p.piece_tiles = plan.piece_tiles;
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.out = out;

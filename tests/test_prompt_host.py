@@ -128,9 +128,10 @@ def test_prefill_workspace(lib):
     for tq, tk, batch, heads in ((1, 5000, 1, 1), (32, 100000, 8, 16), (300, 9000, 2, 8)):
         got, row = size(tq, tk, batch, heads), tq * heads * 129 * 4
         assert got > row and got % row == 0 and got // row <= 16
-    # the most that any sizes ask for: fewer than two cards' units of 256 rows, each cut until there are three cards' worth
+    # the most that any sizes ask for: fewer than two cards' units, cut into up to two cards' pieces if their documents are
+    # alike and up to twice as many if they are not
     most = max(size(tq, 1 << 20, b, h) for tq in (1, 255, 256, 257, 5000, 38912, 77000) for b in (1, 3, 200) for h in (1, 2, 7, 64, 151, 303))
-    assert most <= (3 * 152 + 2 * 152) * 256 * 129 * 4
+    assert most <= 2 * 2 * 152 * 256 * 129 * 4
 
 
 # ---------------------------------------------------------------------------
