@@ -220,6 +220,23 @@ MLA_DEV bool wait_inline(uint32_t bar, uint32_t parity, const Guard& g) {
   }
   return false;
 }
+// A barrier tells one phase from the next by parity alone. A thread that leaves some of a ring's rounds to others may be
+// ahead of its barriers by a phase or more and would take an old phase for the one it wants: so it first waits until the
+// copies have been asked for (`*issued` counts them), when the place's round before is over.
+MLA_DEV void set_issued(uint32_t count, uint32_t n) { asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(count), "r"(n) : "memory"); }
+MLA_DEV bool wait_issued(uint32_t count, uint32_t index, const Guard& g) {
+  const uint64_t t0 = cycles();
+  while (true) {
+    uint32_t n;
+    asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(n) : "r"(count) : "memory");
+    if (n > index) return true;
+    if (*g.abort) return false;
+    if (cycles() - t0 > g.limit) {
+      *g.abort = 1u;
+      atomicOr(g.status, STATUS_TIMEOUT);
+    }
+  }
+}
 template <int kN>
 MLA_DEV void set_registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN)); }
 template <int kN>

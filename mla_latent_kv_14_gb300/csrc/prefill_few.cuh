@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + kOffMisc);  // 16-B aligned
-  // misc: [0, 4) the answer of ask_next, 4 TMEM base, 5 abort, 6 ok, 7 status where none is given, from 16 on the units
+  // misc: [0, 4) the answer of ask_next, 4 TMEM base, 5 abort, 6 ok, 7 status where none is given, 8 chunks asked
+  // for, from 16 on the units
   volatile uint32_t* tmem_slot = misc + 4;
   volatile uint32_t* abort_flag = misc + 5;
   volatile uint32_t* ok_flag = misc + 6;
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(B_STALL), 1);
     *abort_flag = 0u;
     *ok_flag = 1u;
-    misc[7] = 0u;
+    misc[7] = misc[8] = 0u;
     fence_mbar_init();
     if (p.stall_cycles) {
       // test hook: a bounded wait on a barrier nothing arrives at gives up and reports STATUS_TIMEOUT before
@@ -119,8 +120,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const bool ok = *ok_flag != 0u;
 
+  const uint32_t issued = smem_u32(misc + 8);
   auto ready = [&](uint32_t i, uint32_t parity) { return wait_inline<false>(bar(i), parity & 1u, guard); };
   auto ready_all = [&](uint32_t i, uint32_t parity) { return __all_sync(0xffffffffu, ready(i, parity)) != 0; };
+  // a chain waits for its own tiles' chunks only
+  auto landed = [&](uint32_t chunk) { return wait_issued(issued, chunk, guard) && ready(B_FULL + slot_of(chunk), phase_of(chunk)); };
   // the readers' side of the units: the n-th one, into registers; one lane reads for a role of a single thread
   auto take_one = [&](int n, UnitF& u) {
     if (!ready(B_UFULL + n % kUnits, n / kUnits)) return false;
@@ -198,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) {
           mbar_arrive_expect_tx(bar(B_FULL + slot), kChunk);
           tma_load_3d_plain(sb + kOffRing + slot * kChunk, m, bar(B_FULL + slot), x, y, z);
+          set_issued(issued, loads + 1u);
         }
         ++loads;
       };
@@ -244,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                        d_v = sdesc_sw128(sb + kOffRing, kChunk, 1024);
         const uint32_t t_s = tmem + 128u * w, t_o = tmem + kColO + 128u * w;
         uint32_t tile = 0, q_used = 0, p_used = 0, o_used = 0;
-        auto landed = [&](uint32_t chunk) { return ready(B_FULL + slot_of(chunk), phase_of(chunk)); };
         auto scores = [&](const Slots& s, bool last) {   // S = Q K^T
           if (!landed(s.key(0)) || !landed(s.key(1)) || !landed(s.key(2))) return false;
           tc_fence_after();
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // before this tile's P is handed over.
           const Slots at(tile + (uint32_t)(t - u.t0));
           const uint32_t v0 = at.value(0), v1 = at.value(1);
-          if (!ready_all(B_FULL + slot_of(v0), phase_of(v0)) || !ready_all(B_FULL + slot_of(v1), phase_of(v1))) {
+          if (!__all_sync(0xffffffffu, landed(v0) && landed(v1))) {
             failed = true;
             break;
           }

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + kOffMisc);  // 16-B aligned
-  // misc: [0, 4) the answer of ask_next, 4 TMEM base, 5 abort, 6 ok, 7 status where none is given, from 16 on the units
+  // misc: [0, 4) the answer of ask_next, 4 TMEM base, 5 abort, 6 ok, 7 status where none is given, 8 and 9 tiles of keys
+  // and of values asked for, from 16 on the units
   volatile uint32_t* tmem_slot = misc + 4;
   volatile uint32_t* abort_flag = misc + 5;
   volatile uint32_t* ok_flag = misc + 6;
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto lead_bar = [&](uint32_t i) { return mapa(bar(i), 0); };   // CTA 0's
   uint32_t* status = p.status ? p.status : misc + 7;
   const Guard guard{abort_flag, status, kWaitLimitCycles};
+  const uint32_t issued = smem_u32(misc + 8);
   auto ready = [&](uint32_t i, uint32_t parity) { return wait_inline<true>(bar(i), parity & 1u, guard); };
   auto ready_all = [&](uint32_t i, uint32_t parity) { return __all_sync(0xffffffffu, ready(i, parity)) != 0; };
 
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(B_STALL), 1);
     *abort_flag = 0u;
     *ok_flag = 1u;
-    misc[7] = 0u;
+    misc[7] = misc[8] = misc[9] = 0u;
     fence_mbar_init();
     if (p.stall_cycles) {
       // test hook: a bounded wait on a barrier nothing arrives at gives up and reports STATUS_TIMEOUT before
@@ -271,10 +273,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d_pair(to, &tm_k, b, 0, u.head, at + 64 * rank);
             tma_load_3d_pair(to + kChunk / 2, &tm_k, b, 64, u.head, at + 64 * rank);
             tma_load_3d_pair(to + kChunk, &tm_r, b, 0, 0, at + 64 * rank);
+            set_issued(issued, tile + 1u);
           }
           // the second query tile is wanted after the first one's scores
           if (t == u.t0 && e1 > u.t0) queries(1);
           if (stop || !ready_all(B_VEMPTY + s, round ^ 1u)) { stop = true; break; }
+          if (leader) set_issued(issued + 4u, tile + 1u);
           const uint32_t b = lead_bar(B_VFULL + s), to = sb + kOffV + s * kVStage;
           if (rest >= kKeys) {
             if (leader) {
@@ -339,7 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           release(B_KEMPTY + s, alone);
           if (last) umma_commit_both(bar(B_QEMPTY + w));
         };
-        auto keys_ready = [&](uint32_t k_tile) { return ready(B_KFULL + k_tile % kStages, k_tile / kStages); };
+        // tiles of the other query tile only are not waited for
+        auto keys_ready = [&](uint32_t k_tile) {
+          return wait_issued(issued, k_tile, guard) && ready(B_KFULL + k_tile % kStages, k_tile / kStages);
+        };
+        auto values_ready = [&](uint32_t v_tile) {
+          return wait_issued(issued + 4u, v_tile, guard) && ready(B_VFULL + v_tile % kStages, v_tile / kStages);
+        };
         UnitP u;
         bool failed = false;
         for (int n = 0; !failed && take_one(n, u); ++n) {
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           for (int t = u.t0; t < end; ++t) {
             const uint32_t at = tile + (uint32_t)(t - u.t0), s = at % kStages;
-            if (!ready(B_VFULL + s, at / kStages) || (t + 1 < end && !keys_ready(at + 1)) ||
+            if (!values_ready(at) || (t + 1 < end && !keys_ready(at + 1)) ||
                 (t == u.t0 && !ready(B_OEMPTY + w, o_used++ ^ 1u)) || !ready(B_PFULL + w, p_used)) {
               failed = true;
               break;
