@@ -165,6 +165,7 @@ struct NormAppendParams {
   float eps;
   uint16_t* rows;              // [n, latent + 64] or null
   int64_t rows_stride;
+  int wide;                    // rows are 32-B aligned
 };
 
 template <bool kFp16, int kFormat>  // kFormat: mla_kv_format
@@ -236,9 +237,11 @@ __global__ void __launch_bounds__(32 * rows::kAppendWarps) mla_norm_append_kv_ke
   const uint4 y0 = pack8<kFp16>(x), y1 = pack8<kFp16>(x + 8);
   if (q.rows) {
     uint16_t* dst = q.rows + t * q.rows_stride;
-    if (latent) {
+    if (kFormat == 0) {
       reinterpret_cast<uint4*>(dst)[c0] = y0;
       reinterpret_cast<uint4*>(dst)[c1] = y1;
+    } else if (latent) {
+      store16<kFp16>(dst + 16 * lane, x, q.wide);
     }
     store_rope(dst + kLatent);
   }

@@ -109,6 +109,20 @@ MLA_DEV uint4 pack8(const float* x) {
                     pack2<kFp16>(x[6], x[7]));
 }
 
+// sixteen values as 32 consecutive bytes (16-B aligned; one whole sector where 32-B aligned, `wide`: two stores of half
+// a sector each let a warp's request touch every sector twice)
+template <bool kFp16>
+MLA_DEV void store16(uint16_t* dst, const float* x, bool wide) {
+  const uint4 a = pack8<kFp16>(x), b = pack8<kFp16>(x + 8);
+  if (wide) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    st_global_v8(dst, w);
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = a;
+    reinterpret_cast<uint4*>(dst)[1] = b;
+  }
+}
+
 // (a, b) turned by the angle of (c, s)
 MLA_DEV float turn_lo(float a, float b, float c, float s) { return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)); }
 MLA_DEV float turn_hi(float a, float b, float c, float s) { return __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c)); }
