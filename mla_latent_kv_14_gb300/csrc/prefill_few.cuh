@@ -5,9 +5,10 @@
 // counts is how much of them is on its way: the queries take 48 KB, the rest of
 // shared memory is a ring of chunks of 128 rows x 128 bytes (three of keys, two
 // of values a tile), 2.2 tiles. The two chains take every other key tile of the
-// same queries, each with an accumulator and a reference of its own; the first
-// one's warps join them at the unit's end. Warps none of whose 32 rows is a query
-// only pass the tiles on.
+// same queries, each with an accumulator and a reference of its own; the warps of
+// the one that had the first tile join them at the unit's end. It is the other one
+// that begins the next unit, so that units of a single tile overlap too. Warps none
+// of whose 32 rows is a query only pass the tiles on.
 //
 // Warp roles (384 threads): warp 0 issues the copies, warps 1 and 3 the MMAs of
 // the first and the second chain (warp 1 owns TMEM), warp 2 finds the units,
@@ -27,12 +28,12 @@ constexpr uint32_t kOffRing = kQTile;
 constexpr uint32_t kOffBar = kOffRing + kRing * kChunk;
 enum : uint32_t {
   B_FULL = 0, B_EMPTY = B_FULL + kRing, B_QFULL = B_EMPTY + kRing, B_QEMPTY = B_QFULL + 1, B_SFULL = B_QEMPTY + 1,
-  B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 4, B_OEMPTY = B_OFULL + 2, B_LFULL = B_OEMPTY + 2, B_LEMPTY = B_LFULL + 1,
-  B_UFULL = B_LEMPTY + 1, B_UEMPTY = B_UFULL + kUnits, B_WANT = B_UEMPTY + kUnits, B_NEXT = B_WANT + 1, B_DRAIN = B_NEXT + 1, B_STALL = B_DRAIN + 2,
+  B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 4, B_OEMPTY = B_OFULL + 2, B_LFULL = B_OEMPTY + 2,
+  B_UFULL = B_LFULL + 2, B_UEMPTY = B_UFULL + kUnits, B_WANT = B_UEMPTY + kUnits, B_NEXT = B_WANT + 1, B_DRAIN = B_NEXT + 1, B_STALL = B_DRAIN + 2,
   B_COUNT = B_STALL + 1
 };
 constexpr uint32_t kOffMisc = (kOffBar + 8 * B_COUNT + 15) / 16 * 16;
-constexpr uint32_t kOffState = kOffMisc + 64 + 64 * kUnits;   // the second chain's reference and sum of each row
+constexpr uint32_t kOffState = kOffMisc + 64 + 64 * kUnits;   // a chain's reference and sum of each row, for the other
 constexpr uint32_t kSmem = kOffState + 8 * kRows + 1024;
 static_assert(kSmem <= 232448);
 constexpr int kUnitReaders = 11;           // producer, two issuing threads and eight softmax warps
@@ -78,9 +79,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(B_QFULL), 1);
     mbar_init(bar(B_QEMPTY), 2);   // both chains
-    mbar_init(bar(B_LFULL), 4);
-    mbar_init(bar(B_LEMPTY), 4);
     for (int w = 0; w < 2; ++w) {
+      mbar_init(bar(B_LFULL + w), 4);
       mbar_init(bar(B_SFULL + w), 1);
       mbar_init(bar(B_PFULL + w), 4);
       mbar_init(bar(B_PFULL + 2 + w), 4);
@@ -269,11 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; !failed && take_one(n, u); ++n) {
           mbar_arrive(bar(B_UEMPTY + n % kUnits));
           if (u.head < 0) break;
-          const int e = u.end(0, p.causal), first = u.t0 + w;
+          const int e = u.end(0, p.causal), first = u.t0 + (w ^ (n & 1));   // the chains begin a unit in turn
           if (e <= u.t0) continue;
           if (!ready(B_QFULL, q_used++)) break;
           if (first >= e) mbar_arrive(bar(B_QEMPTY));   // no tile for this chain
-          else if (!scores(Slots(tile + w), first + 2 >= e)) break;
+          else if (!scores(Slots(tile + (uint32_t)(first - u.t0)), first + 2 >= e)) break;
           for (int t = first; t < e; t += 2) {
             const Slots s(tile + (uint32_t)(t - u.t0));
             const uint32_t v0 = s.value(0), v1 = s.value(1);
@@ -323,15 +323,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(i));
     };
-    uint32_t s_used = 0, o_used[2] = {0, 0}, l_used = 0, tile = 0;
+    uint32_t s_used = 0, o_used = 0, o_other = 0, l_used = 0, tile = 0;
     bool failed = !ok;
     UnitF u;
     for (int n = 0; !failed && take(n, u); ++n) {
       const int e = u.end(0, p.causal);
       const bool idle = r - lane >= u.rows;          // none of the warp's rows is a query
       const int seen = r < u.rows ? u.visible(r, p.causal) : u.nk, least = u.visible(0, p.causal);   // of the row; of all rows
+      const bool leads = w == (n & 1);
+      const int begin = u.t0 + (leads ? 0 : 1);
       Row state{-INFINITY, 0.f};
-      for (int t = u.t0 + w; t < e; t += 2) {
+      for (int t = begin; t < e; t += 2) {
         if (!ready_all(B_SFULL + w, s_used++)) { failed = true; break; }
         tc_fence_after();
         const int rest = u.nk - t * kKeys;
@@ -356,23 +358,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           arrive(B_PFULL + 2 + w);
           continue;
         }
-        softmax_tile<kFp16>(state, t_s, t_o + 128u * w, p.scale_log2, (t + 1) * kKeys > least, seen - t * kKeys, t == u.t0 + w,
+        softmax_tile<kFp16>(state, t_s, t_o + 128u * w, p.scale_log2, (t + 1) * kKeys > least, seen - t * kKeys, t == begin,
                             [&](int h) { arrive(B_PFULL + 2 * h + w); });
       }
       if (failed) break;
       tile += max(e - u.t0, 0);
-      if (w == 1) {
-        if (!ready_all(B_LEMPTY, l_used++ ^ 1u)) break;
+      const bool some = e > u.t0, both = e > u.t0 + 1;   // tiles of the chain that began, of the other
+      const uint32_t o_round = o_used, other_round = o_other;
+      o_used += leads ? some : both;
+      o_other += leads ? both : some;
+      if (!leads) {
+        // this thread has read what stood here: it wrote the unit before
         states[r] = make_float2(state.m, state.l);
-        arrive(B_LFULL);
+        arrive(B_LFULL + (w ^ 1));
         continue;
       }
-      // the first chain's warps write the unit: both chains' shares, at the larger of their references
-      if (!ready_all(B_LFULL, l_used++)) break;
+      // The warps of the chain that began write the unit: both chains' shares, at the larger of their references. The
+      // other chain's warps have by now seen the accumulators of the unit before, so that no older phase passes for these.
+      if (!ready_all(B_LFULL + w, l_used++)) break;
       const float2 other = states[r];
-      arrive(B_LEMPTY);
-      const bool some = e > u.t0, both = e > u.t0 + 1;
-      if ((some && !ready_all(B_OFULL, o_used[0]++)) || (both && !ready_all(B_OFULL + 1, o_used[1]++))) break;
+      if ((some && !ready_all(B_OFULL + w, o_round)) || (both && !ready_all(B_OFULL + (w ^ 1), other_round))) break;
       tc_fence_after();
       const float m = fmaxf(state.m, other.x), ref = m == -INFINITY ? 0.f : m;
       const float f0 = exp2_approx((state.m - ref) * p.scale_log2), f1 = exp2_approx((other.x - ref) * p.scale_log2);
@@ -392,14 +397,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t a[32], b[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) a[k] = b[k] = 0u;
-        if (some) tmem_ld32(t_o + 32u * c, a);
-        if (both) tmem_ld32(t_o + 128u + 32u * c, b);
+        if (some) tmem_ld32(t_o + 128u * w + 32u * c, a);
+        if (both) tmem_ld32(t_o + 128u * (w ^ 1) + 32u * c, b);
         tmem_wait_ld();
         pin_regs32(a);
         pin_regs32(b);
         if (c == 3) {      // both are read: the next unit may write them
-          if (some) arrive(B_OEMPTY);
-          if (both) arrive(B_OEMPTY + 1);
+          if (some) arrive(B_OEMPTY + w);
+          if (both) arrive(B_OEMPTY + (w ^ 1));
         }
         if (!live) continue;
         float v[32];

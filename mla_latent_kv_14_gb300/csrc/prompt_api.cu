@@ -65,11 +65,15 @@ struct PrefillPlan {
 // pieces; 128 units of 43 to 128 tiles 131 to 140 in 2 to 4 pieces, 154 uncut; but 256 units of 64 tiles 172 uncut, 187
 // in 2 pieces. A piece costs some 4 tiles more than its own (the pipeline's start, its share of the output to memory and
 // back), so that 8 units of 256 tiles take 36 in 16 pieces and 43 in 32.
+//
+// Documents of up to 256 queries on average go to one CTA a unit: 16 of 256 over 4096 keys, 16 heads 162 us, 218 in
+// pairs; of 300 231 and 240; of 400 269 and 243; 64 of 256 by themselves 87 and 99, of 512 250 and 166.
+constexpr int kFewRows = 256;
 PrefillPlan plan_prefill(int64_t tq, int64_t tk, int64_t batch, int64_t heads) {
   PrefillPlan plan{};
   plan.pieces = plan.piece_tiles = 1;
   if (batch <= 0 || tq <= 0) return plan;
-  plan.pair = tq / batch > prefill::kRows;
+  plan.pair = tq / batch > kFewRows;
   const int64_t block = plan.pair ? prefill::pair::UnitP::kBlock : prefill::few::UnitF::kBlock, places = plan.pair ? kCardSms / 2 : kCardSms;
   const int64_t some = batch < tq ? batch : tq;     // documents with a query, at most
   plan.units = (tq + (block - 1) * some) / block * heads;
