@@ -127,7 +127,8 @@ def test_norm_rotate_of_small_and_large_rows(dtype):
     _close(mla.mla_norm_rotate(shared, pos.to(DEV), _table()), want, bound, dtype)
 
 
-@pytest.mark.parametrize("tokens,heads,dim", [(1500, 128, 192), (4099, 3, 128), (9001, 1, 128), (700, 64, 576)])
+@pytest.mark.parametrize("tokens,heads,dim", [(1500, 128, 192), (4099, 3, 128), (11001, 3, 128), (9001, 1, 128), (700, 64, 576),
+                                              (20001, 2, 64), (257, 128, 256)])
 def test_norm_rotate_of_many_rows(tokens, heads, dim):
     """Both sides of the launch's rules; the reference in 64 bits on the GPU."""
     g = torch.Generator(device=DEV).manual_seed(5)
@@ -373,8 +374,13 @@ def test_read_kv_gives_what_the_append_wrote(fmt):
 
 
 # ---------------------------------------------------------------------------
-# attention of many new tokens
+# attention of many new tokens: documents of up to 256 queries on average take one CTA a unit, others two; a long
+# document more (`extra`) takes a test's documents to the other side
 # ---------------------------------------------------------------------------
+LONG = [(1900, 1900)]
+both_kernels = pytest.mark.parametrize("extra", [[], LONG], ids=["few", "pair"])
+
+
 def _inputs(lens, heads, dtype, seed, spread=1.5):
     g = _gen(seed)
     n_q, n_k = sum(a for a, _ in lens), sum(b for _, b in lens)
@@ -392,7 +398,12 @@ def _check(out, lse, q, kv, kr, cu_q, cu_k, causal, prefix, dtype, docs=None, he
     for b in range(len(cu_q) - 1) if docs is None else docs:
         a, z, c, d = cu_q[b], cu_q[b + 1], cu_k[b], cu_k[b + 1]
         seen = oracle.visible(z - a, d - c, causal, 0 if prefix is None else int(prefix[b]))
-        pick = np.arange(z - a) if rows is None else np.array([r for r in rows if r < z - a], dtype=np.int64)
+        if rows is None:     # all of a short document, the edges of a long one's blocks
+            pick = np.arange(z - a)
+            if z - a > 420:
+                pick = np.array([r for r in range(z - a) if r % 128 in (0, 1, 126, 127) or r == z - a - 1][::3] + [z - a - 1])
+        else:
+            pick = np.array([r for r in rows if r < z - a], dtype=np.int64)
         if len(pick) == 0:
             continue
         ro, rl, size, dots = oracle.prefill(q[a:z][pick][:, heads], kv[c:d][:, heads, :128], kr[c:d], kv[c:d][:, heads, 128:],
@@ -423,7 +434,9 @@ def _run(q, kv, kr, cu_q, cu_k, causal, prefix=None, **kw):
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("lens,heads", [([(1, 1)], 1), ([(5, 5)], 2), ([(128, 128)], 1), ([(129, 129)], 3), ([(256, 384)], 2),
-                                        ([(300, 300), (1, 77), (64, 640)], 2), ([(40, 1000), (257, 257)], 4)])
+                                        ([(300, 300), (1, 77), (64, 640)], 2), ([(40, 1000), (257, 257)], 4),
+                                        ([(257, 257)], 2), ([(384, 400)], 1), ([(512, 512)], 2), ([(513, 640), (300, 1000)], 2),
+                                        ([(900, 900), (1, 77), (64, 640)], 2), ([(1025, 1100)], 1)])
 def test_prefill(lens, heads, causal, dtype):
     case = _inputs(lens, heads, dtype, 3 + heads)
     out, lse = _run(*case, causal)
@@ -432,8 +445,10 @@ def test_prefill(lens, heads, causal, dtype):
 
 @pytest.mark.parametrize("lens", [[(0, 0), (3, 0), (0, 5), (7, 3), (0, 0)], [(200, 70), (130, 129), (2, 1)], [(0, 9), (0, 0)]])
 @pytest.mark.parametrize("causal", [True, False])
-def test_prefill_of_empty_documents_and_rows(lens, causal):
+@both_kernels
+def test_prefill_of_empty_documents_and_rows(lens, causal, extra):
     """Documents without queries or keys, causal queries that see nothing."""
+    lens = lens + [(2600, 900)] * len(extra) + [(0, 3)]
     case = _inputs(lens, 3, BF, 5)
     out, lse = _run(*case, causal)
     _check(out, lse, *case, causal, None, BF)
@@ -449,20 +464,22 @@ def test_prefill_without_any_key():
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
-def test_prefill_prefixes(dtype):
+@both_kernels
+def test_prefill_prefixes(dtype, extra):
     """Prefixes of none, some and all keys, and beyond them; queries before the keys' start see the prefix alone."""
     lens, prefix = [(300, 300), (129, 129), (50, 400), (64, 64), (90, 30), (7, 7)], [0, 100, 390, 64, 11, 1 << 30]
+    lens, prefix = lens + extra, prefix + [777] * len(extra)
     case = _inputs(lens, 2, dtype, 9)
     out, lse = _run(*case, True, prefix)
     _check(out, lse, *case, True, prefix, dtype)
-    out, lse = _run(*case, True, [-5] * 6)
-    _check(out, lse, *case, True, [0] * 6, dtype)
+    out, lse = _run(*case, True, [-5] * len(lens))
+    _check(out, lse, *case, True, [0] * len(lens), dtype)
     out, lse = _run(*case, False, prefix)
     _check(out, lse, *case, False, None, dtype)
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
-@pytest.mark.parametrize("lens,heads", [([(1, 5000)], 1), ([(4, 4100), (3, 130), (1, 1), (130, 2600)], 2), ([(260, 9000)], 1)])
+@pytest.mark.parametrize("lens,heads", [([(1, 5000)], 1), ([(4, 4100), (3, 130), (1, 1), (130, 2600)], 2), ([(260, 9000)], 1), ([(700, 6000), (64, 3000)], 1)])
 def test_prefill_of_few_rows_over_long_keys(lens, heads, dtype):
     """Units that are cut along the keys and joined."""
     case = _inputs(lens, heads, dtype, 13)
@@ -487,9 +504,10 @@ def test_prefill_scores_that_grow_and_shrink():
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_prefill_is_not_reached_by_what_lies_outside(bad):
+@both_kernels
+def test_prefill_is_not_reached_by_what_lies_outside(bad, extra):
     """Keys, values and queries behind, before and between the documents poisoned; rows of no document stay."""
-    lens = [(70, 70), (33, 200), (150, 150)]
+    lens = [(70, 70), (33, 200), (150, 150)] + extra
     q, kv, kr, cu_q, cu_k = _inputs(lens, 2, BF, 19)
     pad = 40
     # the middle document becomes a gap that no offsets name: a document of its own with poisoned rows
@@ -501,12 +519,13 @@ def test_prefill_is_not_reached_by_what_lies_outside(bad):
     lse = torch.full((q2.shape[0], 2), 6.0, device=DEV)
     _run(q2, kv2, kr2, cu_q + pad, cu_k + pad, True, out=out, lse=lse)
     assert (out[:pad] == 6.0).all() and (out[-pad:] == 6.0).all() and (lse[:pad] == 6.0).all() and (lse[-pad:] == 6.0).all()
-    _check(out[pad:], lse[pad:], q, kv, kr, cu_q, cu_k, True, None, BF, docs=[0, 2])
+    _check(out[pad:], lse[pad:], q, kv, kr, cu_q, cu_k, True, None, BF, docs=[0, 2, 3][:2 + len(extra)])
 
 
-def test_prefill_strides():
+@both_kernels
+def test_prefill_strides(extra):
     """Heads-major inputs and outputs, column ranges, one head of a wider tensor."""
-    lens, heads = [(140, 140), (20, 150)], 3
+    lens, heads = [(140, 140), (20, 150)] + extra, 3
     q, kv, kr, cu_q, cu_k = _inputs(lens, heads, HF, 23)
     ref, ref_l = _run(q, kv, kr, cu_q, cu_k, True)
     qt = q.transpose(0, 1).contiguous().to(DEV).transpose(0, 1)
@@ -523,13 +542,17 @@ def test_prefill_strides():
 
 
 @pytest.mark.parametrize("heads", [1, 20])
-def test_prefill_of_many_documents(heads):
-    """More documents than a warp looks at together, more units than blocks at once."""
+@pytest.mark.parametrize("most", [300, 800])
+def test_prefill_of_many_documents(heads, most):
+    """More documents than a warp looks at together, more units than blocks at once; the same bits every time."""
     rng = np.random.default_rng(4)
-    lens = [(int(a), int(a) + int(b)) for a, b in zip(rng.integers(0, 300, 75), rng.integers(0, 40, 75))]
+    lens = [(int(a), int(a) + int(b)) for a, b in zip(rng.integers(0, most, 75), rng.integers(0, 40, 75))]
     case = _inputs(lens, heads, BF, 29)
     out, lse = _run(*case, True)
-    _check(out, lse, *case, True, None, BF, heads=[0, heads - 1][:heads], rows=[0, 1, 60, 127, 128, 200, 255, 256, 299])
+    _check(out, lse, *case, True, None, BF, heads=[0, heads - 1][:heads], rows=[0, 1, 60, 127, 128, 200, 255, 256, 299, 511, 512, 700])
+    for _ in range(8):
+        again = _run(*case, True)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
 def test_prefill_of_long_documents_sampled():
@@ -539,13 +562,16 @@ def test_prefill_of_long_documents_sampled():
     _check(out, lse, *case, True, None, BF, heads=[0, 7, 15], rows=[0, 127, 128, 255, 256, 511, 699, 1300, 2303, 2304, 2499])
 
 
-def test_prefill_bad_offsets():
+@pytest.mark.parametrize("k", [1, 30])
+def test_prefill_bad_offsets(k):
     """Documents whose offsets descend or leave the tensors are skipped and recorded; the others are right."""
-    lens = [(40, 40), (30, 30), (20, 20)]
+    lens = [(40 * k, 40 * k), (30 * k, 30 * k), (20 * k, 20 * k)]
     q, kv, kr, cu_q, cu_k = _inputs(lens, 2, BF, 37)
     ref, ref_l = _run(q, kv, kr, cu_q, cu_k, True)
     for cq, ck, good in (([0, 40, 95, 90], cu_k, [0]), ([0, 40, 70, 91], cu_k, [0, 1]), (cu_q, [0, 40, 70, 1 << 30], [0, 1]),
                          ([-1, 40, 70, 90], cu_k, [1, 2]), (cu_q, [0, 40, -7, 90], [0])):
+        cq, ck = ([x if abs(x) in (1, 7, 91, 1 << 30) else x * k for x in c] if isinstance(c, list) else c for c in (cq, ck))
+        cq = [x if x != 91 else 90 * k + 1 for x in cq]
         st = _status()
         dkv = kv.to(DEV)
         out, lse = torch.full_like(ref, 4.0), torch.full_like(ref_l, 4.0)
@@ -559,8 +585,9 @@ def test_prefill_bad_offsets():
                 assert (out[rows] == 4.0).all() and (lse[rows] == 4.0).all()
 
 
-def test_prefill_timeout_is_reported():
-    case = _inputs([(20, 20)], 1, BF, 41)
+@pytest.mark.parametrize("n", [20, 300])
+def test_prefill_timeout_is_reported(n):
+    case = _inputs([(n, n)], 1, BF, 41)
     q, kv, kr = (t.to(DEV) for t in case[:3])
     st = _status()
     mla.mla_set_test_stall(2000000)
@@ -574,7 +601,8 @@ def test_prefill_timeout_is_reported():
 
 
 def test_prefill_same_inputs_same_bits():
-    for lens, heads in (([(700, 1900), (300, 300)], 8), ([(3, 6000)], 4)):
+    for lens, heads in (([(700, 1900), (300, 300)], 8), ([(3, 6000)], 4), ([(5, 200)] * 60 + [(130, 150)] * 30, 16),
+                        ([(300, 310), (900, 900)] * 12, 16)):
         case = _inputs(lens, heads, BF, 43)
         first = _run(*case, True)
         for _ in range(3):
@@ -582,7 +610,7 @@ def test_prefill_same_inputs_same_bits():
             assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
-@pytest.mark.parametrize("lens,heads", [([(300, 300), (64, 500)], 4), ([(2, 5000)], 2)])
+@pytest.mark.parametrize("lens,heads", [([(300, 300), (64, 500)], 4), ([(2, 5000)], 2), ([(700, 9000)], 1)])
 def test_prompt_calls_captured_and_on_another_stream(lens, heads):
     """Norm, read and attention captured into a graph, replayed with new inputs while the same calls run eagerly beside
     it: cut units take their partial results' memory from the graph's own pool."""
@@ -671,3 +699,51 @@ def test_prompt_in_chunks_and_decode(fmt):
         keys = held[at[b, :first[b]]]
         ro, rl = oracle.attend(oracle.to_f64(query[b, 0].cpu()), keys, SCALE)[:2]
         assert_close_attn(o[b, 0], lse[b, 0], ro, rl, "decode")
+
+
+# ---------------------------------------------------------------------------
+# far offsets
+# ---------------------------------------------------------------------------
+def test_prefill_behind_4_gb():
+    """Queries, keys, values and outputs whose rows lie behind 4 GB (2^31 elements and more)."""
+    heads, n_q, n_k = 128, 400, 420
+    far_q, far_k = 100000, 70000            # rows of 192 and of 256 values for 128 heads
+    for n in (n_q, 60):                     # two CTAs a unit, one
+        q, kv, kr, cu_q, cu_k = _inputs([(n, n_k)], heads, BF, 61)
+        q2 = torch.zeros(far_q + n + 9, heads, 192, dtype=BF, device=DEV)
+        kv2 = torch.zeros(far_k + n_k, heads, 256, dtype=BF, device=DEV)
+        kr2 = torch.zeros(far_k + n_k, 64, dtype=BF, device=DEV)
+        q2[far_q:far_q + n], kv2[far_k:], kr2[far_k:] = q.to(DEV), kv.to(DEV), kr.to(DEV)
+        out = torch.zeros(far_q + n + 9, heads, 192, dtype=BF, device=DEV)
+        st = _status()
+        got, lse = mla.mla_prefill(q2, kv2[..., :128], kr2, kv2[..., 128:], _ints(cu_q + far_q), _ints(cu_k + far_k), SCALE,
+                                   out=out[..., :128], status=st)
+        assert _bits(st) == 0
+        _check(got[far_q:], lse[far_q:], q, kv, kr, cu_q, cu_k, True, None, BF, heads=[0, 77, 127], rows=[0, 1, 59, 128, 255, 256, 399])
+        assert (out[:far_q:997] == 0).all() and (out[far_q + n:] == 0).all() and (out[far_q:, :, 128:] == 0).all()
+
+
+def test_rows_behind_4_gb():
+    """Norms, appends and reads of rows and pages behind 4 GB."""
+    tokens, heads = 90001, 128
+    x = torch.zeros(tokens, heads, 192, dtype=BF, device=DEV)
+    x[-3:] = torch.randn(3, heads, 192, generator=_gen(3)).to(BF).to(DEV)
+    pos = torch.arange(tokens, dtype=torch.int32, device=DEV) % 5000
+    out = mla.mla_norm_rotate(x, pos, _table())
+    tail = mla.mla_norm_rotate(x[-3:], pos[-3:].contiguous(), _table())
+    assert torch.equal(out[-3:], tail)
+    bound = oracle.norm_rotate_error(oracle.rms_norm(x[-3:]), 128, False)
+    _close(tail, oracle.norm_rotate(x[-3:], None, 1e-6, TABLE[pos[-3:].cpu().numpy()], 128, False), bound, BF)
+    del x, out
+    pages = 60000                                            # 4.4 GB of 16-bit rows
+    cache = torch.zeros(pages, PAGE, 1, 576, dtype=BF, device=DEV)
+    kv = torch.randn(40, 576, generator=_gen(4)).to(BF).to(DEV)
+    slots = torch.arange(40, dtype=torch.int32, device=DEV) + (pages * PAGE - 50)
+    rows = torch.empty(40, 576, dtype=BF, device=DEV)
+    mla.mla_norm_append_kv(kv[:, :512], kv[:, 512:], None, cache, slots, pos[:40].contiguous(), _table(), rows=rows)
+    wide = torch.zeros(2200000, 1024, dtype=BF, device=DEV)  # 4.5 GB
+    table = _ints([[pages - 1]])
+    n = 2200000
+    mla.mla_read_kv(cache, table.expand(2, 1).contiguous(), _ints([0, n - 30, n]), starts=_ints([0, 20]), out=wide[:, :576],
+                    status=_status())
+    assert torch.equal(wide[-30:, :576], rows[6:36]) and (wide[-30:, 576:] == 0).all()
