@@ -569,8 +569,8 @@ MLA_API mla_status mla_read_status(void* workspace, void* stream, uint32_t* bits
 /*
  * Test hook for the time-out path (0, the default, turns it off). While it is
  * non-zero, every decode kernel (mla_decode_with_kvcache and its variants),
- * absorption kernel (mla_absorb_q, mla_up_project) and index score launched by this
- * library first has one thread per CTA wait `cycles` SM cycles on a barrier
+ * absorption kernel (mla_absorb_q, mla_up_project), index score and prompt attention
+ * (mla_prefill) launched by this library first has one thread per CTA wait `cycles` SM cycles on a barrier
  * that nothing arrives at, before any copy or MMA is issued; the wait gives up, the kernel records the wait
  * time-out (status bit 2, MLA_ERR_TIMEOUT) and the CTA skips its work, so the
  * outputs of those launches are undefined. Process-wide; not for production

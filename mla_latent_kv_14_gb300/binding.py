@@ -373,8 +373,8 @@ def mla_read_status(workspace: Optional[torch.Tensor] = None, device=None) -> Tu
 
 
 def mla_set_test_stall(cycles: int) -> None:
-    """Test hook of the time-out path: while non-zero, every decode and
-    absorption launch first waits ``cycles`` SM cycles on a barrier nothing
+    """Test hook of the time-out path: while non-zero, every decode, absorption,
+    index-score and prompt-attention launch first waits ``cycles`` SM cycles on a barrier nothing
     arrives at, records a wait time-out and skips its work. 0 turns it off."""
     load_library().mla_set_test_stall(int(cycles))
 

@@ -149,17 +149,13 @@ struct Finder {
     before = 0;
     load(p);
   }
-  // the unit of block `id` of the grid; false if there is none (a piece that its unit does not have)
-  MLA_DEV bool find(const PrefillParams& p, int64_t id, U& u, bool& past) {
+  // the unit of block `id` of the grid; false if there is none (behind the last unit, or a piece that it does not have)
+  MLA_DEV bool find(const PrefillParams& p, int64_t id, U& u) {
     const int64_t block = id / p.splits;
     const int piece = (int)(id - block * p.splits);
-    past = false;
     int64_t all = __shfl_sync(0xffffffffu, upto, 31);
     while (block >= before + all) {
-      if (base + 32 >= p.batch) {
-        past = true;
-        return false;
-      }
+      if (base + 32 >= p.batch) return false;
       before += all;
       base += 32;
       load(p);

@@ -151,8 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (true) {
         UnitF u{};
         u.head = -1;
-        bool past = false;
-        const bool found = id >= 0 && finder.find(p, id, u, past);
+        const bool found = id >= 0 && finder.find(p, id, u);
         if (found || id < 0) {
           const int s = n % kUnits;
           if (!ready_all(B_UEMPTY + s, (n / kUnits) ^ 1)) break;
