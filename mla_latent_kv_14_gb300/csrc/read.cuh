@@ -6,7 +6,9 @@
 // in fp32 (4 significant bits times a scale's 24, 1 or 4; the 656-byte rows'
 // product rounds to fp32) and rounded once more to the output's type.
 //
-// Bound by its bytes: a row in, 1152 (1024) bytes out.
+// Bound by its bytes: a row in, 1152 (1024) bytes out. Measured (GB300): 262144
+// rows of 656 bytes 74.3 us (0.94 of the copy bandwidth), 88000 of 288 bytes 19.1
+// us (0.84; 25 with two 16-byte stores of a lane's 32 bytes).
 #pragma once
 #include "rows.cuh"
 
@@ -28,7 +30,7 @@ struct ReadParams {
 };
 
 // one warp takes two consecutive rows, all of their loads in flight together (262144 rows of 656 bytes: 75.8 us, 84.0
-// with one row, 78.5 with four; 88000 of 288 bytes 21.9, 24.3 and 25.1)
+// with one row, 78.5 with four; 88000 of 288 bytes 21.9, 24.3 and 25.1, before the 32-byte stores)
 constexpr int kReadWarps = 8;
 constexpr int kReadRows = 2;
 
