@@ -511,8 +511,8 @@ MLA_API mla_status mla_norm_append_kv(const void* c_kv, int64_t c_stride, const 
  * rows are copied (`dtype` is the cache's type then).
  * offsets (device) int32 [batch + 1], ascending; starts (device) int32 [batch].
  * out     (device) [total, 576] (V4.1 rows: 512, the last 64 of them RoPE dims),
- *         rows out_stride apart. Rows behind offsets[batch] are left as they were;
- *         offsets behind `total` are not written.
+ *         rows out_stride apart. Rows before offsets[0] and behind offsets[batch]
+ *         are left as they were; offsets behind `total` are not written.
  * A token whose page is out of range, or lies behind its block-table row, reads
  * as zeros and is recorded as an index error in `status`.
  */

@@ -70,14 +70,14 @@ __global__ void __launch_bounds__(32 * kReadWarps) mla_read_kv_kernel(const Read
       if (__ldg(p.offsets + mid) <= o) lo = mid;
       else hi = mid;
     }
-    const int64_t token = (p.starts ? __ldg(p.starts + lo) : 0) + (o - __ldg(p.offsets + lo));
+    const int64_t in = o - __ldg(p.offsets + lo), token = (p.starts ? __ldg(p.starts + lo) : 0) + in;
     const int64_t page = token / kTile;
-    row = -1;
-    if (token >= 0 && page < p.max_blocks && o >= __ldg(p.offsets + lo)) {
+    if (in >= 0) row = -1;     // below 0: before the first request
+    if (in >= 0 && token >= 0 && page < p.max_blocks) {
       const int32_t at = __ldg(p.block_table + (int64_t)lo * p.max_blocks + page);
       if (at >= 0 && at < p.num_blocks) row = (int64_t)at * kTile + token % kTile;
     }
-    if (row < 0) rows::flag(p.status, STATUS_INDEX);
+    if (row == -1) rows::flag(p.status, STATUS_INDEX);
   }
   const uint8_t* src[kRows];
 #pragma unroll

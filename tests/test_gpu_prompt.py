@@ -355,6 +355,18 @@ def test_read_kv_bad_pages_and_short_outputs(fmt):
 
 
 @pytest.mark.parametrize("fmt", [0, 1, 2, 3])
+def test_read_kv_leaves_rows_before_the_first_request(fmt):
+    """Offsets that do not start at 0: some requests' part of a larger result."""
+    cache, rows = _cache(fmt, 6, 13)
+    table, offsets, starts = [[4, 1], [0, 5]], [37, 90, 131], [3, 70]
+    st = _status()
+    out = torch.full((140, rows.shape[1]), 9.0, dtype=BF, device=DEV)
+    mla.mla_read_kv(cache, _ints(table), _ints(offsets), starts=_ints(starts), kv_format=fmt, out=out, status=st)
+    assert _bits(st) == 0
+    assert torch.equal(out.cpu(), torch.from_numpy(_read_ref(rows, table, offsets, starts, 140, rows.shape[1])).float().to(BF))
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2, 3])
 def test_read_kv_gives_what_the_append_wrote(fmt):
     n, latent = 500, 448 if fmt >= 2 else 512
     kv = torch.randn(n, latent + 64, generator=_gen(2)).to(BF).to(DEV)
