@@ -530,6 +530,7 @@ MLA_API mla_status mla_read_kv(const void* kvcache, int64_t num_blocks, int page
  * over its visible keys j: all n_k, or with `causal` those below n_k - n_q + i + 1
  * (the last query sees all keys), but at least the first prefix_lens[b] (a prefix
  * that all queries see). A query that sees no key gets out = 0, lse = -inf.
+ * softmax_scale lies between 2^-100 and 2^100.
  * Per (query, key) pair 640 FLOP a head, where the decode's absorbed form takes
  * 2176: the form for prompts and their chunks; keys and values come from the
  * latent rows by the model's up-projections.

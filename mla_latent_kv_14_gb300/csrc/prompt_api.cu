@@ -266,7 +266,8 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   const int64_t tq = tokens_q, tk = tokens_k;
   if (tq < 0 || tk < 0 || batch < 0 || heads < 1 || tq >= kMaxRows - 512 || tk >= kMaxRows - 512 || !dtype_ok(dtype))
     return MLA_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
+  // so that 8 / (scale log2 e), the reference's step in raw scores, and the factor itself stay normal numbers
+  if (!(softmax_scale >= 0x1p-100f) || !(softmax_scale <= 0x1p100f)) return MLA_ERR_INVALID_ARG;
   if (tq >= (int64_t(1) << 44) / heads || tk >= (int64_t(1) << 44) / heads) return MLA_ERR_INVALID_ARG;
   // TMA strides lie below 2^40 bytes
   constexpr int64_t kStride = int64_t(1) << 39;
@@ -302,7 +303,7 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   pf::PrefillParams p{};
   p.cu_q = cu_seqlens_q;
   p.cu_k = cu_seqlens_k;
-  p.prefix = prefix_lens;
+  p.prefix = causal ? prefix_lens : nullptr;
   p.tq = tq;
   p.tk = tk;
   p.batch = batch;

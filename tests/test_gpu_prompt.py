@@ -515,6 +515,16 @@ def test_prefill_scores_that_grow_and_shrink():
     _check(out, lse, q, kv, kr, cu_q, cu_k, False, None, BF)
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -100, 1e-6, 30.0])
+@both_kernels
+def test_prefill_scales(scale, extra):
+    """Weights that are all alike, and rows that a single key takes."""
+    lens = [(40, 300), (129, 129)] + extra
+    case = _inputs(lens, 2, BF, 18)
+    out, lse = _run(*case, True, scale=scale)
+    _check(out, lse, *case, True, None, BF, scale=scale)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @both_kernels
 def test_prefill_is_not_reached_by_what_lies_outside(bad, extra):

@@ -114,7 +114,8 @@ PREFILL = dict(q=_at(0), qt=192 * 8, qh=192, k=_at(1), kt=256 * 8, kh=256, r=_at
     (dict(out=_at(0)), 1), (dict(out=_at(1)), 1), (dict(out=_at(2)), 1), (dict(out=_into(3, 16)), 1), (dict(lse=_at(7)), 1),
     (dict(lse=_at(4)), 1), (dict(status=_at(8)), 1), (dict(status=_at(6)), 1), (dict(heads=1 << 30, tq=1 << 15), 1),
     (dict(tq=4, ws=None), 1), (dict(tq=4, wb=64), 1), (dict(tq=4, ws=ODD), 1), (dict(tq=4, ws=_at(1)), 1),   # cut units need room
-    (dict(tq=4, out=_at(9)), 1),
+    (dict(tq=4, out=_at(9)), 1), (dict(scale=2.0 ** -101), 1), (dict(scale=2.0 ** 101), 1),
+    (dict(tq=0, scale=2.0 ** -100), 0), (dict(tq=0, scale=2.0 ** 100), 0),
 ])
 def test_prefill_argument_checks(lib, kw, code):
     assert _call(lib, "mla_prefill", PREFILL, **kw) == code
