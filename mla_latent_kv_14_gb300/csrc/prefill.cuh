@@ -118,11 +118,11 @@ struct Unit {
 };
 
 // Units in the order of the grid: documents, heads, blocks of queries (those that see most first), pieces. The warp
-// holds 32 documents' counts and moves on only.
+// holds 32 documents' counts; the blocks of the grid that it is given lie further on each time, or it starts over.
 template <class U>
 struct Finder {
   static constexpr int kBlock = U::kBlock;
-  int base;            // first of the 32 documents
+  int base;            // first of the 32 documents, -32: none looked at
   int64_t before;      // blocks (of one head) times heads before them
   int blocks;          // of this lane's document
   int64_t upto;        // inclusive prefix over the lanes, times heads
@@ -143,16 +143,16 @@ struct Finder {
     }
     upto = (int64_t)incl * p.heads;
   }
-  MLA_DEV void start(const PrefillParams& p) {
+  MLA_DEV void start() {
     lane = threadIdx.x & 31;
-    base = 0;
-    before = 0;
-    load(p);
+    base = -32;
+    before = upto = 0;
   }
   // the unit of block `id` of the grid; false if there is none (behind the last unit, or a piece that it does not have)
   MLA_DEV bool find(const PrefillParams& p, int64_t id, U& u) {
     const int64_t block = id / p.splits;
     const int piece = (int)(id - block * p.splits);
+    if (block < before) start();
     int64_t all = __shfl_sync(0xffffffffu, upto, 31);
     while (block >= before + all) {
       if (base + 32 >= p.batch) return false;

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2 && ok) {
       // ---------------- the units ----------------
       Finder<UnitF> finder;
-      finder.start(p);
+      finder.start();
       int64_t id = blockIdx.x;
       // A unit is taken only when the copies of the one before it come to their end: one taken early could not go to a
       // block that is free sooner.

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2 && rank == 0 && ok) {
       // ---------------- the units, for both CTAs ----------------
       Finder<UnitP> finder;
-      finder.start(p);
+      finder.start();
       int64_t id = blockIdx.x >> 1;
       // A unit is taken only when the copies of the one before it come to their end: one taken early could not go to a
       // block that is free sooner.
@@ -313,18 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (leader) mbar_arrive_remote(b);
         }
-      }
-      // never leave with a copy in flight into this CTA's shared memory: without a fault every copy has been waited for
-      // by the issuing threads; with one, CTA 0 waits for what is still counted on its barriers, CTA 1 with it below
-      if (lane == 0 && rank == 0) {
-        const uint64_t t_0 = cycles();
-        for (uint32_t k = tile < kStages ? 0u : tile - kStages; k < tile; ++k) {
-          while (!mbar_try_wait_cluster(bar(B_KFULL + k % kStages), (k / kStages) & 1u) && cycles() - t_0 < kDrainLimitCycles) {}
-          while (!mbar_try_wait_cluster(bar(B_VFULL + k % kStages), (k / kStages) & 1u) && cycles() - t_0 < kDrainLimitCycles) {}
-        }
-        for (int w = 0; w < 2; ++w)
-          if (q_loads[w])
-            while (!mbar_try_wait_cluster(bar(B_QFULL + w), (q_loads[w] - 1u) & 1u) && cycles() - t_0 < kDrainLimitCycles) {}
       }
     } else if ((warp & 1) && rank == 0 && ok) {
       // ---------------- products of query tile w, for both CTAs: one thread ----------------
@@ -457,6 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         [&]() { arrive(B_OEMPTY + w); });
     }
     if (lane == 0) bulk_wait();
+  }
+  // Never leave with a copy in flight into this CTA's shared memory. Without a fault every copy has been waited for, by
+  // the issuing threads or where it was asked for. With one, the last copies may be counted on barriers of CTA 0 that
+  // wait for the other CTA's in vain, so the pair stays for longer than any copy takes.
+  __syncthreads();
+  if (warp == 0 && ok && *abort_flag) {
+    const uint64_t t_0 = cycles();
+    while (cycles() - t_0 < kDrainLimitCycles) {}
   }
   __syncwarp();
   tc_fence_before();
