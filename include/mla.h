@@ -538,8 +538,10 @@ MLA_API mla_status mla_read_kv(const void* kvcache, int64_t num_blocks, int page
  *        least a row (a head stride of 0, shared heads, is refused).
  * k_nope, v (device) [tokens_k, heads, 128] likewise (column ranges of one
  *        projection are fine); k_rope (device) [tokens_k, 64], rotated, shared by
- *        the heads. Keys and values of a document must be finite as far as its
- *        queries' tiles of 128 reach; what stands behind a document's keys does not matter.
+ *        the heads. What stands behind a document's keys does not matter, and a key
+ *        that is not finite reaches only the queries that see it. A value that is not
+ *        finite reaches them too, and, as 0 times it is NaN, may reach queries that
+ *        miss its key by less than 383 keys.
  * cu_seqlens_q, cu_seqlens_k (device) int32 [batch + 1], ascending; prefix_lens
  *        (device, optional) int32 [batch], kept within [0, n_k]; not read unless
  *        causal. A document whose offsets descend or leave the tensors is skipped

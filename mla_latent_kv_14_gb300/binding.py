@@ -541,7 +541,8 @@ def mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: 
     heads, 128], k_rope [tokens_k, 64] shared by the heads; rows cu_seqlens_q[b] ..
     cu_seqlens_q[b + 1] attend to keys cu_seqlens_k[b] .. cu_seqlens_k[b + 1]. Causal:
     the last query sees all keys, each before it one fewer, and every query at least
-    the first ``prefix_lens[b]``. Returns (out [tokens_q, heads, 128], lse fp32
+    the first ``prefix_lens[b]``. Values must be finite: one that is not may reach
+    queries shortly before its key too. Returns (out [tokens_q, heads, 128], lse fp32
     [tokens_q, heads]); a query that sees nothing gets 0 and -inf."""
     return (_host or load_host()).mla_prefill(q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, softmax_scale, causal,
                                                prefix_lens, out, lse, status)

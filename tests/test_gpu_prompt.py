@@ -544,6 +544,33 @@ def test_prefill_is_not_reached_by_what_lies_outside(bad, extra):
     _check(out[pad:], lse[pad:], q, kv, kr, cu_q, cu_k, True, None, BF, docs=[0, 2, 3][:2 + len(extra)])
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens", [[(900, 900)], [(1024, 1300)], [(100, 900), (256, 256)], [(130, 6000)]], ids=["pair", "pair prefix", "few", "cut"])
+def test_prefill_keys_that_a_query_does_not_see(lens, bad):
+    """A key that is not finite reaches only the queries that see it; a value only those that miss it by less than 383."""
+    q, kv, kr, cu_q, cu_k = _inputs(lens, 2, BF, 61)
+    n_q, n_k = lens[0]
+    seen = oracle.visible(n_q, n_k, True)
+    ref, ref_l = _run(q, kv, kr, cu_q, cu_k, True)
+    j = n_k - n_q // 3
+    for where in ("key", "rope", "value"):
+        kv2, kr2 = kv.clone(), kr.clone()
+        if where == "rope":
+            kr2[j] = bad
+        else:
+            kv2[j, :, :128 if where == "key" else 256] = bad
+            if where == "value":
+                kv2[j, :, :128] = kv[j, :, :128]
+        out, lse = _run(q, kv2, kr2, cu_q, cu_k, True)
+        apart = torch.from_numpy(seen + (382 if where == "value" else 0) <= j)
+        first, rest = slice(0, n_q), slice(n_q, None)
+        assert torch.equal(out[first][apart], ref[first][apart]) and torch.equal(lse[first][apart], ref_l[first][apart])
+        assert torch.equal(out[rest], ref[rest]) and torch.equal(lse[rest], ref_l[rest])
+        sees = torch.from_numpy(seen > j)
+        assert where != "value" or (~out[first][sees].isfinite()).all()
+        assert where != "value" or torch.equal(lse, ref_l)
+
+
 @both_kernels
 def test_prefill_strides(extra):
     """Heads-major inputs and outputs, column ranges, one head of a wider tensor."""
@@ -575,6 +602,18 @@ def test_prefill_of_many_documents(heads, most):
     for _ in range(8):
         again = _run(*case, True)
         assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("most", [3, 600])
+def test_prefill_of_a_large_batch(most):
+    """Thousands of documents, many of them empty."""
+    rng = np.random.default_rng(6)
+    n = 5000 if most == 3 else 1300
+    lens = [(int(a), int(a) + int(b)) for a, b in zip(rng.integers(0, most, n) * rng.integers(0, 2, n), rng.integers(0, 30, n))]
+    lens[-1] = (most, most + 9)
+    case = _inputs(lens, 1, BF, 67)
+    out, lse = _run(*case, True)
+    _check(out, lse, *case, True, None, BF, docs=list(range(0, n, 37)) + [n - 2, n - 1], rows=[0, 1, 2, 200, 511, 599])
 
 
 def test_prefill_of_long_documents_sampled():
@@ -663,6 +702,28 @@ def test_prompt_calls_captured_and_on_another_stream(lens, heads):
         torch.cuda.synchronize()
         for a, b in zip(held, beside):
             assert torch.equal(a, b)
+
+
+def test_prompt_calls_on_two_streams_at_once():
+    """Both kernels of the attention, and cut units, in flight together."""
+    cases = [([(600, 900), (900, 900)], 4), ([(3, 5000)], 2), ([(100, 1000)] * 20, 4), ([(700, 9000)], 1)]
+    cases = [[x.to(DEV) for x in c[:3]] + [_ints(x) for x in c[3:]] for c in (_inputs(lens, heads, BF, 59) for lens, heads in cases)]
+
+    def run(c):
+        q, kv, kr, cq, ck = c
+        return mla.mla_prefill(q, kv[..., :128], kr, kv[..., 128:], cq, ck, SCALE)
+
+    alone = [run(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = []
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append([run(c) for _ in range(6)])
+        torch.cuda.synchronize()
+        for (out, lse), runs in zip(alone, got):
+            assert all(torch.equal(out, a) and torch.equal(lse, b) for a, b in runs)
 
 
 # ---------------------------------------------------------------------------
