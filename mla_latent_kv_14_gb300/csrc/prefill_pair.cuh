@@ -188,11 +188,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     u.read(units + 16 * (n % kUnits));
     return true;
   };
-  auto take = [&](int n, UnitP& u) {
-    const bool got = __all_sync(0xffffffffu, take_one(n, u));
-    if (got && lane == 0) mbar_arrive_remote(lead_bar(B_UEMPTY + n % kUnits));
-    return got && u.head >= 0;
+  auto taken = [&](int n) {
+    if (lane == 0) mbar_arrive_remote(lead_bar(B_UEMPTY + n % kUnits));
   };
+  auto look = [&](int n, UnitP& u) { return __all_sync(0xffffffffu, take_one(n, u)) && u.head >= 0; };
 
   if (warp < 4) {
     set_registers_down<kRegsFew>();
@@ -271,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto want_next = [&]() {
         if (leader && rank == 0) mbar_arrive(bar(B_WANT));
       };
-      for (; !stop && take(n, u); ++n) {
+      for (; !stop && look(n, u); ++n) {
+        taken(n);
         const int e0 = u.end(0, p.causal), e1 = u.end(1, p.causal), e = max(e0, e1);
         if (e0 > u.t0) queries(0);
         if (e - u.t0 < 2) want_next();
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s_used = 0, o_used = 0;
     bool failed = !ok;
     UnitP u;
-    for (int n = 0; !failed && take(n, u); ++n) {
+    for (int n = 0; !failed && look(n, u); ++n) {
       const int end = u.end(w, p.causal);
       const int seen = row < u.rows ? u.visible(row, p.causal) : u.nk;
       const bool idle = first_row >= u.rows;                                  // none of this CTA's rows is a query
@@ -432,6 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             [&](int h) { arrive(B_PFULL + 2 * h + w); });
       }
       if (failed) break;
+      // an arrival that orders memory across the pair waits for the warp's stores, some 2000 cycles after a unit's
+      // results: so it comes before them
+      taken(n);
       if (end > u.t0) {
         if (!ready_all(B_OFULL + w, o_used++)) break;
         tc_fence_after();
