@@ -98,8 +98,15 @@ MLA_DEV void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, uint32_t clust
       "l"(reinterpret_cast<uint64_t>(m)), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// Nothing the thread wrote has to be visible with these arrivals, so they are relaxed ones: one that orders memory across
+// the pair takes some 1000 cycles. The keys' is one of those all the same (kLate): with the other copies as early as they
+// can be, keys that follow the values at once let the first query tile run ahead of the second until the ring holds it
+// back, out of step on the tensor pipe (4 x 4096 causal 1926 us; 1754 so, 1767 with a pause of 1100 to 1600 cycles instead,
+// 1879 and 1790 with 700 and 2200, 1776 with the values delayed and the keys not).
+template <bool kLate = false>
 MLA_DEV void mbar_arrive_expect_tx_cluster(uint32_t cluster_bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes) : "memory");
+  if (kLate) asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes) : "memory");
+  else asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes) : "memory");
 }
 MLA_DEV void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
@@ -188,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     u.read(units + 16 * (n % kUnits));
     return true;
   };
+  // orders memory across the pair, so it is called where that delays nothing
   auto taken = [&](int n) {
     if (lane == 0) mbar_arrive_remote(lead_bar(B_UEMPTY + n % kUnits));
   };
@@ -271,10 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader && rank == 0) mbar_arrive(bar(B_WANT));
       };
       for (; !stop && look(n, u); ++n) {
-        taken(n);
         const int e0 = u.end(0, p.causal), e1 = u.end(1, p.causal), e = max(e0, e1);
         if (e0 > u.t0) queries(0);
         if (e - u.t0 < 2) want_next();
+        if (e <= u.t0) taken(n);
         for (int t = u.t0; t < e && !stop; ++t, ++tile) {
           if (t == e - 2) want_next();
           const uint32_t s = tile % kStages, round = tile / kStages;
@@ -282,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ready_all(B_KEMPTY + s, round ^ 1u)) { stop = true; break; }
           if (leader) {
             const uint32_t b = lead_bar(B_KFULL + s), to = sb + kOffK + s * kKStage;
-            mbar_arrive_expect_tx_cluster(b, kKStage);
+            mbar_arrive_expect_tx_cluster<true>(b, kKStage);
             tma_load_3d_pair(to, &tm_k, b, 0, u.head, at + 64 * rank);
             tma_load_3d_pair(to + kChunk / 2, &tm_k, b, 64, u.head, at + 64 * rank);
             tma_load_3d_pair(to + kChunk, &tm_r, b, 0, 0, at + 64 * rank);
@@ -298,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive_expect_tx_cluster(b, kVStage);
               tma_load_3d_pair(to, &tm_v, b, 64 * rank, u.head, at);
             }
+            if (t == u.t0) taken(n);
             continue;
           }
           // The value rows behind the document's keys may hold anything, and zero times NaN is NaN: they are cleared
@@ -312,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (leader) mbar_arrive_remote(b);
+          if (t == u.t0) taken(n);
         }
       }
     } else if ((warp & 1) && rank == 0 && ok) {
@@ -432,9 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             [&](int h) { arrive(B_PFULL + 2 * h + w); });
       }
       if (failed) break;
-      // an arrival that orders memory across the pair waits for the warp's stores, some 2000 cycles after a unit's
-      // results: so it comes before them
-      taken(n);
+      taken(n);      // ahead of the unit's results: it would wait for their stores, some 2000 cycles
       if (end > u.t0) {
         if (!ready_all(B_OFULL + w, o_used++)) break;
         tc_fence_after();
