@@ -59,6 +59,7 @@ struct PrefillParams {
   float* lse;                  // [tq, heads]
   float* o_part;               // [splits][tq][heads][128], splits > 1
   float* lse_part;             // [splits][tq][heads]
+  int wide;                    // 1: rows of out are 32-B aligned, 2: those of o_part
   uint32_t* status;            // or null
   uint32_t stall_cycles;       // test hook, 0 in normal use
 };
@@ -347,6 +348,36 @@ MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2
   row.l += x.x + x.y;
 }
 
+// 16 words of a row to 16-B aligned memory, in stores of 32 bytes where that is aligned for them: the stores of a warp's 32
+// rows touch 32 lines each, whatever their width
+MLA_DEV void store_words16(void* dst, const uint32_t* w, bool wide) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (wide) {
+      st_global_v8(static_cast<uint32_t*>(dst) + 8 * k, w + 8 * k);
+    } else {
+      static_cast<uint4*>(dst)[2 * k] = make_uint4(w[8 * k], w[8 * k + 1], w[8 * k + 2], w[8 * k + 3]);
+      static_cast<uint4*>(dst)[2 * k + 1] = make_uint4(w[8 * k + 4], w[8 * k + 5], w[8 * k + 6], w[8 * k + 7]);
+    }
+  }
+}
+
+// 32 dims of a row: of the output, or, without one, of a piece's share
+template <bool kFp16>
+MLA_DEV void store_share(uint16_t* out, float* part, const float* v, int wide) {
+  uint32_t w[32];
+  if (out) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w[k] = pack_p<kFp16>(v[2 * k], v[2 * k + 1]);
+    store_words16(out, w, wide & 1);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(v[k]);
+    store_words16(part, w, wide & 2);
+    store_words16(part + 16, w + 16, wide & 2);
+  }
+}
+
 // 32 rows of 64 dims of the output from shared memory (128-byte swizzled), rows and dims all inside the tensor
 MLA_DEV void store_rows64(const CUtensorMap* m, uint32_t src, int x, int head, int row) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -369,44 +400,43 @@ MLA_DEV void store_rows(const PrefillParams& p, const CUtensorMap* tm_out, uint3
   const float inv = row.l > 0.f ? 1.f / row.l : row.l;   // a row that sees nothing has l = 0 and gets zeros; NaN stays
   const bool whole = u.pieces == 1, live = first + lane < u.rows;
   const int64_t at = (int64_t)u.row + first + lane;
-  uint32_t o[128];
-  if (some) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(t_o + 32u * c, o + 32 * c);
-    tmem_wait_ld();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) pin_regs32(o + 32 * c);
-    read();
-  } else {
-#pragma unroll
-    for (int k = 0; k < 128; ++k) o[k] = 0u;
-  }
   if (live) {
     const float lse = row.l == 0.f ? -INFINITY : row.m * p.scale + logf(row.l);
     if (whole) p.lse[at * p.heads + u.head] = lse;
     else p.lse_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = lse;
   }
-  if (!whole) {
-    float4* part = reinterpret_cast<float4*>(p.o_part + (((int64_t)u.piece * p.tq + at) * p.heads + u.head) * kV);
-    if (!live) return;
+  // 32 dims of the row, normalised
+  auto share = [&](int c, float* v) {
+    uint32_t o[32];
+    if (some) {
+      tmem_ld32(t_o + 32u * c, o);
+      tmem_wait_ld();
+      pin_regs32(o);
+      if (c == 3) read();
+    } else {
 #pragma unroll
-    for (int k = 0; k < 32; ++k)
-      part[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                            __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
-    return;
-  }
-  uint32_t y[64];
+      for (int k = 0; k < 32; ++k) o[k] = 0u;
+    }
 #pragma unroll
-  for (int k = 0; k < 64; ++k) y[k] = pack_p<kFp16>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-  if (first + 32 <= u.rows) {
-#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]) * inv;
+  };
+  // loops, not straight code: what runs once a unit is not in the instruction cache
+  if (whole && first + 32 <= u.rows) {
+#pragma unroll 1
     for (int h = 0; h < 2; ++h) {
+      uint32_t y[32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float v[32];
+        share(2 * h + c, v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y[16 * c + k] = pack_p<kFp16>(v[2 * k], v[2 * k + 1]);
+      }
       if (lane == 0) bulk_wait_read();   // the stage's last rows are out of it
       __syncwarp();
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        st_shared_v4(stage + 128u * lane + 16u * (k ^ (lane & 7)), y[32 * h + 4 * k], y[32 * h + 4 * k + 1], y[32 * h + 4 * k + 2],
-                     y[32 * h + 4 * k + 3]);
+        st_shared_v4(stage + 128u * lane + 16u * (k ^ (lane & 7)), y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -414,10 +444,15 @@ MLA_DEV void store_rows(const PrefillParams& p, const CUtensorMap* tm_out, uint3
         bulk_commit();
       }
     }
-  } else if (live) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * p.out_token + u.head * p.out_head);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+    return;
+  }
+  uint16_t* dst = static_cast<uint16_t*>(p.out) + at * p.out_token + u.head * p.out_head;
+  float* part = p.o_part + (((int64_t)u.piece * p.tq + at) * p.heads + u.head) * kV;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    share(c, v);
+    if (live) store_share<kFp16>(whole ? dst + 32 * c : nullptr, part + 32 * c, v, p.wide);
   }
 }
 

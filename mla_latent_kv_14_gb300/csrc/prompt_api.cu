@@ -319,6 +319,7 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   p.lse = lse;
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = need ? p.o_part + (int64_t)splits * tq * heads * pf::kV : nullptr;
+  p.wide = (aligned(out, 32) && out_token_stride % 16 == 0 && out_head_stride % 16 == 0 ? 1 : 0) | (aligned(workspace, 32) ? 2 : 0);
   p.status = status;
   p.stall_cycles = g_test_stall.load(std::memory_order_relaxed);
   int dev = 0, sms = 0;

@@ -590,6 +590,32 @@ def test_prefill_strides(extra):
     _check(one, one_l, q[:, 1:2], kv[:, 1:2], kr, cu_q, cu_k, True, None, HF)
 
 
+@pytest.mark.parametrize("lens", [[(140, 140), (20, 150)], [(700, 700), (300, 333)], [(5, 6000)], [(300, 9000)]],
+                         ids=["few", "pair", "few cut", "pair cut"])
+def test_prefill_of_other_alignment(lens):
+    """Outputs and a workspace that are 16-byte aligned and no more."""
+    heads = 2
+    q, kv, kr, cu_q, cu_k = _inputs(lens, heads, BF, 25)
+    ref, ref_l = _run(q, kv, kr, cu_q, cu_k, True)
+    tq, tk = q.shape[0], kv.shape[0]
+    wide = torch.full((tq, heads, 136), 3.0, dtype=BF, device=DEV)
+    out, lse = _run(q, kv, kr, cu_q, cu_k, True, out=wide[..., 8:])
+    assert torch.equal(out, ref) and torch.equal(lse, ref_l) and (wide[..., :8] == 3.0).all()
+    lib = mla.load_library()
+    size = lib.mla_prefill_workspace_size(tq, tk, len(lens), heads)
+    space = torch.empty(size + 64, dtype=torch.uint8, device=DEV)
+    space = space[(16 - space.data_ptr() % 32) % 32:]
+    assert space.data_ptr() % 32 == 16
+    dq, dkv, dkr, cq, ck = q.to(DEV), kv.to(DEV), kr.to(DEV), _ints(cu_q), _ints(cu_k)
+    out, lse = torch.zeros_like(ref), torch.zeros_like(ref_l)
+    code = lib.mla_prefill(dq.data_ptr(), heads * 192, 192, dkv.data_ptr(), heads * 256, 256, dkr.data_ptr(), 64, dkv.data_ptr() + 256,
+                           heads * 256, 256, 0, cq.data_ptr(), ck.data_ptr(), None, len(lens), tq, tk, heads, SCALE, 1, out.data_ptr(),
+                           heads * 128, 128, lse.data_ptr(), space.data_ptr(), size, None, torch.cuda.current_stream().cuda_stream)
+    assert code == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_l)
+
+
 @pytest.mark.parametrize("heads", [1, 20])
 @pytest.mark.parametrize("most", [300, 800])
 def test_prefill_of_many_documents(heads, most):
