@@ -10,19 +10,21 @@
 // 256 queries asked it for 7.5 TB/s and its ring of 1.6 tiles ran dry under that
 // load).
 //
-// Measured (GB300, bf16): 2048 queries behind 32768 keys, 128 heads 2.88 ms in
-// short runs (1.85 PFLOP/s, 0.98 of the cuBLAS burst) and 3.15 in long ones, where
-// power lowers the clock to 1.75 GHz; 4 x 4096 causal 1.82 and 1.95 ms (0.80 and
-// 0.75). In the steady state a chain takes 3000 cycles a tile: 1600 from P to the
-// next S (1280 of products, commits and arrivals across the pair), 1400 of
-// softmax; two chains leave the tensor pipe 15 % idle. A unit's start and end
-// cost some 7000 cycles, 3200 of them for 96 KB of queries at the rate of the
-// copy engine; and a causal unit's second tile sees two key tiles more than the
-// first. Tried without gain: two threads a row (3.37 ms with one CTA a unit where
-// one thread took 3.22: the exchanges cost more than the halves save), outputs by
-// warps of their own, the running maximum left out of the steady state (it hides
-// behind the exponentials), queries by a warp of their own, keys a tile ahead of
-// values, every stream polled (3.18 ms), three stages (no faster than two).
+// Measured (GB300, bf16): 2048 queries behind 32768 keys, 128 heads 2.86 ms in
+// short runs (1.86 PFLOP/s, 0.99 of the cuBLAS burst) and 3.15 in long ones, where
+// power lowers the clock to 1.72 GHz; 4 x 4096 causal 1.76 and 1.91 ms (0.83 and
+// 0.77). In the steady state a chain takes some 3200 cycles a tile: 1600 from P to
+// the next S (1280 of products, commits and arrivals across the pair), 1400 of
+// softmax, and waits for the other chain's products. A unit's start and end: some
+// 1200 cycles from its last P to its results, 2500 to write them, 4000 from there
+// to the next unit's first scores (queries and keys on their way); and a causal
+// unit's second tile sees two key tiles more than the first. Tried without gain:
+// two threads a row (3.37 ms with one CTA a unit where one thread took 3.22: the
+// exchanges cost more than the halves save), outputs by warps of their own, the
+// running maximum left out of the steady state (it hides behind the exponentials),
+// queries by a warp of their own or brought into the L2 ahead, keys a tile ahead
+// of values, every stream polled (3.18 ms), three stages, the two issuing threads
+// taking turns (3.02), waits that order memory in the CTA alone.
 //
 // Warp roles (384 threads a CTA): warp 0 copies this CTA's halves; in CTA 0 warps
 // 1 and 3 issue the products of the first and the second query tile for both

@@ -66,8 +66,8 @@ struct PrefillPlan {
 // in 2 pieces. A piece costs some 4 tiles more than its own (the pipeline's start, its share of the output to memory and
 // back), so that 8 units of 256 tiles take 36 in 16 pieces and 43 in 32.
 //
-// Documents of up to 256 queries on average go to one CTA a unit: 16 of 256 over 4096 keys, 16 heads 162 us, 218 in
-// pairs; of 300 231 and 240; of 400 269 and 243; 64 of 256 by themselves 87 and 99, of 512 250 and 166.
+// Documents of up to 256 queries on average go to one CTA a unit: 16 of 256 over 4096 keys, 16 heads 162 us, 210 in
+// pairs; of 300 228 either way; of 400 269 and 231; 64 of 256 by themselves 92 and 94, of 512 241 and 140.
 constexpr int kFewRows = 256;
 PrefillPlan plan_prefill(int64_t tq, int64_t tk, int64_t batch, int64_t heads) {
   PrefillPlan plan{};
