@@ -18,7 +18,11 @@
 //
 // The softmax is online with a lazy reference: the reference maximum of a row
 // moves only when a score passes it by more than 2^8 (P and its sum stay far
-// from the types' limits), so that the accumulator is rarely rescaled.
+// from the types' limits), so that the accumulator is rarely rescaled. A weight
+// is 2^(c s - c m), c = scale log2 e, its exponent one fma of s with the rounded
+// c m: that rounding, up to 2^-25 c |m|, is the same for all of a row's weights
+// and cancels, but where c |m| is large it would take them out of their types'
+// range, or to zero. Such rows (beyond kFar) subtract first.
 //
 // Blocks are persistent: the next unit is a block of the grid that has not
 // started yet, which the block cancels and takes over (clusterlaunchcontrol), so
@@ -265,6 +269,10 @@ MLA_DEV uint32_t pack_p(float lo, float hi) {
   return kFp16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
+// |c m| from which a row subtracts its reference first: up to there the rounding of c m changes a row's weights by 2^-13 of
+// themselves, no more than the scores' own rounding to fp32 does
+constexpr float kFar = 0x1p12f;
+
 // A thread's row in the softmax of one query tile.
 struct Row {
   float m, l;                  // reference (raw score) and sum of the weights
@@ -288,9 +296,10 @@ MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2
   }
   uint64_t sum[2];
   const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
+  auto reference = [&]() { return row.m == -INFINITY ? 0.f : -row.m * scale_log2; };
+  float ref = reference();
   // 2^(s - m) of keys [32 c, 32 c + 32), packed
   auto weights = [&](int c, uint32_t* q) {
-    const float ref = row.m == -INFINITY ? 0.f : -row.m * scale_log2;
     const uint64_t ref2 = f2_pack(ref, ref);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -301,34 +310,50 @@ MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2
     }
   };
   // The first weights are formed with the reference as it stands, beside the search for the row's maximum; only where
-  // that passes the reference by too much (in a document's first tiles, hardly ever later) are they formed again.
+  // that passes the reference by too much (in a document's first tiles, hardly ever later), or the row's reference is far
+  // off, are they formed again.
   uint32_t q[16];
   sum[0] = sum[1] = 0;
   weights(0, q);
   const float top = fmaxf(tree_max64([&](int k) { return __uint_as_float(s[k]); }),
                           tree_max64([&](int k) { return __uint_as_float(s[64 + k]); }));
-  const bool move = top > row.m + 8.f / scale_log2;   // from -inf with the first key that it sees
-  if (__any_sync(0xffffffffu, move)) {
-    const float next = move ? top : row.m;
-    // rows that have seen nothing keep l = 0 and O = 0
-    const float f = move ? exp2_approx((row.m - next) * scale_log2) : 1.f;
-    row.m = next;
-    row.l *= f;
-    if (!first) {
-      // S of this tile is complete, and with it every product issued before: O holds still until this tile's P is
-      // handed over
+  const bool move = top - row.m > 8.f / scale_log2;   // from -inf with the first key that it sees
+  if (__any_sync(0xffffffffu, move || fabsf(ref) > kFar)) {
+    if (__any_sync(0xffffffffu, move)) {
+      const float next = move ? top : row.m;
+      // rows that have seen nothing keep l = 0 and O = 0
+      const float f = move ? exp2_approx((row.m - next) * scale_log2) : 1.f;
+      row.m = next;
+      row.l *= f;
+      if (!first) {
+        // S of this tile is complete, and with it every product issued before: O holds still until this tile's P is
+        // handed over
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint32_t o[16];
-        tmem_ld16(t_o + 16u * c, o);
-        tmem_wait_ld();
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[16];
+          tmem_ld16(t_o + 16u * c, o);
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          asm volatile("" : "+r"(o[k]));
-          o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+          for (int k = 0; k < 16; ++k) {
+            asm volatile("" : "+r"(o[k]));
+            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+          }
+          tmem_st16(t_o + 16u * c, o);
         }
-        tmem_st16(t_o + 16u * c, o);
       }
+      ref = reference();
+    }
+    const bool far = fabsf(ref) > kFar;
+    if (__any_sync(0xffffffffu, far)) {
+      const float minus = far ? -row.m : 0.f;
+      const uint64_t minus2 = f2_pack(minus, minus);
+#pragma unroll
+      for (int k = 0; k < 128; k += 2) {
+        const float2 x = f2_unpack(f2_add(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), minus2));
+        s[k] = __float_as_uint(x.x);
+        s[k + 1] = __float_as_uint(x.y);
+      }
+      if (far) ref = 0.f;
     }
     sum[0] = sum[1] = 0;
     weights(0, q);

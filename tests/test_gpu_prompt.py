@@ -753,6 +753,89 @@ def test_prompt_calls_on_two_streams_at_once():
 
 
 # ---------------------------------------------------------------------------
+# the ends of the scores' range
+# ---------------------------------------------------------------------------
+U = 2.0 ** -24
+FAR_LENS = {"few": [(40, 700), (129, 129)], "pair": [(600, 700)]}
+
+
+def _far_check(out, lse, q, kv, kr, lens, scale, spread, dtype):
+    """Against the oracle, for dots that fp32 holds exactly. With x = c (s - m), c = scale log2 e: c rounds (U of x, with
+    scale a power of two), the difference and the product too, the reference's own rounding (2^-13 ln 2 at most, where it
+    is not subtracted first) counts twice where the reference has moved, and 2^x is off by 4U: a weight by 4U + 3U |x| +
+    2^-12 of itself, |x| <= 2 * spread for scores that lie `spread` apart. Weights of 2^-25 and less of the largest may
+    be lost in fp16."""
+    q0 = k0 = 0
+    for n_q, n_k in lens:
+        seen = oracle.visible(n_q, n_k, True)
+        pick = np.unique(np.r_[0, 1, n_q // 2, np.arange(min(n_q, 127), n_q, 64), n_q - 1])
+        ro, rl, size, _ = oracle.prefill(q[q0:q0 + n_q][pick], kv[k0:k0 + n_k, :, :128], kr[k0:k0 + n_k],
+                                         kv[k0:k0 + n_k, :, 128:], scale, seen[pick])
+        n = seen[pick].astype(np.float64)[:, None]
+        weight = (4 + 6 * spread) * U + 2.0 ** -12
+        rel = 2 * weight + (2 * n + 64) * U
+        bo = 1.01 * HALF[dtype] * np.abs(ro) + (HALF[dtype] + rel)[..., None] * size
+        if dtype == HF:
+            bo = bo + 2.0 ** -25 * (1 + np.abs(oracle.to_f64(kv[k0:k0 + n_k, :, 128:])).sum(0))
+        bl = weight + (n + 64) * U + 4 * U * np.abs(rl)
+        go, gl = oracle.to_f64(out[q0:q0 + n_q].cpu()[pick]), oracle.to_f64(lse[q0:q0 + n_q].cpu()[pick])
+        assert np.isfinite(go).all()
+        off = np.abs(go - ro) - bo - TINY[dtype]
+        assert (off <= 0).all(), f"{(off > 0).sum()} of {off.size}, worst {off.max()} at {np.unravel_index(off.argmax(), off.shape)}"
+        inside = np.abs(rl) < 3.4e38
+        assert (gl[~inside] == np.sign(rl[~inside]) * np.inf).all()
+        assert (np.abs(np.where(inside, gl, 0) - np.where(inside, rl, 0)) <= bl).all()
+        q0, k0 = q0 + n_q, k0 + n_k
+
+
+def _far_inputs(lens, dtype, level, seed):
+    """Queries and keys of one dim: the scaled scores are 2^(level - 6) times whole numbers up to 61, many of them alike;
+    the dots, whole numbers times a power of two, are exact."""
+    q, kv, kr, cu_q, cu_k = _inputs(lens, 2, dtype, seed)
+    q[:], kv[..., :128], kr[:] = 0, 0, 0
+    top = 60 if level > 120 else 7                     # bf16 reaches scores whose scaled value fp32 cannot hold
+    q[..., 5] = 2.0 ** top
+    steps = torch.randint(3, 62, (kv.shape[0], 2), generator=_gen(seed))     # ends whose product with a scale rounds
+    kv[..., 5] = (steps * 2.0 ** 3).to(dtype)
+    return (q, kv, kr, cu_q, cu_k), 2.0 ** (level - 6 - 3 - top)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("level,dtype", [(16, BF), (20, HF), (24, BF), (27, HF), (28, BF), (28, HF), (30, HF), (32, BF), (32, HF),
+                                         (100, BF), (100, HF), (140, BF)])
+@pytest.mark.parametrize("kind", ["few", "pair"])
+def test_prefill_scores_of_any_size(kind, level, dtype, sign):
+    """Scaled scores up to 2^level, far beyond where the product of reference and scale is exact, many of them alike: the
+    largest share the weight. Beyond fp32's range lse is infinite, out is not."""
+    lens = FAR_LENS[kind]
+    (q, kv, kr, cu_q, cu_k), scale = _far_inputs(lens, dtype, level, 71)
+    q *= sign
+    out, lse = _run(q, kv, kr, cu_q, cu_k, True, scale=scale)
+    _far_check(out, lse, q, kv, kr, lens, scale, 0.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("level", [8, 11, 12, 13, 16, 20])
+@pytest.mark.parametrize("kind", ["few", "pair"])
+def test_prefill_scores_around_a_large_one(kind, level, dtype):
+    """Scaled scores 2^level + t / 2, t up to 31: weights that count, on both sides of where the reference is subtracted
+    first. The second half of the keys lies 2^level higher, so that rows cross over on the way."""
+    lens = FAR_LENS[kind]
+    q, kv, kr, cu_q, cu_k = _inputs(lens, 2, dtype, 73)
+    q[:], kv[..., :128], kr[:] = 0, 0, 0
+    n = kv.shape[0]
+    half = level // 2
+    q[..., 0], q[..., 1] = 2.0 ** half, 1.0
+    kv[..., 0] = 2.0 ** (level - half)
+    kv[..., 1] = (torch.randint(0, 32, (n, 2), generator=_gen(3)) * 0.5).to(dtype)
+    for case in range(2):
+        if case:
+            kv[n // 2:, :, 0] *= 2
+        out, lse = _run(q, kv, kr, cu_q, cu_k, True, scale=1.0)
+        _far_check(out, lse, q, kv, kr, lens, 1.0, 16.0, dtype)
+
+
+# ---------------------------------------------------------------------------
 # a prompt in two chunks, then a decoded token
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("fmt", [0, 1])
