@@ -29,7 +29,10 @@
 // that units of unequal length even out without a counter in memory.
 //
 // Few rows over long keys: a unit's key tiles are cut into pieces (p.splits at
-// most), whose partial outputs mla_prefill_combine_kernel joins.
+// most), whose accumulators, references and sums mla_prefill_combine_kernel
+// joins. References and sums stay apart: a piece's lse would round away the sum
+// beside a large reference. The sums stand in the row of the output that the
+// join writes.
 #pragma once
 #include <cuda.h>
 
@@ -62,7 +65,7 @@ struct PrefillParams {
   int64_t out_token, out_head; // strides in elements
   float* lse;                  // [tq, heads]
   float* o_part;               // [splits][tq][heads][128], splits > 1
-  float* lse_part;             // [splits][tq][heads]
+  float* ref_part;             // [splits][tq][heads]: raw references
   int wide;                    // 1: rows of out are 32-B aligned, 2: those of o_part
   uint32_t* status;            // or null
   uint32_t stall_cycles;       // test hook, 0 in normal use
@@ -373,6 +376,11 @@ MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2
   row.l += x.x + x.y;
 }
 
+// where the sum of a piece's weights waits for the join
+MLA_DEV float* sum_at(const PrefillParams& p, int64_t row, int head, int piece) {
+  return reinterpret_cast<float*>(static_cast<uint16_t*>(p.out) + row * p.out_token + head * p.out_head) + piece;
+}
+
 // 16 words of a row to 16-B aligned memory, in stores of 32 bytes where that is aligned for them: the stores of a warp's 32
 // rows touch 32 lines each, whatever their width
 MLA_DEV void store_words16(void* dst, const uint32_t* w, bool wide) {
@@ -414,7 +422,7 @@ MLA_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" 
 MLA_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 constexpr uint32_t kStage = 32 * 128;   // a warp's 32 rows x 64 dims on their way out
 
-// The warp's 32 results: O / l and lse, or a piece's share of them. `some`: the accumulators hold something; read() is
+// The warp's 32 results: O / l and lse, or a piece's O, m and l. `some`: the accumulators hold something; read() is
 // called when they have been read. Rows of a warp that all belong to the unit leave through shared memory (`stage`) and
 // the copy engine: the plain stores of 32 rows touch 32 lines each and kept the SM's load/store path, and with it every
 // wait on a barrier, busy for some 3400 cycles a unit.
@@ -422,15 +430,17 @@ template <bool kFp16, class U, class F>
 MLA_DEV void store_rows(const PrefillParams& p, const CUtensorMap* tm_out, uint32_t stage, const U& u, const Row& row, uint32_t t_o,
                         bool some, int first, F read) {
   const int lane = threadIdx.x & 31;
-  const float inv = row.l > 0.f ? 1.f / row.l : row.l;   // a row that sees nothing has l = 0 and gets zeros; NaN stays
   const bool whole = u.pieces == 1, live = first + lane < u.rows;
+  // a row that sees nothing has l = 0 and gets zeros; NaN stays
+  const float inv = !whole ? 1.f : row.l > 0.f ? 1.f / row.l : row.l;
   const int64_t at = (int64_t)u.row + first + lane;
-  if (live) {
-    const float lse = row.l == 0.f ? -INFINITY : row.m * p.scale + logf(row.l);
-    if (whole) p.lse[at * p.heads + u.head] = lse;
-    else p.lse_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = lse;
+  if (live && whole) {
+    p.lse[at * p.heads + u.head] = row.l == 0.f ? -INFINITY : row.m * p.scale + logf(row.l);
+  } else if (live) {
+    p.ref_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = row.m;
+    *sum_at(p, at, u.head, u.piece) = row.l;
   }
-  // 32 dims of the row, normalised
+  // 32 dims of the row, normalised if it is whole
   auto share = [&](int c, float* v) {
     uint32_t o[32];
     if (some) {
@@ -481,8 +491,9 @@ MLA_DEV void store_rows(const PrefillParams& p, const CUtensorMap* tm_out, uint3
   }
 }
 
-// Joins the pieces of cut units: out = sum_i e^(lse_i - m) o_i / sum_i e^(lse_i - m), lse = m + ln sum. A warp to a
-// (row, head), four dims a lane; rows whose unit was not cut are left as they are.
+// Joins the pieces of cut units: with f_i = 2^(c (m_i - m)), m the largest m_i, out = sum_i f_i O_i / sum_i f_i l_i and
+// lse = scale m + ln sum_i f_i l_i. A warp to a (row, head), four dims a lane; rows whose unit was not cut are left as they
+// are.
 constexpr int kCombineThreads = 256;
 
 template <bool kFp16, int kBlock>
@@ -505,16 +516,23 @@ __global__ void __launch_bounds__(kCombineThreads) mla_prefill_combine_kernel(co
   const int i = (int)(row - s.q0), last = min((i / kBlock + 1) * kBlock, s.nq) - 1;
   const int pieces = pieces_of(p, (visible(p, s, last) + kKeys - 1) / kKeys);
   if (pieces == 1) return;
-  float m = -INFINITY;
-  for (int k = 0; k < pieces; ++k) m = fmaxf(m, p.lse_part[((int64_t)k * p.tq + row) * p.heads + head]);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float total = 0.f;
+  // lane k: piece k
+  float m = -INFINITY, l = 0.f;
+  if (lane < pieces) {
+    m = p.ref_part[((int64_t)lane * p.tq + row) * p.heads + head];
+    l = *sum_at(p, row, head, lane);
+  }
+  float top = m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float mine = exp2_approx((m - (top == -INFINITY ? 0.f : top)) * p.scale_log2);
+  float total = mine * l;   // all sums are read before any lane writes the row
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k = 0; k < pieces; ++k) {
-    const int64_t at = ((int64_t)k * p.tq + row) * p.heads + head;
-    const float f = expf(p.lse_part[at] - ref);
-    const float4 v = reinterpret_cast<const float4*>(p.o_part + at * kV)[lane];
-    total += f;
+    const float f = __shfl_sync(0xffffffffu, mine, k);
+    const float4 v = reinterpret_cast<const float4*>(p.o_part + (((int64_t)k * p.tq + row) * p.heads + head) * kV)[lane];
     acc.x += f * v.x;
     acc.y += f * v.y;
     acc.z += f * v.z;
@@ -523,7 +541,7 @@ __global__ void __launch_bounds__(kCombineThreads) mla_prefill_combine_kernel(co
   const float inv = total > 0.f ? 1.f / total : total;
   uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * p.out_token + head * p.out_head);
   dst[lane] = make_uint2(pack_p<kFp16>(acc.x * inv, acc.y * inv), pack_p<kFp16>(acc.z * inv, acc.w * inv));
-  if (lane == 0) p.lse[item] = total == 0.f ? -INFINITY : ref + logf(total);
+  if (lane == 0) p.lse[item] = total == 0.f ? -INFINITY : top * p.scale + logf(total);
 }
 
 }  // namespace prefill

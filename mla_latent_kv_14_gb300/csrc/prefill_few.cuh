@@ -389,15 +389,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float m = fmaxf(state.m, other.x), ref = m == -INFINITY ? 0.f : m;
       const float f0 = exp2_approx((state.m - ref) * p.scale_log2), f1 = exp2_approx((other.x - ref) * p.scale_log2);
       const float l = f0 * state.l + f1 * other.y;
-      const float inv = l > 0.f ? 1.f / l : l;       // a row that sees nothing has l = 0 and gets zeros; NaN stays
       const bool whole = u.pieces == 1, live = r < u.rows;
+      // a row that sees nothing has l = 0 and gets zeros; NaN stays
+      const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : l;
       const int64_t at = (int64_t)u.row + r;
-      if (live) {
-        const float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
-        if (whole) p.lse[at * p.heads + u.head] = lse;
-        else p.lse_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = lse;
+      if (live && whole) {
+        p.lse[at * p.heads + u.head] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+      } else if (live) {
+        p.ref_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = m;
+        *sum_at(p, at, u.head, u.piece) = l;
       }
-      // 32 dims of the row: (f0 a + f1 b) / l
+      // 32 dims of the row: f0 a + f1 b, over l if it is whole
       auto share = [&](int c, float* v) {
         uint32_t a[32], b[32];
 #pragma unroll

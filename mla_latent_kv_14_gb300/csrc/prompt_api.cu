@@ -52,6 +52,7 @@ mla_status launch_read(const read::ReadParams& p, void* stream) {
 
 constexpr int kCardSms = 152;
 constexpr int kMostPieces = 16;
+static_assert(kMostPieces <= 32 && 4 * kMostPieces <= 2 * prefill::kV);   // the join: a lane, and a word of a row of out, to a piece
 // How the attention is launched, from sizes that the host knows.
 struct PrefillPlan {
   bool pair;         // two CTAs to a unit of 512 queries, or one to a unit of 128
@@ -318,7 +319,7 @@ mla_status mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
   p.out_head = out_head_stride;
   p.lse = lse;
   p.o_part = static_cast<float*>(workspace);
-  p.lse_part = need ? p.o_part + (int64_t)splits * tq * heads * pf::kV : nullptr;
+  p.ref_part = need ? p.o_part + (int64_t)splits * tq * heads * pf::kV : nullptr;
   p.wide = (aligned(out, 32) && out_token_stride % 16 == 0 && out_head_stride % 16 == 0 ? 1 : 0) | (aligned(workspace, 32) ? 2 : 0);
   p.status = status;
   p.stall_cycles = g_test_stall.load(std::memory_order_relaxed);

@@ -835,6 +835,26 @@ def test_prefill_scores_around_a_large_one(kind, level, dtype):
         _far_check(out, lse, q, kv, kr, lens, 1.0, 16.0, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lens", [[(5, 6000)], [(300, 9000)], [(3, 4100), (130, 2600)]], ids=["few", "pair", "ragged"])
+def test_prefill_cut_units_of_large_scores(lens, dtype):
+    """Largest scores that are alike in several pieces of a unit weigh by how many there are, however large they are; and
+    scores around a large one."""
+    q, kv, kr, cu_q, cu_k = _inputs(lens, 2, dtype, 79)
+    assert mla.load_library().mla_prefill_workspace_size(q.shape[0], kv.shape[0], len(lens), 2) > 0
+    for level in (13, 20, 28, 100):
+        (q, kv, kr, cu_q, cu_k), scale = _far_inputs(lens, dtype, level, 79)
+        out, lse = _run(q, kv, kr, cu_q, cu_k, True, scale=scale)
+        _far_check(out, lse, q, kv, kr, lens, scale, 0.0, dtype)
+    for level in (10, 20):
+        q[:], kv[..., :128], kr[:] = 0, 0, 0
+        q[..., 0], q[..., 1] = 2.0 ** (level // 2), 1.0
+        kv[..., 0] = 2.0 ** (level - level // 2)
+        kv[..., 1] = (torch.randint(0, 32, (kv.shape[0], 2), generator=_gen(3)) * 0.5).to(dtype)
+        out, lse = _run(q, kv, kr, cu_q, cu_k, True, scale=1.0)
+        _far_check(out, lse, q, kv, kr, lens, 1.0, 16.0, dtype)
+
+
 # ---------------------------------------------------------------------------
 # a prompt in two chunks, then a decoded token
 # ---------------------------------------------------------------------------
