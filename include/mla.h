@@ -530,7 +530,9 @@ MLA_API mla_status mla_read_kv(const void* kvcache, int64_t num_blocks, int page
  * over its visible keys j: all n_k, or with `causal` those below n_k - n_q + i + 1
  * (the last query sees all keys), but at least the first prefix_lens[b] (a prefix
  * that all queries see). A query that sees no key gets out = 0, lse = -inf.
- * softmax_scale lies between 2^-100 and 2^100.
+ * softmax_scale lies between 2^-100 and 2^100. The dots q . k are summed in fp32; scaled
+ * scores may lie beyond its range (out is right then, lse infinite). A query with a dot above
+ * that range, or none of whose dots lies within it, gets NaN.
  * Per (query, key) pair 640 FLOP a head, where the decode's absorbed form takes
  * 2176: the form for prompts and their chunks; keys and values come from the
  * latent rows by the model's up-projections.

@@ -376,6 +376,13 @@ MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2
   row.l += x.x + x.y;
 }
 
+// What takes the place of 1 / l and of ln l where l is 0: a query that sees no key gets zeros and -inf, one whose scores all
+// are -inf (dots beyond fp32's range) NaN, as 0 / 0.
+MLA_DEV float inverse(float l, bool sees) { return l == 0.f ? (sees ? NAN : 0.f) : 1.f / l; }
+MLA_DEV float lse_of(const PrefillParams& p, float m, float l, bool sees) {
+  return l == 0.f ? (sees ? NAN : -INFINITY) : m * p.scale + logf(l);
+}
+
 // where the sum of a piece's weights waits for the join
 MLA_DEV float* sum_at(const PrefillParams& p, int64_t row, int head, int piece) {
   return reinterpret_cast<float*>(static_cast<uint16_t*>(p.out) + row * p.out_token + head * p.out_head) + piece;
@@ -431,11 +438,11 @@ MLA_DEV void store_rows(const PrefillParams& p, const CUtensorMap* tm_out, uint3
                         bool some, int first, F read) {
   const int lane = threadIdx.x & 31;
   const bool whole = u.pieces == 1, live = first + lane < u.rows;
-  // a row that sees nothing has l = 0 and gets zeros; NaN stays
-  const float inv = !whole ? 1.f : row.l > 0.f ? 1.f / row.l : row.l;
+  const bool sees = live && u.visible(first + lane, p.causal) > 0;
+  const float inv = whole ? inverse(row.l, sees) : 1.f;
   const int64_t at = (int64_t)u.row + first + lane;
   if (live && whole) {
-    p.lse[at * p.heads + u.head] = row.l == 0.f ? -INFINITY : row.m * p.scale + logf(row.l);
+    p.lse[at * p.heads + u.head] = lse_of(p, row.m, row.l, sees);
   } else if (live) {
     p.ref_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = row.m;
     *sum_at(p, at, u.head, u.piece) = row.l;
@@ -538,10 +545,11 @@ __global__ void __launch_bounds__(kCombineThreads) mla_prefill_combine_kernel(co
     acc.z += f * v.z;
     acc.w += f * v.w;
   }
-  const float inv = total > 0.f ? 1.f / total : total;
+  const bool sees = visible(p, s, i) > 0;
+  const float inv = inverse(total, sees);
   uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * p.out_token + head * p.out_head);
   dst[lane] = make_uint2(pack_p<kFp16>(acc.x * inv, acc.y * inv), pack_p<kFp16>(acc.z * inv, acc.w * inv));
-  if (lane == 0) p.lse[item] = total == 0.f ? -INFINITY : top * p.scale + logf(total);
+  if (lane == 0) p.lse[item] = lse_of(p, top, total, sees);
 }
 
 }  // namespace prefill

@@ -390,11 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f0 = exp2_approx((state.m - ref) * p.scale_log2), f1 = exp2_approx((other.x - ref) * p.scale_log2);
       const float l = f0 * state.l + f1 * other.y;
       const bool whole = u.pieces == 1, live = r < u.rows;
-      // a row that sees nothing has l = 0 and gets zeros; NaN stays
-      const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : l;
+      const float inv = whole ? inverse(l, seen > 0) : 1.f;
       const int64_t at = (int64_t)u.row + r;
       if (live && whole) {
-        p.lse[at * p.heads + u.head] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+        p.lse[at * p.heads + u.head] = lse_of(p, m, l, seen > 0);
       } else if (live) {
         p.ref_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = m;
         *sum_at(p, at, u.head, u.piece) = l;

@@ -855,6 +855,28 @@ def test_prefill_cut_units_of_large_scores(lens, dtype):
         _far_check(out, lse, q, kv, kr, lens, 1.0, 16.0, dtype)
 
 
+@pytest.mark.parametrize("lens", [[(40, 700)], [(600, 700)], [(5, 6000)], [(300, 9000)]], ids=["few", "pair", "few cut", "pair cut"])
+def test_prefill_dots_below_fp32(lens):
+    """A query all of whose dots are -inf gets NaN, not what one that sees no key gets; where one dot is finite, its key
+    takes all. Queries that see nothing keep 0 and -inf."""
+    (n_q, n_k), = lens
+    q, kv, kr, cu_q, cu_k = _inputs(lens, 2, BF, 83)
+    q[..., 5] = 2.0 ** 70
+    kv[..., 5] = -2.0 ** 70
+    out, lse = _run(q, kv, kr, cu_q, cu_k, True)
+    assert out.isnan().all() and lse.isnan().all()
+    kv[n_k - 30, 0, 5] = 0                    # one key of the first head
+    out, lse = _run(q, kv, kr, cu_q, cu_k, True)
+    seen = torch.from_numpy(oracle.visible(n_q, n_k, True))
+    sees = seen > n_k - 30
+    assert torch.equal(out[sees][:, 0].cpu(), kv[n_k - 30, 0, 128:].expand(int(sees.sum()), 128)) and lse[sees][:, 0].isfinite().all()
+    assert out[~sees][:, 0].isnan().all() and lse[~sees][:, 0].isnan().all() and out[:, 1].isnan().all()
+    if n_q > 300:                             # fewer keys than queries: the first ones see none
+        out, lse = _run(q, kv[:300], kr[:300], cu_q, [0, 300], True)
+        none = n_q - 300
+        assert (out[:none] == 0).all() and torch.isneginf(lse[:none]).all() and out[none:].isnan().all()
+
+
 # ---------------------------------------------------------------------------
 # a prompt in two chunks, then a decoded token
 # ---------------------------------------------------------------------------
