@@ -533,6 +533,8 @@ MLA_API mla_status mla_read_kv(const void* kvcache, int64_t num_blocks, int page
  * softmax_scale lies between 2^-100 and 2^100. The dots q . k are summed in fp32; scaled
  * scores may lie beyond its range (out is right then, lse infinite). A query with a dot above
  * that range, or none of whose dots lies within it, gets NaN.
+ * Softmax and sums are fp32; the weights are rounded to `dtype` for the product with v, where
+ * fp16 loses those below 2^-32 of the query's largest.
  * Per (query, key) pair 640 FLOP a head, where the decode's absorbed form takes
  * 2176: the form for prompts and their chunks; keys and values come from the
  * latent rows by the model's up-projections.

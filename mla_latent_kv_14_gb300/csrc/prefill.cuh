@@ -276,6 +276,12 @@ MLA_DEV uint32_t pack_p(float lo, float hi) {
 // themselves, no more than the scores' own rounding to fp32 does
 constexpr float kFar = 0x1p12f;
 
+// Weights of fp16 are formed 2^7 larger: with the reference's slack of 2^8 they reach 2^15, and what fp16 loses, weights below
+// 2^-25 of its units, begins at 2^-32 of the reference's. At a scale of 1 the many small weights of a long row would be
+// missing from O but not from l. The factor cancels in O / l; l carries it until its logarithm is taken.
+template <bool kFp16>
+constexpr float kRaise = kFp16 ? 7.f : 0.f;
+
 // A thread's row in the softmax of one query tile.
 struct Row {
   float m, l;                  // reference (raw score) and sum of the weights
@@ -299,7 +305,8 @@ MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2
   }
   uint64_t sum[2];
   const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
-  auto reference = [&]() { return row.m == -INFINITY ? 0.f : -row.m * scale_log2; };
+  constexpr float raise = kRaise<kFp16>;
+  auto reference = [&]() { return row.m == -INFINITY ? raise : fmaf(-row.m, scale_log2, raise); };
   float ref = reference();
   // 2^(s - m) of keys [32 c, 32 c + 32), packed
   auto weights = [&](int c, uint32_t* q) {
@@ -356,7 +363,7 @@ MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2
         s[k] = __float_as_uint(x.x);
         s[k + 1] = __float_as_uint(x.y);
       }
-      if (far) ref = 0.f;
+      if (far) ref = raise;
     }
     sum[0] = sum[1] = 0;
     weights(0, q);
@@ -379,8 +386,9 @@ MLA_DEV void softmax_tile(Row& row, uint32_t t_s, uint32_t t_o, float scale_log2
 // What takes the place of 1 / l and of ln l where l is 0: a query that sees no key gets zeros and -inf, one whose scores all
 // are -inf (dots beyond fp32's range) NaN, as 0 / 0.
 MLA_DEV float inverse(float l, bool sees) { return l == 0.f ? (sees ? NAN : 0.f) : 1.f / l; }
+template <bool kFp16>
 MLA_DEV float lse_of(const PrefillParams& p, float m, float l, bool sees) {
-  return l == 0.f ? (sees ? NAN : -INFINITY) : m * p.scale + logf(l);
+  return l == 0.f ? (sees ? NAN : -INFINITY) : m * p.scale + logf(kFp16 ? l * 0x1p-7f : l);
 }
 
 // where the sum of a piece's weights waits for the join
@@ -442,7 +450,7 @@ MLA_DEV void store_rows(const PrefillParams& p, const CUtensorMap* tm_out, uint3
   const float inv = whole ? inverse(row.l, sees) : 1.f;
   const int64_t at = (int64_t)u.row + first + lane;
   if (live && whole) {
-    p.lse[at * p.heads + u.head] = lse_of(p, row.m, row.l, sees);
+    p.lse[at * p.heads + u.head] = lse_of<kFp16>(p, row.m, row.l, sees);
   } else if (live) {
     p.ref_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = row.m;
     *sum_at(p, at, u.head, u.piece) = row.l;
@@ -549,7 +557,7 @@ __global__ void __launch_bounds__(kCombineThreads) mla_prefill_combine_kernel(co
   const float inv = inverse(total, sees);
   uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * p.out_token + head * p.out_head);
   dst[lane] = make_uint2(pack_p<kFp16>(acc.x * inv, acc.y * inv), pack_p<kFp16>(acc.z * inv, acc.w * inv));
-  if (lane == 0) p.lse[item] = lse_of(p, top, total, sees);
+  if (lane == 0) p.lse[item] = lse_of<kFp16>(p, top, total, sees);
 }
 
 }  // namespace prefill

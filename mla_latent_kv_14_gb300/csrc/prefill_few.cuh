@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = whole ? inverse(l, seen > 0) : 1.f;
       const int64_t at = (int64_t)u.row + r;
       if (live && whole) {
-        p.lse[at * p.heads + u.head] = lse_of(p, m, l, seen > 0);
+        p.lse[at * p.heads + u.head] = lse_of<kFp16>(p, m, l, seen > 0);
       } else if (live) {
         p.ref_part[((int64_t)u.piece * p.tq + at) * p.heads + u.head] = m;
         *sum_at(p, at, u.head, u.piece) = l;

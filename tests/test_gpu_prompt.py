@@ -877,6 +877,30 @@ def test_prefill_dots_below_fp32(lens):
         assert (out[:none] == 0).all() and torch.isneginf(lse[:none]).all() and out[none:].isnan().all()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lens", [[(40, 700)], [(600, 700)], [(5, 6000)], [(300, 9000)]], ids=["few", "pair", "few cut", "pair cut"])
+def test_prefill_of_many_small_weights(lens, dtype):
+    """One key in 128 with a weight of 1 and a value of 0, the others near 2^-26 and 1024: what fp16 weights lose of them
+    is 2^-32 a key at most, half a step of the subnormals at the 2^7 that they are raised by."""
+    (n_q, n_k), = lens
+    q, kv, kr, cu_q, cu_k = _inputs(lens, 1, dtype, 89)
+    q[:], kv[:], kr[:] = 0, 0, 0
+    q[..., 5] = 1.0
+    small = torch.arange(n_k) % 128 != 77
+    kv[small, :, 5] = -26 * 0.6931471805599453
+    kv[small, :, 128:] = 1024.0
+    out, lse = _run(q, kv, kr, cu_q, cu_k, False, scale=1.0)
+    one = np.ones(1, dtype=np.int64) * n_k
+    ro, rl, size, _ = oracle.prefill(q[:1], kv[..., :128], kr, kv[..., 128:], 1.0, one)
+    weight = (4 + 6 * 27) * U                     # of itself: as in _far_check, for dots that are exact
+    rel = 2 * weight + (2 * n_k + 64) * U
+    bound = 1.01 * HALF[dtype] * np.abs(ro) + (HALF[dtype] + rel) * size
+    if dtype == HF:
+        bound = bound + 2.0 ** -32 * 1024 * int(small.sum()) / np.exp(rl)[..., None]
+    assert (np.abs(oracle.to_f64(out.cpu()) - ro) <= bound).all()
+    assert (np.abs(oracle.to_f64(lse.cpu()) - rl) <= weight + (n_k + 64) * U + 4 * U * np.abs(rl)).all()
+
+
 # ---------------------------------------------------------------------------
 # a prompt in two chunks, then a decoded token
 # ---------------------------------------------------------------------------
