@@ -549,7 +549,9 @@ MLA_API mla_status mla_read_kv(const void* kvcache, int64_t num_blocks, int page
  * cu_seqlens_q, cu_seqlens_k (device) int32 [batch + 1], ascending; prefix_lens
  *        (device, optional) int32 [batch], kept within [0, n_k]; not read unless
  *        causal. A document whose offsets descend or leave the tensors is skipped
- *        and recorded as an index error in `status`.
+ *        and recorded as an index error in `status` (with tokens_q = 0 nothing is
+ *        looked at). Where offsets of queries descend, documents behind may share
+ *        rows with others: what their rows hold then is not defined.
  * out    (device) [tokens_q, heads, 128] with strides; lse (device) fp32 [tokens_q,
  *        heads]. Rows of no document are left as they were.
  * workspace (device, 16-B aligned) of mla_prefill_workspace_size() bytes (0: none

@@ -146,7 +146,6 @@ struct Finder {
       const Span s = span_of(p, b);
       blocks = (s.nq + kBlock - 1) / kBlock;
       keys = s.nk;
-      if (s.bad && p.status) atomicOr(p.status, STATUS_INDEX);
     }
     // lane r takes the document of rank r
     int rank = 0, from = 0;
@@ -208,6 +207,16 @@ struct Finder {
     return true;
   }
 };
+
+// Documents that are skipped are recorded by the block `id` of the `ids` in the grid, whether it starts or is taken over:
+// groups of 32 id, id + ids, ... The search for units is no place for it: it ends with the last unit, and documents
+// behind may have none. Called when the unit is on its way to its readers.
+MLA_DEV void record_bad(const PrefillParams& p, int64_t id, int64_t ids) {
+  if (!p.status) return;
+  for (int64_t b = 32 * id + (threadIdx.x & 31); b < p.batch; b += 32 * ids)
+    if (span_of(p, (int)b).bad) atomicOr(p.status, STATUS_INDEX);
+  __syncwarp();
+}
 
 // asks for a block of the grid that has not started: 16 bytes at `dst`, counted on `bar`
 MLA_DEV void ask_next(uint32_t dst, uint32_t bar) {

@@ -232,8 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_remote(mapa(bar(B_UFULL + s), 1));
           }
           __syncwarp();
-          if (id < 0 || !ready_all(B_WANT, n++)) break;
         }
+        if (id < 0) break;
+        record_bad(p, id, gridDim.x >> 1);
+        if (found && !ready_all(B_WANT, n++)) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(B_NEXT), 16);
           ask_next(smem_u32(misc), bar(B_NEXT));

@@ -901,6 +901,44 @@ def test_prefill_of_many_small_weights(lens, dtype):
     assert (np.abs(oracle.to_f64(lse.cpu()) - rl) <= weight + (n_k + 64) * U + 4 * U * np.abs(rl)).all()
 
 
+@pytest.mark.parametrize("rows", [1, 513], ids=["few", "pair"])
+def test_prefill_bad_offsets_behind_the_last_unit(rows):
+    """Documents behind those that all units belong to, of which the search for units sees nothing: descending queries,
+    keys that leave the tensor, in a group of 32 right behind the last unit's and far behind."""
+    n = 32                                    # their units are as many as the grid has blocks
+    lens = [(rows, rows)] * n
+    q, kv, kr, cu_q, cu_k = _inputs(lens, 1, BF, 97)
+    ref, ref_l = _run(q, kv, kr, cu_q, cu_k, True)
+    _check(ref, ref_l, q, kv, kr, cu_q, cu_k, True, None, BF, docs=[0, 31], rows=[0, 1, 511, 512])
+    dq, dkv, dkr = q.to(DEV), kv.to(DEV), kr.to(DEV)
+    end = rows * n
+    for more in (1, 2, 31, 33):               # documents behind
+        for cq, ck in (([end] * (more - 1) + [end - 1], [end] * more), ([end] * more, [end] * (more - 1) + [end + 1]),
+                       ([end] * more, [end] * (more - 1) + [-1]), ([end] * (more - 1) + [end + 1], [end] * more)):
+            st = _status()
+            out, lse = torch.full_like(ref, 4.0), torch.full_like(ref_l, 4.0)
+            mla.mla_prefill(dq, dkv[..., :128], dkr, dkv[..., 128:], _ints([*cu_q, *cq]), _ints([*cu_k, *ck]), SCALE, out=out,
+                            lse=lse, status=st)
+            assert _bits(st) == 1, (more, cq[-1], ck[-1])
+            if (end // (n + more) > 256) == (rows > 256):        # the same kernel, so the same bits
+                assert torch.equal(out, ref) and torch.equal(lse, ref_l), (more, cq[-1], ck[-1])
+            else:
+                _check(out, lse, q, kv, kr, cu_q, cu_k, True, None, BF, docs=[0, 31], rows=[0, 1, 511, 512])
+
+
+def test_prefill_bad_offsets_of_a_large_batch():
+    """One document with a query, thousands without, the last of them bad; and none bad."""
+    q, kv, kr, _, _ = _inputs([(1, 1)], 2, BF, 98)
+    dkv = kv.to(DEV)
+    for batch in (31, 32, 33, 5000):
+        for last, bits in ((1, 0), (7, 1), (-2, 1)):
+            st = _status()
+            cu_k = [0] + [1] * (batch - 1) + [last]
+            out, _ = mla.mla_prefill(q.to(DEV), dkv[..., :128], kr.to(DEV), dkv[..., 128:], _ints([0] + [1] * batch), _ints(cu_k), SCALE,
+                                     status=st)
+            assert _bits(st) == bits and torch.equal(out, dkv[..., 128:])
+
+
 # ---------------------------------------------------------------------------
 # a prompt in two chunks, then a decoded token
 # ---------------------------------------------------------------------------
