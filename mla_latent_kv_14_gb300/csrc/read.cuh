@@ -134,9 +134,9 @@ __global__ void __launch_bounds__(32 * kReadWarps) mla_read_kv_kernel(const Read
     for (int k = 0; k < kRows; ++k)
       if (src[k]) {
         float f = scale[k];
-        if (kFormat == 2) {   // 2^(byte - 127); byte 0 is 2^-127, a subnormal
+        if (kFormat == 2) {   // 2^(byte - 127); byte 0 is 2^-127, a subnormal, byte 255 NaN
           const uint32_t e = __float_as_uint(f);
-          f = __uint_as_float(e ? e << 23 : 0x00400000u);
+          f = __uint_as_float(e == 255u ? 0x7FFFFFFFu : e ? e << 23 : 0x00400000u);
         } else if (kFormat == 3) {
           f = e4m3x2_f32(__float_as_uint(f)).x;
         }

@@ -5,6 +5,8 @@ against the 64-bit oracle; and a run of them together, as a prompt uses them.
 Tolerances are the oracle's bounds of an fp32 evaluation plus half a step of the
 result's type; rows read back are compared bit for bit.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -353,6 +355,36 @@ def test_read_kv_bad_pages_and_short_outputs(fmt):
     mla.mla_read_kv(cache, _ints([[2, 1, 0]]), _ints([0, 5]), total=5, starts=_ints([-3]), kv_format=fmt, status=st)
     assert _bits(st) == 1
 
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("fmt", [1, 2, 3])
+def test_read_kv_every_code_and_scale(fmt, dtype):
+    """All code bytes beside all scale bytes (656-byte rows: scales over fp32's range and beyond), NaN among both."""
+    byte = torch.arange(256, dtype=torch.uint8)
+    n = {1: 241, 2: 512, 3: 256}[fmt]
+    raw = torch.zeros(n, {1: 656, 2: 528, 3: 288}[fmt], dtype=torch.uint8)
+    if fmt == 1:
+        raw[:, :512] = byte.repeat(2)
+        scale = torch.exp2(torch.arange(-160, 160).float().double()).float()
+        scale = torch.cat((scale, 1.2345 * scale, -scale, torch.tensor([0.0, math.inf, -math.inf, math.nan])))
+        raw[:, 512:528] = scale.view(n, 4).view(torch.uint8)
+        raw[:, 528:] = torch.randn(n, 64, generator=_gen(1)).to(BF).view(torch.uint8)
+    elif fmt == 2:
+        raw[0::2, :512], raw[1::2, :512] = byte.repeat(2), byte.flip(0).roll(16).repeat(2)   # every code meets every scale
+        for k in range(16):
+            raw[:, 512 + k] = (torch.arange(n) // 2 + 16 * k).to(torch.uint8)
+    else:
+        raw[:, :256] = byte
+        for k in range(32):
+            raw[:, 256 + k] = (byte.long() + 8 * k).to(torch.uint8)
+    cache = torch.zeros(-(-n // PAGE), PAGE, 1, raw.shape[1], dtype=torch.uint8)
+    cache.view(-1, raw.shape[1])[:n] = raw
+    table = _ints([list(range(len(cache)))])
+    got = mla.mla_read_kv(cache.to(DEV), table, _ints([0, n]), total=n, kv_format=fmt, dtype=dtype).cpu()
+    with np.errstate(invalid="ignore"):       # 0 times an infinite scale
+        want = torch.from_numpy(oracle.cached_rows(raw.numpy(), fmt)).float().to(dtype)
+    assert want.isnan().any() and want.isfinite().any()
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(1.5, 2.5, -2.5), want.nan_to_num(1.5, 2.5, -2.5))
 
 @pytest.mark.parametrize("fmt", [0, 1, 2, 3])
 def test_read_kv_leaves_rows_before_the_first_request(fmt):
