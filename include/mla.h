@@ -468,7 +468,10 @@ MLA_API mla_status mla_select_topk(const float* scores, int64_t score_stride, in
  * RMS norm of a row of d values: y = x * (1 / sqrt(mean(x^2) + eps)) * weight, in
  * fp32 (the sum of squares too), with weight (device, 16-B aligned) of the row's
  * type or NULL for ones. y stays in fp32 through the rotation or quantisation
- * that follows and is rounded once, to the type it is stored in. eps >= 0.
+ * that follows and is rounded once, to the type it is stored in. eps >= 0. The sum of
+ * squares has to lie within fp32 (rows of bf16 beyond some 2^59 are outside, and, with
+ * eps = 0, those below some 2^-60 and rows of zeros); the product with the weight may lie
+ * anywhere that y does.
  */
 
 /*

@@ -4,13 +4,14 @@
 //     y = x * (1 / sqrt(mean(x^2) + eps)) * w
 //
 // The mean is over a row's d dims (the latent dims of a cache row), summed in
-// fp32. x w is formed first: the product of two 16-bit values is exact in fp32,
-// so that y carries the root's error and one rounding. y stays in fp32 through
-// the rotation (whose products and sums are each rounded to fp32, as in
-// rows.cuh) or the quantisation and is rounded once, to the type that it is
-// stored in. So a row is read once and written once, and both kernels are bound
-// by those bytes (some 2 FLOP a byte) or, for a few tokens, by the latency of
-// position -> table row -> store.
+// fp32. x is brought to the row's own size first, so that a product leaves
+// fp32's range only where y does; x w first would be exact for most values, one
+// rounding less, but overflows or loses bits for bf16 rows and weights near the
+// ends of theirs. y stays in fp32 through the rotation (whose products and sums
+// are each rounded to fp32, as in rows.cuh) or the quantisation and is rounded
+// once, to the type that it is stored in. So a row is read once and written
+// once, and both kernels are bound by those bytes (some 2 FLOP a byte) or, for a
+// few tokens, by the latency of position -> table row -> store.
 #pragma once
 #include "rows.cuh"
 
@@ -122,14 +123,14 @@ __global__ void __launch_bounds__(kNormThreads, 4) mla_norm_rotate_kernel(const 
     const float r = 1.f / sqrtf(group_sum<kLanes>(ss) * inv_dim + p.eps);
     auto normed = [&](int k, float* y) {
       rows::unpack<kFp16, 8>(&raw[u][k], y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= r;
       if (p.weight) {
         float w[8];
         rows::unpack<kFp16, 8>(&weight[k], w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] *= w[j];
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] *= r;
     };
     float y[8];
     normed(kChunks, y);
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kNormThreads, 4) mla_norm_rotate_kernel(const 
 // optionally takes the same row in 16 bits.
 //
 // Measured (GB300): 64 tokens, bf16 rows 1.5 us; 32768 tokens into 656-byte rows
-// and `rows` 19.4 us (0.80 of the copy bandwidth): like mla_append_kv_kernel it
+// and `rows` 19.7 us (0.79 of the copy bandwidth): like mla_append_kv_kernel it
 // waits for its loads in turn (slot and row, then the table row) between two
 // stretches of arithmetic, at half of the issue slots.
 // ---------------------------------------------------------------------------
@@ -229,14 +230,14 @@ __global__ void __launch_bounds__(32 * rows::kAppendWarps) mla_norm_append_kv_ke
 #pragma unroll
   for (int k = 0; k < 16; ++k) ss = fmaf(x[k], x[k], ss);
   const float inv = 1.f / sqrtf(group_sum<32>(ss) * (1.f / kLatent) + q.eps);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) x[k] *= inv;
   if (q.weight && latent) {
     float w[16];
     unpack<kFp16, 16>(wraw, w);
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] *= w[k];
   }
-#pragma unroll
-  for (int k = 0; k < 16; ++k) x[k] *= inv;
   const float lo = turn_lo(a, b, cs, sn), hi = turn_hi(a, b, cs, sn);
   // pair `lane` of the rotated dims at dst, 16 bits each
   auto store_rope = [&](uint16_t* dst) {

@@ -129,6 +129,25 @@ def test_norm_rotate_of_small_and_large_rows(dtype):
     _close(mla.mla_norm_rotate(shared, pos.to(DEV), _table()), want, bound, dtype)
 
 
+ENDS = [(2.0 ** 58, 2.0 ** 80), (2.0 ** 58, 2.0 ** -90), (2.0 ** -58, 2.0 ** -90), (2.0 ** -58, 2.0 ** 80), (2.0 ** 40, 2.0 ** 95)]
+
+
+@pytest.mark.parametrize("dim,heads,tokens", [(192, 3, 5), (128, 1, 40), (576, 2, 9), (192, 64, 600), (128, 64, 600), (256, 2, 7)])
+@pytest.mark.parametrize("size,weight", ENDS)
+def test_norm_rotate_at_the_ends_of_bf16(size, weight, dim, heads, tokens):
+    """Rows and weights whose product leaves fp32's range, or its normal numbers, where the result does not; the squares'
+    sum stays within."""
+    g = _gen(dim + tokens)
+    x = (size * (1 + torch.rand(tokens, heads, dim, generator=g, dtype=torch.float64))).to(BF)
+    w = (weight * (0.5 + torch.rand(dim, generator=g, dtype=torch.float64))).to(BF)
+    pos = torch.randint(0, 5000, (tokens,), generator=g).int()
+    want = oracle.norm_rotate(x, w, 0.0, TABLE[pos.numpy()], dim - 64, False)
+    bound = oracle.norm_rotate_error(oracle.rms_norm(x, w, 0.0), dim - 64, False)
+    _close(mla.mla_norm_rotate(x.to(DEV), pos.to(DEV), _table(), weight=w.to(DEV), eps=0.0), want, bound, BF)
+    _close(mla.mla_norm_rotate(x.to(DEV), pos.to(DEV), _table(), eps=0.0),
+           oracle.norm_rotate(x, None, 0.0, TABLE[pos.numpy()], dim - 64, False),
+           oracle.norm_rotate_error(oracle.rms_norm(x, None, 0.0), dim - 64, False), BF, "no weight")
+
 @pytest.mark.parametrize("tokens,heads,dim", [(1500, 128, 192), (4099, 3, 128), (11001, 3, 128), (9001, 1, 128), (700, 64, 576),
                                               (20001, 2, 64), (257, 128, 256)])
 def test_norm_rotate_of_many_rows(tokens, heads, dim):
@@ -263,6 +282,33 @@ def test_norm_append_kv(n, fmt, dtype, halves, with_rows):
         assert (rows[~torch.from_numpy(keep)] == 5.0).all() and (rows[:, latent + 64:] == 5.0).all()
         _close(rows[torch.from_numpy(keep), :latent + 64], want[keep], bound[keep], dtype)
 
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+@pytest.mark.parametrize("size,weight", ENDS)
+def test_norm_append_at_the_ends_of_bf16(size, weight, fmt):
+    """As for the norm with rotation; 656-byte rows hold any size, 528-byte ones those that a UE8M0 scale does."""
+    n, latent = 70, 448 if fmt == 2 else 512
+    g = _gen(fmt)
+    kv = torch.randn(n, latent + 64, generator=g, dtype=torch.float64)
+    kv[:, :latent] = size * (1 + kv[:, :latent].abs().clamp(max=1))
+    kv = kv.to(BF)
+    w = (weight * (0.5 + torch.rand(latent, generator=g, dtype=torch.float64))).to(BF)
+    width = {0: 576, 1: 656, 2: 528}[fmt]
+    cache = torch.zeros(2, PAGE, 1, width, dtype=torch.uint8 if fmt else BF, device=DEV)
+    rows = torch.empty(n, latent + 64, dtype=BF, device=DEV)
+    at = torch.arange(n, dtype=torch.int32, device=DEV)
+    dev = kv.to(DEV)
+    mla.mla_norm_append_kv(dev[:, :latent], dev[:, latent:], w.to(DEV), cache, at, at, _table(), eps=0.0, kv_format=fmt, rows=rows)
+    want = oracle.rms_norm(kv[:, :latent], w, 0.0)
+    bound = (latent / 2 + 9) * 2.0 ** -24 * np.abs(want)
+    _close(rows[:, :latent], want, bound, BF)
+    if fmt == 0:
+        assert torch.equal(cache.view(-1, 576)[:n], rows)
+        return
+    turned = oracle.rotate(kv[:, latent:], TABLE[:n], False, exact=True)
+    r32 = oracle.rotate(kv[:, latent:], TABLE[:n], False)
+    want, bound = np.concatenate((want, turned), 1), np.concatenate((bound, np.abs(r32.astype(np.float64) - turned)), 1)
+    _check_rows(cache.view(-1, width)[:n].cpu().numpy(), want, bound, fmt)
 
 def test_norm_append_of_unit_rows_is_the_append():
     """Rows whose norm is one and whose mean square is exact: the same bytes as mla_append_kv."""
