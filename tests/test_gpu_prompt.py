@@ -841,7 +841,7 @@ def _far_check(out, lse, q, kv, kr, lens, scale, spread, dtype):
     """Against the oracle, for dots that fp32 holds exactly. With x = c (s - m), c = scale log2 e: c rounds (U of x, with
     scale a power of two), the difference and the product too, the reference's own rounding (2^-13 ln 2 at most, where it
     is not subtracted first) counts twice where the reference has moved, and 2^x is off by 4U: a weight by 4U + 3U |x| +
-    2^-12 of itself, |x| <= 2 * spread for scores that lie `spread` apart. Weights of 2^-25 and less of the largest may
+    2^-12 of itself, |x| <= 2 * spread for scores that lie `spread` apart. Weights of 2^-32 and less of the largest may
     be lost in fp16."""
     q0 = k0 = 0
     for n_q, n_k in lens:
@@ -854,7 +854,7 @@ def _far_check(out, lse, q, kv, kr, lens, scale, spread, dtype):
         rel = 2 * weight + (2 * n + 64) * U
         bo = 1.01 * HALF[dtype] * np.abs(ro) + (HALF[dtype] + rel)[..., None] * size
         if dtype == HF:
-            bo = bo + 2.0 ** -25 * (1 + np.abs(oracle.to_f64(kv[k0:k0 + n_k, :, 128:])).sum(0))
+            bo = bo + 2.0 ** -32 * np.abs(oracle.to_f64(kv[k0:k0 + n_k, :, 128:])).sum(0)
         bl = weight + (n + 64) * U + 4 * U * np.abs(rl)
         go, gl = oracle.to_f64(out[q0:q0 + n_q].cpu()[pick]), oracle.to_f64(lse[q0:q0 + n_q].cpu()[pick])
         assert np.isfinite(go).all()
