@@ -49,10 +49,10 @@ MLA_DEV float group_sum(float v) {
 // token, which share the table row and the weights, all of their loads in flight
 // together.
 //
-// Measured (GB300): 4095 tokens x 128 heads of 192 66.3 us (0.89 of the copy
+// Measured (GB300): 4095 tokens x 128 heads of 192 66.6 us (0.89 of the copy
 // bandwidth; 68.0 at the 80 registers a thread takes unlimited, which leave 24
-// warps an SM instead of 32, 104 and 119 with spills at 48 and 40; 73.5 with one
-// head a lane group). 64 x 128 2.1 us, 32768 rows of 128 5.3: the latency of
+// warps an SM instead of 32, 104 and 119 with spills at 48 and 40; 74.1 with one
+// head a lane group). 64 x 128 2.1 us, 32768 rows of 128 5.4: the latency of
 // position -> table row -> store.
 constexpr int kNormThreads = 256;
 
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kNormThreads, 4) mla_norm_rotate_kernel(const 
 // optionally takes the same row in 16 bits.
 //
 // Measured (GB300): 64 tokens, bf16 rows 1.5 us; 32768 tokens into 656-byte rows
-// and `rows` 19.7 us (0.79 of the copy bandwidth): like mla_append_kv_kernel it
+// and `rows` 19.8 us (0.78 of the copy bandwidth): like mla_append_kv_kernel it
 // waits for its loads in turn (slot and row, then the table row) between two
 // stretches of arithmetic, at half of the issue slots.
 // ---------------------------------------------------------------------------

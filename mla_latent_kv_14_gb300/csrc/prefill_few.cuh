@@ -10,8 +10,8 @@
 // that begins the next unit, so that units of a single tile overlap too. Warps none
 // of whose 32 rows is a query only pass the tiles on.
 //
-// Measured (GB300, bf16): 8 x 4 queries over 5461 to 16384 keys, 16 heads 121 us
-// (0.84 of the copy bandwidth; one query tile beside an empty one, a ring of 1.6
+// Measured (GB300, bf16): 8 x 4 queries over 5461 to 16384 keys, 16 heads 123 us
+// (0.83 of the copy bandwidth; one query tile beside an empty one, a ring of 1.6
 // tiles: 168), 16 x 4 over 8192 175 us (0.92), 16 x 256 over 4096 160 us, 64
 // documents of 128 by themselves 38. The rest is the units' starts and ends (some
 // 6000 cycles where they have one tile: queries wait for the scores before them)

@@ -10,9 +10,9 @@
 // 256 queries asked it for 7.5 TB/s and its ring of 1.6 tiles ran dry under that
 // load).
 //
-// Measured (GB300, bf16): 2048 queries behind 32768 keys, 128 heads 2.86 ms in
-// short runs (1.86 PFLOP/s, 0.99 of the cuBLAS burst) and 3.15 in long ones, where
-// power lowers the clock to 1.72 GHz; 4 x 4096 causal 1.76 and 1.91 ms (0.83 and
+// Measured (GB300, bf16): 2048 queries behind 32768 keys, 128 heads 2.82 ms in
+// short runs (1.89 PFLOP/s, 1.01 of the cuBLAS burst) and 3.15 in long ones, where
+// power lowers the clock to 1.72 GHz; 4 x 4096 causal 1.74 and 1.89 ms (0.84 and
 // 0.77). In the steady state a chain takes some 3200 cycles a tile: 1600 from P to
 // the next S (1280 of products, commits and arrivals across the pair), 1400 of
 // softmax, and waits for the other chain's products. A unit's start and end: some

@@ -30,8 +30,8 @@ mla_status launch_norm(norms::NormRotateParams p, void* stream) {
                 norms::kNormThreads, 0, stream, p);
 }
 // Rows of (token, head) from which a lane group takes two heads of a token, which share the table row and the weights
-// (4095 x 128 rows of 192: 68 us against 73.5 with one and 70 with four; 64 x 128, where one fills the card better,
-// 2.1 against 2.3 and 3.4).
+// (4095 x 128 rows of 192: 66.6 us against 74.1 with one and 86.5 with four; 64 x 128, where one fills the card better,
+// 2.1 against 2.5 and 4.4).
 constexpr int64_t kTwoHeads = 32768;
 template <bool kFp16>
 mla_status launch_norm_dim(const norms::NormRotateParams& p, void* stream) {
