@@ -282,7 +282,8 @@ MLA_DEV uint32_t pack_p(float lo, float hi) {
 }
 
 // |c m| from which a row subtracts its reference first: up to there the rounding of c m changes a row's weights by 2^-13 of
-// themselves, no more than the scores' own rounding to fp32 does
+// themselves, no more than the scores' own rounding to fp32 does. The branch costs calls all of whose rows are such 38 to 43 %
+// (2048 queries behind 32768 keys 3.92 ms, 4 x 4096 causal 2.50) and others nothing: it is the one that moves references.
 constexpr float kFar = 0x1p12f;
 
 // Weights of fp16 are formed 2^7 larger: with the reference's slack of 2^8 they reach 2^15, and what fp16 loses, weights below
